@@ -469,6 +469,77 @@ sixbit_status sixbit_block_stats_noalloc(const uint16_t* x_in, const uint16_t* x
 /* Largest n sixbit_block_stats_noalloc accepts. */
 int64_t sixbit_block_stats_noalloc_max_elems(void);
 
+/* ---- a transformer block's feed-forward layer around the W4A8 products --- */
+
+/*
+ * Residual add, root-mean-square norm, block-Hadamard rotation and INT8
+ * quantization in one call (technical summary section 2.A for the rotation
+ * and the INT8 codes, section 4 for fusing the quantization with the work
+ * around it; the norm in front of a quantized layer is the transformer
+ * block's own and the pages leave it out):
+ *   h = x + residual                      (residual may be NULL: h = x)
+ *   sum_out = bf16(h)
+ *   y = h / sqrt(mean_k h^2 + eps) * weight   (weight [K] float, NULL: 1)
+ *   z = y . blockdiag(H_b / sqrt b)       (had_block 0: z = y)
+ *   out->row_scale[m] = max_k |z| / 127,  out->i8_codes = rint(z / row_scale)
+ * all in FP32 from the bf16 inputs; the norm takes h before its rounding.
+ * X, residual, sum_out [M, K] bf16; out's i8_codes and row_scale as for
+ * sixbit_hadamard_quant (its other fields are ignored).  sum_out may be NULL,
+ * may be X or residual (in place), and without a residual must be NULL.
+ * A row of zeros gives scale 0 and codes 0.  A row with an infinity or a NaN,
+ * or whose sum of squares overflows FP32 (|h| near 1e19), gives a NaN scale
+ * and codes 0, so every product of that row is NaN and no other row changes.
+ * M >= 0 (0: nothing is enqueued), K % 128 == 0, b in {0, 16, 64, 256},
+ * K % b == 0, eps > 0 and finite.  X, residual, sum_out, weight and i8_codes
+ * 16-byte aligned.  With mode_dev, runs only when the mode word is INT8.
+ */
+sixbit_status sixbit_add_rmsnorm_quant(const uint16_t* X, const uint16_t* residual, const float* weight, int M, int K,
+                                       float eps, int had_block, const int32_t* mode_dev, uint16_t* sum_out,
+                                       const sixbit_qact* out, int32_t* err_dev, void* stream);
+
+/* Rows sixbit_qgemv takes at most. */
+enum { SIXBIT_QGEMV_MAX_ROWS = 32 };
+
+/*
+ * The INT8 kind of sixbit_qgemm for 1 to 32 rows (single tokens): the same
+ * product of A's i8_codes / row_scale and W's i4_codes / i4_scales (their
+ * other fields are ignored), group sums exact, FP32 from there on, with the
+ * same epilogues; the weights are read once, as INT4, and no workspace is
+ * needed.  Y [M, N] bf16, or Y_f32 when it is non-NULL; residual [M, N] bf16
+ * may be Y.  0 <= M <= SIXBIT_QGEMV_MAX_ROWS (0: nothing is enqueued), any
+ * N >= 1, K % 128 == 0; i8_codes and i4_codes 16-byte aligned, the others
+ * aligned to their type.  With mode_dev, runs only when the mode word is INT8.
+ */
+sixbit_status sixbit_qgemv(const sixbit_qact* A, const sixbit_weights* W, int M, int N, int K, const int32_t* mode_dev,
+                           int epilogue, const uint16_t* residual, uint16_t* Y, float* Y_f32, int32_t* err_dev,
+                           void* stream);
+
+/* Experts sixbit_qgemm_grouped takes at most. */
+enum { SIXBIT_MAX_EXPERTS = 1024 };
+
+/*
+ * The same product grouped by expert: rows [offsets[e], offsets[e + 1]) of A
+ * and Y belong to expert e and meet its weight
+ *   W->i4_codes [E][N, K/2],  W->i4_scales [E][K/128][N]
+ * (E sixbit_pack_weights results side by side).  offsets is a DEVICE array of
+ * E + 1 ascending int32 in [0, M], as a router's count leaves it; row counts
+ * may be ragged, an expert may have none, and the host never reads them.  A
+ * pair that is not ascending within [0, M] is reported as SIXBIT_EDEVICE in
+ * err_dev and read as an expert without rows (a row that two other experts
+ * then claim holds either's result); no memory outside the arrays is
+ * touched.  Rows outside every expert's range are not written.  M: rows of A
+ * and Y (0: nothing is enqueued).  Any N >= 1, K % 128 == 0,
+ * 1 <= E <= SIXBIT_MAX_EXPERTS.  workspace: device memory of
+ * sixbit_qgemm_grouped_workspace_bytes(M, K) bytes, 16-byte aligned; scratch.
+ * Epilogues, alignment and mode_dev as for sixbit_qgemv.
+ */
+sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W, const int32_t* offsets, int E, int M,
+                                   int N, int K, const int32_t* mode_dev, int epilogue, const uint16_t* residual,
+                                   uint16_t* Y, float* Y_f32, void* workspace, int32_t* err_dev, void* stream);
+
+/* Bytes of the workspace sixbit_qgemm_grouped needs for M rows of K. */
+size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K);
+
 /* ---- device-decided branches in a captured CUDA graph ------------------- */
 
 /*

@@ -11,6 +11,7 @@ c_p = C.c_void_p
 MODE_NVFP4, MODE_INT8, MODE_BF16, MODE_SKIP = 1, 2, 3, 4
 FLAG_REFRESH, FLAG_PDR, FLAG_POSTSKIP, FLAG_NEAR = 1 << 8, 1 << 9, 1 << 10, 1 << 11
 EPI_NONE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
+QGEMV_MAX_ROWS, MAX_EXPERTS = 32, 1024
 MODE_NAMES = {MODE_NVFP4: "NVFP4", MODE_INT8: "INT8", MODE_BF16: "BF16", MODE_SKIP: "SKIP"}
 
 
@@ -71,6 +72,13 @@ EXPORTS = {
     "sixbit_skip_apply": (C.c_int, [c_p, c_p, c_p, C.c_int64, c_p, c_p, c_p, c_p, c_p]),
     "sixbit_block_stats_mxfp8": (C.c_int, [c_p, c_p, c_p, c_p, C.c_int64, c_p, c_p, c_p, c_p, c_p]),
     "sixbit_skip_apply_mxfp8": (C.c_int, [c_p, c_p, c_p, c_p, C.c_int64, c_p, c_p, c_p, c_p, c_p]),
+    "sixbit_add_rmsnorm_quant": (C.c_int, [c_p, c_p, c_p, C.c_int, C.c_int, C.c_float, C.c_int, c_p, c_p,
+                                           C.POINTER(QAct), c_p, c_p]),
+    "sixbit_qgemv": (C.c_int, [C.POINTER(QAct), C.POINTER(Weights), C.c_int, C.c_int, C.c_int, c_p, C.c_int, c_p,
+                               c_p, c_p, c_p, c_p]),
+    "sixbit_qgemm_grouped": (C.c_int, [C.POINTER(QAct), C.POINTER(Weights), c_p, C.c_int, C.c_int, C.c_int, C.c_int,
+                                       c_p, C.c_int, c_p, c_p, c_p, c_p, c_p, c_p]),
+    "sixbit_qgemm_grouped_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int]),
     "sixbit_block_stats_noalloc": (C.c_int, [c_p, c_p, c_p, C.c_int64, c_p, c_p, c_p, c_p]),
     "sixbit_block_stats_noalloc_max_elems": (C.c_int64, []),
     "sixbit_dit_begin": (C.c_int, [C.POINTER(PolicyCfg), C.POINTER(DitBlocks), c_p, c_p, c_p]),

@@ -2,6 +2,7 @@
 // construction for the GEMM's TMA loads, and kernel dispatch.  The library
 // allocates no device memory.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cudaTypedefs.h>
 
@@ -62,6 +63,8 @@ void gemm_debug_params(GemmParams& p) {
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 static bool valid_block(int b) { return b == 16 || b == 64 || b == 256; }
 
@@ -536,6 +539,96 @@ sixbit_status sixbit_dit_skip_run(const sixbit_policy_cfg* cfg, const sixbit_dit
   const sixbit_status s = check_blocks(cfg, blocks, l, scratch);
   if (s != SIXBIT_OK) return s;
   return cuda_status(launch_dit_skip_run(*cfg, *blocks, l, scratch, err_dev, static_cast<cudaStream_t>(stream)));
+}
+
+sixbit_status sixbit_add_rmsnorm_quant(const uint16_t* X, const uint16_t* residual, const float* weight, int M, int K,
+                                       float eps, int had_block, const int32_t* mode_dev, uint16_t* sum_out,
+                                       const sixbit_qact* out, int32_t* err_dev, void* stream) {
+  (void)err_dev;
+  if (M < 0 || K <= 0 || K % 128 != 0 || (had_block != 0 && (!valid_block(had_block) || K % had_block != 0)))
+    return SIXBIT_ESHAPE;
+  if (!(eps > 0.f) || !std::isfinite(eps) || out == nullptr || (sum_out != nullptr && residual == nullptr))
+    return SIXBIT_EINVAL;
+  if (M == 0) return SIXBIT_OK;
+  if (X == nullptr || out->i8_codes == nullptr || out->row_scale == nullptr) return SIXBIT_EINVAL;
+  if (!aligned16(X) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum_out) ||
+      !aligned16(out->i8_codes) || !aligned_to(out->row_scale, 4))
+    return SIXBIT_EALIGN;
+  const sixbit_status s = check_device();
+  if (s != SIXBIT_OK) return s;
+  return cuda_status(launch_add_rmsnorm_quant(X, residual, weight, M, K, eps, had_block, mode_dev, sum_out,
+                                              out->i8_codes, out->row_scale, static_cast<cudaStream_t>(stream)));
+}
+
+// The checks that sixbit_qgemv and sixbit_qgemm_grouped share, and their
+// kernels' parameters.  *empty: there is nothing to do.
+static sixbit_status rows_params(const sixbit_qact* A, const sixbit_weights* W, const int32_t* offsets, int E, int M,
+                                 int N, int K, const int32_t* mode_dev, int epilogue, const uint16_t* residual,
+                                 uint16_t* Y, float* Y_f32, int32_t* err_dev, RowsParams* p, bool* empty) {
+  *empty = false;
+  if (A == nullptr || W == nullptr) return SIXBIT_EINVAL;
+  if (epilogue != SIXBIT_EPI_NONE && epilogue != SIXBIT_EPI_GELU && epilogue != SIXBIT_EPI_RESIDUAL)
+    return SIXBIT_EINVAL;
+  if (M < 0 || N <= 0 || K <= 0 || K % 128 != 0) return SIXBIT_ESHAPE;
+  if (M == 0) {
+    *empty = true;
+    return SIXBIT_OK;
+  }
+  if (A->i8_codes == nullptr || A->row_scale == nullptr || W->i4_codes == nullptr || W->i4_scales == nullptr ||
+      (Y == nullptr && Y_f32 == nullptr) || (epilogue == SIXBIT_EPI_RESIDUAL && residual == nullptr))
+    return SIXBIT_EINVAL;
+  if (!aligned16(A->i8_codes) || !aligned16(W->i4_codes) || !aligned_to(A->row_scale, 4) ||
+      !aligned_to(W->i4_scales, 4) || !aligned_to(offsets, 4) || !aligned_to(residual, 2) || !aligned_to(Y, 2) ||
+      !aligned_to(Y_f32, 4))
+    return SIXBIT_EALIGN;
+  *p = RowsParams{};
+  p->codes = A->i8_codes;
+  p->row_scale = A->row_scale;
+  p->w4 = W->i4_codes;
+  p->w4_scale = W->i4_scales;
+  p->offsets = offsets;
+  p->M = M;
+  p->N = N;
+  p->K = K;
+  p->E = E;
+  p->mode_dev = mode_dev;
+  p->epilogue = epilogue;
+  p->residual = residual;
+  p->Y = Y_f32 != nullptr ? nullptr : Y;
+  p->Yf = Y_f32;
+  p->err = err_dev;
+  return check_device();
+}
+
+sixbit_status sixbit_qgemv(const sixbit_qact* A, const sixbit_weights* W, int M, int N, int K, const int32_t* mode_dev,
+                           int epilogue, const uint16_t* residual, uint16_t* Y, float* Y_f32, int32_t* err_dev,
+                           void* stream) {
+  if (M > SIXBIT_QGEMV_MAX_ROWS) return SIXBIT_ESHAPE;
+  RowsParams p;
+  bool empty;
+  const sixbit_status s = rows_params(A, W, nullptr, 1, M, N, K, mode_dev, epilogue, residual, Y, Y_f32, err_dev, &p,
+                                      &empty);
+  if (s != SIXBIT_OK || empty) return s;
+  return cuda_status(launch_w4a8_rows(p, M, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K) {
+  if (M <= 0 || K <= 0) return 0;
+  return static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
+}
+
+sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W, const int32_t* offsets, int E, int M,
+                                   int N, int K, const int32_t* mode_dev, int epilogue, const uint16_t* residual,
+                                   uint16_t* Y, float* Y_f32, void* workspace, int32_t* err_dev, void* stream) {
+  if (E < 1 || E > SIXBIT_MAX_EXPERTS) return SIXBIT_ESHAPE;
+  RowsParams p;
+  bool empty;
+  const sixbit_status s = rows_params(A, W, offsets, E, M, N, K, mode_dev, epilogue, residual, Y, Y_f32, err_dev, &p,
+                                      &empty);
+  if (s != SIXBIT_OK || empty) return s;
+  if (offsets == nullptr || workspace == nullptr) return SIXBIT_EINVAL;
+  if (!aligned16(workspace)) return SIXBIT_EALIGN;
+  return cuda_status(launch_w4a8_rows(p, M, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

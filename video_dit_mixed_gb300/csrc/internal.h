@@ -105,4 +105,28 @@ cudaError_t launch_w4_expand(const uint8_t* codes, int N, int K, uint16_t* ws, c
 cudaError_t launch_qgemm_w4a8(const CUtensorMap& a_s8, const CUtensorMap& w_f16, const CUtensorMap& y,
                               const GemmParams& p, cudaStream_t st);
 
+
+// Residual add, RMS norm, rotation (b = 0: none) and INT8 quantization of [M, K] rows; res, w and sum_out may be NULL.
+cudaError_t launch_add_rmsnorm_quant(const uint16_t* x, const uint16_t* res, const float* w, int M, int K, float eps,
+                                     int b, const int32_t* mode_dev, uint16_t* sum_out, int8_t* codes,
+                                     float* row_scale, cudaStream_t st);
+
+// A W4A8 product on the stored operands: one weight (offsets NULL, E 1) or
+// E of them, expert e's rows [offsets[e], offsets[e + 1]) of [M, K].
+struct RowsParams {
+  const int8_t* codes;     // [M, K]
+  const float* row_scale;  // [M]
+  const uint8_t* w4;       // [E][N, K/2]
+  const float* w4_scale;   // [E][K/128][N]
+  const int32_t* offsets;  // [E + 1] on the device, or NULL
+  int M, N, K, E;
+  const int32_t* mode_dev;
+  int epilogue;
+  const uint16_t* residual;
+  uint16_t* Y;
+  float* Yf;
+  int32_t* err;
+};
+cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st);
+
 }  // namespace sixbit

@@ -1,0 +1,239 @@
+// W4A8 products of few rows: INT8 activation codes against INT4 weights with
+// one scale per 128 inputs, for single tokens and for experts that got a few
+// (technical summary sections 2.A and 4; the GEMM form is qgemm_w4a8.cu).
+//
+//   Y[m, n] = s_m[m] * sum_g s_w[g][n] * acc_g[m, n]
+//   acc_g[m, n] = sum_{k in group g} qa[m, k] * qw[n, k]    (exact integers)
+//
+// With 1..32 rows the call reads each weight byte once and multiplies it a few
+// times: the weights' bytes bound it, so they go straight from global memory
+// to registers as INT4 and are never expanded in memory.
+//
+// The products run on mma.m16n8k16 with fp16 operands and FP32 accumulation:
+// weight rows are the 16-row operand, tokens the 8-column one.  Codes and
+// nibbles are exact in fp16 and a group's sum stays below 2^17, so the
+// accumulator holds the exact integer; the scale is applied after each group.
+// The sum over k may be taken in any order as long as both operands agree, so
+// a lane keeps 32 consecutive k of a group (16 bytes of nibbles, 32 code
+// bytes: whole 16-byte loads) and hands four of them to each MMA.  Within a
+// word of eight nibbles the pairs are (k, k + 4): the two halves of one
+// masked word.
+//
+// A CTA owns 16 MT weight rows and its eight warps split the groups of K; their
+// FP32 sums meet in shared memory in a fixed order, where the epilogue runs.
+#include <cstdint>
+
+#include "common.cuh"
+#include "ctx_cache.h"
+#include "gemm_common.cuh"
+#include "internal.h"
+
+namespace sixbit {
+namespace rows {
+
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One FMA or subtraction per fp16 pair, exact (integers below 2048).
+__device__ __forceinline__ uint32_t sub2(uint32_t x, uint32_t c) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t m, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(m), "r"(c));
+  return d;
+}
+
+// Eight nibbles -> pairs o[j] = (k = j, k = j + 4).  Flipping a nibble's sign
+// bit makes it v + 8; under the exponent of 1024 the low nibbles read
+// 1032 + v, the high ones 1024 + 16 (v + 8).
+__device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t (&o)[4]) {
+  const uint32_t h = w >> 8;
+  o[0] = sub2((w & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
+  o[1] = fma2((w & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);  // / 16 - 72
+  o[2] = sub2((h & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
+  o[3] = fma2((h & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);
+}
+
+// Eight s8 codes (k = 0..3 in a, 4..7 in b) -> the same pairs.
+__device__ __forceinline__ void codes_f16(uint32_t a, uint32_t b, uint32_t (&o)[4]) {
+  a ^= 0x80808080u;
+  b ^= 0x80808080u;
+  const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);
+  o[0] = sub2(__byte_perm(lo, 0x64646464u, 0x4140), 0x64806480u);
+  o[1] = sub2(__byte_perm(lo, 0x64646464u, 0x4342), 0x64806480u);
+  o[2] = sub2(__byte_perm(hi, 0x64646464u, 0x4140), 0x64806480u);
+  o[3] = sub2(__byte_perm(hi, 0x64646464u, 0x4342), 0x64806480u);
+}
+
+// Rows [*first, *first + *count) of expert e; an offset pair that is not
+// ascending within [0, M] is reported and read as an expert without rows.
+__device__ __forceinline__ void expert_rows(const RowsParams& p, int e, int* first, int* count) {
+  *first = 0;
+  *count = p.M;
+  if (p.offsets == nullptr) return;
+  const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+  const bool ok = a >= 0 && a <= b && b <= p.M;
+  if (!ok && threadIdx.x == 0) set_error(p.err, SIXBIT_EDEVICE);
+  *first = ok ? a : 0;
+  *count = ok ? b - a : 0;
+}
+
+template <int MT, int NT>
+__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsParams p) {
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  constexpr int kN = 16 * MT, kT = 8 * NT;
+  __shared__ float part[kWarps][kT][kN + 1];
+  int first, count;
+  expert_rows(p, blockIdx.y, &first, &count);
+  if (count == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int groups = p.K / 128, n0 = blockIdx.x * kN;
+  const size_t kb = static_cast<size_t>(p.K) / 2;
+  const uint8_t* w4 = p.w4 + static_cast<size_t>(blockIdx.y) * p.N * kb;
+  const float* w4s = p.w4_scale + static_cast<size_t>(blockIdx.y) * groups * p.N;
+
+  int n[MT][2];
+  const uint8_t* wrow[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      n[m][h] = min(n0 + 16 * m + 8 * h + g, p.N - 1);  // (the surplus rows are not stored)
+      wrow[m][h] = w4 + n[m][h] * kb + t * 16;
+    }
+  }
+
+  for (int t0 = 0; t0 < count; t0 += kT) {
+    const int8_t* xrow[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      xrow[j] = p.codes + static_cast<size_t>(first + min(t0 + 8 * j + g, count - 1)) * p.K + t * 32;
+    float sum[MT][NT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[m][j][i] = 0.f;
+
+    uint4 w[MT][2];
+    float sc[MT][2];
+    auto fetch = [&](int gr) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[m][h] = __ldg(reinterpret_cast<const uint4*>(wrow[m][h] + static_cast<size_t>(gr) * 64));
+          sc[m][h] = __ldg(w4s + static_cast<size_t>(gr) * p.N + n[m][h]);
+        }
+    };
+    if (warp < groups) fetch(warp);
+    for (int gr = warp; gr < groups; gr += kWarps) {
+      uint4 wc[MT][2];
+      float s[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wc[m][h] = w[m][h];
+          s[m][h] = sc[m][h];
+        }
+      uint4 x[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint4* xp = reinterpret_cast<const uint4*>(xrow[j] + gr * 128);
+        x[j][0] = __ldg(xp);
+        x[j][1] = __ldg(xp + 1);
+      }
+      if (gr + kWarps < groups) fetch(gr + kWarps);
+      float acc[MT][NT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // eight k of the lane
+        uint32_t b[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4& v = x[j][q >> 1];
+          codes_f16((q & 1) ? v.z : v.x, (q & 1) ? v.w : v.y, b[j]);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          uint32_t lo[4], hi[4];
+          nibbles_f16(q == 0 ? wc[m][0].x : q == 1 ? wc[m][0].y : q == 2 ? wc[m][0].z : wc[m][0].w, lo);
+          nibbles_f16(q == 0 ? wc[m][1].x : q == 1 ? wc[m][1].y : q == 2 ? wc[m][1].z : wc[m][1].w, hi);
+          const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma16816(acc[m][j], a0, b[j][0], b[j][1]);
+            mma16816(acc[m][j], a1, b[j][2], b[j][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[m][j][i] = fmaf(s[m][i >> 1], acc[m][j][i], sum[m][j][i]);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] = sum[m][j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kT * kN; i += kWarps * 32) {
+      const int tok = i / kN, c = i % kN, col = n0 + c, row = first + t0 + tok;
+      if (t0 + tok >= count || col >= p.N) continue;
+      float y = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) y += part[k][tok][c];
+      y = __fmul_rn(y, __ldg(p.row_scale + row));
+      const size_t at = static_cast<size_t>(row) * p.N + col;
+      if (p.epilogue == SIXBIT_EPI_GELU)
+        y = f2_lo(gelu_pair(f2_pack(y, y)));
+      else if (p.epilogue == SIXBIT_EPI_RESIDUAL)
+        y = __fadd_rn(y, __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16));
+      if (p.Yf != nullptr)
+        p.Yf[at] = y;
+      else
+        p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(y, 0.f)) & 0xFFFFu);
+    }
+    if (t0 + kT < count) __syncthreads();
+  }
+}
+
+template <int MT>
+cudaError_t launch(const RowsParams& p, int most, cudaStream_t st) {
+  const dim3 grid((p.N + 16 * MT - 1) / (16 * MT), p.E);
+  if (most <= 8)
+    rows_kernel<MT, 1><<<grid, kWarps * 32, 0, st>>>(p);
+  else if (most <= 16)
+    rows_kernel<MT, 2><<<grid, kWarps * 32, 0, st>>>(p);
+  else
+    rows_kernel<MT, 4><<<grid, kWarps * 32, 0, st>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace rows
+
+// most: rows of one expert at most (they may be fewer; more are walked in turn).
+cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st) { return rows::launch<1>(p, most, st); }
+
+}  // namespace sixbit

@@ -12,8 +12,8 @@ import ctypes as C
 import torch
 
 from . import abi
-from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MODE_BF16, MODE_INT8, MODE_NVFP4, MODE_SKIP,  # noqa: F401
-                  DitBlocks, PolicyCfg, PolicyState, QAct, Stats, Weights, check, lib)
+from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MAX_EXPERTS, MODE_BF16, MODE_INT8, MODE_NVFP4,  # noqa: F401
+                  MODE_SKIP, QGEMV_MAX_ROWS, DitBlocks, PolicyCfg, PolicyState, QAct, Stats, Weights, check, lib)
 
 _lib = lib()
 
@@ -235,6 +235,162 @@ def skip_apply_mxfp8(x_in, codes, scales, x_out, stats: torch.Tensor, scratch: t
     check(_lib.sixbit_skip_apply_mxfp8(_p(x_in), _p(codes), _p(scales), _p(x_out), n, _p(mode_dev), _p(stats),
                                        _p(scratch), None, _stream(stream)), "skip_apply_mxfp8")
     return x_out
+
+
+# ---- a feed-forward layer around the W4A8 products --------------------------
+# These three check their tensors (type, shape, density, device) before the
+# pointers leave Python, and raise ValueError.
+
+def _tensor(t, name: str, dtype, shape, like=None):
+    """t's data pointer (None for None) after checking that it is a dense CUDA tensor of this type and shape."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be densely packed (row-major), strides {t.stride()}")
+    if not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError(f"{name} must be on {'the GPU' if like is None else like.device}, not {t.device}")
+    return t.data_ptr()
+
+
+def _new(stream, *shape_dtype_device):
+    """Empty tensors for a call on `stream` (None: the current one), allocated on that stream."""
+    if stream is None:
+        return [torch.empty(s, dtype=d, device=v) for s, d, v in shape_dtype_device]
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=d, device=v) for s, d, v in shape_dtype_device]
+
+
+def _word(t, name: str, like):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < 1 or t.device != like.device:
+        raise ValueError(f"{name}: an int32 word on {like.device} expected")
+    return t.data_ptr()
+
+
+def int8_act(codes: torch.Tensor, row_scale: torch.Tensor) -> QActTensors:
+    """INT8 activations that already exist: codes int8 [M, K], row_scale float32 [M]."""
+    a = QActTensors.__new__(QActTensors)
+    a.m, a.k = codes.shape
+    a.fp4_codes = a.fp4_scales = a.tensor_amax = a.tensor_scale = a.rotated = None
+    a.i8_codes, a.row_scale = codes, row_scale
+    return a
+
+
+class Int4Weights:
+    """The INT4 form alone of one layer (codes [N, K/2] uint8, scales [K/128, N] float32) or of E experts
+    (codes [E, N, K/2], scales [E, K/128, N]): what qgemv and qgemm_grouped read, 0.53 bytes a weight."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        self.i4_codes, self.i4_scales = codes, scales
+        self.n, self.k = codes.shape[-2], 2 * codes.shape[-1]
+        self.experts = codes.shape[0] if codes.dim() == 3 else None
+
+
+def pack_experts(w: torch.Tensor, had_block: int, stream=None) -> Int4Weights:
+    """Experts' weights [E, N, K] float32, each packed by pack_weights, INT4 form kept."""
+    if w.dim() != 3:
+        raise ValueError(f"w: [E, N, K] expected, got {tuple(w.shape)}")
+    e, n, k = w.shape
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(w.device)):
+        codes = torch.empty((e, n, k // 2), dtype=torch.uint8, device=w.device)
+        scales = torch.empty((e, k // 128, n), dtype=torch.float32, device=w.device)
+        one = PackedWeights(n, k, w.device)
+        for i in range(e):
+            pack_weights(w[i], had_block, one)
+            codes[i].copy_(one.i4_codes)
+            scales[i].copy_(one.i4_scales)
+    return Int4Weights(codes, scales)
+
+
+def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                      eps: float = 1e-6, had_block: int = 0, out: QActTensors | None = None, sum_out=None,
+                      mode_dev=None, stream=None):
+    """h = x + residual, RMS norm times weight, rotation by had_block (0: none), INT8 codes and row scales.
+
+    x, residual: bf16 [M, K]; weight: float32 [K].  Returns (activations, h): the QActTensors that qgemv,
+    qgemm_grouped and qgemm read, and bf16(h) (in sum_out, which may be x or residual; x itself when there
+    is no residual)."""
+    if x.dim() != 2:
+        raise ValueError(f"x: [M, K] expected, got {tuple(x.shape)}")
+    m, k = x.shape
+    bf = torch.bfloat16
+    px, pr = _tensor(x, "x", bf, (m, k)), _tensor(residual, "residual", bf, (m, k), x)
+    pw = _tensor(weight, "weight", torch.float32, (k,), x)
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out without a residual")
+    elif sum_out is None:
+        sum_out, = _new(stream, ((m, k), bf, x.device))
+    if out is None:
+        codes, scale = _new(stream, ((m, k), torch.int8, x.device), ((m,), torch.float32, x.device))
+        out = int8_act(codes, scale)
+    a = QAct(None, None, None, None, _tensor(out.i8_codes, "out.i8_codes", torch.int8, (m, k), x),
+             _tensor(out.row_scale, "out.row_scale", torch.float32, (m,), x), None)
+    check(_lib.sixbit_add_rmsnorm_quant(px, pr, pw, m, k, eps, had_block, _word(mode_dev, "mode_dev", x),
+                                        _tensor(sum_out, "sum_out", bf, (m, k), x), C.byref(a), None,
+                                        _stream(stream)), "add_rmsnorm_quant")
+    return out, (x if residual is None else sum_out)
+
+
+def _w4a8(a, w, lead, epilogue, residual, out, out_f32, mode_dev, err, stream):
+    """Checked operands of qgemv and qgemm_grouped: (A, W, epilogue arguments, out, m, n, k)."""
+    codes = a.i8_codes
+    if codes is None or codes.dim() != 2:
+        raise ValueError("INT8 activations expected")
+    m, k = codes.shape
+    n = w.n
+    if w.k != k:
+        raise ValueError(f"activations have {k} inputs, the weights {w.k}")
+    ca = QAct(None, None, None, None, _tensor(codes, "i8_codes", torch.int8, (m, k)),
+              _tensor(a.row_scale, "row_scale", torch.float32, (m,), codes), None)
+    cw = Weights(None, None, None, None, _tensor(w.i4_codes, "i4_codes", torch.uint8, lead + (n, k // 2), codes),
+                 _tensor(w.i4_scales, "i4_scales", torch.float32, lead + (k // 128, n), codes), None)
+    if out is None:
+        out, = _new(stream, ((m, n), torch.float32 if out_f32 else torch.bfloat16, codes.device))
+    f32 = out.dtype == torch.float32
+    py = _tensor(out, "out", torch.float32 if f32 else torch.bfloat16, (m, n), codes)
+    if residual is not None and epilogue != EPI_RESIDUAL:
+        raise ValueError("a residual without the residual epilogue")
+    pr = _tensor(residual, "residual", torch.bfloat16, (m, n), codes)
+    return ca, cw, (_word(mode_dev, "mode_dev", codes), epilogue, pr, None if f32 else py, py if f32 else None), out, \
+        _word(err, "err", codes), m, n, k
+
+
+def qgemv(a: QActTensors, w, epilogue: int = EPI_NONE, residual=None, out=None, out_f32: bool = False, mode_dev=None,
+          err=None, stream=None):
+    """The W4A8 product of 1 to QGEMV_MAX_ROWS rows (sixbit_qgemv).  w: PackedWeights or Int4Weights.  Returns
+    out: bf16 [M, N], or float32 with out_f32 or a float32 `out`."""
+    ca, cw, epi, out, perr, m, n, k = _w4a8(a, w, (), epilogue, residual, out, out_f32, mode_dev, err, stream)
+    check(_lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, *epi, perr, _stream(stream)), "qgemv")
+    return out
+
+
+def qgemm_grouped_workspace_bytes(m: int, k: int) -> int:
+    return int(_lib.sixbit_qgemm_grouped_workspace_bytes(m, k))
+
+
+def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogue: int = EPI_NONE, residual=None,
+                  out=None, out_f32: bool = False, mode_dev=None, err=None, stream=None, ws=None):
+    """The W4A8 product grouped by expert (sixbit_qgemm_grouped): rows offsets[e] .. offsets[e + 1] - 1 of `a`
+    times expert e's weight.  offsets: int32 [E + 1] on the GPU; it is not read on the host.  Rows of `out`
+    outside every expert's range are left as they are.  ws: qgemm_grouped_workspace_bytes(M, K) bytes (uint8),
+    allocated for the call by default."""
+    if w.experts is None:
+        raise ValueError("experts' weights expected (Int4Weights with [E, N, K/2] codes)")
+    ca, cw, epi, out, perr, m, n, k = _w4a8(a, w, (w.experts,), epilogue, residual, out, out_f32, mode_dev, err,
+                                            stream)
+    po = _tensor(offsets, "offsets", torch.int32, (w.experts + 1,), out)
+    need = qgemm_grouped_workspace_bytes(m, k)
+    if ws is None:
+        ws, = _new(stream, ((need,), torch.uint8, out.device))
+    elif not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} dense bytes on the GPU expected")
+    check(_lib.sixbit_qgemm_grouped(C.byref(ca), C.byref(cw), po, w.experts, m, n, k, *epi, ws.data_ptr(), perr,
+                                    _stream(stream)), "qgemm_grouped")
+    return out
 
 
 def policy_cfg(gamma_thr=0.1, cos_thr=0.99, err_cap=0.05, pdr_ratio=30.0, near_rel=1e-6, refresh_bf16=False):
