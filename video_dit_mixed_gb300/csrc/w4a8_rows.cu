@@ -87,6 +87,157 @@ __device__ __forceinline__ void expert_rows(const RowsParams& p, int e, int* fir
   *count = ok ? b - a : 0;
 }
 
+// The row's scale, the epilogue and the store of one output.
+__device__ __forceinline__ void finish(const RowsParams& p, int row, int col, float y) {
+  y = __fmul_rn(y, __ldg(p.row_scale + row));
+  const size_t at = static_cast<size_t>(row) * p.N + col;
+  if (p.epilogue == SIXBIT_EPI_GELU)
+    y = f2_lo(gelu_pair(f2_pack(y, y)));
+  else if (p.epilogue == SIXBIT_EPI_RESIDUAL)
+    y = __fadd_rn(y, __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16));
+  if (p.Yf != nullptr)
+    p.Yf[at] = y;
+  else
+    p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(y, 0.f)) & 0xFFFFu);
+}
+
+// ------------------------------------------------------- one to four tokens --
+constexpr int kR = 4;         // weight rows of a warp
+constexpr int kChunk = 1024;  // k of a warp's load: 16 bytes of nibbles a lane
+
+// T tokens at a time; p.split warps share a row's chunks.
+template <int T>
+__global__ void __launch_bounds__(256) dot_kernel(const RowsParams p, int split) {
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  constexpr int kV = kR * T;
+  __shared__ float part[8 * kV];
+  int first, count;
+  expert_rows(p, blockIdx.y, &first, &count);
+  if (count == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = (blockDim.x >> 5) / split;  // row blocks of the CTA
+  const int kw = warp % split, rw = warp / split;
+  const int groups = p.K / 128, chunks = (p.K + kChunk - 1) / kChunk;
+  const int nc = blockIdx.x * wr * kR, n0 = nc + rw * kR;
+  const size_t kb = static_cast<size_t>(p.K) / 2;
+  const uint8_t* w4 = p.w4 + static_cast<size_t>(blockIdx.y) * p.N * kb + lane * 16;
+  const float* w4s = p.w4_scale + static_cast<size_t>(blockIdx.y) * groups * p.N;
+  int n[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) n[r] = min(n0 + r, p.N - 1);  // (the surplus rows are not stored)
+
+  for (int t0 = 0; t0 < count; t0 += T) {
+    const int8_t* xrow[T];
+#pragma unroll
+    for (int j = 0; j < T; ++j) xrow[j] = p.codes + static_cast<size_t>(first + min(t0 + j, count - 1)) * p.K + lane * 32;
+    float v[T];  // of row n0 + lane % 4, this lane's groups (lane / 4 and every eighth after it)
+#pragma unroll
+    for (int j = 0; j < T; ++j) v[j] = 0.f;
+    for (int c = kw; c < chunks; c += split) {
+      const int gr = c * 8 + (lane >> 2);
+      const bool live = gr < groups;
+      uint4 w[kR], x[T][2];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        w[r] = make_uint4(0, 0, 0, 0);
+        if (live) w[r] = __ldg(reinterpret_cast<const uint4*>(w4 + n[r] * kb + static_cast<size_t>(c) * 512));
+      }
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+        if (live) {
+          const uint4* xp = reinterpret_cast<const uint4*>(xrow[j] + c * kChunk);
+          x[j][0] = __ldg(xp);
+          x[j][1] = __ldg(xp + 1);
+        }
+      }
+      // (a nibble stands 4 bits up in its byte: 1 / 16)
+      const float s = live ? __ldg(w4s + static_cast<size_t>(gr) * p.N + min(n0 + (lane & 3), p.N - 1)) * 0.0625f : 0.f;
+      // codes: even k in one word, odd k in the other, as the two nibbles of a byte stand
+      uint32_t e[T][4], o[T][4];
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        const uint32_t q[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[j][i] = __byte_perm(q[2 * i], q[2 * i + 1], 0x6420);
+          o[j][i] = __byte_perm(q[2 * i], q[2 * i + 1], 0x7531);
+        }
+      }
+      int acc[T][kR];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const uint32_t q[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+        for (int j = 0; j < T; ++j) acc[j][r] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int we = static_cast<int>((q[i] << 4) & 0xF0F0F0F0u), wo = static_cast<int>(q[i] & 0xF0F0F0F0u);
+#pragma unroll
+          for (int j = 0; j < T; ++j) {
+            acc[j][r] = __dp4a(we, static_cast<int>(e[j][i]), acc[j][r]);
+            acc[j][r] = __dp4a(wo, static_cast<int>(o[j][i]), acc[j][r]);
+          }
+        }
+      }
+      // The group's sum over its four lanes, exact, row lane % 4 to each lane.
+      const bool up2 = (lane & 2) != 0, up1 = (lane & 1) != 0;
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        int a[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          a[i] = (up2 ? acc[j][i + 2] : acc[j][i]) + __shfl_xor_sync(0xFFFFFFFFu, up2 ? acc[j][i] : acc[j][i + 2], 2);
+        const int sum = (up1 ? a[1] : a[0]) + __shfl_xor_sync(0xFFFFFFFFu, up1 ? a[0] : a[1], 1);
+        v[j] = fmaf(s, static_cast<float>(sum), v[j]);
+      }
+    }
+    // Sum over the eight groups: while more than one token is left, a lane
+    // hands half of them to its partner and keeps the other half.
+    int o = 16;
+#pragma unroll
+    for (int m = T; m > 1; m >>= 1, o >>= 1) {
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < m / 2; ++i) {
+        const float send = up ? v[i] : v[i + m / 2], keep = up ? v[i + m / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+      }
+    }
+#pragma unroll
+    for (; o > 2; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    if (lane % (32 / T) < kR) part[warp * kV + lane / (32 / T) * kR + (lane & 3)] = v[0];
+    __syncthreads();
+    const int width = wr * kR;
+    for (int i = threadIdx.x; i < width * T; i += blockDim.x) {
+      const int j = i / width, c = i % width;
+      if (t0 + j < count && nc + c < p.N) {
+        float y = 0.f;
+        for (int k = 0; k < split; ++k) y += part[((c / kR) * split + k) * kV + j * kR + c % kR];
+        finish(p, first + t0 + j, nc + c, y);
+      }
+    }
+    if (t0 + T < count) __syncthreads();
+  }
+}
+
+cudaError_t launch_dot(const RowsParams& p, int tokens, cudaStream_t st) {
+  const int chunks = (p.K + kChunk - 1) / kChunk;
+  const int turns = (chunks + 7) / 8, split = (chunks + turns - 1) / turns, wr = 8 / split;
+  const dim3 grid((p.N + wr * kR - 1) / (wr * kR), p.E);
+  const int threads = split * wr * 32;
+  if (tokens == 1)
+    dot_kernel<1><<<grid, threads, 0, st>>>(p, split);
+  else if (tokens == 2)
+    dot_kernel<2><<<grid, threads, 0, st>>>(p, split);
+  else
+    dot_kernel<4><<<grid, threads, 0, st>>>(p, split);
+  note_launch();
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------- up to eight a tile --
+
 template <int MT, int NT>
 __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsParams p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
@@ -203,16 +354,7 @@ __global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsParams p) {
       float y = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) y += part[k][tok][c];
-      y = __fmul_rn(y, __ldg(p.row_scale + row));
-      const size_t at = static_cast<size_t>(row) * p.N + col;
-      if (p.epilogue == SIXBIT_EPI_GELU)
-        y = f2_lo(gelu_pair(f2_pack(y, y)));
-      else if (p.epilogue == SIXBIT_EPI_RESIDUAL)
-        y = __fadd_rn(y, __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16));
-      if (p.Yf != nullptr)
-        p.Yf[at] = y;
-      else
-        p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(y, 0.f)) & 0xFFFFu);
+      finish(p, row, col, y);
     }
     if (t0 + kT < count) __syncthreads();
   }
@@ -234,6 +376,9 @@ cudaError_t launch(const RowsParams& p, int most, cudaStream_t st) {
 }  // namespace rows
 
 // most: rows of one expert at most (they may be fewer; more are walked in turn).
-cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st) { return rows::launch<1>(p, most, st); }
+cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st) {
+  if (most <= 4 || (p.E > 1 && most <= 32)) return rows::launch_dot(p, most, st);
+  return rows::launch<1>(p, most, st);
+}
 
 }  // namespace sixbit

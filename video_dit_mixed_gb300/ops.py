@@ -238,36 +238,44 @@ def skip_apply_mxfp8(x_in, codes, scales, x_out, stats: torch.Tensor, scratch: t
 
 
 # ---- a feed-forward layer around the W4A8 products --------------------------
-# These three check their tensors (type, shape, density, device) before the
-# pointers leave Python, and raise ValueError.
+# These check their tensors (type, shape, density, device) before the pointers
+# leave Python, and raise ValueError.  A call of a single token takes a few
+# microseconds on the GPU, so they do little else: addresses go to ctypes as
+# plain integers and the stream's handle is asked for directly.
 
-def _tensor(t, name: str, dtype, shape, like=None):
-    """t's data pointer (None for None) after checking that it is a dense CUDA tensor of this type and shape."""
+_BF16, _F32, _I8, _I32, _U8 = torch.bfloat16, torch.float32, torch.int8, torch.int32, torch.uint8
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _ptr(t, name: str, dtype, shape, dev: int) -> int:
+    """t's address after checking that it is a dense tensor of this type and shape on GPU `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: a dense {dtype} {tuple(shape)} tensor on GPU {dev} expected, got {t.dtype} "
+                     f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+
+
+def _gpu(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU, not on {t.device}")
+    return dev
+
+
+def _word(t, name: str, dev: int):
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be densely packed (row-major), strides {t.stride()}")
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{name} must be on {'the GPU' if like is None else like.device}, not {t.device}")
+    if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != dev:
+        raise ValueError(f"{name}: an int32 word on GPU {dev} expected")
     return t.data_ptr()
 
 
-def _new(stream, *shape_dtype_device):
-    """Empty tensors for a call on `stream` (None: the current one), allocated on that stream."""
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor allocated on `stream` (None: the current one)."""
     if stream is None:
-        return [torch.empty(s, dtype=d, device=v) for s, d, v in shape_dtype_device]
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return [torch.empty(s, dtype=d, device=v) for s, d, v in shape_dtype_device]
-
-
-def _word(t, name: str, like):
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.numel() < 1 or t.device != like.device:
-        raise ValueError(f"{name}: an int32 word on {like.device} expected")
-    return t.data_ptr()
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def int8_act(codes: torch.Tensor, row_scale: torch.Tensor) -> QActTensors:
@@ -285,8 +293,9 @@ class Int4Weights:
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         self.i4_codes, self.i4_scales = codes, scales
-        self.n, self.k = codes.shape[-2], 2 * codes.shape[-1]
-        self.experts = codes.shape[0] if codes.dim() == 3 else None
+        shape = codes.shape
+        self.n, self.k = shape[-2], 2 * shape[-1]
+        self.experts = shape[0] if len(shape) == 3 else None
 
 
 def pack_experts(w: torch.Tensor, had_block: int, stream=None) -> Int4Weights:
@@ -313,58 +322,73 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, wei
     x, residual: bf16 [M, K]; weight: float32 [K].  Returns (activations, h): the QActTensors that qgemv,
     qgemm_grouped and qgemm read, and bf16(h) (in sum_out, which may be x or residual; x itself when there
     is no residual)."""
-    if x.dim() != 2:
-        raise ValueError(f"x: [M, K] expected, got {tuple(x.shape)}")
-    m, k = x.shape
-    bf = torch.bfloat16
-    px, pr = _tensor(x, "x", bf, (m, k)), _tensor(residual, "residual", bf, (m, k), x)
-    pw = _tensor(weight, "weight", torch.float32, (k,), x)
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out without a residual")
-    elif sum_out is None:
-        sum_out, = _new(stream, ((m, k), bf, x.device))
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: [M, K] expected, got {tuple(shape)}")
+    m, k = shape
+    dev = _gpu(x, "x")
+    px = _ptr(x, "x", _BF16, shape, dev)
+    pw = None if weight is None else _ptr(weight, "weight", _F32, (k,), dev)
+    pr = ps = None
+    if residual is not None:
+        pr = _ptr(residual, "residual", _BF16, shape, dev)
+        if sum_out is None:
+            sum_out = _empty(shape, _BF16, x.device, stream)
+        ps = _ptr(sum_out, "sum_out", _BF16, shape, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual")
     if out is None:
-        codes, scale = _new(stream, ((m, k), torch.int8, x.device), ((m,), torch.float32, x.device))
-        out = int8_act(codes, scale)
-    a = QAct(None, None, None, None, _tensor(out.i8_codes, "out.i8_codes", torch.int8, (m, k), x),
-             _tensor(out.row_scale, "out.row_scale", torch.float32, (m,), x), None)
-    check(_lib.sixbit_add_rmsnorm_quant(px, pr, pw, m, k, eps, had_block, _word(mode_dev, "mode_dev", x),
-                                        _tensor(sum_out, "sum_out", bf, (m, k), x), C.byref(a), None,
-                                        _stream(stream)), "add_rmsnorm_quant")
+        device = x.device
+        out = int8_act(_empty(shape, _I8, device, stream), _empty((m,), _F32, device, stream))
+    a = QAct(None, None, None, None, _ptr(out.i8_codes, "out.i8_codes", _I8, shape, dev),
+             _ptr(out.row_scale, "out.row_scale", _F32, (m,), dev), None)
+    status = _lib.sixbit_add_rmsnorm_quant(px, pr, pw, m, k, eps, had_block,
+                                           None if mode_dev is None else _word(mode_dev, "mode_dev", dev), ps,
+                                           C.byref(a), None,
+                                           _current_raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, "add_rmsnorm_quant")
     return out, (x if residual is None else sum_out)
 
 
 def _w4a8(a, w, lead, epilogue, residual, out, out_f32, mode_dev, err, stream):
-    """Checked operands of qgemv and qgemm_grouped: (A, W, epilogue arguments, out, m, n, k)."""
+    """Checked operands of qgemv and qgemm_grouped, up to `err` in the C calls' order."""
     codes = a.i8_codes
     if codes is None or codes.dim() != 2:
-        raise ValueError("INT8 activations expected")
-    m, k = codes.shape
+        raise ValueError("INT8 activations [M, K] expected")
+    shape = codes.shape
+    m, k = shape
     n = w.n
     if w.k != k:
         raise ValueError(f"activations have {k} inputs, the weights {w.k}")
-    ca = QAct(None, None, None, None, _tensor(codes, "i8_codes", torch.int8, (m, k)),
-              _tensor(a.row_scale, "row_scale", torch.float32, (m,), codes), None)
-    cw = Weights(None, None, None, None, _tensor(w.i4_codes, "i4_codes", torch.uint8, lead + (n, k // 2), codes),
-                 _tensor(w.i4_scales, "i4_scales", torch.float32, lead + (k // 128, n), codes), None)
+    dev = _gpu(codes, "i8_codes")
+    ca = QAct(None, None, None, None, _ptr(codes, "i8_codes", _I8, shape, dev),
+              _ptr(a.row_scale, "row_scale", _F32, (m,), dev), None)
+    cw = Weights(None, None, None, None, _ptr(w.i4_codes, "i4_codes", _U8, lead + (n, k // 2), dev),
+                 _ptr(w.i4_scales, "i4_scales", _F32, lead + (k // 128, n), dev), None)
     if out is None:
-        out, = _new(stream, ((m, n), torch.float32 if out_f32 else torch.bfloat16, codes.device))
-    f32 = out.dtype == torch.float32
-    py = _tensor(out, "out", torch.float32 if f32 else torch.bfloat16, (m, n), codes)
-    if residual is not None and epilogue != EPI_RESIDUAL:
-        raise ValueError("a residual without the residual epilogue")
-    pr = _tensor(residual, "residual", torch.bfloat16, (m, n), codes)
-    return ca, cw, (_word(mode_dev, "mode_dev", codes), epilogue, pr, None if f32 else py, py if f32 else None), out, \
-        _word(err, "err", codes), m, n, k
+        out = _empty((m, n), _F32 if out_f32 else _BF16, codes.device, stream)
+    f32 = out.dtype is _F32
+    py = _ptr(out, "out", _F32 if f32 else _BF16, (m, n), dev)
+    pr = None
+    if residual is not None:
+        if epilogue != EPI_RESIDUAL:
+            raise ValueError("a residual without the residual epilogue")
+        pr = _ptr(residual, "residual", _BF16, (m, n), dev)
+    return (ca, cw, (m, n, k), None if mode_dev is None else _word(mode_dev, "mode_dev", dev), pr,
+            None if f32 else py, py if f32 else None, None if err is None else _word(err, "err", dev), dev, out)
 
 
 def qgemv(a: QActTensors, w, epilogue: int = EPI_NONE, residual=None, out=None, out_f32: bool = False, mode_dev=None,
           err=None, stream=None):
     """The W4A8 product of 1 to QGEMV_MAX_ROWS rows (sixbit_qgemv).  w: PackedWeights or Int4Weights.  Returns
     out: bf16 [M, N], or float32 with out_f32 or a float32 `out`."""
-    ca, cw, epi, out, perr, m, n, k = _w4a8(a, w, (), epilogue, residual, out, out_f32, mode_dev, err, stream)
-    check(_lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, *epi, perr, _stream(stream)), "qgemv")
+    ca, cw, (m, n, k), pm, pr, py, pf, pe, dev, out = _w4a8(a, w, (), epilogue, residual, out, out_f32, mode_dev, err,
+                                                           stream)
+    status = _lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, pm, epilogue, pr, py, pf, pe,
+                               _current_raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, "qgemv")
     return out
 
 
@@ -378,18 +402,22 @@ def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogu
     times expert e's weight.  offsets: int32 [E + 1] on the GPU; it is not read on the host.  Rows of `out`
     outside every expert's range are left as they are.  ws: qgemm_grouped_workspace_bytes(M, K) bytes (uint8),
     allocated for the call by default."""
-    if w.experts is None:
+    experts = getattr(w, "experts", None)
+    if experts is None:
         raise ValueError("experts' weights expected (Int4Weights with [E, N, K/2] codes)")
-    ca, cw, epi, out, perr, m, n, k = _w4a8(a, w, (w.experts,), epilogue, residual, out, out_f32, mode_dev, err,
-                                            stream)
-    po = _tensor(offsets, "offsets", torch.int32, (w.experts + 1,), out)
-    need = qgemm_grouped_workspace_bytes(m, k)
+    ca, cw, (m, n, k), pm, pr, py, pf, pe, dev, out = _w4a8(a, w, (experts,), epilogue, residual, out, out_f32,
+                                                           mode_dev, err, stream)
+    po = _ptr(offsets, "offsets", _I32, (experts + 1,), dev)
+    need = _lib.sixbit_qgemm_grouped_workspace_bytes(m, k)
     if ws is None:
-        ws, = _new(stream, ((need,), torch.uint8, out.device))
-    elif not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws: {need} dense bytes on the GPU expected")
-    check(_lib.sixbit_qgemm_grouped(C.byref(ca), C.byref(cw), po, w.experts, m, n, k, *epi, ws.data_ptr(), perr,
-                                    _stream(stream)), "qgemm_grouped")
+        ws = _empty((need,), _U8, out.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
+    status = _lib.sixbit_qgemm_grouped(C.byref(ca), C.byref(cw), po, experts, m, n, k, pm, epilogue, pr, py, pf,
+                                       ws.data_ptr(), pe,
+                                       _current_raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        check(status, "qgemm_grouped")
     return out
 
 
