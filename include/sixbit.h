@@ -529,7 +529,7 @@ enum { SIXBIT_MAX_EXPERTS = 1024 };
  * then claim holds either's result); no memory outside the arrays is
  * touched.  Rows outside every expert's range are not written.  M: rows of A
  * and Y (0: nothing is enqueued).  Any N >= 1, K % 128 == 0,
- * 1 <= E <= SIXBIT_MAX_EXPERTS.  workspace: device memory of
+ * 1 <= E <= SIXBIT_MAX_EXPERTS, E N < 2^31 - 128.  workspace: device memory of
  * sixbit_qgemm_grouped_workspace_bytes(M, K) bytes, 16-byte aligned; scratch.
  * Epilogues, alignment and mode_dev as for sixbit_qgemv.
  */

@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsixbit.so")
 SOURCES = ["api.cu", "hadamard_quant.cu", "stats_policy.cu", "qgemm.cu", "qgemm_w4a8.cu", "noalloc.cu", "graph.cu",
-           "rmsnorm_quant.cu", "w4a8_rows.cu"]
+           "rmsnorm_quant.cu", "w4a8_rows.cu", "w4a8_grouped.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

@@ -138,6 +138,22 @@ static bool make_map_s8(CUtensorMap* m, const int8_t* base, int rows, int cols) 
   return r == CUDA_SUCCESS;
 }
 
+// INT4 codes [rows, K/2] bytes for the grouped product: box 64 bytes (one
+// scale group) x 128 rows, 64-byte swizzle (16-byte chunk c of row r at chunk
+// c ^ ((r >> 1) & 3)), out-of-bounds rows read as zero.
+static bool make_w4_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int K) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  cuuint32_t box[2] = {64, 128};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // bf16 output Y [rows, cols] for the GEMM epilogue's TMA stores: box 32
 // columns (64 bytes) x 32 rows, 64-byte swizzle.
 static bool make_store_map(CUtensorMap* m, const uint16_t* Y, int rows, int cols) {
@@ -620,7 +636,8 @@ size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K) {
 sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W, const int32_t* offsets, int E, int M,
                                    int N, int K, const int32_t* mode_dev, int epilogue, const uint16_t* residual,
                                    uint16_t* Y, float* Y_f32, void* workspace, int32_t* err_dev, void* stream) {
-  if (E < 1 || E > SIXBIT_MAX_EXPERTS) return SIXBIT_ESHAPE;
+  // (E N weight rows are a tensor map's coordinate)
+  if (E < 1 || E > SIXBIT_MAX_EXPERTS || static_cast<int64_t>(E) * N > INT32_MAX - 128) return SIXBIT_ESHAPE;
   RowsParams p;
   bool empty;
   const sixbit_status s = rows_params(A, W, offsets, E, M, N, K, mode_dev, epilogue, residual, Y, Y_f32, err_dev, &p,
@@ -628,7 +645,19 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   if (s != SIXBIT_OK || empty) return s;
   if (offsets == nullptr || workspace == nullptr) return SIXBIT_EINVAL;
   if (!aligned16(workspace)) return SIXBIT_EALIGN;
-  return cuda_status(launch_w4a8_rows(p, M, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M <= 32) return cuda_status(launch_w4a8_rows(p, M, st));
+  GemmParams dbg;
+  gemm_debug_params(dbg);
+  p.wait_ns = dbg.wait_ns;
+  p.withhold_first = dbg.withhold_first;
+  uint16_t* x16 = static_cast<uint16_t*>(workspace);
+  CUtensorMap mw, mx;
+  if (!make_w4_map(&mw, W->i4_codes, static_cast<int64_t>(E) * N, K) ||
+      !make_map(&mx, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, M, K, 32))
+    return SIXBIT_ECUDA;
+  if (launch_codes_f16(p.codes, M, K, mode_dev, x16, st) != cudaSuccess) return SIXBIT_ECUDA;
+  return cuda_status(launch_w4a8_grouped(mw, mx, p, M < 64 * static_cast<int64_t>(E), st));
 }
 
 }  // extern "C"

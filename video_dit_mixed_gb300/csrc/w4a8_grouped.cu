@@ -1,0 +1,587 @@
+// W4A8 product grouped by expert on the tcgen05 tensor cores of sm_103a:
+// ragged row counts on the device, INT4 weights read as they are stored
+// (technical summary sections 2.A and 4; the dense GEMM is qgemm_w4a8.cu).
+//
+//   rows m of expert e:  Y[m, n] = s_m[m] * sum_g s_w[e][g][n] * acc_g[m, n]
+//   acc_g[m, n] = sum_{k in group g} qa[m, k] * qw[e][n, k]   (exact integers)
+//
+// Integers run through kind::f16 as in the dense GEMM: codes and nibbles are
+// exact in fp16, a group's sum (below 2^17) exact in the FP32 accumulator, and
+// the group's scale is applied when the accumulator is read back.
+//
+// The operands' roles are the dense GEMM's swapped.  There the weights are
+// expanded to fp16 in memory once per call, which many rows pay for; an expert
+// with few rows cannot pay 4.5 bytes of traffic for a weight that holds half
+// of one.  Here the 128 weight rows of a tile are the A operand in tensor
+// memory: converter warps take a group's nibbles (64 bytes of a row) from
+// shared memory, turn them into fp16 in registers and store them into the row's
+// tensor-memory lane.  The tokens are the B operand in shared memory; their
+// codes are expanded to fp16 once per call (2 bytes a code, written and read
+// mostly in L2).  A weight's nibble pair (k, k + 4) is what one mask of a
+// 32-bit word leaves, so within each eight inputs both operands hold the
+// order 0 4 1 5 2 6 3 7.  An accumulator lane is a weight row, so a group's
+// scale is one number a thread.
+//
+// Work.  A tile is 128 weight rows by up to NT rows of one expert; tiles are
+// numbered expert by expert, weight tiles fastest, and a persistent CTA per SM
+// takes every gridDim-th one, finding its expert by bisection in the prefix
+// sums that each CTA takes of the row counts on entry.  The MMA's token
+// count is the tile's own (rounded up to 16), as are the boxes copied (32
+// rows each), so a ragged end costs what it holds.  Two forms, by the mean
+// rows per expert:
+//   NT = 192  eight fold warps, two accumulators; the tensor cores bound it
+//   NT = 32   for experts with few rows: eight converter warps and deep rings
+//             (12 weight tiles of 8 KB in flight); the weights' bytes bound it
+//
+// Warps (16):
+//   0       TMA producer: 128 x 64-byte nibble tiles
+//   2       TMA producer: fp16 token tiles
+//   1, 3    MMA issuers, even and odd groups (one issuer's waits leave the
+//           tensor core idle, as measured in the dense GEMM); warp 1 also
+//           allocates tensor memory
+//   4 ..    converters, one warp per 32-lane quarter (narrow form: two such
+//           sets, even and odd groups)
+//   .. 15   fold + epilogue
+// One commit per group, onto the token slot's barrier, tells the producer that
+// the slot is free, the converters that the group's A slot is, and the fold
+// warps that its accumulator is complete.  That barrier cannot run a phase
+// past any of these waits: its next phase is group g + SX, whose MMAs need a
+// fold of group g + SX - NB > g and a conversion of group g + SX > g + NA.
+//
+// Every mbarrier wait is bounded; on expiry the kernel records
+// SIXBIT_ETIMEOUT, raises the abort flag, waits (bounded) for its copies and
+// tensor-core work in flight, frees tensor memory and returns.
+#include <cstdint>
+
+#include "common.cuh"
+#include "ctx_cache.h"
+#include "gemm_common.cuh"
+#include "internal.h"
+#include "w4a8_common.cuh"
+
+namespace sixbit {
+namespace grouped {
+
+constexpr int kBM = 128;         // weight rows of a tile
+constexpr int kThreads = 512;
+constexpr int kWSlot = kBM * 64;  // a group's nibbles, 8 KB
+constexpr int kSwRing = 4;       // groups of scales in flight per fold thread
+constexpr int kConvWarp0 = 4;
+
+template <bool NARROW>
+struct Cfg;
+template <>
+struct Cfg<false> {
+  static constexpr int NT = 192, SW = 4, SX = 3, NA = 2, NB = 2, kConv = 4, kFold = 8;
+  __host__ __device__ static constexpr int acc_col(int b) { return b * 256; }
+  __host__ __device__ static constexpr int a_col(int a) { return a * 256 + 192; }
+};
+template <>
+struct Cfg<true> {
+  static constexpr int NT = 32, SW = 12, SX = 12, NA = 4, NB = 4, kConv = 8, kFold = 4;
+  __host__ __device__ static constexpr int acc_col(int b) { return b * 32; }
+  __host__ __device__ static constexpr int a_col(int a) { return 128 + a * 64; }
+};
+constexpr int kRegsLaunch = 128, kRegsLow = 40, kRegsConv = 80, kRegsHigh = 192;  // the wide form's split
+static_assert(4 * kRegsLow + 4 * kRegsConv + 8 * kRegsHigh <= 16 * kRegsLaunch &&
+                  kRegsLow + kRegsConv + 2 * kRegsHigh <= 4 * kRegsLaunch,
+              "the register split must fit in what the CTA is launched with");
+
+template <bool NARROW>
+struct Smem {
+  using C = Cfg<NARROW>;
+  static constexpr int kXSlot = C::NT * 256;  // a group's fp16 tokens: two halves of 64 k
+  static constexpr int kCols = C::kFold == 8 ? C::NT / 2 : C::NT;
+  static constexpr int kWarpArea = kSwRing * 32 * 4 + kCols * 4;  // a fold warp's scale ring and row scales
+  static constexpr int kBars = 2 * C::SW + 2 * C::SX + C::NA + C::NB + 1;
+  static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
+                       kBarAt = kFoldArea + C::kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
+  // tables: prefix [E + 1], first row [E], rows [E]
+  static size_t bytes(int E) { return 1024 + kTables + static_cast<size_t>(3 * E + 1) * 4; }
+};
+static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
+static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
+static_assert(Cfg<false>::SX > Cfg<false>::NB && Cfg<false>::SX > Cfg<false>::NA && Cfg<true>::SX > Cfg<true>::NB &&
+                  Cfg<true>::SX > Cfg<true>::NA,
+              "one commit per group serves three waits");
+
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Each thread of the warp writes 32 consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 4-byte global -> shared copy of one thread, in its own cp.async group.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+struct Tile {
+  int e, row, rows, n0;  // expert, first row of Y, rows of the tile, first weight row
+};
+
+template <bool NARROW>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const RowsParams p) {
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  using C = Cfg<NARROW>;
+  using L = Smem<NARROW>;
+  constexpr int NT = C::NT, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
+  constexpr int kFoldWarp0 = 16 - C::kFold;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarAt);
+  uint64_t* w_full = bars;          // [SW] nibble tile landed
+  uint64_t* w_empty = w_full + SW;  // [SW] its four converter warps have read it
+  uint64_t* x_full = w_empty + SW;  // [SX] token tile landed
+  uint64_t* x_empty = x_full + SX;  // [SX] the group's MMAs are complete
+  uint64_t* a_full = x_empty + SX;  // [NA] four converter warps stored the A slot
+  uint64_t* afree = a_full + NA;    // [NB] accumulator read back by the fold warps
+  uint64_t* drain = afree + NB;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* prefix = reinterpret_cast<int*>(smem + L::kTables);  // [E + 1] token tiles of the experts before e
+  int* first = prefix + p.E + 1;                            // [E]
+  int* count = first + p.E;                                 // [E]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nk = p.K / 128, tiles_n = (p.N + kBM - 1) / kBM;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < SW; ++s) {
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_empty[s], 4);
+    }
+    for (int s = 0; s < SX; ++s) {
+      mbar_init(&x_full[s], 1);
+      mbar_init(&x_empty[s], 1);
+    }
+    for (int a = 0; a < NA; ++a) mbar_init(&a_full[a], 4);
+    for (int b = 0; b < NB; ++b) mbar_init(&afree[b], C::kFold);
+    mbar_init(drain, 2);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) {  // row counts and the prefix sums of token tiles, 32 experts at a time
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int f = 0, c = 0;
+      if (e < p.E) {
+        expert_rows(p, e, blockIdx.x == 0, &f, &c);
+        first[e] = f;
+        count[e] = c;
+      }
+      int t = (c + NT - 1) / NT;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, t, o);
+        if (lane >= o) t += u;
+      }
+      if (e < p.E) prefix[e + 1] = before + t;
+      before += __shfl_sync(0xFFFFFFFFu, t, 31);
+    }
+    if (lane == 0) prefix[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t ntiles = static_cast<int64_t>(prefix[p.E]) * tiles_n;
+
+  auto tile_at = [&](int64_t id) {
+    const int q = static_cast<int>(id / tiles_n);
+    int lo = 0, hi = p.E;  // prefix[lo] <= q < prefix[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= q)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int r = (q - prefix[lo]) * NT;
+    return Tile{lo, first[lo] + r, min(NT, count[lo] - r), static_cast<int>(id - static_cast<int64_t>(q) * tiles_n) * kBM};
+  };
+
+  if (warp < kConvWarp0) {
+    if constexpr (!NARROW) setmaxnreg_dec<kRegsLow>();
+    if (warp == 0) {
+      if (lane == 0) {
+        // -------------------------------------------------- nibble producer --
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+          const Tile t = tile_at(id);
+          const int wrow = t.e * p.N + t.n0;
+          for (int kb = 0; kb < nk; ++kb, ++it) {
+            const int s = it % SW;
+            if (it >= SW && !mbar_wait(&w_empty[s], ((it / SW) - 1) & 1, abort_flag, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            mbar_expect_tx(&w_full[s], kWSlot);
+            tma_load_2d(smem + L::kW + s * kWSlot, &tmW, &w_full[s], kb * 64, wrow);
+          }
+        }
+        if (!ok) {
+          set_error(p.err, SIXBIT_ETIMEOUT);
+          *abort_flag = 1;
+        }
+        // every copy this warp started lands before it can exit
+        for (uint32_t j = (it > SW ? it - SW : 0); j < it; ++j)
+          (void)mbar_wait(&w_full[j % SW], (j / SW) & 1, nullptr, p.wait_ns);
+      }
+    } else if (warp == 2) {
+      if (lane == 0) {
+        // --------------------------------------------------- token producer --
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+          const Tile t = tile_at(id);
+          const int boxes = (t.rows + 31) / 32;
+          for (int kb = 0; kb < nk; ++kb, ++it) {
+            const int s = it % SX;
+            if (it >= SX && !mbar_wait(&x_empty[s], ((it / SX) - 1) & 1, abort_flag, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            if (p.withhold_first && it == 0) continue;  // failure-path test: slot 0 never lands
+            mbar_expect_tx(&x_full[s], boxes * 8192);
+            uint8_t* dst = smem + L::kX + s * L::kXSlot;
+            for (int b = 0; b < boxes; ++b) {
+              tma_load_2d(dst + b * 4096, &tmX, &x_full[s], kb * 128, t.row + 32 * b);
+              tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], kb * 128 + 64, t.row + 32 * b);
+            }
+          }
+        }
+        if (!ok) {
+          set_error(p.err, SIXBIT_ETIMEOUT);
+          *abort_flag = 1;
+        }
+        for (uint32_t j = (it > SX ? it - SX : 0); j < it; ++j)
+          (void)mbar_wait(&x_full[j % SX], (j / SX) & 1, nullptr, p.wait_ns);
+      }
+    } else if (lane == 0) {
+      // --------------------------------------------------------- MMA issuers --
+      const uint32_t par = warp == 1 ? 0u : 1u;
+      uint32_t gi = 0;
+      bool ok = true;
+      for (int64_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+        const Tile t = tile_at(id);
+        const uint32_t nt = static_cast<uint32_t>((t.rows + 15) & ~15);
+        const uint32_t idesc = (1u << 4) | ((nt >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
+        for (int g = 0; g < nk; ++g, ++gi) {
+          if ((gi & 1) != par) continue;
+          const int s = static_cast<int>(gi % SX);
+          if ((gi >= NB && !mbar_wait(&afree[gi % NB], ((gi / NB) - 1) & 1, abort_flag, p.wait_ns)) ||
+              !mbar_wait(&x_full[s], (gi / SX) & 1, abort_flag, p.wait_ns) ||
+              !mbar_wait(&a_full[gi % NA], (gi / NA) & 1, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + C::acc_col(gi % NB), a_tmem = tmem + C::a_col(gi % NA);
+          const uint32_t b_base = smem_u32(smem + L::kX + s * L::kXSlot);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_f16_tmem_a(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + (k >> 2) * (NT * 128) + 32 * (k & 3)), idesc,
+                           k == 0 ? 0u : 1u);
+          tc_commit(&x_empty[s]);
+        }
+      }
+      if (!ok) {
+        set_error(p.err, SIXBIT_ETIMEOUT);
+        *abort_flag = 1;
+      }
+      tc_commit(drain);  // both issuers: all tensor-core work completes before exit
+      (void)mbar_wait(drain, 0, nullptr, p.wait_ns);
+    }
+  } else if (warp < kFoldWarp0) {
+    if constexpr (!NARROW) setmaxnreg_dec<kRegsConv>();
+    // ------------------------------------------------------------ converters --
+    // Thread `lane` of the warp of quarter q converts weight row 32 q + lane,
+    // the row of its tensor-memory lane.  The slot goes back once every lane's
+    // reads have returned (`zero` needs them) and behind a proxy fence: the
+    // refill is an async-proxy write.
+    const int q = warp & 3, myrow = 32 * q + lane;
+    const uint32_t mine = C::kConv == 8 ? static_cast<uint32_t>((warp - kConvWarp0) >> 2) : 0u;
+    const int swz = (myrow >> 1) & 3;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int64_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        if (C::kConv == 8 && (it & 1) != mine) continue;
+        const int s = it % SW, a = it % NA;
+        if (!mbar_wait(&w_full[s], (it / SW) & 1, abort_flag, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* row = smem + L::kW + s * kWSlot + myrow * 64;
+        uint4 in[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) in[c] = *reinterpret_cast<const uint4*>(row + ((c ^ swz) << 4));
+        uint32_t zero;
+        asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(in[0].x ^ in[1].x ^ in[2].x ^ in[3].x));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[s]);
+        if (it >= NA && !mbar_wait(&x_empty[(it - NA) % SX], ((it - NA) / SX) & 1, abort_flag, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::a_col(a);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint4& u = in[2 * h + c];
+            const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+              nibbles_f16(word[i], o);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[16 * c + 4 * i + j] = o[j];
+            }
+          }
+          tmem_st32(acol + 32 * h, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_full[a]);
+      }
+    }
+    if (!ok && lane == 0) {
+      set_error(p.err, SIXBIT_ETIMEOUT);
+      *abort_flag = 1;
+    }
+  } else {
+    if constexpr (!NARROW) setmaxnreg_inc<kRegsHigh>();
+    // -------------------------------------------------------- fold + epilogue --
+    constexpr int kCols = L::kCols;
+    const int ew = warp - kFoldWarp0, q = warp & 3;
+    const int cs = (ew >> 2) * kCols;  // first token of this thread within the tile
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + cs;
+    float* my_sw = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + lane;  // [slot][32]
+    float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * 32;
+    const bool pairs = (p.N & 1) == 0 && ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
+    uint32_t gi = 0;
+    bool ok = true;
+    for (int64_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+      const Tile t = tile_at(id);
+      const int n = t.n0 + 32 * q + lane, mine = t.rows - cs;  // tokens of this thread: min(mine, kCols)
+      const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
+      auto fetch_sw = [&](int g) {
+        const bool v = g < nk && n < p.N;
+        cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), v ? sw + static_cast<size_t>(g) * p.N : p.w4_scale, v);
+      };
+#pragma unroll
+      for (int g = 0; g < kSwRing - 1; ++g) fetch_sw(g);
+      __syncwarp();
+      for (int j = lane; j < kCols; j += 32) my_rs[j] = j < mine ? __ldg(p.row_scale + t.row + cs + j) : 0.f;
+      float sum[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
+      for (int g = 0; g < nk; ++g, ++gi) {
+        fetch_sw(g + kSwRing - 1);
+        cp_async_wait_newest<kSwRing - 1>();  // this thread's scale of group g has landed
+        const float s = my_sw[(g % kSwRing) * 32];
+        if (!mbar_wait(&x_empty[gi % SX], (gi / SX) & 1, abort_flag, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = lane_addr + C::acc_col(gi % NB);
+        const uint64_t s2 = f2_pack(s, s);
+        auto fold16 = [&](int c, const uint32_t (&r)[16]) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float* sm = sum + 16 * c + j;
+            const uint64_t v = f2_fma(s2, f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_pack(sm[0], sm[1]));
+            sm[0] = f2_lo(v);
+            sm[1] = f2_hi(v);
+          }
+        };
+        if (mine > 0) {
+          uint32_t r0[16], r1[16];
+          tmem_ld16(acc, r0);
+          tmem_ld16(acc + 16, r1);
+          if constexpr (NARROW) {
+            tmem_ld_wait(r0);
+            tmem_ld_wait(r1);
+            release_acc(&afree[gi % NB], lane);
+            fold16(0, r0);
+            fold16(1, r1);
+          } else {
+            uint32_t r2[16];
+            tmem_ld16(acc + 32, r2);
+            tmem_ld_wait(r0);
+            tmem_ld_wait(r1);
+            tmem_ld_wait(r2);
+            fold16(0, r0);
+            tmem_ld16(acc + 48, r0);
+            fold16(1, r1);
+            tmem_ld16(acc + 64, r1);
+            fold16(2, r2);
+            tmem_ld16(acc + 80, r2);
+            tmem_ld_wait(r0);
+            tmem_ld_wait(r1);
+            tmem_ld_wait(r2);
+            release_acc(&afree[gi % NB], lane);
+            fold16(3, r0);
+            fold16(4, r1);
+            fold16(5, r2);
+          }
+        } else {
+          release_acc(&afree[gi % NB], lane);
+        }
+      }
+      cp_async_wait_all();  // no scale copy outlives the tile
+      __syncwarp();
+      if (!ok) break;
+      // Tokens two at a time: with even N, neighbouring lanes exchange one
+      // value each, so that a lane holds two outputs of one token (4 bytes).
+      const size_t row0 = static_cast<size_t>(t.row + cs);
+#pragma unroll
+      for (int j = 0; j < kCols; j += 2) {
+        if (j >= mine) break;  // warp-uniform
+        const float2 rs = *reinterpret_cast<const float2*>(my_rs + j);
+        float v0 = __fmul_rn(sum[j], rs.x), v1 = __fmul_rn(sum[j + 1], rs.y);
+        if (p.epilogue == SIXBIT_EPI_GELU) {
+          const uint64_t gl = gelu_pair(f2_pack(v0, v1));
+          v0 = f2_lo(gl);
+          v1 = f2_hi(gl);
+        }
+        if (p.Yf == nullptr && pairs) {
+          const bool odd = (lane & 1) != 0;
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+          float a = odd ? other : v0, b = odd ? v1 : other;
+          const size_t at = (row0 + j + odd) * p.N + (n & ~1);
+          if ((n & ~1) < p.N && j + odd < mine) {
+            if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
+              const uint32_t r = *reinterpret_cast<const uint32_t*>(p.residual + at);
+              a = __fadd_rn(a, __uint_as_float(r << 16));
+              b = __fadd_rn(b, __uint_as_float(r & 0xFFFF0000u));
+            }
+            *reinterpret_cast<uint32_t*>(p.Y + at) = f2_to_bf16x2(f2_pack(a, b));
+          }
+        } else if (n < p.N) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j + h >= mine) break;
+            const size_t at = (row0 + j + h) * p.N + n;
+            float v = h ? v1 : v0;
+            if (p.epilogue == SIXBIT_EPI_RESIDUAL) v = __fadd_rn(v, __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16));
+            if (p.Yf != nullptr)
+              p.Yf[at] = v;
+            else
+              p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(v, 0.f)) & 0xFFFFu);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      set_error(p.err, SIXBIT_ETIMEOUT);
+      *abort_flag = 1;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// s8 [M, K] -> fp16 [M, K], each eight in the order 0 4 1 5 2 6 3 7.
+__global__ void __launch_bounds__(256) codes_f16_kernel(const int8_t* __restrict__ codes, int64_t n16,
+                                                        uint16_t* __restrict__ out, const int32_t* mode_dev) {
+  if (mode_dev != nullptr && SIXBIT_MODE_OF(*mode_dev) != SIXBIT_MODE_INT8) return;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes) + i);
+    uint32_t lo[4], hi[4];
+    codes_f16(c.x, c.y, lo);
+    codes_f16(c.z, c.w, hi);
+    uint4* o = reinterpret_cast<uint4*>(out) + 2 * i;
+    o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    o[1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+}
+
+template <bool NARROW>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const RowsParams& p, cudaStream_t st) {
+  cudaError_t e = set_smem_once<grouped_kernel<NARROW>>(static_cast<int>(Smem<NARROW>::bytes(SIXBIT_MAX_EXPERTS)));
+  if (e != cudaSuccess) return e;
+  if constexpr (!NARROW) {
+    static ContextCache<int> regs_cache;
+    int regs = 0;
+    e = regs_cache.get(&regs, [](int* o) {
+      cudaFuncAttributes fa;
+      const cudaError_t r = cudaFuncGetAttributes(&fa, grouped_kernel<NARROW>);
+      *o = fa.numRegs;
+      return r;
+    });
+    if (e != cudaSuccess) return e;
+    // setmaxnreg.inc waits until the block's own registers cover the increase:
+    // launch only with the register count the split was sized for.
+    if (regs < kRegsLaunch || 4 * (kRegsLow + kRegsConv) + 8 * kRegsHigh > 16 * regs) return cudaErrorInvalidConfiguration;
+  }
+  // at most one token tile per row, and one more per expert than rows / NT
+  const int64_t tiles_n = (p.N + kBM - 1) / kBM;
+  const int64_t tiles_t = min(static_cast<int64_t>(p.M), p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
+  const int sms = sm_count();
+  const int grid = tiles_t * tiles_n < sms ? static_cast<int>(tiles_t * tiles_n) : sms;
+  grouped_kernel<NARROW><<<grid, kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, p);
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace grouped
+
+cudaError_t launch_codes_f16(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint16_t* out,
+                             cudaStream_t st) {
+  const int64_t n16 = static_cast<int64_t>(M) * K / 16;
+  const int64_t want = (n16 + 255) / 256, cap = static_cast<int64_t>(sm_count()) * 8;
+  grouped::codes_f16_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(codes, n16, out, mode_dev);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const CUtensorMap& x, const RowsParams& p, bool narrow,
+                                cudaStream_t st) {
+  return narrow ? grouped::launch<true>(w, x, p, st) : grouped::launch<false>(w, x, p, st);
+}
+
+}  // namespace sixbit
