@@ -128,11 +128,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 4-byte global -> shared copy of one thread, in its own cp.async group.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-  asm volatile("cp.async.commit_group;" ::: "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // The epilogue and the store of 16 tokens (rows row .. row + 15 of Y, the first
 // `left` of them valid) of output column n, one column a lane.  With pairs (N
@@ -464,20 +463,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* my_sw = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + lane;  // [slot][32]
     float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * 32;
     const bool pairs = (p.N & 1) == 0 && ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
-    uint32_t gi = 0;
-    bool ok = true;
-    for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
-      const Tile t = tile_at(id);
-      const int n = t.n0 + 32 * q + lane, mine = t.rows - cs;  // tokens of this thread: min(mine, kCols)
-      const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
-      auto fetch_sw = [&](int g) {
-        const bool v = g < nk && n < p.N;
-        cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), v ? sw + static_cast<size_t>(g) * p.N : p.w4_scale, v);
-      };
+    // A tile's first scales and its tokens' row scales are asked for before
+    // the epilogue of the tile before it, which hides their latency.
+    constexpr int kRs = kCols / 32, kChunks = kCols / 16, kBuf = kChunks < 3 ? kChunks : 3;
+    Tile t{};
+    int n = 0, mine = 0;  // output column; tokens of this thread: min(mine, kCols)
+    const float* sw = nullptr;
+    float rs[kRs];
+    auto fetch_sw = [&](int g) {  // a group of copies even when it holds none
+      if (g < nk && n < p.N) cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), sw + static_cast<size_t>(g) * p.N);
+      cp_async_commit();
+    };
+    auto begin = [&](uint32_t id) {
+      t = tile_at(id);
+      n = t.n0 + 32 * q + lane;
+      mine = t.rows - cs;
+      sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
 #pragma unroll
       for (int g = 0; g < kSwRing - 1; ++g) fetch_sw(g);
-      __syncwarp();
-      for (int j = lane; j < kCols; j += 32) my_rs[j] = j < mine ? __ldg(p.row_scale + t.row + cs + j) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kRs; ++j) rs[j] = 32 * j + lane < mine ? __ldg(p.row_scale + t.row + cs + 32 * j + lane) : 0.f;
+    };
+    uint32_t gi = 0;
+    bool ok = true;
+    if (blockIdx.x < ntiles) begin(blockIdx.x);
+    for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+      __syncwarp();  // every lane is done with the last tile's row scales
+#pragma unroll
+      for (int j = 0; j < kRs; ++j) my_rs[32 * j + lane] = rs[j];
       float sum[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
@@ -502,60 +515,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         if (mine > 0) {
-          uint32_t r0[16], r1[16];
-          tmem_ld16(acc, r0);
-          tmem_ld16(acc + 16, r1);
-          if constexpr (NARROW) {
-            tmem_ld_wait(r0);
-            tmem_ld_wait(r1);
+          // Three 16-column loads in flight; a chunk's buffer is reloaded as
+          // soon as it is folded, and the accumulator goes back with the last load.
+          uint32_t r[kBuf][16];
+#pragma unroll
+          for (int c = 0; c < kBuf; ++c) tmem_ld16(acc + 16 * c, r[c]);
+#pragma unroll
+          for (int c = 0; c < kBuf; ++c) tmem_ld_wait(r[c]);
+          if constexpr (kChunks > kBuf) {
+#pragma unroll
+            for (int c = 0; c < kBuf; ++c) {
+              fold16(c, r[c]);
+              if (c + kBuf < kChunks) tmem_ld16(acc + 16 * (c + kBuf), r[c]);
+            }
+#pragma unroll
+            for (int c = 0; c + kBuf < kChunks; ++c) tmem_ld_wait(r[c]);
             release_acc(&afree[gi % NB], lane);
-            fold16(0, r0);
-            fold16(1, r1);
+#pragma unroll
+            for (int c = 0; c + kBuf < kChunks; ++c) fold16(c + kBuf, r[c]);
           } else {
-            uint32_t r2[16];
-            tmem_ld16(acc + 32, r2);
-            tmem_ld_wait(r0);
-            tmem_ld_wait(r1);
-            tmem_ld_wait(r2);
-            fold16(0, r0);
-            tmem_ld16(acc + 48, r0);
-            fold16(1, r1);
-            tmem_ld16(acc + 64, r1);
-            fold16(2, r2);
-            tmem_ld16(acc + 80, r2);
-            tmem_ld_wait(r0);
-            tmem_ld_wait(r1);
-            tmem_ld_wait(r2);
             release_acc(&afree[gi % NB], lane);
-            fold16(3, r0);
-            fold16(4, r1);
-            fold16(5, r2);
+#pragma unroll
+            for (int c = 0; c < kBuf; ++c) fold16(c, r[c]);
           }
         } else {
           release_acc(&afree[gi % NB], lane);
         }
       }
-      cp_async_wait_all();  // no scale copy outlives the tile
       __syncwarp();
       if (!ok) break;
+      const size_t row0 = static_cast<size_t>(t.row + cs);
+      const int n_now = n, mine_now = mine;
+      if (id + gridDim.x < ntiles) begin(id + gridDim.x);
       // Sixteen tokens at a time, so that their chains overlap (one pair after
       // the other took 30,000 cycles a tile, clock64 trace).
 #pragma unroll
-      for (int c = 0; c < kCols / 16; ++c) {
-        const int left = mine - 16 * c;  // warp-uniform
+      for (int c = 0; c < kChunks; ++c) {
+        const int left = mine_now - 16 * c;  // warp-uniform
         if (left <= 0) break;
         float v[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-          const float4 rs = *reinterpret_cast<const float4*>(my_rs + 16 * c + j);
-          v[j] = __fmul_rn(sum[16 * c + j], rs.x);
-          v[j + 1] = __fmul_rn(sum[16 * c + j + 1], rs.y);
-          v[j + 2] = __fmul_rn(sum[16 * c + j + 2], rs.z);
-          v[j + 3] = __fmul_rn(sum[16 * c + j + 3], rs.w);
+          const float4 rv = *reinterpret_cast<const float4*>(my_rs + 16 * c + j);
+          v[j] = __fmul_rn(sum[16 * c + j], rv.x);
+          v[j + 1] = __fmul_rn(sum[16 * c + j + 1], rv.y);
+          v[j + 2] = __fmul_rn(sum[16 * c + j + 2], rv.z);
+          v[j + 3] = __fmul_rn(sum[16 * c + j + 3], rv.w);
         }
-        store16(p, static_cast<size_t>(t.row + cs + 16 * c), n, left, pairs, lane, v);
+        store16(p, row0 + 16 * c, n_now, left, pairs, lane, v);
       }
     }
+    cp_async_wait_all();  // no scale copy outlives the CTA
     if (!ok && lane == 0) {
       set_error(p.err, SIXBIT_ETIMEOUT);
       *abort_flag = 1;
