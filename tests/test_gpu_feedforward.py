@@ -314,6 +314,28 @@ def test_grouped_epilogues(ops, epi, f32, n):
     _grouped(ops, g, [0, 7, 7, 300, 420], 420, n, 640, epi, f32)
 
 
+@pytest.mark.parametrize("counts", [[3, 20], [90, 40], [300, 217]])
+def test_grouped_extreme_codes(ops, counts):
+    """Every code with every nibble, and group sums at their largest: exact integers in a float32 output."""
+    n, k, m = 160, 512, sum(counts)
+    q = np.full((m, k), 127, np.int8)
+    q[1::3] = -127
+    q[2::3] = (np.arange(k) % 255 - 127).astype(np.int8)
+    q[::7, 1::2] *= -1
+    w4 = np.empty((2, n, k // 2), np.uint8)
+    w4[0] = (9 << 4) | 7                                                    # 7 at even k, -7 at odd k
+    w4[0, 1] = (7 << 4) | 8                                                 # -8, 7
+    w4[1] = ((np.arange(n)[:, None] + np.arange(k // 2)[None]) % 256).astype(np.uint8)
+    ws = np.ones((2, k // 128, n), np.float32)
+    offsets = [0, counts[0], m]
+    y = ops.qgemm_grouped(ops.int8_act(torch.from_numpy(q).cuda(), torch.ones(m, device="cuda")),
+                          ops.Int4Weights(torch.from_numpy(w4).cuda(), torch.from_numpy(ws).cuda()),
+                          torch.tensor(offsets, dtype=torch.int32, device="cuda"), out_f32=True).cpu().numpy()
+    for e in range(2):
+        r = slice(offsets[e], offsets[e + 1])
+        assert np.array_equal(y[r], (q[r].astype(np.int64) @ _unpack(w4[e]).astype(np.int64).T).astype(np.float32))
+
+
 def test_grouped_many_experts(ops):
     g = np.random.default_rng(5)
     counts = g.integers(0, 4, size=300)

@@ -651,14 +651,14 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   gemm_debug_params(dbg);
   p.wait_ns = dbg.wait_ns;
   p.withhold_first = dbg.withhold_first;
-  uint16_t* x16 = static_cast<uint16_t*>(workspace);
+  uint8_t* xd = static_cast<uint8_t*>(workspace);
   const bool narrow = M < 64 * static_cast<int64_t>(E);
   CUtensorMap mw, mx, mxf;
   if (!make_w4_map(&mw, W->i4_codes, static_cast<int64_t>(E) * N, K) ||
-      !make_map(&mx, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, M, K, 32) ||
-      !make_map(&mxf, x16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, M, K, grouped_tokens(narrow)))
+      !make_map(&mx, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, 32) ||
+      !make_map(&mxf, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, grouped_tokens(narrow)))
     return SIXBIT_ECUDA;
-  if (launch_codes_f16(p.codes, M, K, mode_dev, x16, st) != cudaSuccess) return SIXBIT_ECUDA;
+  if (launch_digits(p.codes, M, K, mode_dev, xd, st) != cudaSuccess) return SIXBIT_ECUDA;
   return cuda_status(launch_w4a8_grouped(mw, mx, mxf, p, narrow, st));
 }
 

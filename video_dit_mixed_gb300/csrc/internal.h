@@ -130,13 +130,12 @@ struct RowsParams {
   int withhold_first;
 };
 cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st);
-// Codes [M, K] -> fp16 [M, K] in the grouped kernel's order of k.
-cudaError_t launch_codes_f16(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint16_t* out,
-                             cudaStream_t st);
+// Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row.
+cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st);
 // w: map of the INT4 codes [E N, K/2] (box 64 bytes x 128 rows, 64-byte
-// swizzle); x, xfull: maps of the fp16 codes (boxes 64 x 32 and 64 x
-// grouped_tokens(narrow), 128-byte swizzle).  narrow: token tiles of 32
-// instead of 192.
+// swizzle); x, xfull: maps of the token operand (boxes of 128 bytes x 32 rows
+// and x grouped_tokens(narrow) rows, 128-byte swizzle).  narrow: token tiles of
+// 32 instead of 128.
 int grouped_tokens(bool narrow);
 cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull,
                                 const RowsParams& p, bool narrow, cudaStream_t st);

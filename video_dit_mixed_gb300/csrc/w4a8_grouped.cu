@@ -42,15 +42,17 @@
 //   4 ..    converters, one warp per 32-lane quarter (narrow form: two such
 //           sets, even and odd groups)
 //   .. 15   fold + epilogue
-// One commit per group, onto the token slot's barrier, tells the producer that
-// the slot is free, the converters that the group's A slot is, and the fold
-// warps that its accumulator is complete.  That barrier cannot run a phase
-// past any of these waits: its next phase is group g + SX, whose MMAs need a
-// fold of group g + SX - NB > g and a conversion of group g + SX > g + NA.
+// A group's MMAs are followed by two commits: onto the token slot's barrier
+// (the producer may refill it; the converters may refill the group's A slot:
+// that barrier's next phase is group g + SX > g + NA, whose conversion comes
+// after this wait), and onto the accumulator's barrier of the team that folds
+// the tile.  Each team has barriers of its own, so that it sees every phase of
+// the barriers it waits on.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records
 // SIXBIT_ETIMEOUT, raises the abort flag, waits (bounded) for its copies and
 // tensor-core work in flight, frees tensor memory and returns.
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
@@ -72,17 +74,17 @@ template <bool NARROW>
 struct Cfg;
 template <>
 struct Cfg<false> {
-  static constexpr int NT = 192, SW = 4, SX = 3, NA = 2, NB = 2, kConv = 4, kFold = 8;
-  __host__ __device__ static constexpr int acc_col(int b) { return b * 256; }
-  __host__ __device__ static constexpr int a_col(int a) { return a * 256 + 192; }
+  static constexpr int NT = 128, SW = 4, SX = 5, NA = 4, NB = 3, kConv = 4, kTeams = 2;
+  __host__ __device__ static constexpr int acc_col(int b) { return b * 128; }
+  __host__ __device__ static constexpr int a_col(int a) { return 384 + a * 32; }
 };
 template <>
 struct Cfg<true> {
-  static constexpr int NT = 32, SW = 12, SX = 12, NA = 4, NB = 4, kConv = 8, kFold = 4;
+  static constexpr int NT = 32, SW = 12, SX = 12, NA = 4, NB = 4, kConv = 8, kTeams = 1;
   __host__ __device__ static constexpr int acc_col(int b) { return b * 32; }
-  __host__ __device__ static constexpr int a_col(int a) { return 128 + a * 64; }
+  __host__ __device__ static constexpr int a_col(int a) { return 128 + a * 32; }
 };
-constexpr int kRegsLaunch = 128, kRegsLow = 40, kRegsConv = 80, kRegsHigh = 192;  // the wide form's split
+constexpr int kRegsLaunch = 128, kRegsLow = 40, kRegsConv = 88, kRegsHigh = 192;  // the wide form's split
 static_assert(4 * kRegsLow + 4 * kRegsConv + 8 * kRegsHigh <= 16 * kRegsLaunch &&
                   kRegsLow + kRegsConv + 2 * kRegsHigh <= 4 * kRegsLaunch,
               "the register split must fit in what the CTA is launched with");
@@ -90,27 +92,26 @@ static_assert(4 * kRegsLow + 4 * kRegsConv + 8 * kRegsHigh <= 16 * kRegsLaunch &
 template <bool NARROW>
 struct Smem {
   using C = Cfg<NARROW>;
-  static constexpr int kXSlot = C::NT * 256;  // a group's fp16 tokens: two halves of 64 k
-  static constexpr int kCols = C::kFold == 8 ? C::NT / 2 : C::NT;
-  static constexpr int kWarpArea = kSwRing * 32 * 4 + kCols * 4;  // a fold warp's scale ring and row scales
-  static constexpr int kBars = 2 * C::SW + 2 * C::SX + C::NA + C::NB + 1;
+  static constexpr int kXSlot = C::NT * 256;  // a group's tokens: the high digits' 128 bytes, then the low ones'
+  static constexpr int kFold = 4 * C::kTeams;
+  static constexpr int kWarpArea = kSwRing * 32 * 4 + C::NT * 4;  // a fold warp's scale ring and row scales
+  static constexpr int kBars = 2 * C::SW + 2 * C::SX + C::NA + (C::kTeams + 1) * C::NB + 1;
   static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
-                       kBarAt = kFoldArea + C::kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
+                       kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
   // tables: prefix [E + 1], first row [E], rows [E]
   static size_t bytes(int E) { return 1024 + kTables + static_cast<size_t>(3 * E + 1) * 4; }
 };
 static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
-static_assert(Cfg<false>::SX > Cfg<false>::NB && Cfg<false>::SX > Cfg<false>::NA && Cfg<true>::SX > Cfg<true>::NB &&
-                  Cfg<true>::SX > Cfg<true>::NA,
-              "one commit per group serves three waits");
+static_assert(Cfg<false>::SX > Cfg<false>::NA && Cfg<true>::SX > Cfg<true>::NA, "a token slot's commit frees the A slot");
 
-__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T, E4M3 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -133,63 +134,75 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// The epilogue and the store of 16 tokens (rows row .. row + 15 of Y, the first
-// `left` of them valid) of output column n, one column a lane.  With pairs (N
-// even, Y and residual 4-byte aligned), neighbouring lanes exchange one value
-// of each two tokens, so that a lane holds two outputs of one token and a
-// store writes 4 bytes.
-__device__ __forceinline__ void store16(const RowsParams& p, size_t row, int n, int left, bool pairs, int lane,
-                                        float (&v)[16]) {
-  if (p.epilogue == SIXBIT_EPI_GELU) {
+// How a tile's outputs are written.  kPair*: bf16, N even, Y and residual
+// 4-byte aligned: neighbouring lanes exchange one value of each two tokens, so
+// that a lane holds two outputs of one token and a store writes 4 bytes.  kAny:
+// whatever else, one output at a time.  They are forms of the kernel: one code
+// path a kernel, since its instruction fetch (92% hits) paced the epilogue.
+enum Out { kPair, kPairGelu, kPairResidual, kAny };
+
+__device__ __forceinline__ void gelu16(float (&v)[16]) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const uint64_t g = gelu_pair(f2_pack(v[j], v[j + 1]));
-      v[j] = f2_lo(g);
-      v[j + 1] = f2_hi(g);
-    }
+  for (int j = 0; j < 16; j += 2) {
+    const uint64_t g = gelu_pair(f2_pack(v[j], v[j + 1]));
+    v[j] = f2_lo(g);
+    v[j + 1] = f2_hi(g);
   }
-  if (p.Yf == nullptr && pairs) {
+}
+
+// The epilogue and the store of 16 tokens (rows row .. row + 15 of Y, the first
+// `left` of them valid) of output column n, one column a lane.
+template <Out OUT>
+__device__ __forceinline__ void store16(const RowsParams& p, size_t row, int n, int left, int lane, float (&v)[16]) {
+  if constexpr (OUT != kAny) {
+    if constexpr (OUT == kPairGelu) gelu16(v);
     const int odd = lane & 1, nb = n & ~1;
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-      v[j] = odd ? other : v[j];
-      v[j + 1] = odd ? v[j + 1] : other;
-    }
-    if (nb >= p.N) return;
-    const size_t at = (row + odd) * p.N + nb, step = 2 * static_cast<size_t>(p.N);
-    if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;  // own and other -> columns (n, n + 1) of token j, or of j + 1
+    const int some = nb < p.N ? left - odd : 0;    // token 2 i + odd is there when 2 i < some
+    const uint32_t step = 4u * static_cast<uint32_t>(p.N);  // bytes of two rows
+    const size_t at = 2 * ((row + odd) * p.N + nb);
+    const char* in = reinterpret_cast<const char*>(p.residual) + at;
+    char* out = reinterpret_cast<char*>(p.Y) + at;
+    if constexpr (OUT == kPairResidual) {
       uint32_t r[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        r[i] = 2 * i + odd < left ? *reinterpret_cast<const uint32_t*>(p.residual + at + i * step) : 0u;
+        r[i] = 2 * i < some ? *reinterpret_cast<const uint32_t*>(in + static_cast<uint64_t>(i) * step) : 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i) {  // the exchange below, backwards
+        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, r[i], 1);
+        r[i] = __byte_perm(r[i], o, sel);
         v[2 * i] = __fadd_rn(v[2 * i], __uint_as_float(r[i] << 16));
         v[2 * i + 1] = __fadd_rn(v[2 * i + 1], __uint_as_float(r[i] & 0xFFFF0000u));
       }
     }
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (2 * i + odd < left)
-        *reinterpret_cast<uint32_t*>(p.Y + at + i * step) = f2_to_bf16x2(f2_pack(v[2 * i], v[2 * i + 1]));
-  } else if (n < p.N) {
-    const size_t at = row * p.N + n;
-    if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
-      uint16_t r[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) r[i] = i < left ? p.residual[at + i * static_cast<size_t>(p.N)] : uint16_t{0};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(v[i], __uint_as_float(static_cast<uint32_t>(r[i]) << 16));
+    for (int i = 0; i < 8; ++i) {
+      w[i] = f2_to_bf16x2(f2_pack(v[2 * i], v[2 * i + 1]));  // tokens 2 i, 2 i + 1 of column n
+      w[i] = __byte_perm(w[i], __shfl_xor_sync(0xFFFFFFFFu, w[i], 1), sel);
     }
+    if (some >= 15) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i < left) {
-        if (p.Yf != nullptr)
-          p.Yf[at + i * static_cast<size_t>(p.N)] = v[i];
-        else
-          p.Y[at + i * static_cast<size_t>(p.N)] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(v[i], 0.f)) & 0xFFFFu);
-      }
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t*>(out + static_cast<uint64_t>(i) * step) = w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (2 * i < some) *reinterpret_cast<uint32_t*>(out + static_cast<uint64_t>(i) * step) = w[i];
+    }
+  } else {
+    if (p.epilogue == SIXBIT_EPI_GELU) gelu16(v);
+    if (n >= p.N) return;
+    size_t at = row * p.N + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, at += p.N) {
+      if (i >= left) break;
+      if (p.epilogue == SIXBIT_EPI_RESIDUAL)
+        v[i] = __fadd_rn(v[i], __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16));
+      if (p.Yf != nullptr)
+        p.Yf[at] = v[i];
+      else
+        p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(v[i], 0.f)) & 0xFFFFu);
     }
   }
 }
@@ -198,7 +211,7 @@ struct Tile {
   int e, row, rows, n0;  // expert, first row of Y, rows of the tile, first weight row
 };
 
-template <bool NARROW>
+template <bool NARROW, Out OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmXfull, const RowsParams p) {
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<NARROW>;
   using L = Smem<NARROW>;
   constexpr int NT = C::NT, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
-  constexpr int kFoldWarp0 = 16 - C::kFold;
+  constexpr int kFoldWarp0 = 16 - L::kFold;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -216,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* x_full = w_empty + SW;  // [SX] token tile landed
   uint64_t* x_empty = x_full + SX;  // [SX] the group's MMAs are complete
   uint64_t* a_full = x_empty + SX;  // [NA] four converter warps stored the A slot
-  uint64_t* afree = a_full + NA;    // [NB] accumulator read back by the fold warps
+  uint64_t* acc_full = a_full + NA;                // [team][NB] a group of the team's tile is complete
+  uint64_t* afree = acc_full + C::kTeams * NB;     // [NB] accumulator read back by a team's four warps
   uint64_t* drain = afree + NB;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -238,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&x_empty[s], 1);
     }
     for (int a = 0; a < NA; ++a) mbar_init(&a_full[a], 4);
-    for (int b = 0; b < NB; ++b) mbar_init(&afree[b], C::kFold);
+    for (int b = 0; b < C::kTeams * NB; ++b) mbar_init(&acc_full[b], 1);
+    for (int b = 0; b < NB; ++b) mbar_init(&afree[b], 4);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
@@ -339,13 +354,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(&x_full[s], boxes * 8192);
             uint8_t* dst = smem + L::kX + s * L::kXSlot;
             if (boxes == NT / 32) {
-              tma_load_2d(dst, &tmXfull, &x_full[s], kb * 128, t.row);
-              tma_load_2d(dst + NT * 128, &tmXfull, &x_full[s], kb * 128 + 64, t.row);
+              tma_load_2d(dst, &tmXfull, &x_full[s], kb * 256, t.row);
+              tma_load_2d(dst + NT * 128, &tmXfull, &x_full[s], kb * 256 + 128, t.row);
               continue;
             }
             for (int b = 0; b < boxes; ++b) {
-              tma_load_2d(dst + b * 4096, &tmX, &x_full[s], kb * 128, t.row + 32 * b);
-              tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], kb * 128 + 64, t.row + 32 * b);
+              tma_load_2d(dst + b * 4096, &tmX, &x_full[s], kb * 256, t.row + 32 * b);
+              tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], kb * 256 + 128, t.row + 32 * b);
             }
           }
         }
@@ -359,18 +374,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane == 0) {
       // --------------------------------------------------------- MMA issuers --
       const uint32_t par = warp == 1 ? 0u : 1u;
-      uint32_t gi = 0;
+      // The accumulator is waited for last: with NB odd an issuer meets a buffer
+      // at every second phase only, and the A slot's arrival (which follows the
+      // MMAs of group gi - 3) is what rules out that the phase before is still open.
+      uint32_t gi = 0, turn = 0;
       bool ok = true;
-      for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+      for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
         const Tile t = tile_at(id);
+        uint64_t* done = acc_full + (C::kTeams > 1 ? (turn & 1) * NB : 0);
         const uint32_t nt = static_cast<uint32_t>((t.rows + 15) & ~15);
         const uint32_t idesc = (1u << 4) | ((nt >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
         for (int g = 0; g < nk; ++g, ++gi) {
           if ((gi & 1) != par) continue;
           const int s = static_cast<int>(gi % SX);
-          if ((gi >= NB && !mbar_wait(&afree[gi % NB], ((gi / NB) - 1) & 1, abort_flag, p.wait_ns)) ||
-              !mbar_wait(&x_full[s], (gi / SX) & 1, abort_flag, p.wait_ns) ||
-              !mbar_wait(&a_full[gi % NA], (gi / NA) & 1, abort_flag, p.wait_ns)) {
+          if (!mbar_wait(&x_full[s], (gi / SX) & 1, abort_flag, p.wait_ns) ||
+              !mbar_wait(&a_full[gi % NA], (gi / NA) & 1, abort_flag, p.wait_ns) ||
+              (gi >= NB && !mbar_wait(&afree[gi % NB], ((gi / NB) - 1) & 1, abort_flag, p.wait_ns))) {
             ok = false;
             break;
           }
@@ -378,9 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d_tmem = tmem + C::acc_col(gi % NB), a_tmem = tmem + C::a_col(gi % NA);
           const uint32_t b_base = smem_u32(smem + L::kX + s * L::kXSlot);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_f16_tmem_a(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + (k >> 2) * (NT * 128) + 32 * (k & 3)), idesc,
-                           k == 0 ? 0u : 1u);
+          for (int k = 0; k < 8; ++k)  // 32 k: the high digits, then the low ones
+            mma_e4m3_tmem_a(d_tmem, a_tmem + 8 * (k >> 1), sdesc_sw128(b_base + (k & 1) * (NT * 128) + 32 * (k >> 1)),
+                            idesc, k == 0 ? 0u : 1u);
+          tc_commit(&done[gi % NB]);
           tc_commit(&x_empty[s]);
         }
       }
@@ -395,59 +415,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!NARROW) setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------------------ converters --
     // Thread `lane` of the warp of quarter q converts weight row 32 q + lane,
-    // the row of its tensor-memory lane.  The slot goes back once every lane's
-    // reads have returned (`zero` needs them) and behind a proxy fence: the
-    // refill is an async-proxy write.
+    // the row of its tensor-memory lane.  The next group's nibbles are read
+    // while this one's are stored, and half of them are converted before the
+    // A slot is waited for: one step after the other, a group took the
+    // converters 1,100 cycles, more than its MMAs.  A nibble slot goes back
+    // once every lane's reads have returned (`zero` needs them) and behind a
+    // proxy fence: the refill is an async-proxy write.
+    constexpr uint32_t kSets = C::kConv / 4;
     const int q = warp & 3, myrow = 32 * q + lane;
-    const uint32_t mine = C::kConv == 8 ? static_cast<uint32_t>((warp - kConvWarp0) >> 2) : 0u;
     const int swz = (myrow >> 1) & 3;
-    uint32_t it = 0;
+    const uint32_t total = blockIdx.x < ntiles ? ((ntiles - blockIdx.x - 1) / gridDim.x + 1) * nk : 0;
+    const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    uint32_t it = static_cast<uint32_t>((warp - kConvWarp0) >> 2);
     bool ok = true;
-    for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
-      for (int kb = 0; kb < nk; ++kb, ++it) {
-        if (C::kConv == 8 && (it & 1) != mine) continue;
-        const int s = it % SW, a = it % NA;
-        if (!mbar_wait(&w_full[s], (it / SW) & 1, abort_flag, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* row = smem + L::kW + s * kWSlot + myrow * 64;
-        uint4 in[4];
+    uint4 in[4];
+    auto read = [&](uint32_t i) {
+      if (!mbar_wait(&w_full[i % SW], (i / SW) & 1, abort_flag, p.wait_ns)) return false;
+      const uint8_t* row = smem + L::kW + (i % SW) * kWSlot + myrow * 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) in[c] = *reinterpret_cast<const uint4*>(row + ((c ^ swz) << 4));
-        uint32_t zero;
-        asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(in[0].x ^ in[1].x ^ in[2].x ^ in[3].x));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&w_empty[s]);
-        if (it >= NA && !mbar_wait(&x_empty[(it - NA) % SX], ((it - NA) / SX) & 1, abort_flag, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16) + C::a_col(a);
+      for (int c = 0; c < 4; ++c) in[c] = *reinterpret_cast<const uint4*>(row + ((c ^ swz) << 4));
+      return true;
+    };
+    auto give_back = [&](uint32_t i) {
+      uint32_t zero;
+      asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(in[0].x ^ in[1].x ^ in[2].x ^ in[3].x));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[i % SW]);
+    };
+    if (it < total) ok = read(it);
+    for (; it < total && ok; it += kSets) {
+      const int a = it % NA;
+      give_back(it);
+      uint32_t v[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[32];
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t word[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint4& u = in[2 * h + c];
-            const uint32_t word[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t o[4];
-              nibbles_f16(word[i], o);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[16 * c + 4 * i + j] = o[j];
-            }
-          }
-          tmem_st32(acol + 32 * h, v);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a_full[a]);
+        for (int i = 0; i < 4; ++i) nibbles_e4m3(word[i], v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
       }
+      if (it >= NA && !mbar_wait(&x_empty[(it - NA) % SX], ((it - NA) / SX) & 1, abort_flag, p.wait_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_st32(acol + C::a_col(a), v);
+      if (it + kSets < total && !read(it + kSets)) {
+        ok = false;
+        break;
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_full[a]);
     }
     if (!ok && lane == 0) {
       set_error(p.err, SIXBIT_ETIMEOUT);
@@ -456,55 +476,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     if constexpr (!NARROW) setmaxnreg_inc<kRegsHigh>();
     // -------------------------------------------------------- fold + epilogue --
-    constexpr int kCols = L::kCols;
+    // A team of four warps takes a whole tile, every kTeams-th of the CTA's.
+    constexpr int kChunks = NT / 16, kBuf = 2;
     const int ew = warp - kFoldWarp0, q = warp & 3;
-    const int cs = (ew >> 2) * kCols;  // first token of this thread within the tile
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + cs;
+    const uint32_t team = static_cast<uint32_t>(ew >> 2);
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     float* my_sw = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + lane;  // [slot][32]
     float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * 32;
-    const bool pairs = (p.N & 1) == 0 && ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
-    // A tile's first scales and its tokens' row scales are asked for before
-    // the epilogue of the tile before it, which hides their latency.
-    constexpr int kRs = kCols / 32, kChunks = kCols / 16, kBuf = kChunks < 3 ? kChunks : 3;
-    Tile t{};
-    int n = 0, mine = 0;  // output column; tokens of this thread: min(mine, kCols)
-    const float* sw = nullptr;
-    float rs[kRs];
-    auto fetch_sw = [&](int g) {  // a group of copies even when it holds none
-      if (g < nk && n < p.N) cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), sw + static_cast<size_t>(g) * p.N);
-      cp_async_commit();
-    };
-    auto begin = [&](uint32_t id) {
-      t = tile_at(id);
-      n = t.n0 + 32 * q + lane;
-      mine = t.rows - cs;
-      sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
+    uint64_t* full = acc_full + team * NB;
+    uint32_t phases = 0;  // bit b: parity of this team's next wait for buffer b
+    uint32_t gi = 0, turn = 0;
+    bool ok = true;
+    for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
+      if (C::kTeams > 1 && (turn & 1) != team) {
+        gi += nk;
+        continue;
+      }
+      const Tile t = tile_at(id);
+      const int n = t.n0 + 32 * q + lane;  // output column
+      const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
+      auto fetch_sw = [&](int g) {  // a group of copies even when it holds none
+        if (g < nk && n < p.N) cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), sw + static_cast<size_t>(g) * p.N);
+        cp_async_commit();
+      };
 #pragma unroll
       for (int g = 0; g < kSwRing - 1; ++g) fetch_sw(g);
-#pragma unroll
-      for (int j = 0; j < kRs; ++j) rs[j] = 32 * j + lane < mine ? __ldg(p.row_scale + t.row + cs + 32 * j + lane) : 0.f;
-    };
-    uint32_t gi = 0;
-    bool ok = true;
-    if (blockIdx.x < ntiles) begin(blockIdx.x);
-    for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
       __syncwarp();  // every lane is done with the last tile's row scales
 #pragma unroll
-      for (int j = 0; j < kRs; ++j) my_rs[32 * j + lane] = rs[j];
-      float sum[kCols];
+      for (int j = lane; j < NT; j += 32) my_rs[j] = j < t.rows ? __ldg(p.row_scale + t.row + j) : 0.f;
+      float sum[NT];
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
+      for (int j = 0; j < NT; ++j) sum[j] = 0.f;
       for (int g = 0; g < nk; ++g, ++gi) {
         fetch_sw(g + kSwRing - 1);
         cp_async_wait_newest<kSwRing - 1>();  // this thread's scale of group g has landed
         const float s = my_sw[(g % kSwRing) * 32];
-        if (!mbar_wait(&x_empty[gi % SX], (gi / SX) & 1, abort_flag, p.wait_ns)) {
+        const uint32_t b = gi % NB;
+        if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
           ok = false;
           break;
         }
+        phases ^= 1u << b;
         tc_fence_after();
-        const uint32_t acc = lane_addr + C::acc_col(gi % NB);
-        const uint64_t s2 = f2_pack(s, s);
+        const uint32_t acc = lane_addr + C::acc_col(b);
+        const uint64_t s2 = f2_pack(s * 262144.f, s * 262144.f);  // (2^18: both operands stand in units of 2^-9)
         auto fold16 = [&](int c, const uint32_t (&r)[16]) {
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
@@ -514,55 +529,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm[1] = f2_hi(v);
           }
         };
-        if (mine > 0) {
-          // Three 16-column loads in flight; a chunk's buffer is reloaded as
-          // soon as it is folded, and the accumulator goes back with the last load.
-          uint32_t r[kBuf][16];
+        // Two 16-column loads in flight: chunk c is folded while c + 1 loads.
+        uint32_t r[kBuf][16];
+        tmem_ld16(acc, r[0]);
+        tmem_ld_wait(r[0]);
 #pragma unroll
-          for (int c = 0; c < kBuf; ++c) tmem_ld16(acc + 16 * c, r[c]);
-#pragma unroll
-          for (int c = 0; c < kBuf; ++c) tmem_ld_wait(r[c]);
-          if constexpr (kChunks > kBuf) {
-#pragma unroll
-            for (int c = 0; c < kBuf; ++c) {
-              fold16(c, r[c]);
-              if (c + kBuf < kChunks) tmem_ld16(acc + 16 * (c + kBuf), r[c]);
-            }
-#pragma unroll
-            for (int c = 0; c + kBuf < kChunks; ++c) tmem_ld_wait(r[c]);
-            release_acc(&afree[gi % NB], lane);
-#pragma unroll
-            for (int c = 0; c + kBuf < kChunks; ++c) fold16(c + kBuf, r[c]);
-          } else {
-            release_acc(&afree[gi % NB], lane);
-#pragma unroll
-            for (int c = 0; c < kBuf; ++c) fold16(c, r[c]);
-          }
-        } else {
-          release_acc(&afree[gi % NB], lane);
+        for (int c = 0; c < kChunks; ++c) {
+          if (c + 1 < kChunks) tmem_ld16(acc + 16 * (c + 1), r[(c + 1) % kBuf]);
+          fold16(c, r[c % kBuf]);
+          if (c + 1 < kChunks) tmem_ld_wait(r[(c + 1) % kBuf]);
+          if (c + 2 == kChunks) release_acc(&afree[b], lane);
         }
       }
       __syncwarp();
       if (!ok) break;
-      const size_t row0 = static_cast<size_t>(t.row + cs);
-      const int n_now = n, mine_now = mine;
-      if (id + gridDim.x < ntiles) begin(id + gridDim.x);
-      // Sixteen tokens at a time, so that their chains overlap (one pair after
-      // the other took 30,000 cycles a tile, clock64 trace).
+      // One copy of the epilogue's code, 32 tokens a turn, the sums moved down
+      // in between.
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 32) {
+        if (c >= t.rows) break;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int left = mine_now - 16 * c;  // warp-uniform
-        if (left <= 0) break;
-        float v[16];
+        for (int h = 0; h < 2; ++h) {
+          float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 rv = *reinterpret_cast<const float4*>(my_rs + 16 * c + j);
-          v[j] = __fmul_rn(sum[16 * c + j], rv.x);
-          v[j + 1] = __fmul_rn(sum[16 * c + j + 1], rv.y);
-          v[j + 2] = __fmul_rn(sum[16 * c + j + 2], rv.z);
-          v[j + 3] = __fmul_rn(sum[16 * c + j + 3], rv.w);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 rv = *reinterpret_cast<const float4*>(my_rs + c + 16 * h + j);
+            v[j] = __fmul_rn(sum[16 * h + j], rv.x);
+            v[j + 1] = __fmul_rn(sum[16 * h + j + 1], rv.y);
+            v[j + 2] = __fmul_rn(sum[16 * h + j + 2], rv.z);
+            v[j + 3] = __fmul_rn(sum[16 * h + j + 3], rv.w);
+          }
+          if (t.rows > c + 16 * h)
+            store16<OUT>(p, static_cast<size_t>(t.row + c + 16 * h), n, t.rows - c - 16 * h, lane, v);
         }
-        store16(p, row0 + 16 * c, n_now, left, pairs, lane, v);
+#pragma unroll
+        for (int j = 0; j + 32 < NT; ++j) sum[j] = sum[j + 32];
       }
     }
     cp_async_wait_all();  // no scale copy outlives the CTA
@@ -579,32 +580,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// s8 [M, K] -> fp16 [M, K], each eight in the order 0 4 1 5 2 6 3 7.
-__global__ void __launch_bounds__(256) codes_f16_kernel(const int8_t* __restrict__ codes, int64_t n16,
-                                                        uint16_t* __restrict__ out, const int32_t* mode_dev) {
+// s8 [M, K] -> the token operand, 2 K bytes a row: per group of 128 the high
+// digits h of q = 16 h + l as E4M3 of h 2^-5, then the low ones (0 .. 15) as
+// E4M3 of l 2^-9, each eight in the order 0 2 4 6 1 3 5 7.
+__device__ __forceinline__ uint32_t high_digits(uint32_t q) {
+  const uint32_t n = (q >> 7) & 0x01010101u;                         // negative
+  const uint32_t mag = (((q >> 4) & 0x0F0F0F0Fu) ^ (n * 15u)) + n;   // |h|, 0 .. 8
+  const uint32_t t = mag | (mag >> 4);
+  const uint32_t code = __byte_perm(0x1C181000u, 0x26242220u, __byte_perm(t, 0u, 0x4420));  // |h| = 0 .. 7 (8 -> 0)
+  return code + ((mag >> 3) & 0x01010101u) * 0x28u + n * 0x80u;
+}
+__global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ codes, int64_t n16,
+                                              uint8_t* __restrict__ out, const int32_t* mode_dev) {
   if (mode_dev != nullptr && SIXBIT_MODE_OF(*mode_dev) != SIXBIT_MODE_INT8) return;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes) + i);
-    uint32_t lo[4], hi[4];
-    codes_f16(c.x, c.y, lo);
-    codes_f16(c.z, c.w, hi);
-    uint4* o = reinterpret_cast<uint4*>(out) + 2 * i;
-    o[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    o[1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    const uint4 s = make_uint4(__byte_perm(c.x, c.y, 0x6420), __byte_perm(c.x, c.y, 0x7531),
+                               __byte_perm(c.z, c.w, 0x6420), __byte_perm(c.z, c.w, 0x7531));
+    uint4* o = reinterpret_cast<uint4*>(out) + (i >> 3) * 16 + (i & 7);  // (128 codes are 8 reads; K % 128 == 0)
+    o[0] = make_uint4(high_digits(s.x), high_digits(s.y), high_digits(s.z), high_digits(s.w));
+    o[8] = make_uint4(s.x & 0x0F0F0F0Fu, s.y & 0x0F0F0F0Fu, s.z & 0x0F0F0F0Fu, s.w & 0x0F0F0F0Fu);
   }
 }
 
-template <bool NARROW>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull, const RowsParams& p, cudaStream_t st) {
-  cudaError_t e = set_smem_once<grouped_kernel<NARROW>>(static_cast<int>(Smem<NARROW>::bytes(SIXBIT_MAX_EXPERTS)));
+template <bool NARROW, Out OUT>
+cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull, const RowsParams& p,
+                   cudaStream_t st) {
+  cudaError_t e = set_smem_once<grouped_kernel<NARROW, OUT>>(static_cast<int>(Smem<NARROW>::bytes(SIXBIT_MAX_EXPERTS)));
   if (e != cudaSuccess) return e;
   if constexpr (!NARROW) {
     static ContextCache<int> regs_cache;
     int regs = 0;
     e = regs_cache.get(&regs, [](int* o) {
       cudaFuncAttributes fa;
-      const cudaError_t r = cudaFuncGetAttributes(&fa, grouped_kernel<NARROW>);
+      const cudaError_t r = cudaFuncGetAttributes(&fa, grouped_kernel<NARROW, OUT>);
       *o = fa.numRegs;
       return r;
     });
@@ -615,22 +625,31 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap
   }
   // at most one token tile per row, and one more per expert than rows / NT
   const int64_t tiles_n = (p.N + kBM - 1) / kBM;
-  const int64_t tiles_t = min(static_cast<int64_t>(p.M), p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
+  const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
   if (tiles_t * tiles_n > INT32_MAX) return cudaErrorInvalidValue;  // tile numbers are 32 bits
-  const int sms = sm_count();
-  const int grid = tiles_t * tiles_n < sms ? static_cast<int>(tiles_t * tiles_n) : sms;
-  grouped_kernel<NARROW><<<grid, kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, xfull, p);
+  const int grid = static_cast<int>(std::min<int64_t>(tiles_t * tiles_n, sm_count()));
+  grouped_kernel<NARROW, OUT><<<grid, kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, xfull, p);
   note_launch();
   return cudaGetLastError();
 }
 
+template <bool NARROW>
+cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull, const RowsParams& p,
+                        cudaStream_t st) {
+  const bool pairs = p.Yf == nullptr && (p.N & 1) == 0 &&
+                     ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
+  if (!pairs) return launch<NARROW, kAny>(w, x, xfull, p, st);
+  if (p.epilogue == SIXBIT_EPI_GELU) return launch<NARROW, kPairGelu>(w, x, xfull, p, st);
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL) return launch<NARROW, kPairResidual>(w, x, xfull, p, st);
+  return launch<NARROW, kPair>(w, x, xfull, p, st);
+}
+
 }  // namespace grouped
 
-cudaError_t launch_codes_f16(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint16_t* out,
-                             cudaStream_t st) {
+cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st) {
   const int64_t n16 = static_cast<int64_t>(M) * K / 16;
   const int64_t want = (n16 + 255) / 256, cap = static_cast<int64_t>(sm_count()) * 8;
-  grouped::codes_f16_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(codes, n16, out, mode_dev);
+  grouped::digits_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(codes, n16, out, mode_dev);
   note_launch();
   return cudaGetLastError();
 }
@@ -639,7 +658,7 @@ int grouped_tokens(bool narrow) { return narrow ? grouped::Cfg<true>::NT : group
 
 cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull,
                                 const RowsParams& p, bool narrow, cudaStream_t st) {
-  return narrow ? grouped::launch<true>(w, x, xfull, p, st) : grouped::launch<false>(w, x, xfull, p, st);
+  return narrow ? grouped::launch_form<true>(w, x, xfull, p, st) : grouped::launch_form<false>(w, x, xfull, p, st);
 }
 
 }  // namespace sixbit
