@@ -105,6 +105,17 @@ static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 
 static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 static_assert(Cfg<false>::SX > Cfg<false>::NA && Cfg<true>::SX > Cfg<true>::NA, "a token slot's commit frees the A slot");
 
+// One lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, E4M3 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -371,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t j = (it > SX ? it - SX : 0); j < it; ++j)
           (void)mbar_wait(&x_full[j % SX], (j / SX) & 1, nullptr, p.wait_ns);
       }
-    } else if (lane == 0) {
+    } else {
       // --------------------------------------------------------- MMA issuers --
       const uint32_t par = warp == 1 ? 0u : 1u;
       // The accumulator is waited for last: with NB odd an issuer meets a buffer
@@ -396,20 +407,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d_tmem = tmem + C::acc_col(gi % NB), a_tmem = tmem + C::a_col(gi % NA);
           const uint32_t b_base = smem_u32(smem + L::kX + s * L::kXSlot);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 32 k: the high digits, then the low ones
-            mma_e4m3_tmem_a(d_tmem, a_tmem + 8 * (k >> 1), sdesc_sw128(b_base + (k & 1) * (NT * 128) + 32 * (k >> 1)),
-                            idesc, k == 0 ? 0u : 1u);
-          tc_commit(&done[gi % NB]);
-          tc_commit(&x_empty[s]);
+            for (int k = 0; k < 8; ++k)  // 32 k: the high digits, then the low ones
+              mma_e4m3_tmem_a(d_tmem, a_tmem + 8 * (k >> 1), sdesc_sw128(b_base + (k & 1) * (NT * 128) + 32 * (k >> 1)),
+                              idesc, k == 0 ? 0u : 1u);
+            tc_commit(&done[gi % NB]);
+            tc_commit(&x_empty[s]);
+          }
+          __syncwarp();
         }
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         set_error(p.err, SIXBIT_ETIMEOUT);
         *abort_flag = 1;
       }
-      tc_commit(drain);  // both issuers: all tensor-core work completes before exit
-      (void)mbar_wait(drain, 0, nullptr, p.wait_ns);
+      __syncwarp();
+      if (elect_one()) {
+        tc_commit(drain);  // both issuers: all tensor-core work completes before exit
+        (void)mbar_wait(drain, 0, nullptr, p.wait_ns);
+      }
+      __syncwarp();
     }
   } else if (warp < kFoldWarp0) {
     if constexpr (!NARROW) setmaxnreg_dec<kRegsConv>();
