@@ -138,22 +138,6 @@ static bool make_map_s8(CUtensorMap* m, const int8_t* base, int rows, int cols) 
   return r == CUDA_SUCCESS;
 }
 
-// INT4 codes [rows, K/2] bytes for the grouped product: box 64 bytes (one
-// scale group) x 128 rows, 64-byte swizzle (16-byte chunk c of row r at chunk
-// c ^ ((r >> 1) & 3)), out-of-bounds rows read as zero.
-static bool make_w4_map(CUtensorMap* m, const uint8_t* base, int64_t rows, int K) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
-  cuuint32_t box[2] = {64, 128};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 // bf16 output Y [rows, cols] for the GEMM epilogue's TMA stores: box 32
 // columns (64 bytes) x 32 rows, 64-byte swizzle.
 static bool make_store_map(CUtensorMap* m, const uint16_t* Y, int rows, int cols) {
@@ -654,7 +638,7 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   uint8_t* xd = static_cast<uint8_t*>(workspace);
   const bool narrow = M < 64 * static_cast<int64_t>(E);
   CUtensorMap mw, mx, mxf;
-  if (!make_w4_map(&mw, W->i4_codes, static_cast<int64_t>(E) * N, K) ||
+  if (!make_map(&mw, W->i4_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, E * N, K / 2, 128) ||
       !make_map(&mx, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, 32) ||
       !make_map(&mxf, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, grouped_tokens(narrow)))
     return SIXBIT_ECUDA;

@@ -132,8 +132,8 @@ struct RowsParams {
 cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st);
 // Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row.
 cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st);
-// w: map of the INT4 codes [E N, K/2] (box 64 bytes x 128 rows, 64-byte
-// swizzle); x, xfull: maps of the token operand (boxes of 128 bytes x 32 rows
+// w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows,
+// 128-byte swizzle); x, xfull: maps of the token operand (boxes of 128 bytes x 32 rows
 // and x grouped_tokens(narrow) rows, 128-byte swizzle).  narrow: token tiles of
 // 32 instead of 128.
 int grouped_tokens(bool narrow);

@@ -64,46 +64,51 @@
 namespace sixbit {
 namespace grouped {
 
-constexpr int kBM = 128;         // weight rows of a tile
-constexpr int kThreads = 512;
-constexpr int kWSlot = kBM * 64;  // a group's nibbles, 8 KB
-constexpr int kSwRing = 4;       // groups of scales in flight per fold thread
+constexpr int kBM = 128;           // weight rows of a tile
 constexpr int kConvWarp0 = 4;
+constexpr int kPairBytes = kBM * 128;  // nibbles of two groups: 128 rows of 128 bytes, 128-byte swizzle
+constexpr int kSwRing = 3;             // batches of scales in flight per fold thread
 
+// GB: groups of a batch.  XG, CG: groups of a token slot and of an accumulator.
+// SW, SX, NA, NB: slots of the nibble, token, A and accumulator rings.
 template <bool NARROW>
 struct Cfg;
 template <>
 struct Cfg<false> {
-  static constexpr int NT = 128, SW = 4, SX = 5, NA = 4, NB = 3, kConv = 4, kTeams = 2;
-  __host__ __device__ static constexpr int acc_col(int b) { return b * 128; }
-  __host__ __device__ static constexpr int a_col(int a) { return 384 + a * 32; }
+  static constexpr int NT = 128, GB = 2, XG = 1, CG = 1, SW = 2, SX = 5, NA = 2, NB = 3, kTeams = 2, kTeamWarps = 8;
 };
 template <>
 struct Cfg<true> {
-  static constexpr int NT = 32, SW = 12, SX = 12, NA = 4, NB = 4, kConv = 8, kTeams = 1;
-  __host__ __device__ static constexpr int acc_col(int b) { return b * 32; }
-  __host__ __device__ static constexpr int a_col(int a) { return 128 + a * 32; }
+  static constexpr int NT = 32, GB = 4, XG = 4, CG = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 1, kTeamWarps = 4;
 };
-constexpr int kRegsLaunch = 128, kRegsLow = 40, kRegsConv = 88, kRegsHigh = 192;  // the wide form's split
-static_assert(4 * kRegsLow + 4 * kRegsConv + 8 * kRegsHigh <= 16 * kRegsLaunch &&
-                  kRegsLow + kRegsConv + 2 * kRegsHigh <= 4 * kRegsLaunch,
-              "the register split must fit in what the CTA is launched with");
+// The wide form's registers: 768 threads launch with 80 each; warps 0 - 3 keep
+// 32, the converters 64, the fold warps get 96 (24 x 80 = 4 x 32 + 4 x 64 + 16 x 96).
+constexpr int kRegsLaunch = 80, kRegsLow = 32, kRegsConv = 64, kRegsHigh = 96;
 
 template <bool NARROW>
 struct Smem {
   using C = Cfg<NARROW>;
-  static constexpr int kXSlot = C::NT * 256;  // a group's tokens: the high digits' 128 bytes, then the low ones'
-  static constexpr int kFold = 4 * C::kTeams;
-  static constexpr int kWarpArea = kSwRing * 32 * 4 + C::NT * 4;  // a fold warp's scale ring and row scales
-  static constexpr int kBars = 2 * C::SW + 2 * C::SX + C::NA + (C::kTeams + 1) * C::NB + 1;
+  static constexpr int kConv = 4 * (C::GB / 2), kFold = C::kTeamWarps * C::kTeams;  // warps
+  static constexpr int kWarps = kConvWarp0 + kConv + kFold, kThreads = 32 * kWarps;
+  static constexpr int kCols = C::NT / (C::kTeamWarps / 4);  // tokens of a fold thread
+  static constexpr int kXGroup = C::NT * 256;  // a group's tokens: the high digits' 128 bytes, then the low ones'
+  static constexpr int kXSlot = C::XG * kXGroup, kWSlot = (C::GB / 2) * kPairBytes;
+  static constexpr int kWarpArea = kSwRing * C::GB * 32 * 4 + kCols * 4;  // a fold warp's scale ring and row scales
+  static constexpr int kBars = 2 * C::SW + 2 * C::SX + 2 * C::NA + (C::kTeams + 1) * C::NB + 3;
   static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
                        kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
+  static constexpr int kAccCols = C::CG * C::NT, kACol0 = C::NB * kAccCols, kACols = C::GB * 32;
+  static_assert(kACol0 + C::NA * kACols <= 512, "tensor memory columns");
   // tables: prefix [E + 1], first row [E], rows [E]
   static size_t bytes(int E) { return 1024 + kTables + static_cast<size_t>(3 * E + 1) * 4; }
 };
+static_assert(4 * kRegsLow + Smem<false>::kConv * kRegsConv + Smem<false>::kFold * kRegsHigh <=
+                  Smem<false>::kWarps * kRegsLaunch,
+              "the register split must fit in what the CTA is launched with");
+// setmaxnreg.dec may not raise a warp's count, nor .inc lower it
+static_assert(kRegsLow <= kRegsLaunch && kRegsConv <= kRegsLaunch && kRegsHigh >= kRegsLaunch, "register split");
 static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
-static_assert(Cfg<false>::SX > Cfg<false>::NA && Cfg<true>::SX > Cfg<true>::NA, "a token slot's commit frees the A slot");
 
 // One lane of the (converged) warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
@@ -116,14 +121,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, E4M3 inputs, fp32 accumulate.
-__device__ __forceinline__ void mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T, E4M3 inputs, fp32 accumulate.  The first
+// of two MMAs with the same A leaves it in the collector buffer, the second
+// takes it from there.
+__device__ __forceinline__ void mma_e4m3_fill(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_e4m3_lastuse(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc)
       : "memory");
 }
 // Each thread of the warp writes 32 consecutive 32-bit columns of its lane.
@@ -218,31 +233,45 @@ __device__ __forceinline__ void store16(const RowsParams& p, size_t row, int n, 
   }
 }
 
+// sum += s * accumulator columns
+template <int COLS>
+__device__ __forceinline__ void fold(float s, const uint32_t (&r)[COLS], float* sum) {
+  const uint64_t s2 = f2_pack(s, s);
+#pragma unroll
+  for (int i = 0; i < COLS; i += 2) {
+    const uint64_t v = f2_fma(s2, f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(sum[i], sum[i + 1]));
+    sum[i] = f2_lo(v);
+    sum[i + 1] = f2_hi(v);
+  }
+}
+
 struct Tile {
   int e, row, rows, n0;  // expert, first row of Y, rows of the tile, first weight row
 };
 
 template <bool NARROW, Out OUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ CUtensorMap tmXfull, const RowsParams p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   using C = Cfg<NARROW>;
   using L = Smem<NARROW>;
-  constexpr int NT = C::NT, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
-  constexpr int kFoldWarp0 = 16 - L::kFold;
+  constexpr int NT = C::NT, GB = C::GB, XG = C::XG, CG = C::CG, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
+  constexpr int kFoldWarp0 = kConvWarp0 + L::kConv;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarAt);
-  uint64_t* w_full = bars;          // [SW] nibble tile landed
-  uint64_t* w_empty = w_full + SW;  // [SW] its four converter warps have read it
-  uint64_t* x_full = w_empty + SW;  // [SX] token tile landed
-  uint64_t* x_empty = x_full + SX;  // [SX] the group's MMAs are complete
-  uint64_t* a_full = x_empty + SX;  // [NA] four converter warps stored the A slot
-  uint64_t* acc_full = a_full + NA;                // [team][NB] a group of the team's tile is complete
-  uint64_t* afree = acc_full + C::kTeams * NB;     // [NB] accumulator read back by a team's four warps
-  uint64_t* drain = afree + NB;
+  uint64_t* w_full = bars;                      // [SW] a batch's nibbles landed
+  uint64_t* w_empty = w_full + SW;              // [SW] the converter warps have read them
+  uint64_t* x_full = w_empty + SW;              // [SX] a token slot landed
+  uint64_t* x_empty = x_full + SX;              // [SX] its MMAs are complete
+  uint64_t* a_full = x_empty + SX;              // [NA] the converter warps stored a batch's A
+  uint64_t* a_empty = a_full + NA;              // [NA] the batch's MMAs are complete
+  uint64_t* acc_full = a_empty + NA;            // [team][NB] an accumulator of the team's tile is complete
+  uint64_t* afree = acc_full + C::kTeams * NB;  // [NB] it has been read back by the team's four warps
+  uint64_t* turns = afree + NB;                 // [2] the other issuer has issued its batch
+  uint64_t* drain = turns + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* prefix = reinterpret_cast<int*>(smem + L::kTables);  // [E + 1] token tiles of the experts before e
@@ -250,21 +279,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* count = first + p.E;                                 // [E]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nk = p.K / 128;
+  const int nk = p.K / 128, np = (nk + GB - 1) / GB;  // groups, batches of a tile
   const uint32_t tiles_n = (p.N + kBM - 1) / kBM;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < SW; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], 4);
+      mbar_init(&w_empty[s], L::kConv);
     }
     for (int s = 0; s < SX; ++s) {
       mbar_init(&x_full[s], 1);
       mbar_init(&x_empty[s], 1);
     }
-    for (int a = 0; a < NA; ++a) mbar_init(&a_full[a], 4);
+    for (int a = 0; a < NA; ++a) {
+      mbar_init(&a_full[a], L::kConv);
+      mbar_init(&a_empty[a], 1);
+    }
     for (int b = 0; b < C::kTeams * NB; ++b) mbar_init(&acc_full[b], 1);
-    for (int b = 0; b < NB; ++b) mbar_init(&afree[b], 4);
+    for (int b = 0; b < NB; ++b) mbar_init(&afree[b], C::kTeamWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&turns[i], 1);
     mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
@@ -324,19 +357,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       if (lane == 0) {
         // -------------------------------------------------- nibble producer --
-        uint32_t it = 0;
+        uint32_t bi = 0;
         bool ok = true;
         for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
           const Tile t = tile_at(id);
           const int wrow = t.e * p.N + t.n0;
-          for (int kb = 0; kb < nk; ++kb, ++it) {
-            const int s = it % SW;
-            if (it >= SW && !mbar_wait(&w_empty[s], ((it / SW) - 1) & 1, abort_flag, p.wait_ns)) {
+          for (int j = 0; j < np; ++j, ++bi) {
+            const int s = bi % SW;
+            if (bi >= SW && !mbar_wait(&w_empty[s], ((bi / SW) - 1) & 1, abort_flag, p.wait_ns)) {
               ok = false;
               break;
             }
-            mbar_expect_tx(&w_full[s], kWSlot);
-            tma_load_2d(smem + L::kW + s * kWSlot, &tmW, &w_full[s], kb * 64, wrow);
+            const int boxes = min(GB / 2, (nk - j * GB + 1) / 2);  // (a last, odd group's box is half past the row: zeros)
+            mbar_expect_tx(&w_full[s], boxes * kPairBytes);
+            for (int h = 0; h < boxes; ++h)
+              tma_load_2d(smem + L::kW + s * L::kWSlot + h * kPairBytes, &tmW, &w_full[s], (j * GB + 2 * h) * 64, wrow);
           }
         }
         if (!ok) {
@@ -344,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *abort_flag = 1;
         }
         // every copy this warp started lands before it can exit
-        for (uint32_t j = (it > SW ? it - SW : 0); j < it; ++j)
+        for (uint32_t j = (bi > SW ? bi - SW : 0); j < bi; ++j)
           (void)mbar_wait(&w_full[j % SW], (j / SW) & 1, nullptr, p.wait_ns);
       }
     } else if (warp == 2) {
@@ -355,23 +390,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
           const Tile t = tile_at(id);
           const int boxes = t.rows > NT - 32 ? NT / 32 : (t.rows + 31) / 32;
-          for (int kb = 0; kb < nk; ++kb, ++it) {
+          for (int g0 = 0; g0 < nk; g0 += XG, ++it) {
             const int s = it % SX;
             if (it >= SX && !mbar_wait(&x_empty[s], ((it / SX) - 1) & 1, abort_flag, p.wait_ns)) {
               ok = false;
               break;
             }
             if (p.withhold_first && it == 0) continue;  // failure-path test: slot 0 never lands
-            mbar_expect_tx(&x_full[s], boxes * 8192);
-            uint8_t* dst = smem + L::kX + s * L::kXSlot;
-            if (boxes == NT / 32) {
-              tma_load_2d(dst, &tmXfull, &x_full[s], kb * 256, t.row);
-              tma_load_2d(dst + NT * 128, &tmXfull, &x_full[s], kb * 256 + 128, t.row);
-              continue;
-            }
-            for (int b = 0; b < boxes; ++b) {
-              tma_load_2d(dst + b * 4096, &tmX, &x_full[s], kb * 256, t.row + 32 * b);
-              tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], kb * 256 + 128, t.row + 32 * b);
+            const int groups = min(XG, nk - g0);
+            mbar_expect_tx(&x_full[s], groups * boxes * 8192);
+            for (int g = 0; g < groups; ++g) {
+              uint8_t* dst = smem + L::kX + s * L::kXSlot + g * L::kXGroup;
+              const int c = (g0 + g) * 256;
+              if (boxes == NT / 32) {
+                tma_load_2d(dst, &tmXfull, &x_full[s], c, t.row);
+                tma_load_2d(dst + NT * 128, &tmXfull, &x_full[s], c + 128, t.row);
+                continue;
+              }
+              for (int b = 0; b < boxes; ++b) {
+                tma_load_2d(dst + b * 4096, &tmX, &x_full[s], c, t.row + 32 * b);
+                tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], c + 128, t.row + 32 * b);
+              }
             }
           }
         }
@@ -384,38 +423,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // --------------------------------------------------------- MMA issuers --
+      // Warp 1 issues the even batches, warp 3 the odd ones (the whole warp
+      // keeps the loop, so that the operands stay in uniform registers; one
+      // elected lane issues: with the loop in one lane, an MMA took some 100
+      // cycles of issue), strictly in turn: one's waits and commits (some 120 cycles each) overlap the
+      // other's MMAs, and no MMA comes between two that share the collector
+      // buffer.  A wait that an issuer meets at every second phase only cannot
+      // mistake an older phase for its own: x and the first accumulator of a
+      // batch were last waited for by a batch that this issuer's last turn
+      // came after; the second accumulator is waited for within the turn.
       const uint32_t par = warp == 1 ? 0u : 1u;
-      // The accumulator is waited for last: with NB odd an issuer meets a buffer
-      // at every second phase only, and the A slot's arrival (which follows the
-      // MMAs of group gi - 3) is what rules out that the phase before is still open.
-      uint32_t gi = 0, turn = 0;
+      uint32_t bi = 0, xi = 0, ci = 0, turn = 0;  // batches, token slots, accumulators, tiles so far
       bool ok = true;
       for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
         const Tile t = tile_at(id);
         uint64_t* done = acc_full + (C::kTeams > 1 ? (turn & 1) * NB : 0);
         const uint32_t nt = static_cast<uint32_t>((t.rows + 15) & ~15);
         const uint32_t idesc = (1u << 4) | ((nt >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
-        for (int g = 0; g < nk; ++g, ++gi) {
-          if ((gi & 1) != par) continue;
-          const int s = static_cast<int>(gi % SX);
-          if (!mbar_wait(&x_full[s], (gi / SX) & 1, abort_flag, p.wait_ns) ||
-              !mbar_wait(&a_full[gi % NA], (gi / NA) & 1, abort_flag, p.wait_ns) ||
-              (gi >= NB && !mbar_wait(&afree[gi % NB], ((gi / NB) - 1) & 1, abort_flag, p.wait_ns))) {
-            ok = false;
-            break;
+        for (int j = 0; j < np; ++j, ++bi) {
+          const int groups = min(GB, nk - j * GB), xs = XG == 1 ? groups : 1, cs = CG == 1 ? groups : 1;
+          if ((bi & 1) != par) {
+            xi += xs;
+            ci += cs;
+            continue;
           }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem + C::acc_col(gi % NB), a_tmem = tmem + C::a_col(gi % NA);
-          const uint32_t b_base = smem_u32(smem + L::kX + s * L::kXSlot);
-          if (elect_one()) {
+          const int a = bi % NA;
+          ok = mbar_wait(&a_full[a], (bi / NA) & 1, abort_flag, p.wait_ns);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)  // 32 k: the high digits, then the low ones
-              mma_e4m3_tmem_a(d_tmem, a_tmem + 8 * (k >> 1), sdesc_sw128(b_base + (k & 1) * (NT * 128) + 32 * (k >> 1)),
-                              idesc, k == 0 ? 0u : 1u);
-            tc_commit(&done[gi % NB]);
-            tc_commit(&x_empty[s]);
+          for (int i = 0; i < (XG == 1 ? GB : 1); ++i)
+            if (i < xs && ok) ok = mbar_wait(&x_full[(xi + i) % SX], ((xi + i) / SX) & 1, abort_flag, p.wait_ns);
+          if (ok && ci >= NB) ok = mbar_wait(&afree[ci % NB], ((ci / NB) - 1) & 1, abort_flag, p.wait_ns);
+          if (ok && bi > 0) ok = mbar_wait(&turns[par], ((bi - 1) >> 1) & 1, abort_flag, p.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < GB; ++g) {
+            if (g >= groups || !ok) break;
+            if (CG == 1 && g > 0) {
+              if (ci + g >= NB) ok = mbar_wait(&afree[(ci + g) % NB], (((ci + g) / NB) - 1) & 1, abort_flag, p.wait_ns);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint32_t d_tmem = tmem + (CG == 1 ? ((ci + g) % NB) * NT : (ci % NB) * L::kAccCols + g * NT);
+            const uint32_t a_tmem = tmem + L::kACol0 + a * L::kACols + g * 32;
+            const uint32_t b_base = smem_u32(smem + L::kX) +
+                                    (XG == 1 ? ((xi + g) % SX) * L::kXSlot : (xi % SX) * L::kXSlot + g * L::kXGroup);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
+                mma_e4m3_fill(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + 32 * k), idesc, k == 0 ? 0u : 1u);
+                mma_e4m3_lastuse(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + NT * 128 + 32 * k), idesc);
+              }
+              if (CG == 1) {
+                tc_commit(&done[(ci + g) % NB]);
+                tc_commit(&x_empty[(xi + g) % SX]);
+              }
+            }
+            __syncwarp();
+          }
+          if (elect_one()) {
+            mbar_arrive(&turns[par ^ 1]);
+            if (ok) {
+              if (CG != 1) {
+                tc_commit(&done[ci % NB]);
+                tc_commit(&x_empty[xi % SX]);
+              }
+              tc_commit(&a_empty[a]);
+            }
           }
           __syncwarp();
+          if (!ok) break;
+          xi += xs;
+          ci += cs;
         }
       }
       if (!ok && lane == 0) {
@@ -433,55 +512,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!NARROW) setmaxnreg_dec<kRegsConv>();
     // ------------------------------------------------------------ converters --
     // Thread `lane` of the warp of quarter q converts weight row 32 q + lane,
-    // the row of its tensor-memory lane.  The next group's nibbles are read
-    // while this one's are stored, and half of them are converted before the
-    // A slot is waited for: one step after the other, a group took the
-    // converters 1,100 cycles, more than its MMAs.  A nibble slot goes back
-    // once every lane's reads have returned (`zero` needs them) and behind a
-    // proxy fence: the refill is an async-proxy write.
-    constexpr uint32_t kSets = C::kConv / 4;
-    const int q = warp & 3, myrow = 32 * q + lane;
-    const int swz = (myrow >> 1) & 3;
-    const uint32_t total = blockIdx.x < ntiles ? ((ntiles - blockIdx.x - 1) / gridDim.x + 1) * nk : 0;
-    const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    uint32_t it = static_cast<uint32_t>((warp - kConvWarp0) >> 2);
+    // the row of its tensor-memory lane; each set of four warps takes two
+    // groups of every batch (one group at a time, the barriers and fences took
+    // the converters 1,100 cycles a group, more than its MMAs).  A nibble slot
+    // goes back once every lane's reads have returned (`zero` needs them) and
+    // behind a proxy fence: the refill is an async-proxy write.
+    const int q = warp & 3, myrow = 32 * q + lane, pair = (warp - kConvWarp0) >> 2;
+    const int swz = myrow & 7;
+    const uint32_t total = blockIdx.x < ntiles ? ((ntiles - blockIdx.x - 1) / gridDim.x + 1) * np : 0;
+    const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16) + L::kACol0 + pair * 64;
+    const uint8_t* row = smem + L::kW + pair * kPairBytes + myrow * 128;
     bool ok = true;
-    uint4 in[4];
-    auto read = [&](uint32_t i) {
-      if (!mbar_wait(&w_full[i % SW], (i / SW) & 1, abort_flag, p.wait_ns)) return false;
-      const uint8_t* row = smem + L::kW + (i % SW) * kWSlot + myrow * 64;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) in[c] = *reinterpret_cast<const uint4*>(row + ((c ^ swz) << 4));
-      return true;
-    };
-    auto give_back = [&](uint32_t i) {
-      uint32_t zero;
-      asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(in[0].x ^ in[1].x ^ in[2].x ^ in[3].x));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&w_empty[i % SW]);
-    };
-    if (it < total) ok = read(it);
-    for (; it < total && ok; it += kSets) {
-      const int a = it % NA;
-      give_back(it);
-      uint32_t v[32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint32_t word[4] = {in[c].x, in[c].y, in[c].z, in[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) nibbles_e4m3(word[i], v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
-      }
-      if (it >= NA && !mbar_wait(&x_empty[(it - NA) % SX], ((it - NA) / SX) & 1, abort_flag, p.wait_ns)) {
+    for (uint32_t bi = 0; bi < total; ++bi) {
+      const int s = bi % SW, a = bi % NA;
+      if (!mbar_wait(&w_full[s], (bi / SW) & 1, abort_flag, p.wait_ns)) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      tmem_st32(acol + C::a_col(a), v);
-      if (it + kSets < total && !read(it + kSets)) {
-        ok = false;
-        break;
+      bool waited = bi < NA;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 in[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          in[c] = *reinterpret_cast<const uint4*>(row + s * L::kWSlot + (((4 * h + c) ^ swz) << 4));
+        if (h == 1) {
+          uint32_t zero;
+          asm volatile("and.b32 %0, %1, 0;" : "=r"(zero) : "r"(in[0].x ^ in[1].x ^ in[2].x ^ in[3].x));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&w_empty[s]);
+        }
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4& u = in[c];
+          nibbles_e4m3(u.x, v[8 * c], v[8 * c + 1]);
+          nibbles_e4m3(u.y, v[8 * c + 2], v[8 * c + 3]);
+          nibbles_e4m3(u.z, v[8 * c + 4], v[8 * c + 5]);
+          nibbles_e4m3(u.w, v[8 * c + 6], v[8 * c + 7]);
+        }
+        if (!waited) {
+          waited = true;
+          if (!mbar_wait(&a_empty[a], ((bi / NA) - 1) & 1, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        tmem_st32(acol + a * L::kACols + 32 * h, v);
       }
+      if (!ok) break;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -494,69 +575,112 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     if constexpr (!NARROW) setmaxnreg_inc<kRegsHigh>();
     // -------------------------------------------------------- fold + epilogue --
-    // A team of four warps takes a whole tile, every kTeams-th of the CTA's.
-    constexpr int kChunks = NT / 16, kBuf = 2;
+    // A team takes a whole tile, every kTeams-th of the CTA's; a thread one
+    // weight row and kCols tokens of it.
+    constexpr int kCols = L::kCols, kChunks = kCols / 16;
     const int ew = warp - kFoldWarp0, q = warp & 3;
-    const uint32_t team = static_cast<uint32_t>(ew >> 2);
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t team = static_cast<uint32_t>(ew / C::kTeamWarps);
+    const int cs = (ew % C::kTeamWarps) / 4 * kCols;  // first token of this thread
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + cs;
     float* my_sw = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + lane;  // [slot][32]
-    float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * 32;
+    float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * GB * 32;
     uint64_t* full = acc_full + team * NB;
     uint32_t phases = 0;  // bit b: parity of this team's next wait for buffer b
-    uint32_t gi = 0, turn = 0;
+    uint32_t ci = 0, turn = 0;
+    const int accs = CG == 1 ? nk : np;  // accumulators of a tile
     bool ok = true;
     for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
       if (C::kTeams > 1 && (turn & 1) != team) {
-        gi += nk;
+        ci += accs;
         continue;
       }
       const Tile t = tile_at(id);
       const int n = t.n0 + 32 * q + lane;  // output column
       const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
-      auto fetch_sw = [&](int g) {  // a group of copies even when it holds none
-        if (g < nk && n < p.N) cp_async4(smem_u32(my_sw + (g % kSwRing) * 32), sw + static_cast<size_t>(g) * p.N);
+      auto fetch_sw = [&](int j) {  // a batch's scales; a group of copies even when it holds none
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+          if (j * GB + g < nk && n < p.N)
+            cp_async4(smem_u32(my_sw + ((j % kSwRing) * GB + g) * 32), sw + static_cast<size_t>(j * GB + g) * p.N);
         cp_async_commit();
       };
 #pragma unroll
-      for (int g = 0; g < kSwRing - 1; ++g) fetch_sw(g);
+      for (int j = 0; j < kSwRing - 1; ++j) fetch_sw(j);
       __syncwarp();  // every lane is done with the last tile's row scales
+      const int mine = t.rows - cs;  // tokens of this thread: min(mine, kCols)
 #pragma unroll
-      for (int j = lane; j < NT; j += 32) my_rs[j] = j < t.rows ? __ldg(p.row_scale + t.row + j) : 0.f;
-      float sum[NT];
+      for (int j = lane; j < kCols; j += 32) my_rs[j] = j < mine ? __ldg(p.row_scale + t.row + cs + j) : 0.f;
+      float sum[kCols];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) sum[j] = 0.f;
-      for (int g = 0; g < nk; ++g, ++gi) {
-        fetch_sw(g + kSwRing - 1);
-        cp_async_wait_newest<kSwRing - 1>();  // this thread's scale of group g has landed
-        const float s = my_sw[(g % kSwRing) * 32];
-        const uint32_t b = gi % NB;
-        if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        phases ^= 1u << b;
-        tc_fence_after();
-        const uint32_t acc = lane_addr + C::acc_col(b);
-        const uint64_t s2 = f2_pack(s * 262144.f, s * 262144.f);  // (2^18: both operands stand in units of 2^-9)
-        auto fold16 = [&](int c, const uint32_t (&r)[16]) {
+      for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
+      for (int j = 0; j < np && ok; ++j) {
+        cp_async_wait_newest<kSwRing - 2>();  // this thread's scales of batch j have landed
+        float s[GB];
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float* sm = sum + 16 * c + j;
-            const uint64_t v = f2_fma(s2, f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f2_pack(sm[0], sm[1]));
-            sm[0] = f2_lo(v);
-            sm[1] = f2_hi(v);
+        for (int g = 0; g < GB; ++g) s[g] = my_sw[((j % kSwRing) * GB + g) * 32] * 262144.f;  // (2^18: both operands
+                                                                                             //  in units of 2^-9)
+        fetch_sw(j + kSwRing - 1);
+        if constexpr (CG == 1) {
+#pragma unroll
+          for (int g = 0; g < GB; ++g) {
+            if (j * GB + g >= nk) break;
+            const uint32_t b = ci % NB;
+            if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
+              ok = false;
+              break;
+            }
+            phases ^= 1u << b;
+            tc_fence_after();
+            if (mine > 0) {
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                uint32_t r[16];
+                tmem_ld16(lane_addr + b * NT + 16 * c, r);
+                tmem_ld_wait(r);
+                if (c + 1 == kChunks) release_acc(&afree[b], lane);
+                fold(s[g], r, sum + 16 * c);
+              }
+            } else {
+              release_acc(&afree[b], lane);
+            }
+            ++ci;
           }
-        };
-        // Two 16-column loads in flight: chunk c is folded while c + 1 loads.
-        uint32_t r[kBuf][16];
-        tmem_ld16(acc, r[0]);
-        tmem_ld_wait(r[0]);
+        } else {
+          const uint32_t b = ci % NB;
+          if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          phases ^= 1u << b;
+          tc_fence_after();
+          // Two groups' loads are in flight together (one at a time, the
+          // round trips made the fold the slowest role); of a tile with up to
+          // 16 rows, half the columns.
+          const uint32_t acc = lane_addr + b * L::kAccCols;
+          const int left = nk - j * GB;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c + 1 < kChunks) tmem_ld16(acc + 16 * (c + 1), r[(c + 1) % kBuf]);
-          fold16(c, r[c % kBuf]);
-          if (c + 1 < kChunks) tmem_ld_wait(r[(c + 1) % kBuf]);
-          if (c + 2 == kChunks) release_acc(&afree[b], lane);
+          for (int g = 0; g < GB; g += 2) {
+            if (mine > 16) {
+              uint32_t r0[32], r1[32];
+              tmem_ld32(acc + g * NT, r0);
+              tmem_ld32(acc + (g + 1) * NT, r1);
+              tmem_ld_wait(r0);
+              tmem_ld_wait(r1);
+              if (g + 2 >= GB) release_acc(&afree[b], lane);
+              if (g < left) fold(s[g], r0, sum);
+              if (g + 1 < left) fold(s[g + 1], r1, sum);
+            } else {
+              uint32_t r0[16], r1[16];
+              tmem_ld16(acc + g * NT, r0);
+              tmem_ld16(acc + (g + 1) * NT, r1);
+              tmem_ld_wait(r0);
+              tmem_ld_wait(r1);
+              if (g + 2 >= GB) release_acc(&afree[b], lane);
+              if (g < left) fold(s[g], r0, sum);
+              if (g + 1 < left) fold(s[g + 1], r1, sum);
+            }
+          }
+          ++ci;
         }
       }
       __syncwarp();
@@ -564,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // One copy of the epilogue's code, 32 tokens a turn, the sums moved down
       // in between.
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 32) {
-        if (c >= t.rows) break;
+      for (int c = 0; c < kCols; c += 32) {
+        if (c >= mine) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[16];
@@ -577,11 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[j + 2] = __fmul_rn(sum[16 * h + j + 2], rv.z);
             v[j + 3] = __fmul_rn(sum[16 * h + j + 3], rv.w);
           }
-          if (t.rows > c + 16 * h)
-            store16<OUT>(p, static_cast<size_t>(t.row + c + 16 * h), n, t.rows - c - 16 * h, lane, v);
+          if (mine > c + 16 * h)
+            store16<OUT>(p, static_cast<size_t>(t.row + cs + c + 16 * h), n, mine - c - 16 * h, lane, v);
         }
 #pragma unroll
-        for (int j = 0; j + 32 < NT; ++j) sum[j] = sum[j + 32];
+        for (int j = 0; j + 32 < kCols; ++j) sum[j] = sum[j + 32];
       }
     }
     cp_async_wait_all();  // no scale copy outlives the CTA
@@ -639,14 +763,16 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap
     if (e != cudaSuccess) return e;
     // setmaxnreg.inc waits until the block's own registers cover the increase:
     // launch only with the register count the split was sized for.
-    if (regs < kRegsLaunch || 4 * (kRegsLow + kRegsConv) + 8 * kRegsHigh > 16 * regs) return cudaErrorInvalidConfiguration;
+    using L = Smem<NARROW>;
+    if (regs < kRegsLaunch || 4 * kRegsLow + L::kConv * kRegsConv + L::kFold * kRegsHigh > L::kWarps * regs)
+      return cudaErrorInvalidConfiguration;
   }
   // at most one token tile per row, and one more per expert than rows / NT
   const int64_t tiles_n = (p.N + kBM - 1) / kBM;
   const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
   if (tiles_t * tiles_n > INT32_MAX) return cudaErrorInvalidValue;  // tile numbers are 32 bits
   const int grid = static_cast<int>(std::min<int64_t>(tiles_t * tiles_n, sm_count()));
-  grouped_kernel<NARROW, OUT><<<grid, kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, xfull, p);
+  grouped_kernel<NARROW, OUT><<<grid, Smem<NARROW>::kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, xfull, p);
   note_launch();
   return cudaGetLastError();
 }
