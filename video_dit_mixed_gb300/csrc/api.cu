@@ -597,6 +597,10 @@ static sixbit_status rows_params(const sixbit_qact* A, const sixbit_weights* W, 
   p->Y = Y_f32 != nullptr ? nullptr : Y;
   p->Yf = Y_f32;
   p->err = err_dev;
+  GemmParams dbg;
+  gemm_debug_params(dbg);
+  p->wait_ns = dbg.wait_ns;
+  p->withhold_first = dbg.withhold_first;
   return check_device();
 }
 
@@ -609,7 +613,7 @@ sixbit_status sixbit_qgemv(const sixbit_qact* A, const sixbit_weights* W, int M,
   const sixbit_status s = rows_params(A, W, nullptr, 1, M, N, K, mode_dev, epilogue, residual, Y, Y_f32, err_dev, &p,
                                       &empty);
   if (s != SIXBIT_OK || empty) return s;
-  return cuda_status(launch_w4a8_rows(p, M, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_w4a8_rows(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K) {
@@ -630,13 +634,15 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   if (offsets == nullptr || workspace == nullptr) return SIXBIT_EINVAL;
   if (!aligned16(workspace)) return SIXBIT_EALIGN;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (M <= 32) return cuda_status(launch_w4a8_rows(p, M, st));
-  GemmParams dbg;
-  gemm_debug_params(dbg);
-  p.wait_ns = dbg.wait_ns;
-  p.withhold_first = dbg.withhold_first;
+  // Up to 16 rows: dot products, an expert's rows one or two at a time (16 rows
+  // over 8 experts of 7680 x 1920 20.4 us against 22.2 on the tensor cores, 2
+  // rows 6.0 against 10.7, but 32 rows 36.1 against 23.7).  Above: token tiles
+  // of 32 up to 48 rows an expert on average, else of 128 (7680 x 1920, 8
+  // experts: 256 rows 29.7 against 37.9 us, 512 rows 43.3 against 42.0, 1024
+  // rows 68.2 against 52.3).
+  if (M <= 16) return cuda_status(launch_w4a8_rows(p, st));
   uint8_t* xd = static_cast<uint8_t*>(workspace);
-  const bool narrow = M < 64 * static_cast<int64_t>(E);
+  const bool narrow = M < 48 * static_cast<int64_t>(E);
   CUtensorMap mw, mx, mxf;
   if (!make_map(&mw, W->i4_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, E * N, K / 2, 128) ||
       !make_map(&mx, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, 32) ||

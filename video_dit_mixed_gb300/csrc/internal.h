@@ -129,7 +129,7 @@ struct RowsParams {
   uint64_t wait_ns;        // as in GemmParams (grouped kernel)
   int withhold_first;
 };
-cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st);
+cudaError_t launch_w4a8_rows(const RowsParams& p, cudaStream_t st);
 // Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row.
 cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st);
 // w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows,

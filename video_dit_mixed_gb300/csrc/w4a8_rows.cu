@@ -5,22 +5,9 @@
 //   Y[m, n] = s_m[m] * sum_g s_w[g][n] * acc_g[m, n]
 //   acc_g[m, n] = sum_{k in group g} qa[m, k] * qw[n, k]    (exact integers)
 //
-// With 1..32 rows the call reads each weight byte once and multiplies it a few
+// With so few rows the call reads each weight byte once and multiplies it a few
 // times: the weights' bytes bound it, so they go straight from global memory
 // to registers as INT4 and are never expanded in memory.
-//
-// The products run on mma.m16n8k16 with fp16 operands and FP32 accumulation:
-// weight rows are the 16-row operand, tokens the 8-column one.  Codes and
-// nibbles are exact in fp16 and a group's sum stays below 2^17, so the
-// accumulator holds the exact integer; the scale is applied after each group.
-// The sum over k may be taken in any order as long as both operands agree, so
-// a lane keeps 32 consecutive k of a group (16 bytes of nibbles, 32 code
-// bytes: whole 16-byte loads) and hands four of them to each MMA.  Within a
-// word of eight nibbles the pairs are (k, k + 4): the two halves of one
-// masked word.
-//
-// A CTA owns 16 MT weight rows and its eight warps split the groups of K; their
-// FP32 sums meet in shared memory in a fixed order, where the epilogue runs.
 #include <cstdint>
 
 #include "common.cuh"
@@ -32,7 +19,7 @@
 namespace sixbit {
 namespace rows {
 
-constexpr int kWarps = 8;
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -55,19 +42,18 @@ __device__ __forceinline__ void finish(const RowsParams& p, int row, int col, fl
     p.Y[at] = static_cast<uint16_t>(f2_to_bf16x2(f2_pack(y, 0.f)) & 0xFFFFu);
 }
 
-// ------------------------------------------------------- one to four tokens --
+// -------------------------------------------------------- one or two tokens --
+// Four-byte dot products: a warp takes four weight rows by 1024 k, 16 bytes of
+// nibbles a lane and row in one load each (a nibble stands in the upper half
+// of its byte: 16 v).  A group's sum is joined over its four lanes as
+// integers, exact, before the scale.  `split` warps share a row's chunks.
 constexpr int kR = 4;         // weight rows of a warp
-constexpr int kChunk = 1024;  // k of a warp's load: 16 bytes of nibbles a lane
+constexpr int kChunk = 1024;  // k of a warp's load
 
-// T tokens at a time; p.split warps share a row's chunks.
+// Rows [first, first + count) of the expert blockIdx.y, T tokens at a time.
 template <int T>
-__global__ void __launch_bounds__(256) dot_kernel(const RowsParams p, int split) {
-  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+__device__ __forceinline__ void dot_rows(const RowsParams& p, int split, int first, int count, float* part) {
   constexpr int kV = kR * T;
-  __shared__ float part[8 * kV];
-  int first, count;
-  expert_rows(p, blockIdx.y, threadIdx.x == 0, &first, &count);
-  if (count == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = (blockDim.x >> 5) / split;  // row blocks of the CTA
   const int kw = warp % split, rw = warp / split;
@@ -175,164 +161,162 @@ __global__ void __launch_bounds__(256) dot_kernel(const RowsParams p, int split)
   }
 }
 
-cudaError_t launch_dot(const RowsParams& p, int tokens, cudaStream_t st) {
+// T tokens at a time; T = 0: one or two, by the expert's own count.
+template <int T>
+__global__ void __launch_bounds__(256) dot_kernel(const RowsParams p, int split) {
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  __shared__ float part[8 * kR * (T > 0 ? T : 2)];
+  int first, count;
+  expert_rows(p, blockIdx.y, threadIdx.x == 0, &first, &count);
+  if (count == 0) return;
+  if constexpr (T > 0)
+    dot_rows<T>(p, split, first, count, part);
+  else if (count == 1)
+    dot_rows<1>(p, split, first, count, part);
+  else
+    dot_rows<2>(p, split, first, count, part);
+}
+
+cudaError_t launch_dot(const RowsParams& p, cudaStream_t st) {
   const int chunks = (p.K + kChunk - 1) / kChunk;
   const int turns = (chunks + 7) / 8, split = (chunks + turns - 1) / turns, wr = 8 / split;
   const dim3 grid((p.N + wr * kR - 1) / (wr * kR), p.E);
   const int threads = split * wr * 32;
-  if (tokens == 1)
+  if (p.offsets != nullptr)
+    dot_kernel<0><<<grid, threads, 0, st>>>(p, split);
+  else if (p.M == 1)
     dot_kernel<1><<<grid, threads, 0, st>>>(p, split);
-  else if (tokens == 2)
-    dot_kernel<2><<<grid, threads, 0, st>>>(p, split);
   else
-    dot_kernel<4><<<grid, threads, 0, st>>>(p, split);
+    dot_kernel<2><<<grid, threads, 0, st>>>(p, split);
   note_launch();
   return cudaGetLastError();
 }
 
-// ------------------------------------------------------- up to eight a tile --
+// ------------------------------------------------------ three to 32 tokens --
+// The products run on mma.m16n8k16 with fp16 operands and FP32 accumulation:
+// weight rows are the 16-row operand, tokens the 8-column one (NT tiles).  Codes and nibbles are exact in fp16 and a group's sum stays below
+// 2^17, so the accumulator holds the exact integer; the scale is applied after
+// each group.  The sum over k may be taken in any order as long as both
+// operands agree, so a lane keeps 32 consecutive k of a group (16 bytes of
+// nibbles, 32 code bytes) and hands four of them to each MMA; within a word of
+// eight nibbles the pairs are (k, k + 4), the two halves of one masked word.
+//
+// A CTA owns 16 weight rows and its W warps split the groups of K (the next
+// group's nibbles are loaded while this one's are multiplied); their FP32 sums
+// meet in shared memory in a fixed order, where the epilogue runs.
+constexpr int kN = 16;
 
-template <int MT, int NT>
-__global__ void __launch_bounds__(kWarps * 32) rows_kernel(const RowsParams p) {
+template <int NT, int W>
+__global__ void __launch_bounds__(W * 32) tile_kernel(const RowsParams p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
-  constexpr int kN = 16 * MT, kT = 8 * NT;
-  __shared__ float part[kWarps][kT][kN + 1];
-  int first, count;
-  expert_rows(p, blockIdx.y, threadIdx.x == 0, &first, &count);
-  if (count == 0) return;
+  constexpr int kT = 8 * NT;
+  __shared__ float part[W][kT][kN + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int groups = p.K / 128, n0 = blockIdx.x * kN;
   const size_t kb = static_cast<size_t>(p.K) / 2;
-  const uint8_t* w4 = p.w4 + static_cast<size_t>(blockIdx.y) * p.N * kb;
-  const float* w4s = p.w4_scale + static_cast<size_t>(blockIdx.y) * groups * p.N;
-
-  int n[MT][2];
-  const uint8_t* wrow[MT][2];
+  int n[2];
+  const uint8_t* wrow[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int h = 0; h < 2; ++h) {
+    n[h] = min(n0 + 8 * h + g, p.N - 1);  // (the surplus rows are not stored)
+    wrow[h] = p.w4 + n[h] * kb + t * 16;
+  }
+  const int8_t* xrow = p.codes + static_cast<size_t>(g) * p.K + t * 32;
+  float sum[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[j][i] = 0.f;
+
+  uint4 w[2];
+  float sc[2];
+  auto fetch = [&](int gr) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      n[m][h] = min(n0 + 16 * m + 8 * h + g, p.N - 1);  // (the surplus rows are not stored)
-      wrow[m][h] = w4 + n[m][h] * kb + t * 16;
+      w[h] = __ldg(reinterpret_cast<const uint4*>(wrow[h] + static_cast<size_t>(gr) * 64));
+      sc[h] = __ldg(p.w4_scale + static_cast<size_t>(gr) * p.N + n[h]);
     }
-  }
-
-  for (int t0 = 0; t0 < count; t0 += kT) {
-    const int8_t* xrow[NT];
+  };
+  if (warp < groups) fetch(warp);
+  for (int gr = warp; gr < groups; gr += W) {
+    const uint4 wc[2] = {w[0], w[1]};
+    const float s[2] = {sc[0], sc[1]};
+    uint4 x[NT][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      xrow[j] = p.codes + static_cast<size_t>(first + min(t0 + 8 * j + g, count - 1)) * p.K + t * 32;
-    float sum[MT][NT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[m][j][i] = 0.f;
-
-    uint4 w[MT][2];
-    float sc[MT][2];
-    auto fetch = [&](int gr) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[m][h] = __ldg(reinterpret_cast<const uint4*>(wrow[m][h] + static_cast<size_t>(gr) * 64));
-          sc[m][h] = __ldg(w4s + static_cast<size_t>(gr) * p.N + n[m][h]);
-        }
-    };
-    if (warp < groups) fetch(warp);
-    for (int gr = warp; gr < groups; gr += kWarps) {
-      uint4 wc[MT][2];
-      float s[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          wc[m][h] = w[m][h];
-          s[m][h] = sc[m][h];
-        }
-      uint4 x[NT][2];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const uint4* xp = reinterpret_cast<const uint4*>(xrow[j] + gr * 128);
+    for (int j = 0; j < NT; ++j) {
+      x[j][0] = x[j][1] = make_uint4(0, 0, 0, 0);
+      if (8 * j + g < p.M) {  // (a surplus token's column is not stored)
+        const uint4* xp = reinterpret_cast<const uint4*>(xrow + static_cast<size_t>(8 * j) * p.K + gr * 128);
         x[j][0] = __ldg(xp);
         x[j][1] = __ldg(xp + 1);
       }
-      if (gr + kWarps < groups) fetch(gr + kWarps);
-      float acc[MT][NT][4];
+    }
+    if (gr + W < groups) fetch(gr + W);
+    float acc[NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.f;
+    for (int q = 0; q < 4; ++q) {  // eight k of the lane
+      uint32_t lo[4], hi[4];
+      nibbles_f16(word(wc[0], q), lo);
+      nibbles_f16(word(wc[1], q), hi);
+      const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // eight k of the lane
-        uint32_t b[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint4& v = x[j][q >> 1];
-          codes_f16((q & 1) ? v.z : v.x, (q & 1) ? v.w : v.y, b[j]);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t lo[4], hi[4];
-          nibbles_f16(q == 0 ? wc[m][0].x : q == 1 ? wc[m][0].y : q == 2 ? wc[m][0].z : wc[m][0].w, lo);
-          nibbles_f16(q == 0 ? wc[m][1].x : q == 1 ? wc[m][1].y : q == 2 ? wc[m][1].z : wc[m][1].w, hi);
-          const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            mma16816(acc[m][j], a0, b[j][0], b[j][1]);
-            mma16816(acc[m][j], a1, b[j][2], b[j][3]);
-          }
-        }
+      for (int j = 0; j < NT; ++j) {
+        uint32_t b[4];
+        codes_f16(word(x[j][q >> 1], 2 * (q & 1)), word(x[j][q >> 1], 2 * (q & 1) + 1), b);
+        mma16816(acc[j], a0, b[0], b[1]);
+        mma16816(acc[j], a1, b[2], b[3]);
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[m][j][i] = fmaf(s[m][i >> 1], acc[m][j][i], sum[m][j][i]);
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int i = 0; i < 4; ++i) sum[j][i] = fmaf(s[i >> 1], acc[j][i], sum[j][i]);
+  }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] = sum[m][j][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < kT * kN; i += kWarps * 32) {
-      const int tok = i / kN, c = i % kN, col = n0 + c, row = first + t0 + tok;
-      if (t0 + tok >= count || col >= p.N) continue;
-      float y = 0.f;
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) y += part[k][tok][c];
-      finish(p, row, col, y);
-    }
-    if (t0 + kT < count) __syncthreads();
+    for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * t + (i & 1)][8 * (i >> 1) + g] = sum[j][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kT * kN; i += W * 32) {
+    const int tok = i / kN, c = i % kN;
+    if (tok >= p.M || n0 + c >= p.N) continue;
+    float y = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) y += part[k][tok][c];
+    finish(p, tok, n0 + c, y);
   }
 }
 
-template <int MT>
-cudaError_t launch(const RowsParams& p, int most, cudaStream_t st) {
-  const dim3 grid((p.N + 16 * MT - 1) / (16 * MT), p.E);
-  if (most <= 8)
-    rows_kernel<MT, 1><<<grid, kWarps * 32, 0, st>>>(p);
-  else if (most <= 16)
-    rows_kernel<MT, 2><<<grid, kWarps * 32, 0, st>>>(p);
-  else
-    rows_kernel<MT, 4><<<grid, kWarps * 32, 0, st>>>(p);
+template <int NT, int W>
+cudaError_t launch_tile(const RowsParams& p, cudaStream_t st) {
+  tile_kernel<NT, W><<<(p.N + kN - 1) / kN, W * 32, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
+}
+
+// Sixteen warps a CTA where K has groups for them and every CTA is resident
+// at once (two of them an SM with one token tile, one with two), else eight:
+// 8 tokens, 1920 x 7680 weights 10.7 -> 6.9 us, 3072 x 12288 15.0 -> 10.9, but
+// 5760 x 1920 4.7 -> 5.6 and 16 tokens, 3072 x 12288 17.1 -> 18.8.
+cudaError_t launch_tiles(const RowsParams& p, cudaStream_t st) {
+  const int tiles = (p.N + 15) / 16;
+  const bool deep = p.K > 16 * 128;
+  if (p.M <= 8) return deep && tiles <= 2 * sm_count() ? launch_tile<1, 16>(p, st) : launch_tile<1, 8>(p, st);
+  if (p.M <= 16) return deep && tiles <= sm_count() ? launch_tile<2, 16>(p, st) : launch_tile<2, 8>(p, st);
+  return p.M <= 24 ? launch_tile<3, 8>(p, st) : launch_tile<4, 8>(p, st);
 }
 
 }  // namespace rows
 
-// most: rows of one expert at most (they may be fewer; more are walked in turn).
-cudaError_t launch_w4a8_rows(const RowsParams& p, int most, cudaStream_t st) {
-  if (most <= 4 || (p.E > 1 && most <= 32)) return rows::launch_dot(p, most, st);
-  return rows::launch<1>(p, most, st);
+// One weight (up to 32 rows): dot products up to two rows, MMAs above (two
+// tokens, 7680 x 1920: 4.7 us against 4.8 for any three to eight; 3072 x 12288
+// 6.9 against 10.8).  Experts: any rows, one or two at a time.
+cudaError_t launch_w4a8_rows(const RowsParams& p, cudaStream_t st) {
+  return p.offsets != nullptr || p.M <= 2 ? rows::launch_dot(p, st) : rows::launch_tiles(p, st);
 }
 
 }  // namespace sixbit

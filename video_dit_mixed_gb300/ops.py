@@ -61,6 +61,8 @@ def workspace(n: int, k: int, device) -> torch.Tensor:
 class QActTensors:
     """Device buffers of one quantized activation tensor [M, K]."""
 
+    fp4_codes = fp4_scales = tensor_amax = tensor_scale = i8_codes = row_scale = rotated = None
+
     def __init__(self, m: int, k: int, device="cuda", nvfp4=True, int8=True, rotated=False):
         self.m, self.k = m, k
         dev = torch.device(device)
@@ -255,13 +257,6 @@ def _ptr(t, name: str, dtype, shape, dev: int) -> int:
                      f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
-def _gpu(t, name: str) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be on the GPU, not on {t.device}")
-    return dev
-
-
 def _word(t, name: str, dev: int):
     if t is None:
         return None
@@ -282,7 +277,6 @@ def int8_act(codes: torch.Tensor, row_scale: torch.Tensor) -> QActTensors:
     """INT8 activations that already exist: codes int8 [M, K], row_scale float32 [M]."""
     a = QActTensors.__new__(QActTensors)
     a.m, a.k = codes.shape
-    a.fp4_codes = a.fp4_scales = a.tensor_amax = a.tensor_scale = a.rotated = None
     a.i8_codes, a.row_scale = codes, row_scale
     return a
 
@@ -326,7 +320,9 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, wei
     if len(shape) != 2:
         raise ValueError(f"x: [M, K] expected, got {tuple(shape)}")
     m, k = shape
-    dev = _gpu(x, "x")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError(f"x must be on the GPU, not on {x.device}")
     px = _ptr(x, "x", _BF16, shape, dev)
     pw = None if weight is None else _ptr(weight, "weight", _F32, (k,), dev)
     pr = ps = None
@@ -334,25 +330,30 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, wei
         pr = _ptr(residual, "residual", _BF16, shape, dev)
         if sum_out is None:
             sum_out = _empty(shape, _BF16, x.device, stream)
-        ps = _ptr(sum_out, "sum_out", _BF16, shape, dev)
+            ps = sum_out.data_ptr()
+        else:
+            ps = _ptr(sum_out, "sum_out", _BF16, shape, dev)
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     if out is None:
         device = x.device
-        out = int8_act(_empty(shape, _I8, device, stream), _empty((m,), _F32, device, stream))
-    a = QAct(None, None, None, None, _ptr(out.i8_codes, "out.i8_codes", _I8, shape, dev),
-             _ptr(out.row_scale, "out.row_scale", _F32, (m,), dev), None)
+        codes, scale = _empty(shape, _I8, device, stream), _empty((m,), _F32, device, stream)
+        out = int8_act(codes, scale)
+        pc, pscale = codes.data_ptr(), scale.data_ptr()
+    else:
+        pc, pscale = (_ptr(out.i8_codes, "out.i8_codes", _I8, shape, dev),
+                      _ptr(out.row_scale, "out.row_scale", _F32, (m,), dev))
     status = _lib.sixbit_add_rmsnorm_quant(px, pr, pw, m, k, eps, had_block,
                                            None if mode_dev is None else _word(mode_dev, "mode_dev", dev), ps,
-                                           C.byref(a), None,
+                                           C.byref(QAct(None, None, None, None, pc, pscale, None)), None,
                                            _current_raw_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         check(status, "add_rmsnorm_quant")
     return out, (x if residual is None else sum_out)
 
 
-def _w4a8(a, w, lead, epilogue, residual, out, out_f32, mode_dev, err, stream):
-    """Checked operands of qgemv and qgemm_grouped, up to `err` in the C calls' order."""
+def _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, err, stream, ws):
+    """qgemv (experts None) and qgemm_grouped: checks, the output, the call."""
     codes = a.i8_codes
     if codes is None or codes.dim() != 2:
         raise ValueError("INT8 activations [M, K] expected")
@@ -361,35 +362,58 @@ def _w4a8(a, w, lead, epilogue, residual, out, out_f32, mode_dev, err, stream):
     n = w.n
     if w.k != k:
         raise ValueError(f"activations have {k} inputs, the weights {w.k}")
-    dev = _gpu(codes, "i8_codes")
+    dev = codes.get_device()
+    if dev < 0:
+        raise ValueError(f"i8_codes must be on the GPU, not on {codes.device}")
+    if experts is None:
+        shape4, shapes = (n, k // 2), (k // 128, n)
+    else:
+        shape4, shapes = (experts, n, k // 2), (experts, k // 128, n)
     ca = QAct(None, None, None, None, _ptr(codes, "i8_codes", _I8, shape, dev),
               _ptr(a.row_scale, "row_scale", _F32, (m,), dev), None)
-    cw = Weights(None, None, None, None, _ptr(w.i4_codes, "i4_codes", _U8, lead + (n, k // 2), dev),
-                 _ptr(w.i4_scales, "i4_scales", _F32, lead + (k // 128, n), dev), None)
+    cw = Weights(None, None, None, None, _ptr(w.i4_codes, "i4_codes", _U8, shape4, dev),
+                 _ptr(w.i4_scales, "i4_scales", _F32, shapes, dev), None)
+    py = pf = pr = None
     if out is None:
         out = _empty((m, n), _F32 if out_f32 else _BF16, codes.device, stream)
-    f32 = out.dtype is _F32
-    py = _ptr(out, "out", _F32 if f32 else _BF16, (m, n), dev)
-    pr = None
+        if out_f32:
+            pf = out.data_ptr()
+        else:
+            py = out.data_ptr()
+    elif out.dtype is _F32:
+        pf = _ptr(out, "out", _F32, (m, n), dev)
+    else:
+        py = _ptr(out, "out", _BF16, (m, n), dev)
     if residual is not None:
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    return (ca, cw, (m, n, k), None if mode_dev is None else _word(mode_dev, "mode_dev", dev), pr,
-            None if f32 else py, py if f32 else None, None if err is None else _word(err, "err", dev), dev, out)
+    pm = None if mode_dev is None else _word(mode_dev, "mode_dev", dev)
+    pe = None if err is None else _word(err, "err", dev)
+    st = _current_raw_stream(dev) if stream is None else stream.cuda_stream
+    if experts is None:
+        status = _lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, pm, epilogue, pr, py, pf, pe, st)
+        if status:
+            check(status, "qgemv")
+        return out
+    po = _ptr(offsets, "offsets", _I32, (experts + 1,), dev)
+    need = 2 * m * k  # sixbit_qgemm_grouped_workspace_bytes
+    if ws is None:
+        ws = _empty((need,), _U8, out.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
+    status = _lib.sixbit_qgemm_grouped(C.byref(ca), C.byref(cw), po, experts, m, n, k, pm, epilogue, pr, py, pf,
+                                       ws.data_ptr(), pe, st)
+    if status:
+        check(status, "qgemm_grouped")
+    return out
 
 
 def qgemv(a: QActTensors, w, epilogue: int = EPI_NONE, residual=None, out=None, out_f32: bool = False, mode_dev=None,
           err=None, stream=None):
     """The W4A8 product of 1 to QGEMV_MAX_ROWS rows (sixbit_qgemv).  w: PackedWeights or Int4Weights.  Returns
     out: bf16 [M, N], or float32 with out_f32 or a float32 `out`."""
-    ca, cw, (m, n, k), pm, pr, py, pf, pe, dev, out = _w4a8(a, w, (), epilogue, residual, out, out_f32, mode_dev, err,
-                                                           stream)
-    status = _lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, pm, epilogue, pr, py, pf, pe,
-                               _current_raw_stream(dev) if stream is None else stream.cuda_stream)
-    if status:
-        check(status, "qgemv")
-    return out
+    return _w4a8(a, w, None, None, epilogue, residual, out, out_f32, mode_dev, err, stream, None)
 
 
 def qgemm_grouped_workspace_bytes(m: int, k: int) -> int:
@@ -405,20 +429,7 @@ def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogu
     experts = getattr(w, "experts", None)
     if experts is None:
         raise ValueError("experts' weights expected (Int4Weights with [E, N, K/2] codes)")
-    ca, cw, (m, n, k), pm, pr, py, pf, pe, dev, out = _w4a8(a, w, (experts,), epilogue, residual, out, out_f32,
-                                                           mode_dev, err, stream)
-    po = _ptr(offsets, "offsets", _I32, (experts + 1,), dev)
-    need = _lib.sixbit_qgemm_grouped_workspace_bytes(m, k)
-    if ws is None:
-        ws = _empty((need,), _U8, out.device, stream)
-    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
-        raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
-    status = _lib.sixbit_qgemm_grouped(C.byref(ca), C.byref(cw), po, experts, m, n, k, pm, epilogue, pr, py, pf,
-                                       ws.data_ptr(), pe,
-                                       _current_raw_stream(dev) if stream is None else stream.cuda_stream)
-    if status:
-        check(status, "qgemm_grouped")
-    return out
+    return _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, err, stream, ws)
 
 
 def policy_cfg(gamma_thr=0.1, cos_thr=0.99, err_cap=0.05, pdr_ratio=30.0, near_rel=1e-6, refresh_bf16=False):
