@@ -107,11 +107,10 @@ __device__ __forceinline__ void fwht(uint64_t (&u)[8]) {
   }
 }
 
-// h = x + r of one chunk, its contribution to the sum of squares, the bf16 sum
-// (stored when `put`), and u = the rotated h . w.
-template <int B>
-__device__ __forceinline__ void chunk(const Params& p, size_t at, int k, bool live, bool put, const uint32_t (&xr)[8],
-                                      const uint32_t (&rr)[8], uint64_t& ss, uint64_t (&u)[8]) {
+// h = x + r of one chunk (into u) and its contribution to the sum of squares;
+// the bf16 sum is stored when `put`.
+__device__ __forceinline__ void add(const Params& p, size_t at, bool live, bool put, const uint32_t (&xr)[8],
+                                    const uint32_t (&rr)[8], uint64_t& ss, uint64_t (&u)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) u[i] = f2_from_bf16x2(xr[i]);
   if (p.res != nullptr) {
@@ -125,16 +124,21 @@ __device__ __forceinline__ void chunk(const Params& p, size_t at, int k, bool li
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss = f2_fma(u[i], u[i], ss);
+}
+
+// 16 weights from channel k on, as pairs (1 without weights, or beyond the row).
+__device__ __forceinline__ void load_weights(const Params& p, int k, bool live, uint64_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = f2_pack(1.f, 1.f);
   if (p.w != nullptr && live) {
     const float4* w4 = reinterpret_cast<const float4*>(p.w + k);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(w4 + i);
-      u[2 * i] = f2_mul(u[2 * i], f2_pack(w.x, w.y));
-      u[2 * i + 1] = f2_mul(u[2 * i + 1], f2_pack(w.z, w.w));
+      const float4 v = __ldg(w4 + i);
+      w[2 * i] = f2_pack(v.x, v.y);
+      w[2 * i + 1] = f2_pack(v.z, v.w);
     }
   }
-  fwht<B>(u);
 }
 
 // max over |u| as bit patterns: a NaN compares above infinity, so it is kept
@@ -181,74 +185,100 @@ __device__ __forceinline__ void store_codes(const Params& p, size_t at, const Ro
   *reinterpret_cast<uint4*>(p.codes + at) = make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-// One CTA per row, V chunks a thread, kept in registers.  V = 0: any K, each
-// chunk computed twice (the second time the row comes from L2).
+// A CTA takes whole rows, every gridDim-th one, V chunks a thread, kept in
+// registers; the thread's weights stay there too, and the next row's loads are
+// in flight while this one is rotated, reduced and stored.  (One CTA per row,
+// which read the weights again for each row, was bound by L1: 17776 x 1920
+// 47.2 us.)  V = 0: any K, each chunk computed twice (the second time the row
+// comes from L2).
 template <int B, int V>
 __global__ void __launch_bounds__(512) row_kernel(const Params p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
-  __shared__ float s_ss[16];
-  __shared__ uint32_t s_mx[16];
+  __shared__ float s_ss[2][16];
+  __shared__ uint32_t s_mx[2][16];
   constexpr int R = V > 0 ? V : 1;
-  const int row = blockIdx.x, chunks = p.K / kE;
+  constexpr bool kKeep = V > 0;  // weights in registers
+  const int chunks = p.K / kE;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
-  const size_t base = static_cast<size_t>(row) * p.K;
-  uint64_t u[R][8], ss2 = 0;
-  uint32_t mb = 0;
-  uint32_t xr[R][8], rr[R][8];
   const int loops = V > 0 ? 1 : (chunks + blockDim.x - 1) / blockDim.x;
-  for (int it = 0; it < loops; ++it) {
+  uint64_t w[kKeep ? R : 1][8];
+  uint32_t xr[R][8], rr[R][8];
+  auto at_of = [&](int row, int c) { return static_cast<size_t>(row) * p.K + static_cast<size_t>(c) * kE; };
+  auto load = [&](int row, int it) {
 #pragma unroll
     for (int v = 0; v < R; ++v) {
       const int c = threadIdx.x + (it + v) * blockDim.x;
 #pragma unroll
       for (int i = 0; i < 8; ++i) xr[v][i] = rr[v][i] = 0;
       if (c < chunks) {
-        load32(p.x + base + static_cast<size_t>(c) * kE, p.wide, xr[v]);
-        if (p.res != nullptr) load32(p.res + base + static_cast<size_t>(c) * kE, p.wide, rr[v]);
+        load32(p.x + at_of(row, c), p.wide, xr[v]);
+        if (p.res != nullptr) load32(p.res + at_of(row, c), p.wide, rr[v]);
       }
     }
+  };
+  if constexpr (kKeep) {
 #pragma unroll
     for (int v = 0; v < R; ++v) {
-      const int c = threadIdx.x + (it + v) * blockDim.x;
-      chunk<B>(p, base + static_cast<size_t>(c) * kE, c * kE, c < chunks, V > 0, xr[v], rr[v], ss2, u[v]);
-      mb = max_bits(u[v], mb);
+      const int c = threadIdx.x + v * blockDim.x;
+      load_weights(p, c * kE, c < chunks, w[v]);
     }
   }
-  float ss = f2_lo(ss2) + f2_hi(ss2);
+  auto rotate = [&](int v, int c, uint64_t (&u)[8]) {
+    if constexpr (!kKeep) load_weights(p, c * kE, c < chunks, w[0]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-  mb = __reduce_max_sync(0xFFFFFFFFu, mb);
-  if (nwarps > 1) {
-    if (lane == 0) {
-      s_ss[warp] = ss;
-      s_mx[warp] = mb;
+    for (int i = 0; i < 8; ++i) u[i] = f2_mul(u[i], w[kKeep ? v : 0][i]);
+    fwht<B>(u);
+  };
+  if (V > 0) load(blockIdx.x, 0);
+  int buf = 0;
+  for (int row = blockIdx.x; row < p.M; row += gridDim.x, buf ^= 1) {
+    uint64_t u[R][8], ss2 = 0;
+    uint32_t mb = 0;
+    for (int it = 0; it < loops; ++it) {
+      if (V == 0) load(row, it);
+#pragma unroll
+      for (int v = 0; v < R; ++v) {
+        const int c = threadIdx.x + (it + v) * blockDim.x;
+        add(p, at_of(row, c), c < chunks, V > 0, xr[v], rr[v], ss2, u[v]);
+      }
+      if (V > 0 && row + gridDim.x < p.M) load(row + gridDim.x, 0);
+#pragma unroll
+      for (int v = 0; v < R; ++v) {
+        rotate(v, threadIdx.x + (it + v) * blockDim.x, u[v]);
+        mb = max_bits(u[v], mb);
+      }
     }
-    __syncthreads();
-    ss = 0.f;
-    mb = 0;
-    for (int i = 0; i < nwarps; ++i) {
-      ss += s_ss[i];
-      mb = max(mb, s_mx[i]);
+    float ss = f2_lo(ss2) + f2_hi(ss2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    mb = __reduce_max_sync(0xFFFFFFFFu, mb);
+    if (nwarps > 1) {
+      if (lane == 0) {
+        s_ss[buf][warp] = ss;
+        s_mx[buf][warp] = mb;
+      }
+      __syncthreads();  // (two buffers: the next row's writes need no barrier of their own)
+      ss = 0.f;
+      mb = 0;
+      for (int i = 0; i < nwarps; ++i) {
+        ss += s_ss[buf][i];
+        mb = max(mb, s_mx[buf][i]);
+      }
     }
-  }
-  const RowOut o = row_out(p, ss, mb);
-  if (threadIdx.x == 0) p.row_scale[row] = o.scale;
-  for (int it = 0; it < loops; ++it) {
+    const RowOut o = row_out(p, ss, mb);
+    if (threadIdx.x == 0) p.row_scale[row] = o.scale;
+    for (int it = 0; it < loops; ++it) {
 #pragma unroll
-    for (int v = 0; v < R; ++v) {
-      const int c = threadIdx.x + (it + v) * blockDim.x;
-      const size_t at = base + static_cast<size_t>(c) * kE;
-      if constexpr (V == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) xr[v][i] = rr[v][i] = 0;
-        if (c < chunks) {
-          load32(p.x + at, p.wide, xr[v]);
-          if (p.res != nullptr) load32(p.res + at, p.wide, rr[v]);
+      for (int v = 0; v < R; ++v) {
+        const int c = threadIdx.x + (it + v) * blockDim.x;
+        if constexpr (V == 0) {
+          load(row, it);
+          uint64_t unused = 0;
+          add(p, at_of(row, c), c < chunks, true, xr[v], rr[v], unused, u[v]);
+          rotate(v, c, u[v]);
         }
-        uint64_t unused = 0;
-        chunk<B>(p, at, c * kE, c < chunks, true, xr[v], rr[v], unused, u[v]);
+        if (c < chunks) store_codes(p, at_of(row, c), o, u[v]);
       }
-      if (c < chunks) store_codes(p, at, o, u[v]);
     }
   }
 }
@@ -269,8 +299,12 @@ __global__ void __launch_bounds__(kWarpThreads) team_kernel(const Params p) {
     load32(p.x + at, p.wide, xr);
     if (p.res != nullptr) load32(p.res + at, p.wide, rr);
   }
-  uint64_t u[8], ss2 = 0;
-  chunk<B>(p, at, t * kE, live, true, xr, rr, ss2, u);
+  uint64_t u[8], w[8], ss2 = 0;
+  add(p, at, live, true, xr, rr, ss2, u);
+  load_weights(p, t * kE, live, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = f2_mul(u[i], w[i]);
+  fwht<B>(u);
   uint32_t mb = max_bits(u, 0);
   float ss = f2_lo(ss2) + f2_hi(ss2);
   for (int o = team >> 1; o > 0; o >>= 1) {
@@ -282,28 +316,35 @@ __global__ void __launch_bounds__(kWarpThreads) team_kernel(const Params p) {
   if (live) store_codes(p, at, o, u);
 }
 
+template <int B, int V>
+cudaError_t launch_rows(const Params& p, int threads, cudaStream_t st) {
+  static ContextCache<int> cache[17];  // resident CTAs an SM, by warps
+  int per_sm = 0;
+  const cudaError_t e = cache[threads / 32].get(&per_sm, [&](int* o) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(o, row_kernel<B, V>, threads, 0);
+  });
+  if (e != cudaSuccess) return e;
+  const int most = sm_count() * (per_sm > 0 ? per_sm : 1);
+  row_kernel<B, V><<<p.M < most ? p.M : most, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int B>
 cudaError_t launch(Params& p, cudaStream_t st) {
   const int chunks = p.K / kE;
+  note_launch();
   if (chunks <= 32) {
     p.team_log = chunks <= 8 ? 3 : chunks <= 16 ? 4 : 5;
     const int rows = kWarpThreads >> p.team_log;
     team_kernel<B><<<(p.M + rows - 1) / rows, kWarpThreads, 0, st>>>(p);
-  } else {
-    const int v = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
-    int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
-    if (threads > 512) {
-      row_kernel<B, 0><<<p.M, 512, 0, st>>>(p);
-    } else if (v == 1) {
-      row_kernel<B, 1><<<p.M, threads, 0, st>>>(p);
-    } else if (v == 2) {
-      row_kernel<B, 2><<<p.M, threads, 0, st>>>(p);
-    } else {
-      row_kernel<B, 4><<<p.M, threads, 0, st>>>(p);
-    }
+    return cudaGetLastError();
   }
-  note_launch();
-  return cudaGetLastError();
+  // one chunk a thread up to K = 4096, two up to 16384 (four spill: 4444 x
+  // 12288 119.7 us)
+  const int v = chunks <= 256 ? 1 : 2;
+  const int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
+  if (threads > 512) return launch_rows<B, 0>(p, 512, st);
+  return v == 1 ? launch_rows<B, 1>(p, threads, st) : launch_rows<B, 2>(p, threads, st);
 }
 
 }  // namespace arq
