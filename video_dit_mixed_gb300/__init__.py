@@ -5,4 +5,4 @@ C ABI, see ``include/sixbit.h``); this package is a thin ctypes binding that
 marshals torch tensors (device memory) and streams into those calls.  There is
 no CPU fallback: if the library is missing, importing ``ops`` raises.
 """
-__all__ = ["ops", "abi"]
+__all__ = ["ops", "abi", "dit", "ffn"]
