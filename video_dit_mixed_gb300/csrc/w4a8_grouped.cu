@@ -67,23 +67,24 @@ namespace grouped {
 constexpr int kBM = 128;           // weight rows of a tile
 constexpr int kConvWarp0 = 4;
 constexpr int kPairBytes = kBM * 128;  // nibbles of two groups: 128 rows of 128 bytes, 128-byte swizzle
-constexpr int kSwRing = 3;             // batches of scales in flight per fold thread
 
-// GB: groups of a batch.  XG, CG: groups of a token slot and of an accumulator.
-// SW, SX, NA, NB: slots of the nibble, token, A and accumulator rings.
+// NT: tokens of a tile.  GB: groups of a batch, the unit of every ring.  SW, SX,
+// NA, NB: slots of the nibble, token, A and accumulator rings.
 template <bool NARROW>
 struct Cfg;
 template <>
 struct Cfg<false> {
-  static constexpr int NT = 128, GB = 2, XG = 1, CG = 1, SW = 2, SX = 5, NA = 2, NB = 3, kTeams = 2, kTeamWarps = 8;
+  static constexpr int NT = 96, GB = 2, SW = 2, SX = 3, NA = 2, NB = 2, kTeams = 2, kTeamWarps = 8;
 };
 template <>
 struct Cfg<true> {
-  static constexpr int NT = 32, GB = 4, XG = 4, CG = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 1, kTeamWarps = 4;
+  static constexpr int NT = 32, GB = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 1, kTeamWarps = 4;
 };
 // The wide form's registers: 768 threads launch with 80 each; warps 0 - 3 keep
-// 32, the converters 64, the fold warps get 96 (24 x 80 = 4 x 32 + 4 x 64 + 16 x 96).
-constexpr int kRegsLaunch = 80, kRegsLow = 32, kRegsConv = 64, kRegsHigh = 96;
+// 48, the converters all of them, the fold warps get 88 (24 x 80 = 4 x 48 +
+// 4 x 80 + 16 x 88).  (With 64 sums a thread they need 96 and more, and the
+// spilled ones cost each batch a round trip to L2.)
+constexpr int kRegsLaunch = 80, kRegsLow = 48, kRegsConv = 80, kRegsHigh = 88;
 
 template <bool NARROW>
 struct Smem {
@@ -92,12 +93,12 @@ struct Smem {
   static constexpr int kWarps = kConvWarp0 + kConv + kFold, kThreads = 32 * kWarps;
   static constexpr int kCols = C::NT / (C::kTeamWarps / 4);  // tokens of a fold thread
   static constexpr int kXGroup = C::NT * 256;  // a group's tokens: the high digits' 128 bytes, then the low ones'
-  static constexpr int kXSlot = C::XG * kXGroup, kWSlot = (C::GB / 2) * kPairBytes;
-  static constexpr int kWarpArea = kSwRing * C::GB * 32 * 4 + kCols * 4;  // a fold warp's scale ring and row scales
+  static constexpr int kXSlot = C::GB * kXGroup, kWSlot = (C::GB / 2) * kPairBytes;
+  static constexpr int kWarpArea = kCols * 4;  // a fold warp's row scales
   static constexpr int kBars = 2 * C::SW + 2 * C::SX + 2 * C::NA + (C::kTeams + 1) * C::NB + 3;
   static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
                        kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
-  static constexpr int kAccCols = C::CG * C::NT, kACol0 = C::NB * kAccCols, kACols = C::GB * 32;
+  static constexpr int kAccCols = C::GB * C::NT, kACol0 = C::NB * kAccCols, kACols = C::GB * 32;
   static_assert(kACol0 + C::NA * kACols <= 512, "tensor memory columns");
   // tables: prefix [E + 1], first row [E], rows [E]
   static size_t bytes(int E) { return 1024 + kTables + static_cast<size_t>(3 * E + 1) * 4; }
@@ -154,11 +155,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // How a tile's outputs are written.  kPair*: bf16, N even, Y and residual
 // 4-byte aligned: neighbouring lanes exchange one value of each two tokens, so
@@ -233,6 +229,14 @@ __device__ __forceinline__ void store16(const RowsParams& p, size_t row, int n, 
   }
 }
 
+// A load that stays where it is written (moved down to its use, it cost the
+// fold an L2 latency a batch).
+__device__ __forceinline__ float load_now(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // sum += s * accumulator columns
 template <int COLS>
 __device__ __forceinline__ void fold(float s, const uint32_t (&r)[COLS], float* sum) {
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   using C = Cfg<NARROW>;
   using L = Smem<NARROW>;
-  constexpr int NT = C::NT, GB = C::GB, XG = C::XG, CG = C::CG, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
+  constexpr int NT = C::NT, GB = C::GB, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
   constexpr int kFoldWarp0 = kConvWarp0 + L::kConv;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -390,14 +394,14 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
           const Tile t = tile_at(id);
           const int boxes = t.rows > NT - 32 ? NT / 32 : (t.rows + 31) / 32;
-          for (int g0 = 0; g0 < nk; g0 += XG, ++it) {
+          for (int g0 = 0; g0 < nk; g0 += GB, ++it) {
             const int s = it % SX;
             if (it >= SX && !mbar_wait(&x_empty[s], ((it / SX) - 1) & 1, abort_flag, p.wait_ns)) {
               ok = false;
               break;
             }
             if (p.withhold_first && it == 0) continue;  // failure-path test: slot 0 never lands
-            const int groups = min(XG, nk - g0);
+            const int groups = min(GB, nk - g0);
             mbar_expect_tx(&x_full[s], groups * boxes * 8192);
             for (int g = 0; g < groups; ++g) {
               uint8_t* dst = smem + L::kX + s * L::kXSlot + g * L::kXGroup;
@@ -426,14 +430,14 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       // Warp 1 issues the even batches, warp 3 the odd ones (the whole warp
       // keeps the loop, so that the operands stay in uniform registers; one
       // elected lane issues: with the loop in one lane, an MMA took some 100
-      // cycles of issue), strictly in turn: one's waits and commits (some 120 cycles each) overlap the
-      // other's MMAs, and no MMA comes between two that share the collector
-      // buffer.  A wait that an issuer meets at every second phase only cannot
-      // mistake an older phase for its own: x and the first accumulator of a
-      // batch were last waited for by a batch that this issuer's last turn
-      // came after; the second accumulator is waited for within the turn.
+      // cycles of issue).  They take strict turns, so that no MMA comes between
+      // two that share the collector buffer, and a wait that an issuer meets
+      // at every second phase only cannot mistake an older phase for its own:
+      // the batch three before was issued before this warp's last turn.  All
+      // waits (some 130 cycles each when the phase is there) come before the
+      // turn and the commits after it, beside the other issuer's MMAs.
       const uint32_t par = warp == 1 ? 0u : 1u;
-      uint32_t bi = 0, xi = 0, ci = 0, turn = 0;  // batches, token slots, accumulators, tiles so far
+      uint32_t bi = 0, turn = 0;  // batches, tiles so far
       bool ok = true;
       for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
         const Tile t = tile_at(id);
@@ -441,60 +445,35 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         const uint32_t nt = static_cast<uint32_t>((t.rows + 15) & ~15);
         const uint32_t idesc = (1u << 4) | ((nt >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
         for (int j = 0; j < np; ++j, ++bi) {
-          const int groups = min(GB, nk - j * GB), xs = XG == 1 ? groups : 1, cs = CG == 1 ? groups : 1;
-          if ((bi & 1) != par) {
-            xi += xs;
-            ci += cs;
-            continue;
-          }
-          const int a = bi % NA;
-          ok = mbar_wait(&a_full[a], (bi / NA) & 1, abort_flag, p.wait_ns);
-#pragma unroll
-          for (int i = 0; i < (XG == 1 ? GB : 1); ++i)
-            if (i < xs && ok) ok = mbar_wait(&x_full[(xi + i) % SX], ((xi + i) / SX) & 1, abort_flag, p.wait_ns);
-          if (ok && ci >= NB) ok = mbar_wait(&afree[ci % NB], ((ci / NB) - 1) & 1, abort_flag, p.wait_ns);
+          if ((bi & 1) != par) continue;
+          const int groups = min(GB, nk - j * GB);
+          ok = mbar_wait(&x_full[bi % SX], (bi / SX) & 1, abort_flag, p.wait_ns);
+          if (ok && bi >= NB) ok = mbar_wait(&afree[bi % NB], ((bi / NB) - 1) & 1, abort_flag, p.wait_ns);
+          if (ok) ok = mbar_wait(&a_full[bi % NA], (bi / NA) & 1, abort_flag, p.wait_ns);
           if (ok && bi > 0) ok = mbar_wait(&turns[par], ((bi - 1) >> 1) & 1, abort_flag, p.wait_ns);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int g = 0; g < GB; ++g) {
-            if (g >= groups || !ok) break;
-            if (CG == 1 && g > 0) {
-              if (ci + g >= NB) ok = mbar_wait(&afree[(ci + g) % NB], (((ci + g) / NB) - 1) & 1, abort_flag, p.wait_ns);
-              if (!ok) break;
-              tc_fence_after();
-            }
-            const uint32_t d_tmem = tmem + (CG == 1 ? ((ci + g) % NB) * NT : (ci % NB) * L::kAccCols + g * NT);
-            const uint32_t a_tmem = tmem + L::kACol0 + a * L::kACols + g * 32;
-            const uint32_t b_base = smem_u32(smem + L::kX) +
-                                    (XG == 1 ? ((xi + g) % SX) * L::kXSlot : (xi % SX) * L::kXSlot + g * L::kXGroup);
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
-                mma_e4m3_fill(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + 32 * k), idesc, k == 0 ? 0u : 1u);
-                mma_e4m3_lastuse(d_tmem, a_tmem + 8 * k, sdesc_sw128(b_base + NT * 128 + 32 * k), idesc);
-              }
-              if (CG == 1) {
-                tc_commit(&done[(ci + g) % NB]);
-                tc_commit(&x_empty[(xi + g) % SX]);
-              }
-            }
-            __syncwarp();
-          }
+          const uint32_t d_tmem = tmem + (bi % NB) * L::kAccCols, a_tmem = tmem + L::kACol0 + (bi % NA) * L::kACols;
+          const uint32_t b_base = smem_u32(smem + L::kX) + (bi % SX) * L::kXSlot;
           if (elect_one()) {
-            mbar_arrive(&turns[par ^ 1]);
-            if (ok) {
-              if (CG != 1) {
-                tc_commit(&done[ci % NB]);
-                tc_commit(&x_empty[xi % SX]);
+#pragma unroll
+            for (int g = 0; g < GB; ++g) {
+              if (g < groups) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
+                  const uint32_t b = b_base + g * L::kXGroup + 32 * k, a = a_tmem + g * 32 + 8 * k;
+                  mma_e4m3_fill(d_tmem + g * NT, a, sdesc_sw128(b), idesc, k == 0 ? 0u : 1u);
+                  mma_e4m3_lastuse(d_tmem + g * NT, a, sdesc_sw128(b + NT * 128), idesc);
+                }
               }
-              tc_commit(&a_empty[a]);
             }
+            tc_fence_before();
+            mbar_arrive(&turns[par ^ 1]);
+            tc_commit(&done[bi % NB]);
+            tc_commit(&a_empty[bi % NA]);
+            tc_commit(&x_empty[bi % SX]);
           }
           __syncwarp();
-          if (!ok) break;
-          xi += xs;
-          ci += cs;
         }
       }
       if (!ok && lane == 0) {
@@ -520,7 +499,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     const int q = warp & 3, myrow = 32 * q + lane, pair = (warp - kConvWarp0) >> 2;
     const int swz = myrow & 7;
     const uint32_t total = blockIdx.x < ntiles ? ((ntiles - blockIdx.x - 1) / gridDim.x + 1) * np : 0;
-    const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16) + L::kACol0 + pair * 64;
+    const uint32_t acol = tmem + (static_cast<uint32_t>(32 * q) << 16) + L::kACol0;
     const uint8_t* row = smem + L::kW + pair * kPairBytes + myrow * 128;
     bool ok = true;
     for (uint32_t bi = 0; bi < total; ++bi) {
@@ -529,7 +508,6 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         ok = false;
         break;
       }
-      bool waited = bi < NA;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint4 in[4];
@@ -552,15 +530,14 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           nibbles_e4m3(u.z, v[8 * c + 4], v[8 * c + 5]);
           nibbles_e4m3(u.w, v[8 * c + 6], v[8 * c + 7]);
         }
-        if (!waited) {
-          waited = true;
-          if (!mbar_wait(&a_empty[a], ((bi / NA) - 1) & 1, abort_flag, p.wait_ns)) {
+        if (h == 0) {
+          if (bi >= NA && !mbar_wait(&a_empty[a], ((bi / NA) - 1) & 1, abort_flag, p.wait_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
         }
-        tmem_st32(acol + a * L::kACols + 32 * h, v);
+        tmem_st32(acol + a * L::kACols + pair * 64 + 32 * h, v);
       }
       if (!ok) break;
       tmem_st_wait();
@@ -582,82 +559,67 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     const uint32_t team = static_cast<uint32_t>(ew / C::kTeamWarps);
     const int cs = (ew % C::kTeamWarps) / 4 * kCols;  // first token of this thread
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + cs;
-    float* my_sw = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + lane;  // [slot][32]
-    float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea) + kSwRing * GB * 32;
+    float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea);
     uint64_t* full = acc_full + team * NB;
     uint32_t phases = 0;  // bit b: parity of this team's next wait for buffer b
-    uint32_t ci = 0, turn = 0;
-    const int accs = CG == 1 ? nk : np;  // accumulators of a tile
+    uint32_t bi = 0, turn = 0;
     bool ok = true;
     for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
       if (C::kTeams > 1 && (turn & 1) != team) {
-        ci += accs;
+        bi += np;
         continue;
       }
       const Tile t = tile_at(id);
       const int n = t.n0 + 32 * q + lane;  // output column
-      const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + n;
-      auto fetch_sw = [&](int j) {  // a batch's scales; a group of copies even when it holds none
+      const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + min(n, p.N - 1);
+      float next[GB];  // the next batch's scales, asked for a batch ahead
+      auto fetch_sw = [&](int left) {
 #pragma unroll
-        for (int g = 0; g < GB; ++g)
-          if (j * GB + g < nk && n < p.N)
-            cp_async4(smem_u32(my_sw + ((j % kSwRing) * GB + g) * 32), sw + static_cast<size_t>(j * GB + g) * p.N);
-        cp_async_commit();
+        for (int g = 0; g < GB; ++g, sw += p.N)
+          if (g < left) next[g] = load_now(sw);
       };
-#pragma unroll
-      for (int j = 0; j < kSwRing - 1; ++j) fetch_sw(j);
+      fetch_sw(nk);
       __syncwarp();  // every lane is done with the last tile's row scales
-      const int mine = t.rows - cs;  // tokens of this thread: min(mine, kCols)
+      const int mine = min(t.rows - cs, kCols);  // tokens of this thread (none: <= 0)
 #pragma unroll
       for (int j = lane; j < kCols; j += 32) my_rs[j] = j < mine ? __ldg(p.row_scale + t.row + cs + j) : 0.f;
       float sum[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
-      for (int j = 0; j < np && ok; ++j) {
-        cp_async_wait_newest<kSwRing - 2>();  // this thread's scales of batch j have landed
+      for (int j = 0; j < np; ++j, ++bi) {
         float s[GB];
 #pragma unroll
-        for (int g = 0; g < GB; ++g) s[g] = my_sw[((j % kSwRing) * GB + g) * 32] * 262144.f;  // (2^18: both operands
-                                                                                             //  in units of 2^-9)
-        fetch_sw(j + kSwRing - 1);
-        if constexpr (CG == 1) {
+        for (int g = 0; g < GB; ++g) s[g] = next[g] * 262144.f;  // (2^18: both operands stand in units of 2^-9)
+        const int left = nk - j * GB;
+        fetch_sw(left - GB);
+        const uint32_t b = bi % NB;
+        if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        phases ^= 1u << b;
+        tc_fence_after();
+        const uint32_t acc = lane_addr + b * L::kAccCols;
+        if constexpr (!NARROW) {
+          if (mine <= 0) {
+            release_acc(&afree[b], lane);
+            continue;
+          }
 #pragma unroll
           for (int g = 0; g < GB; ++g) {
-            if (j * GB + g >= nk) break;
-            const uint32_t b = ci % NB;
-            if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
-              ok = false;
-              break;
-            }
-            phases ^= 1u << b;
-            tc_fence_after();
-            if (mine > 0) {
 #pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                uint32_t r[16];
-                tmem_ld16(lane_addr + b * NT + 16 * c, r);
-                tmem_ld_wait(r);
-                if (c + 1 == kChunks) release_acc(&afree[b], lane);
-                fold(s[g], r, sum + 16 * c);
-              }
-            } else {
-              release_acc(&afree[b], lane);
+            for (int c = 0; c < kChunks; ++c) {
+              uint32_t r[16];
+              tmem_ld16(acc + g * NT + 16 * c, r);
+              tmem_ld_wait(r);
+              if (g + 1 == GB && c + 1 == kChunks) release_acc(&afree[b], lane);
+              if (g < left) fold(s[g], r, sum + 16 * c);
             }
-            ++ci;
           }
         } else {
-          const uint32_t b = ci % NB;
-          if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          phases ^= 1u << b;
-          tc_fence_after();
           // Two groups' loads are in flight together (one at a time, the
           // round trips made the fold the slowest role); of a tile with up to
           // 16 rows, half the columns.
-          const uint32_t acc = lane_addr + b * L::kAccCols;
-          const int left = nk - j * GB;
 #pragma unroll
           for (int g = 0; g < GB; g += 2) {
             if (mine > 16) {
@@ -680,7 +642,6 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
               if (g + 1 < left) fold(s[g + 1], r1, sum);
             }
           }
-          ++ci;
         }
       }
       __syncwarp();
@@ -692,6 +653,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         if (c >= mine) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (mine <= c + 16 * h) break;
           float v[16];
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
@@ -701,14 +663,12 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
             v[j + 2] = __fmul_rn(sum[16 * h + j + 2], rv.z);
             v[j + 3] = __fmul_rn(sum[16 * h + j + 3], rv.w);
           }
-          if (mine > c + 16 * h)
-            store16<OUT>(p, static_cast<size_t>(t.row + cs + c + 16 * h), n, mine - c - 16 * h, lane, v);
+          store16<OUT>(p, static_cast<size_t>(t.row + cs + c + 16 * h), n, mine - c - 16 * h, lane, v);
         }
 #pragma unroll
         for (int j = 0; j + 32 < kCols; ++j) sum[j] = sum[j + 32];
       }
     }
-    cp_async_wait_all();  // no scale copy outlives the CTA
     if (!ok && lane == 0) {
       set_error(p.err, SIXBIT_ETIMEOUT);
       *abort_flag = 1;
