@@ -237,6 +237,8 @@ __device__ __forceinline__ float load_now(const float* p) {
   return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // sum += s * accumulator columns
 template <int COLS>
 __device__ __forceinline__ void fold(float s, const uint32_t (&r)[COLS], float* sum) {
@@ -359,25 +361,32 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   if (warp < kConvWarp0) {
     if constexpr (!NARROW) setmaxnreg_dec<kRegsLow>();
     if (warp == 0) {
-      if (lane == 0) {
-        // -------------------------------------------------- nibble producer --
-        uint32_t bi = 0;
-        bool ok = true;
-        for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
-          const Tile t = tile_at(id);
-          const int wrow = t.e * p.N + t.n0;
-          for (int j = 0; j < np; ++j, ++bi) {
-            const int s = bi % SW;
-            if (bi >= SW && !mbar_wait(&w_empty[s], ((bi / SW) - 1) & 1, abort_flag, p.wait_ns)) {
-              ok = false;
-              break;
-            }
+      // ---------------------------------------------------- nibble producer --
+      // Lane 0 copies; the others ask L2 for the batch's scales, which the fold
+      // reads some five batches later.
+      uint32_t bi = 0;
+      bool ok = true;
+      for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
+        const Tile t = tile_at(id);
+        const int wrow = t.e * p.N + t.n0;
+        const float* sw = p.w4_scale + static_cast<size_t>(t.e) * nk * p.N + min(t.n0 + 32 * (lane & 3), p.N - 1);
+        for (int j = 0; j < np; ++j, ++bi) {
+          const int s = bi % SW;
+          if (bi >= SW && !mbar_wait(&w_empty[s], ((bi / SW) - 1) & 1, abort_flag, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
             const int boxes = min(GB / 2, (nk - j * GB + 1) / 2);  // (a last, odd group's box is half past the row: zeros)
             mbar_expect_tx(&w_full[s], boxes * kPairBytes);
             for (int h = 0; h < boxes; ++h)
               tma_load_2d(smem + L::kW + s * L::kWSlot + h * kPairBytes, &tmW, &w_full[s], (j * GB + 2 * h) * 64, wrow);
           }
+          const int g = j * GB + (lane >> 2);
+          if ((lane >> 2) < GB && g < nk) prefetch_l2(sw + static_cast<size_t>(g) * p.N);
         }
+      }
+      if (lane == 0) {
         if (!ok) {
           set_error(p.err, SIXBIT_ETIMEOUT);
           *abort_flag = 1;
