@@ -194,53 +194,59 @@ cudaError_t launch_dot(const RowsParams& p, cudaStream_t st) {
 
 // ------------------------------------------------------ three to 32 tokens --
 // The products run on mma.m16n8k16 with fp16 operands and FP32 accumulation:
-// weight rows are the 16-row operand, tokens the 8-column one (NT tiles).  Codes and nibbles are exact in fp16 and a group's sum stays below
+// weight rows are the 16-row operand (MT of them), tokens the 8-column one (NT
+// tiles).  Codes and nibbles are exact in fp16 and a group's sum stays below
 // 2^17, so the accumulator holds the exact integer; the scale is applied after
-// each group.  The sum over k may be taken in any order as long as both
-// operands agree, so a lane keeps 32 consecutive k of a group (16 bytes of
-// nibbles, 32 code bytes) and hands four of them to each MMA; within a word of
-// eight nibbles the pairs are (k, k + 4), the two halves of one masked word.
+// each group.  (The other integer forms lose: s8 MMAs take 64 cycles on this
+// part for 8 of the fp16 one at half the k, and E4M3 ones, with both digits of
+// a code, measured 38 us against 20 at 32 tokens, 12288 x 3072.)  The sum over
+// k may be taken in any order as long as both operands agree, so a lane keeps
+// 32 consecutive k of a group (16 bytes of nibbles, 32 code bytes) and hands
+// four of them to each MMA; within a word of eight nibbles the pairs are
+// (k, k + 4), the two halves of one masked word.
 //
-// A CTA owns 16 weight rows and its W warps split the groups of K (the next
+// A CTA owns 16 MT weight rows and its W warps split the groups of K (the next
 // group's nibbles are loaded while this one's are multiplied); their FP32 sums
-// meet in shared memory in a fixed order, where the epilogue runs.
-constexpr int kN = 16;
-
-template <int NT, int W>
-__global__ void __launch_bounds__(W * 32) tile_kernel(const RowsParams p) {
+// meet in shared memory in a fixed order, where the epilogue runs.  The
+// conversions bound it from 16 tokens on (integer instructions issue every
+// second cycle): per 16 rows, 16 k and eight tokens the MMA takes 8 cycles, the
+// codes 10, the nibbles 18 shared by all tokens.
+template <int MT, int NT, int W>
+__global__ void __launch_bounds__(W * 32, MT > 1 ? 3 : (NT == 1 ? 32 : NT == 2 ? 24 : 16) / W) tile_kernel(const RowsParams p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
-  constexpr int kT = 8 * NT;
+  constexpr int kT = 8 * NT, kN = 16 * MT;
   __shared__ float part[W][kT][kN + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int groups = p.K / 128, n0 = blockIdx.x * kN;
   const size_t kb = static_cast<size_t>(p.K) / 2;
-  int n[2];
-  const uint8_t* wrow[2];
+  int n[2 * MT];
+  const uint8_t* wrow[2 * MT];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2 * MT; ++h) {
     n[h] = min(n0 + 8 * h + g, p.N - 1);  // (the surplus rows are not stored)
     wrow[h] = p.w4 + n[h] * kb + t * 16;
   }
   const int8_t* xrow = p.codes + static_cast<size_t>(g) * p.K + t * 32;
-  float sum[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[j][i] = 0.f;
+  float sum[MT][NT][4] = {};
 
-  uint4 w[2];
-  float sc[2];
+  uint4 w[2 * MT];
+  float sc[2 * MT];
   auto fetch = [&](int gr) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2 * MT; ++h) {
       w[h] = __ldg(reinterpret_cast<const uint4*>(wrow[h] + static_cast<size_t>(gr) * 64));
       sc[h] = __ldg(p.w4_scale + static_cast<size_t>(gr) * p.N + n[h]);
     }
   };
   if (warp < groups) fetch(warp);
   for (int gr = warp; gr < groups; gr += W) {
-    const uint4 wc[2] = {w[0], w[1]};
-    const float s[2] = {sc[0], sc[1]};
+    uint4 wc[2 * MT];
+    float s[2 * MT];
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      wc[h] = w[h];
+      s[h] = sc[h];
+    }
     uint4 x[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -252,34 +258,47 @@ __global__ void __launch_bounds__(W * 32) tile_kernel(const RowsParams p) {
       }
     }
     if (gr + W < groups) fetch(gr + W);
-    float acc[NT][4];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    float acc[MT][NT][4] = {};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {  // eight k of the lane
-      uint32_t lo[4], hi[4];
-      nibbles_f16(word(wc[0], q), lo);
-      nibbles_f16(word(wc[1], q), hi);
-      const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+      uint32_t a0[MT][4], a1[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t lo[4], hi[4];
+        nibbles_f16(word(wc[2 * m], q), lo);
+        nibbles_f16(word(wc[2 * m + 1], q), hi);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a0[m][2 * i] = lo[i];
+          a0[m][2 * i + 1] = hi[i];
+          a1[m][2 * i] = lo[2 + i];
+          a1[m][2 * i + 1] = hi[2 + i];
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint32_t b[4];
         codes_f16(word(x[j][q >> 1], 2 * (q & 1)), word(x[j][q >> 1], 2 * (q & 1) + 1), b);
-        mma16816(acc[j], a0, b[0], b[1]);
-        mma16816(acc[j], a1, b[2], b[3]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma16816(acc[m][j], a0[m], b[0], b[1]);
+          mma16816(acc[m][j], a1[m], b[2], b[3]);
+        }
       }
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[j][i] = fmaf(s[i >> 1], acc[j][i], sum[j][i]);
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[m][j][i] = fmaf(s[2 * m + (i >> 1)], acc[m][j][i], sum[m][j][i]);
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * t + (i & 1)][8 * (i >> 1) + g] = sum[j][i];
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * t + (i & 1)][16 * m + 8 * (i >> 1) + g] = sum[m][j][i];
   __syncthreads();
   for (int i = threadIdx.x; i < kT * kN; i += W * 32) {
     const int tok = i / kN, c = i % kN;
@@ -291,9 +310,9 @@ __global__ void __launch_bounds__(W * 32) tile_kernel(const RowsParams p) {
   }
 }
 
-template <int NT, int W>
+template <int MT, int NT, int W>
 cudaError_t launch_tile(const RowsParams& p, cudaStream_t st) {
-  tile_kernel<NT, W><<<(p.N + kN - 1) / kN, W * 32, 0, st>>>(p);
+  tile_kernel<MT, NT, W><<<(p.N + 16 * MT - 1) / (16 * MT), W * 32, 0, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
@@ -301,13 +320,17 @@ cudaError_t launch_tile(const RowsParams& p, cudaStream_t st) {
 // Sixteen warps a CTA where K has groups for them and every CTA is resident
 // at once (two of them an SM with one token tile, one with two), else eight:
 // 8 tokens, 1920 x 7680 weights 10.7 -> 6.9 us, 3072 x 12288 15.0 -> 10.9, but
-// 5760 x 1920 4.7 -> 5.6 and 16 tokens, 3072 x 12288 17.1 -> 18.8.
+// 5760 x 1920 4.7 -> 5.6 and 16 tokens, 3072 x 12288 17.1 -> 18.8.  Above 16
+// tokens and with more 16-row tiles than four an SM, a warp takes two of them
+// for each conversion of the codes, four warps a CTA: 32 tokens, 12288 x 3072
+// 19.6 -> 16.5 us, but 5760 x 1920 9.4 -> 10.6 and 3072 x 12288 22 -> 44.
 cudaError_t launch_tiles(const RowsParams& p, cudaStream_t st) {
   const int tiles = (p.N + 15) / 16;
   const bool deep = p.K > 16 * 128;
-  if (p.M <= 8) return deep && tiles <= 2 * sm_count() ? launch_tile<1, 16>(p, st) : launch_tile<1, 8>(p, st);
-  if (p.M <= 16) return deep && tiles <= sm_count() ? launch_tile<2, 16>(p, st) : launch_tile<2, 8>(p, st);
-  return p.M <= 24 ? launch_tile<3, 8>(p, st) : launch_tile<4, 8>(p, st);
+  if (p.M <= 8) return deep && tiles <= 2 * sm_count() ? launch_tile<1, 1, 16>(p, st) : launch_tile<1, 1, 8>(p, st);
+  if (p.M <= 16) return deep && tiles <= sm_count() ? launch_tile<1, 2, 16>(p, st) : launch_tile<1, 2, 8>(p, st);
+  if (tiles > 4 * sm_count()) return p.M <= 24 ? launch_tile<2, 3, 4>(p, st) : launch_tile<2, 4, 4>(p, st);
+  return p.M <= 24 ? launch_tile<1, 3, 8>(p, st) : launch_tile<1, 4, 8>(p, st);
 }
 
 }  // namespace rows
