@@ -75,17 +75,17 @@ struct Cfg;
 template <>
 struct Cfg<false> {
   static constexpr int NT = 96, GB = 2, SW = 2, SX = 3, NA = 2, NB = 2, kTeams = 2, kTeamWarps = 8;
+  // Registers: 24 warps launch with 80 each; warps 0 - 3 keep 48, the converters
+  // 80, the fold warps get 88.  (With 64 sums a thread they need 96 and more,
+  // and the spilled ones cost each batch a round trip to L2.)
+  static constexpr int kRegs = 80, kRegsLow = 48, kRegsConv = 80, kRegsFold = 88;
 };
 template <>
 struct Cfg<true> {
-  static constexpr int NT = 32, GB = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 1, kTeamWarps = 4;
+  static constexpr int NT = 32, GB = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 2, kTeamWarps = 4;
+  // 20 warps of 96; 32 sums and two groups' loads in flight
+  static constexpr int kRegs = 96, kRegsLow = 48, kRegsConv = 80, kRegsFold = 136;
 };
-// The wide form's registers: 768 threads launch with 80 each; warps 0 - 3 keep
-// 48, the converters all of them, the fold warps get 88 (24 x 80 = 4 x 48 +
-// 4 x 80 + 16 x 88).  (With 64 sums a thread they need 96 and more, and the
-// spilled ones cost each batch a round trip to L2.)
-constexpr int kRegsLaunch = 80, kRegsLow = 48, kRegsConv = 80, kRegsHigh = 88;
-
 template <bool NARROW>
 struct Smem {
   using C = Cfg<NARROW>;
@@ -100,14 +100,14 @@ struct Smem {
                        kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
   static constexpr int kAccCols = C::GB * C::NT, kACol0 = C::NB * kAccCols, kACols = C::GB * 32;
   static_assert(kACol0 + C::NA * kACols <= 512, "tensor memory columns");
+  // The register split must fit in what the CTA is launched with;
+  // setmaxnreg.dec may not raise a warp's count, nor .inc lower it.
+  static_assert(4 * C::kRegsLow + kConv * C::kRegsConv + kFold * C::kRegsFold <= kWarps * C::kRegs &&
+                    C::kRegsLow <= C::kRegs && C::kRegsConv <= C::kRegs && C::kRegsFold >= C::kRegs,
+                "register split");
   // tables: prefix [E + 1], first row [E], rows [E]
   static size_t bytes(int E) { return 1024 + kTables + static_cast<size_t>(3 * E + 1) * 4; }
 };
-static_assert(4 * kRegsLow + Smem<false>::kConv * kRegsConv + Smem<false>::kFold * kRegsHigh <=
-                  Smem<false>::kWarps * kRegsLaunch,
-              "the register split must fit in what the CTA is launched with");
-// setmaxnreg.dec may not raise a warp's count, nor .inc lower it
-static_assert(kRegsLow <= kRegsLaunch && kRegsConv <= kRegsLaunch && kRegsHigh >= kRegsLaunch, "register split");
 static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   };
 
   if (warp < kConvWarp0) {
-    if constexpr (!NARROW) setmaxnreg_dec<kRegsLow>();
+    setmaxnreg_dec<C::kRegsLow>();
     if (warp == 0) {
       // ---------------------------------------------------- nibble producer --
       // Lane 0 copies; the others ask L2 for the batch's scales, which the fold
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       __syncwarp();
     }
   } else if (warp < kFoldWarp0) {
-    if constexpr (!NARROW) setmaxnreg_dec<kRegsConv>();
+    setmaxnreg_dec<C::kRegsConv>();
     // ------------------------------------------------------------ converters --
     // Thread `lane` of the warp of quarter q converts weight row 32 q + lane,
     // the row of its tensor-memory lane; each set of four warps takes two
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       *abort_flag = 1;
     }
   } else {
-    if constexpr (!NARROW) setmaxnreg_inc<kRegsHigh>();
+    setmaxnreg_inc<C::kRegsFold>();
     // -------------------------------------------------------- fold + epilogue --
     // A team takes a whole tile, every kTeams-th of the CTA's; a thread one
     // weight row and kCols tokens of it.
@@ -720,22 +720,18 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap
                    cudaStream_t st) {
   cudaError_t e = set_smem_once<grouped_kernel<NARROW, OUT>>(static_cast<int>(Smem<NARROW>::bytes(SIXBIT_MAX_EXPERTS)));
   if (e != cudaSuccess) return e;
-  if constexpr (!NARROW) {
-    static ContextCache<int> regs_cache;
-    int regs = 0;
-    e = regs_cache.get(&regs, [](int* o) {
-      cudaFuncAttributes fa;
-      const cudaError_t r = cudaFuncGetAttributes(&fa, grouped_kernel<NARROW, OUT>);
-      *o = fa.numRegs;
-      return r;
-    });
-    if (e != cudaSuccess) return e;
-    // setmaxnreg.inc waits until the block's own registers cover the increase:
-    // launch only with the register count the split was sized for.
-    using L = Smem<NARROW>;
-    if (regs < kRegsLaunch || 4 * kRegsLow + L::kConv * kRegsConv + L::kFold * kRegsHigh > L::kWarps * regs)
-      return cudaErrorInvalidConfiguration;
-  }
+  static ContextCache<int> regs_cache;
+  int regs = 0;
+  e = regs_cache.get(&regs, [](int* o) {
+    cudaFuncAttributes fa;
+    const cudaError_t r = cudaFuncGetAttributes(&fa, grouped_kernel<NARROW, OUT>);
+    *o = fa.numRegs;
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  // setmaxnreg.inc waits until the block's own registers cover the increase:
+  // launch only with the register count the split was sized for.
+  if (regs != Cfg<NARROW>::kRegs) return cudaErrorInvalidConfiguration;
   // at most one token tile per row, and one more per expert than rows / NT
   const int64_t tiles_n = (p.N + kBM - 1) / kBM;
   const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
