@@ -121,6 +121,22 @@ static bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dtype
   return r == CUDA_SUCCESS;
 }
 
+// The grouped product's token operand [rows, 2 K bytes] as [K/64][rows][128
+// bytes]: a box holds box_chunks chunks of box_rows rows, chunk by chunk, with
+// 128-byte swizzle; rows and chunks out of bounds read as zero.
+static bool make_token_map(CUtensorMap* m, const uint8_t* base, int rows, int K, int box_rows, int box_chunks) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(K / 64)};
+  cuuint64_t strides[2] = {2 * static_cast<cuuint64_t>(K), 128};
+  cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks)};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // int8 [rows, cols] for the W4A8 GEMM's activation codes: box 128 bytes of
 // columns x 128 rows, 128-byte swizzle (16-byte chunk c of row r lands at
 // chunk c ^ (r & 7), so each converter thread's reads of its own row are
@@ -643,13 +659,13 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   if (M <= 16) return cuda_status(launch_w4a8_rows(p, st));
   uint8_t* xd = static_cast<uint8_t*>(workspace);
   const bool narrow = M < 48 * static_cast<int64_t>(E);
-  CUtensorMap mw, mx, mxf;
-  if (!make_map(&mw, W->i4_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, E * N, K / 2, 128) ||
-      !make_map(&mx, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, 32) ||
-      !make_map(&mxf, xd, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, M, 2 * K, grouped_tokens(narrow)))
-    return SIXBIT_ECUDA;
+  CUtensorMap mw;
+  TokenMaps mx;
+  if (!make_map(&mw, W->i4_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, E * N, K / 2, 128)) return SIXBIT_ECUDA;
+  for (int i = 0; i < token_maps(narrow); ++i)
+    if (!make_token_map(&mx.map[i], xd, M, K, (i + 1) * token_box(narrow), token_chunks(narrow))) return SIXBIT_ECUDA;
   if (launch_digits(p.codes, M, K, mode_dev, xd, st) != cudaSuccess) return SIXBIT_ECUDA;
-  return cuda_status(launch_w4a8_grouped(mw, mx, mxf, p, narrow, st));
+  return cuda_status(launch_w4a8_grouped(mw, mx, p, narrow, st));
 }
 
 }  // extern "C"

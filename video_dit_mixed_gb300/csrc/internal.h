@@ -132,12 +132,18 @@ struct RowsParams {
 cudaError_t launch_w4a8_rows(const RowsParams& p, cudaStream_t st);
 // Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row.
 cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st);
-// w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows,
-// 128-byte swizzle); x, xfull: maps of the token operand (boxes of 128 bytes x 32 rows
-// and x grouped_tokens(narrow) rows, 128-byte swizzle).  narrow: token tiles of
-// 32 instead of 128.
-int grouped_tokens(bool narrow);
-cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull,
-                                const RowsParams& p, bool narrow, cudaStream_t st);
+// Maps of the token operand, seen as [K/64 chunks][M rows][128 bytes], 128-byte
+// swizzle: map i has boxes of token_chunks() chunks x (i + 1) token_box() rows,
+// so that a copy of any tile's batch is one box.
+constexpr int token_box(bool narrow) { return narrow ? 16 : 32; }
+constexpr int token_chunks(bool narrow) { return narrow ? 8 : 4; }
+constexpr int token_maps(bool narrow) { return narrow ? 2 : 3; }
+struct TokenMaps {
+  CUtensorMap map[3];
+};
+// w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows, 128-byte
+// swizzle).  narrow: token tiles of 32 instead of 96.
+cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p, bool narrow,
+                                cudaStream_t st);
 
 }  // namespace sixbit

@@ -84,7 +84,7 @@ template <>
 struct Cfg<true> {
   static constexpr int NT = 32, GB = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 2, kTeamWarps = 4;
   // 20 warps of 96; 32 sums and two groups' loads in flight
-  static constexpr int kRegs = 96, kRegsLow = 48, kRegsConv = 80, kRegsFold = 136;
+  static constexpr int kRegs = 96, kRegsLow = 56, kRegsConv = 80, kRegsFold = 128;
 };
 template <bool NARROW>
 struct Smem {
@@ -92,13 +92,14 @@ struct Smem {
   static constexpr int kConv = 4 * (C::GB / 2), kFold = C::kTeamWarps * C::kTeams;  // warps
   static constexpr int kWarps = kConvWarp0 + kConv + kFold, kThreads = 32 * kWarps;
   static constexpr int kCols = C::NT / (C::kTeamWarps / 4);  // tokens of a fold thread
-  static constexpr int kXGroup = C::NT * 256;  // a group's tokens: the high digits' 128 bytes, then the low ones'
-  static constexpr int kXSlot = C::GB * kXGroup, kWSlot = (C::GB / 2) * kPairBytes;
+    static constexpr int kBox = token_box(NARROW);
+  static constexpr int kXSlot = C::GB * C::NT * 256, kWSlot = (C::GB / 2) * kPairBytes;
   static constexpr int kWarpArea = kCols * 4;  // a fold warp's row scales
   static constexpr int kBars = 2 * C::SW + 2 * C::SX + 2 * C::NA + (C::kTeams + 1) * C::NB + 3;
   static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
                        kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
   static constexpr int kAccCols = C::GB * C::NT, kACol0 = C::NB * kAccCols, kACols = C::GB * 32;
+  static_assert(C::NT == token_maps(NARROW) * kBox && 2 * C::GB == token_chunks(NARROW), "the token maps' boxes");
   static_assert(kACol0 + C::NA * kACols <= 512, "tensor memory columns");
   // The register split must fit in what the CTA is launched with;
   // setmaxnreg.dec may not raise a warp's count, nor .inc lower it.
@@ -251,19 +252,31 @@ __device__ __forceinline__ void fold(float s, const uint32_t (&r)[COLS], float* 
   }
 }
 
+// sum += s * (high + low digits' columns)
+__device__ __forceinline__ void fold_digits(float s, const uint32_t (&r)[32], float* sum) {
+  const uint64_t s2 = f2_pack(s, s);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const uint64_t d = f2_add(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                              f2_pack(__uint_as_float(r[16 + i]), __uint_as_float(r[17 + i])));
+    const uint64_t v = f2_fma(s2, d, f2_pack(sum[i], sum[i + 1]));
+    sum[i] = f2_lo(v);
+    sum[i + 1] = f2_hi(v);
+  }
+}
+
 struct Tile {
   int e, row, rows, n0;  // expert, first row of Y, rows of the tile, first weight row
 };
 
 template <bool NARROW, Out OUT>
 __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const __grid_constant__ CUtensorMap tmXfull, const RowsParams p) {
+    grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ TokenMaps tmX, const RowsParams p) {
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   using C = Cfg<NARROW>;
   using L = Smem<NARROW>;
   constexpr int NT = C::NT, GB = C::GB, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
-  constexpr int kFoldWarp0 = kConvWarp0 + L::kConv;
+  constexpr int kFoldWarp0 = kConvWarp0 + L::kConv, kBox = L::kBox;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -310,8 +323,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmW);
-    prefetch_tmap(&tmX);
-    prefetch_tmap(&tmXfull);
+    for (int i = 0; i < NT / L::kBox; ++i) prefetch_tmap(&tmX.map[i]);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
@@ -402,29 +414,18 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         bool ok = true;
         for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
           const Tile t = tile_at(id);
-          const int boxes = t.rows > NT - 32 ? NT / 32 : (t.rows + 31) / 32;
-          for (int g0 = 0; g0 < nk; g0 += GB, ++it) {
+          const int box = (t.rows - 1) / kBox;
+          const CUtensorMap* map = &tmX.map[box];
+          for (int j = 0; j < np; ++j, ++it) {
             const int s = it % SX;
             if (it >= SX && !mbar_wait(&x_empty[s], ((it / SX) - 1) & 1, abort_flag, p.wait_ns)) {
               ok = false;
               break;
             }
             if (p.withhold_first && it == 0) continue;  // failure-path test: slot 0 never lands
-            const int groups = min(GB, nk - g0);
-            mbar_expect_tx(&x_full[s], groups * boxes * 8192);
-            for (int g = 0; g < groups; ++g) {
-              uint8_t* dst = smem + L::kX + s * L::kXSlot + g * L::kXGroup;
-              const int c = (g0 + g) * 256;
-              if (boxes == NT / 32) {
-                tma_load_2d(dst, &tmXfull, &x_full[s], c, t.row);
-                tma_load_2d(dst + NT * 128, &tmXfull, &x_full[s], c + 128, t.row);
-                continue;
-              }
-              for (int b = 0; b < boxes; ++b) {
-                tma_load_2d(dst + b * 4096, &tmX, &x_full[s], c, t.row + 32 * b);
-                tma_load_2d(dst + NT * 128 + b * 4096, &tmX, &x_full[s], c + 128, t.row + 32 * b);
-              }
-            }
+            // (chunks past K are filled with zeros and counted like the others)
+            mbar_expect_tx(&x_full[s], 2 * GB * (box + 1) * kBox * 128);
+            tma_load_3d(smem + L::kX + s * L::kXSlot, map, &x_full[s], 0, t.row, 2 * j * GB);
           }
         }
         if (!ok) {
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
         const Tile t = tile_at(id);
         uint64_t* done = acc_full + (C::kTeams > 1 ? (turn & 1) * NB : 0);
-        const uint32_t nt = static_cast<uint32_t>((t.rows + 15) & ~15);
+        const bool few = NARROW && t.rows <= 16;
+        const uint32_t nt = few ? 32 : static_cast<uint32_t>((t.rows + 15) & ~15);
+        const uint32_t chunk = ((t.rows - 1) / kBox + 1) * kBox * 128;  // bytes of the tile's digits of a group
         const uint32_t idesc = (1u << 4) | ((nt >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
         for (int j = 0; j < np; ++j, ++bi) {
           if ((bi & 1) != par) continue;
@@ -465,17 +468,25 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           const uint32_t d_tmem = tmem + (bi % NB) * L::kAccCols, a_tmem = tmem + L::kACol0 + (bi % NA) * L::kACols;
           const uint32_t b_base = smem_u32(smem + L::kX) + (bi % SX) * L::kXSlot;
           if (elect_one()) {
+            auto issue = [&](uint32_t chunk, bool apart) {  // (the narrow form's are constants)
 #pragma unroll
-            for (int g = 0; g < GB; ++g) {
-              if (g < groups) {
+              for (int g = 0; g < GB; ++g) {
+                if (g < groups) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
-                  const uint32_t b = b_base + g * L::kXGroup + 32 * k, a = a_tmem + g * 32 + 8 * k;
-                  mma_e4m3_fill(d_tmem + g * NT, a, sdesc_sw128(b), idesc, k == 0 ? 0u : 1u);
-                  mma_e4m3_lastuse(d_tmem + g * NT, a, sdesc_sw128(b + NT * 128), idesc);
+                  for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
+                    const uint32_t b = b_base + 2 * g * chunk + 32 * k, a = a_tmem + g * 32 + 8 * k;
+                    mma_e4m3_fill(d_tmem + g * NT, a, sdesc_sw128(b), idesc, k == 0 ? 0u : 1u);
+                    if (apart) mma_e4m3_lastuse(d_tmem + g * NT, a, sdesc_sw128(b + chunk), idesc);
+                  }
                 }
               }
-            }
+            };
+            if (!NARROW)
+              issue(chunk, true);
+            else if (few)
+              issue(L::kBox * 128, false);
+            else
+              issue(2 * L::kBox * 128, true);
             tc_fence_before();
             mbar_arrive(&turns[par ^ 1]);
             tc_commit(&done[bi % NB]);
@@ -627,8 +638,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           }
         } else {
           // Two groups' loads are in flight together (one at a time, the
-          // round trips made the fold the slowest role); of a tile with up to
-          // 16 rows, half the columns.
+          // round trips made the fold the slowest role).
 #pragma unroll
           for (int g = 0; g < GB; g += 2) {
             if (mine > 16) {
@@ -641,14 +651,14 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
               if (g < left) fold(s[g], r0, sum);
               if (g + 1 < left) fold(s[g + 1], r1, sum);
             } else {
-              uint32_t r0[16], r1[16];
-              tmem_ld16(acc + g * NT, r0);
-              tmem_ld16(acc + (g + 1) * NT, r1);
+              uint32_t r0[32], r1[32];
+              tmem_ld32(acc + g * NT, r0);
+              tmem_ld32(acc + (g + 1) * NT, r1);
               tmem_ld_wait(r0);
               tmem_ld_wait(r1);
               if (g + 2 >= GB) release_acc(&afree[b], lane);
-              if (g < left) fold(s[g], r0, sum);
-              if (g + 1 < left) fold(s[g + 1], r1, sum);
+              if (g < left) fold_digits(s[g], r0, sum);
+              if (g + 1 < left) fold_digits(s[g + 1], r1, sum);
             }
           }
         }
@@ -716,7 +726,7 @@ __global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ 
 }
 
 template <bool NARROW, Out OUT>
-cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull, const RowsParams& p,
+cudaError_t launch(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p,
                    cudaStream_t st) {
   cudaError_t e = set_smem_once<grouped_kernel<NARROW, OUT>>(static_cast<int>(Smem<NARROW>::bytes(SIXBIT_MAX_EXPERTS)));
   if (e != cudaSuccess) return e;
@@ -737,20 +747,20 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap
   const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
   if (tiles_t * tiles_n > INT32_MAX) return cudaErrorInvalidValue;  // tile numbers are 32 bits
   const int grid = static_cast<int>(std::min<int64_t>(tiles_t * tiles_n, sm_count()));
-  grouped_kernel<NARROW, OUT><<<grid, Smem<NARROW>::kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, xfull, p);
+  grouped_kernel<NARROW, OUT><<<grid, Smem<NARROW>::kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, p);
   note_launch();
   return cudaGetLastError();
 }
 
 template <bool NARROW>
-cudaError_t launch_form(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull, const RowsParams& p,
+cudaError_t launch_form(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p,
                         cudaStream_t st) {
   const bool pairs = p.Yf == nullptr && (p.N & 1) == 0 &&
                      ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
-  if (!pairs) return launch<NARROW, kAny>(w, x, xfull, p, st);
-  if (p.epilogue == SIXBIT_EPI_GELU) return launch<NARROW, kPairGelu>(w, x, xfull, p, st);
-  if (p.epilogue == SIXBIT_EPI_RESIDUAL) return launch<NARROW, kPairResidual>(w, x, xfull, p, st);
-  return launch<NARROW, kPair>(w, x, xfull, p, st);
+  if (!pairs) return launch<NARROW, kAny>(w, x, p, st);
+  if (p.epilogue == SIXBIT_EPI_GELU) return launch<NARROW, kPairGelu>(w, x, p, st);
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL) return launch<NARROW, kPairResidual>(w, x, p, st);
+  return launch<NARROW, kPair>(w, x, p, st);
 }
 
 }  // namespace grouped
@@ -763,11 +773,9 @@ cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode
   return cudaGetLastError();
 }
 
-int grouped_tokens(bool narrow) { return narrow ? grouped::Cfg<true>::NT : grouped::Cfg<false>::NT; }
-
-cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xfull,
-                                const RowsParams& p, bool narrow, cudaStream_t st) {
-  return narrow ? grouped::launch_form<true>(w, x, xfull, p, st) : grouped::launch_form<false>(w, x, xfull, p, st);
+cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p, bool narrow,
+                                cudaStream_t st) {
+  return narrow ? grouped::launch_form<true>(w, x, p, st) : grouped::launch_form<false>(w, x, p, st);
 }
 
 }  // namespace sixbit
