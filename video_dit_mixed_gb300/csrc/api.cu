@@ -650,13 +650,15 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   if (offsets == nullptr || workspace == nullptr) return SIXBIT_EINVAL;
   if (!aligned16(workspace)) return SIXBIT_EALIGN;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Up to 16 rows: dot products, an expert's rows one or two at a time (16 rows
-  // over 8 experts of 7680 x 1920 20.4 us against 22.2 on the tensor cores, 2
-  // rows 6.0 against 10.7, but 32 rows 36.1 against 23.7).  Above: token tiles
-  // of 32 up to 48 rows an expert on average, else of 128 (7680 x 1920, 8
-  // experts: 256 rows 29.7 against 37.9 us, 512 rows 43.3 against 42.0, 1024
-  // rows 68.2 against 52.3).
-  if (M <= 16) return cuda_status(launch_w4a8_rows(p, st));
+  // Up to 8 rows over up to 16 experts: dot products, an expert's rows one or
+  // two at a time, an empty expert's CTAs in vain (7680 x 1920, against the
+  // tensor cores: 1 row over 8 experts 5.8 us / 10.2, 8 rows 14.4 / 15.1, over
+  // 16 18.9 / 18.6, over 32 23.9 / 18.7; 1920 x 7680, 8 rows over 8 14.1 / 18.4;
+  // but 16 skewed rows over 8 20.2 / 17.8, 16 of one expert 17.6 / 10.0).
+  // Above: token tiles of 32 up to 48 rows an expert on average, else of 96
+  // (8 experts: 256 rows 26.4 us against 31.1, 384 rows 32.5 against 31.9, 1024
+  // rows 58.4 against 49.6).
+  if (M <= 8 && E <= 16) return cuda_status(launch_w4a8_rows(p, st));
   uint8_t* xd = static_cast<uint8_t*>(workspace);
   const bool narrow = M < 48 * static_cast<int64_t>(E);
   CUtensorMap mw;
