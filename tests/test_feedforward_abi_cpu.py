@@ -70,5 +70,5 @@ def test_products(lib, buf, grouped):
             assert call(**kw) == want, kw
     assert call(m=0, codes=None, scale=None, y=None) == 0
     assert lib.sixbit_launch_count() == before
-    assert lib.sixbit_qgemm_grouped_workspace_bytes(35552, 12288) == 35552 * 12288 * 2
+    assert lib.sixbit_qgemm_grouped_workspace_bytes(35552, 12288) == 35552 * 12288 * 2 + 35552 * 96 * 4
     assert lib.sixbit_qgemm_grouped_workspace_bytes(0, 128) == 0

@@ -634,7 +634,8 @@ sixbit_status sixbit_qgemv(const sixbit_qact* A, const sixbit_weights* W, int M,
 
 size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K) {
   if (M <= 0 || K <= 0) return 0;
-  return static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
+  // two digits a code, a sum of each group's codes
+  return static_cast<size_t>(M) * static_cast<size_t>(K) * 2 + static_cast<size_t>(M) * (static_cast<size_t>(K) / 128) * 4;
 }
 
 sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W, const int32_t* offsets, int E, int M,
@@ -666,7 +667,9 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   if (!make_map(&mw, W->i4_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, E * N, K / 2, 128)) return SIXBIT_ECUDA;
   for (int i = 0; i < token_maps(narrow); ++i)
     if (!make_token_map(&mx.map[i], xd, M, K, (i + 1) * token_box(narrow), token_chunks(narrow))) return SIXBIT_ECUDA;
-  if (launch_digits(p.codes, M, K, mode_dev, xd, st) != cudaSuccess) return SIXBIT_ECUDA;
+  float* less = narrow ? reinterpret_cast<float*>(xd + static_cast<size_t>(M) * K * 2) : nullptr;
+  p.less = less;
+  if (launch_digits(p.codes, M, K, mode_dev, xd, less, st) != cudaSuccess) return SIXBIT_ECUDA;
   return cuda_status(launch_w4a8_grouped(mw, mx, p, narrow, st));
 }
 

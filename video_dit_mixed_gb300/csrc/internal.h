@@ -128,10 +128,13 @@ struct RowsParams {
   int32_t* err;
   uint64_t wait_ns;        // as in GemmParams (grouped kernel)
   int withhold_first;
+  const float* less;       // narrow grouped kernel: [K/128][M], -8 x a group's sum of codes x 2^-18
 };
 cudaError_t launch_w4a8_rows(const RowsParams& p, cudaStream_t st);
-// Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row.
-cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st);
+// Codes [M, K] -> the grouped kernel's token operand, 2 K bytes a row, and, if
+// less is not NULL, its RowsParams::less.
+cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, float* less,
+                          cudaStream_t st);
 // Maps of the token operand, seen as [K/64 chunks][M rows][128 bytes], 128-byte
 // swizzle: map i has boxes of token_chunks() chunks x (i + 1) token_box() rows,
 // so that a copy of any tile's batch is one box.

@@ -32,16 +32,6 @@ __device__ __forceinline__ void nibbles_f16(uint32_t w, uint32_t (&o)[4]) {
   o[3] = fma2((h & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);
 }
 
-// Eight nibbles -> E4M3 of v 2^-9, even k in `even`, odd k in `odd`.  E4M3
-// codes 0 .. 15 (its subnormals and first binade) are the value in units of
-// 2^-9, so a byte needs only sign and magnitude: v >= 0 stays, v < 0 becomes
-// 0x90 - (v + 16) = ((v + 16) ^ 15) + 0x81.
-__device__ __forceinline__ void nibbles_e4m3(uint32_t w, uint32_t& even, uint32_t& odd) {
-  const uint32_t ne = (w >> 3) & 0x01010101u, no = (w >> 7) & 0x01010101u;  // negative
-  even = ((w & 0x0F0F0F0Fu) ^ (ne * 15u)) + ne * 0x81u;
-  odd = (((w >> 4) & 0x0F0F0F0Fu) ^ (no * 15u)) + no * 0x81u;
-}
-
 // Eight s8 codes (k = 0..3 in a, 4..7 in b) -> the same pairs.
 __device__ __forceinline__ void codes_f16(uint32_t a, uint32_t b, uint32_t (&o)[4]) {
   a ^= 0x80808080u;

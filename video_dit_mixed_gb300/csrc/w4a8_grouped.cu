@@ -84,7 +84,7 @@ template <>
 struct Cfg<true> {
   static constexpr int NT = 32, GB = 4, SW = 3, SX = 3, NA = 2, NB = 2, kTeams = 2, kTeamWarps = 4;
   // 20 warps of 96; 32 sums and two groups' loads in flight
-  static constexpr int kRegs = 96, kRegsLow = 56, kRegsConv = 80, kRegsFold = 128;
+  static constexpr int kRegs = 96, kRegsLow = 56, kRegsConv = 64, kRegsFold = 144;
 };
 template <bool NARROW>
 struct Smem {
@@ -94,7 +94,8 @@ struct Smem {
   static constexpr int kCols = C::NT / (C::kTeamWarps / 4);  // tokens of a fold thread
     static constexpr int kBox = token_box(NARROW);
   static constexpr int kXSlot = C::GB * C::NT * 256, kWSlot = (C::GB / 2) * kPairBytes;
-  static constexpr int kWarpArea = kCols * 4;  // a fold warp's row scales
+  // a fold warp's row scales, and the narrow form's sums of codes
+  static constexpr int kWarpArea = kCols * 4 * (NARROW ? 1 + C::GB : 1);
   static constexpr int kBars = 2 * C::SW + 2 * C::SX + 2 * C::NA + (C::kTeams + 1) * C::NB + 3;
   static constexpr int kX = 0, kW = C::SX * kXSlot, kFoldArea = kW + C::SW * kWSlot,
                        kBarAt = kFoldArea + kFold * kWarpArea, kTables = kBarAt + kBars * 8 + 16;
@@ -111,6 +112,24 @@ struct Smem {
 };
 static_assert(Smem<false>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
 static_assert(Smem<true>::kTables + 1024 + (3 * SIXBIT_MAX_EXPERTS + 1) * 4 <= 227 * 1024, "shared memory per CTA");
+
+// Eight nibbles -> E4M3 of v 2^-9, or OFFSET, of (v + 8) 2^-9, even k in
+// `even`, odd k in `odd`.  E4M3 codes 0 .. 15 (its subnormals and first binade)
+// are the value in units of 2^-9, so a byte needs only sign and magnitude:
+// v >= 0 stays, v < 0 becomes 0x90 - (v + 16) = ((v + 16) ^ 15) + 0x81.  With
+// the offset it needs no more than the nibble, its sign bit flipped: three
+// instructions instead of eleven, for which the fold takes the offset out.
+template <bool OFFSET>
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if (OFFSET) {
+    even = (w & 0x0F0F0F0Fu) ^ 0x08080808u;
+    odd = ((w >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+  } else {
+    const uint32_t ne = (w >> 3) & 0x01010101u, no = (w >> 7) & 0x01010101u;  // negative
+    even = ((w & 0x0F0F0F0Fu) ^ (ne * 15u)) + ne * 0x81u;
+    odd = (((w >> 4) & 0x0F0F0F0Fu) ^ (no * 15u)) + no * 0x81u;
+  }
+}
 
 // One lane of the (converged) warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
@@ -241,27 +260,32 @@ __device__ __forceinline__ float load_now(const float* p) {
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // sum += s * accumulator columns
-template <int COLS>
-__device__ __forceinline__ void fold(float s, const uint32_t (&r)[COLS], float* sum) {
+__device__ __forceinline__ void fold16(float s, const uint32_t (&r)[16], float* sum) {
   const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-  for (int i = 0; i < COLS; i += 2) {
+  for (int i = 0; i < 16; i += 2) {
     const uint64_t v = f2_fma(s2, f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(sum[i], sum[i + 1]));
     sum[i] = f2_lo(v);
     sum[i + 1] = f2_hi(v);
   }
 }
-
-// sum += s * (high + low digits' columns)
-__device__ __forceinline__ void fold_digits(float s, const uint32_t (&r)[32], float* sum) {
+// The narrow form's: sum += s * (columns + less) for 32 tokens, or, APART, for
+// 16 with the high digits' columns before the low ones'.
+template <bool APART>
+__device__ __forceinline__ void fold32(float s, const uint32_t (&r)[32], const float* less, float* sum) {
   const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const uint64_t d = f2_add(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                              f2_pack(__uint_as_float(r[16 + i]), __uint_as_float(r[17 + i])));
-    const uint64_t v = f2_fma(s2, d, f2_pack(sum[i], sum[i + 1]));
-    sum[i] = f2_lo(v);
-    sum[i + 1] = f2_hi(v);
+  for (int i = 0; i < (APART ? 16 : 32); i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(less + i);
+#pragma unroll
+    for (int j = i; j < i + 4; j += 2) {
+      uint64_t d = f2_pack(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+      if (APART) d = f2_add(d, f2_pack(__uint_as_float(r[(16 + j) % 32]), __uint_as_float(r[(17 + j) % 32])));
+      d = f2_add(d, j == i ? f2_pack(l.x, l.y) : f2_pack(l.z, l.w));
+      const uint64_t v = f2_fma(s2, d, f2_pack(sum[j], sum[j + 1]));
+      sum[j] = f2_lo(v);
+      sum[j + 1] = f2_hi(v);
+    }
   }
 }
 
@@ -545,10 +569,10 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint4& u = in[c];
-          nibbles_e4m3(u.x, v[8 * c], v[8 * c + 1]);
-          nibbles_e4m3(u.y, v[8 * c + 2], v[8 * c + 3]);
-          nibbles_e4m3(u.z, v[8 * c + 4], v[8 * c + 5]);
-          nibbles_e4m3(u.w, v[8 * c + 6], v[8 * c + 7]);
+          nibbles<NARROW>(u.x, v[8 * c], v[8 * c + 1]);
+          nibbles<NARROW>(u.y, v[8 * c + 2], v[8 * c + 3]);
+          nibbles<NARROW>(u.z, v[8 * c + 4], v[8 * c + 5]);
+          nibbles<NARROW>(u.w, v[8 * c + 6], v[8 * c + 7]);
         }
         if (h == 0) {
           if (bi >= NA && !mbar_wait(&a_empty[a], ((bi / NA) - 1) & 1, abort_flag, p.wait_ns)) {
@@ -599,6 +623,17 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           if (g < left) next[g] = load_now(sw);
       };
       fetch_sw(nk);
+      // The narrow form's weights stand 8 too high: -8 of the sums of the codes
+      // goes onto every accumulator column.  A lane fetches its token's.
+      float* my_less = my_rs + kCols;
+      const float* less = p.less + t.row + min(lane, t.rows - 1);
+      float next_less[GB];
+      auto fetch_less = [&](int left) {
+#pragma unroll
+        for (int g = 0; g < GB; ++g, less += p.M)
+          if (g < left) next_less[g] = load_now(less);
+      };
+      if (NARROW) fetch_less(nk);
       __syncwarp();  // every lane is done with the last tile's row scales
       const int mine = min(t.rows - cs, kCols);  // tokens of this thread (none: <= 0)
 #pragma unroll
@@ -612,6 +647,13 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         for (int g = 0; g < GB; ++g) s[g] = next[g] * 262144.f;  // (2^18: both operands stand in units of 2^-9)
         const int left = nk - j * GB;
         fetch_sw(left - GB);
+        if (NARROW) {
+          __syncwarp();  // every lane is done with the last batch's
+#pragma unroll
+          for (int g = 0; g < GB; ++g) my_less[g * NT + lane] = next_less[g];
+          __syncwarp();
+          fetch_less(left - GB);
+        }
         const uint32_t b = bi % NB;
         if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
           ok = false;
@@ -633,7 +675,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
               tmem_ld16(acc + g * NT + 16 * c, r);
               tmem_ld_wait(r);
               if (g + 1 == GB && c + 1 == kChunks) release_acc(&afree[b], lane);
-              if (g < left) fold(s[g], r, sum + 16 * c);
+              if (g < left) fold16(s[g], r, sum + 16 * c);
             }
           }
         } else {
@@ -641,24 +683,18 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           // round trips made the fold the slowest role).
 #pragma unroll
           for (int g = 0; g < GB; g += 2) {
+            uint32_t r0[32], r1[32];
+            tmem_ld32(acc + g * NT, r0);
+            tmem_ld32(acc + (g + 1) * NT, r1);
+            tmem_ld_wait(r0);
+            tmem_ld_wait(r1);
+            if (g + 2 >= GB) release_acc(&afree[b], lane);
             if (mine > 16) {
-              uint32_t r0[32], r1[32];
-              tmem_ld32(acc + g * NT, r0);
-              tmem_ld32(acc + (g + 1) * NT, r1);
-              tmem_ld_wait(r0);
-              tmem_ld_wait(r1);
-              if (g + 2 >= GB) release_acc(&afree[b], lane);
-              if (g < left) fold(s[g], r0, sum);
-              if (g + 1 < left) fold(s[g + 1], r1, sum);
+              if (g < left) fold32<false>(s[g], r0, my_less + g * NT, sum);
+              if (g + 1 < left) fold32<false>(s[g + 1], r1, my_less + (g + 1) * NT, sum);
             } else {
-              uint32_t r0[32], r1[32];
-              tmem_ld32(acc + g * NT, r0);
-              tmem_ld32(acc + (g + 1) * NT, r1);
-              tmem_ld_wait(r0);
-              tmem_ld_wait(r1);
-              if (g + 2 >= GB) release_acc(&afree[b], lane);
-              if (g < left) fold_digits(s[g], r0, sum);
-              if (g + 1 < left) fold_digits(s[g + 1], r1, sum);
+              if (g < left) fold32<true>(s[g], r0, my_less + g * NT, sum);
+              if (g + 1 < left) fold32<true>(s[g + 1], r1, my_less + (g + 1) * NT, sum);
             }
           }
         }
@@ -711,8 +747,10 @@ __device__ __forceinline__ uint32_t high_digits(uint32_t q) {
   const uint32_t code = __byte_perm(0x1C181000u, 0x26242220u, __byte_perm(t, 0u, 0x4420));  // |h| = 0 .. 7 (8 -> 0)
   return code + ((mag >> 3) & 0x01010101u) * 0x28u + n * 0x80u;
 }
-__global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ codes, int64_t n16,
-                                              uint8_t* __restrict__ out, const int32_t* mode_dev) {
+// less, if not NULL: [K/128][M], -8 of the sum of a group's codes in units of 2^-18.
+__global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ codes, int64_t n16, int M, int groups,
+                                                     uint8_t* __restrict__ out, float* __restrict__ less,
+                                                     const int32_t* mode_dev) {
   if (mode_dev != nullptr && SIXBIT_MODE_OF(*mode_dev) != SIXBIT_MODE_INT8) return;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -722,6 +760,17 @@ __global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ 
     uint4* o = reinterpret_cast<uint4*>(out) + (i >> 3) * 16 + (i & 7);  // (128 codes are 8 reads; K % 128 == 0)
     o[0] = make_uint4(high_digits(s.x), high_digits(s.y), high_digits(s.z), high_digits(s.w));
     o[8] = make_uint4(s.x & 0x0F0F0F0Fu, s.y & 0x0F0F0F0Fu, s.z & 0x0F0F0F0Fu, s.w & 0x0F0F0F0Fu);
+    if (less != nullptr) {  // eight neighbouring lanes hold a group, all of them or none
+      const uint32_t eight = 0xFFu << (threadIdx.x & 24);
+      int q = __dp4a(static_cast<int>(c.x), 0x01010101, __dp4a(static_cast<int>(c.y), 0x01010101, 0));
+      q = __dp4a(static_cast<int>(c.z), 0x01010101, __dp4a(static_cast<int>(c.w), 0x01010101, q));
+#pragma unroll
+      for (int m = 1; m < 8; m <<= 1) q += __shfl_xor_sync(eight, q, m);
+      if ((i & 7) == 0) {
+        const int64_t row = (i >> 3) / groups, g = (i >> 3) % groups;
+        less[g * M + row] = static_cast<float>(q) * (-8.f / 262144.f);
+      }
+    }
   }
 }
 
@@ -765,10 +814,12 @@ cudaError_t launch_form(const CUtensorMap& w, const TokenMaps& x, const RowsPara
 
 }  // namespace grouped
 
-cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, cudaStream_t st) {
+cudaError_t launch_digits(const int8_t* codes, int M, int K, const int32_t* mode_dev, uint8_t* out, float* less,
+                          cudaStream_t st) {
   const int64_t n16 = static_cast<int64_t>(M) * K / 16;
   const int64_t want = (n16 + 255) / 256, cap = static_cast<int64_t>(sm_count()) * 8;
-  grouped::digits_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(codes, n16, out, mode_dev);
+  grouped::digits_kernel<<<static_cast<int>(want < cap ? want : cap), 256, 0, st>>>(codes, n16, M, K / 128, out, less,
+                                                                                   mode_dev);
   note_launch();
   return cudaGetLastError();
 }

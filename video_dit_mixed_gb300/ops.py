@@ -397,7 +397,7 @@ def _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, er
             check(status, "qgemv")
         return out
     po = _ptr(offsets, "offsets", _I32, (experts + 1,), dev)
-    need = 2 * m * k  # sixbit_qgemm_grouped_workspace_bytes
+    need = 2 * m * k + m * (k // 128) * 4  # sixbit_qgemm_grouped_workspace_bytes
     if ws is None:
         ws = _empty((need,), _U8, out.device, stream)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
