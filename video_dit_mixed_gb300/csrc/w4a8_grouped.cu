@@ -642,18 +642,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
       for (int j = 0; j < np; ++j, ++bi) {
-        float s[GB];
-#pragma unroll
-        for (int g = 0; g < GB; ++g) s[g] = next[g] * 262144.f;  // (2^18: both operands stand in units of 2^-9)
         const int left = nk - j * GB;
-        fetch_sw(left - GB);
-        if (NARROW) {
-          __syncwarp();  // every lane is done with the last batch's
-#pragma unroll
-          for (int g = 0; g < GB; ++g) my_less[g * NT + lane] = next_less[g];
-          __syncwarp();
-          fetch_less(left - GB);
-        }
         const uint32_t b = bi % NB;
         if (!mbar_wait(&full[b], (phases >> b) & 1, abort_flag, p.wait_ns)) {
           ok = false;
@@ -661,18 +650,33 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         }
         phases ^= 1u << b;
         tc_fence_after();
+        if (mine <= 0) {
+          release_acc(&afree[b], lane);
+          continue;
+        }
         const uint32_t acc = lane_addr + b * L::kAccCols;
-        if constexpr (!NARROW) {
-          if (mine <= 0) {
-            release_acc(&afree[b], lane);
-            continue;
+        float s[GB];
+        // The batch's scales and the loads of the next one's, while the first
+        // accumulator columns are on their way.
+        auto scales = [&] {
+#pragma unroll
+          for (int g = 0; g < GB; ++g) s[g] = next[g] * 262144.f;  // (2^18: both operands stand in units of 2^-9)
+          if (NARROW) {
+#pragma unroll
+            for (int g = 0; g < GB; ++g) my_less[g * NT + lane] = next_less[g];
+            __syncwarp();
+            fetch_less(left - GB);
           }
+          fetch_sw(left - GB);
+        };
+        if constexpr (!NARROW) {
 #pragma unroll
           for (int g = 0; g < GB; ++g) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
               uint32_t r[16];
               tmem_ld16(acc + g * NT + 16 * c, r);
+              if (g == 0 && c == 0) scales();
               tmem_ld_wait(r);
               if (g + 1 == GB && c + 1 == kChunks) release_acc(&afree[b], lane);
               if (g < left) fold16(s[g], r, sum + 16 * c);
@@ -686,6 +690,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
             uint32_t r0[32], r1[32];
             tmem_ld32(acc + g * NT, r0);
             tmem_ld32(acc + (g + 1) * NT, r1);
+            if (g == 0) scales();
             tmem_ld_wait(r0);
             tmem_ld_wait(r1);
             if (g + 2 >= GB) release_acc(&afree[b], lane);
@@ -697,6 +702,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
               if (g + 1 < left) fold32<true>(s[g + 1], r1, my_less + (g + 1) * NT, sum);
             }
           }
+          __syncwarp();  // every lane is done with this batch's sums of codes
         }
       }
       __syncwarp();
