@@ -22,7 +22,9 @@
 // stay in the thread (packed f32x2), 16 and up go across lanes (2 shuffle
 // stages for b = 64, 4 for b = 256).
 //
-// The floor is bytes: 7 an element with a residual, 3 without.
+// The floor is bytes: 7 an element with a residual, 3 without.  17,776 rows of
+// 1920 with a residual 40.3 us (5.9 TB/s, 89% of a copy), of 12288 69 us (4,444
+// rows); one row 1.9 us, 226 rows 2.7 us (a launch and two round trips).
 #include <cstdint>
 
 #include "common.cuh"

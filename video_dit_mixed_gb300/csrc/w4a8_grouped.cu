@@ -5,49 +5,68 @@
 //   rows m of expert e:  Y[m, n] = s_m[m] * sum_g s_w[e][g][n] * acc_g[m, n]
 //   acc_g[m, n] = sum_{k in group g} qa[m, k] * qw[e][n, k]   (exact integers)
 //
-// Integers run through kind::f16 as in the dense GEMM: codes and nibbles are
-// exact in fp16, a group's sum (below 2^17) exact in the FP32 accumulator, and
-// the group's scale is applied when the accumulator is read back.
+// Integers run through kind::f8f6f4 as E4M3, whose codes 0 .. 15 are the
+// integers 0 .. 15 in units of 2^-9.  A weight is one such code with its sign;
+// a token's code q is two digits, q = 16 h + l, l a code 0 .. 15 and h (-8 .. 7)
+// the E4M3 of h 2^-5.  Both products go into one FP32 accumulator, whose 2^18
+// fold is the group's exact integer (below 2^18); the group's scale is applied
+// when it is read back.  Two E4M3 MMAs take as long as one in fp16, and the
+// operands half the tensor memory and, for a weight, a third of the conversion.
 //
 // The operands' roles are the dense GEMM's swapped.  There the weights are
 // expanded to fp16 in memory once per call, which many rows pay for; an expert
 // with few rows cannot pay 4.5 bytes of traffic for a weight that holds half
 // of one.  Here the 128 weight rows of a tile are the A operand in tensor
-// memory: converter warps take a group's nibbles (64 bytes of a row) from
-// shared memory, turn them into fp16 in registers and store them into the row's
-// tensor-memory lane.  The tokens are the B operand in shared memory; their
-// codes are expanded to fp16 once per call (2 bytes a code, written and read
-// mostly in L2).  A weight's nibble pair (k, k + 4) is what one mask of a
-// 32-bit word leaves, so within each eight inputs both operands hold the
-// order 0 4 1 5 2 6 3 7.  An accumulator lane is a weight row, so a group's
-// scale is one number a thread.
+// memory: converter warps take the nibbles from shared memory, turn them into
+// E4M3 in registers and store them into the row's tensor-memory lane.  The
+// tokens are the B operand in shared memory; their codes are expanded to
+// digits once per call (2 bytes a code, written and read mostly in L2).  A
+// byte's two nibbles go to different words, so within each eight inputs both
+// operands hold the order 0 2 4 6 1 3 5 7.  An accumulator lane is a weight
+// row, so a group's scale is one number a thread.
 //
 // Work.  A tile is 128 weight rows by up to NT rows of one expert; tiles are
 // numbered expert by expert, weight tiles fastest, and a persistent CTA per SM
 // takes every gridDim-th one, finding its expert by bisection in the prefix
-// sums that each CTA takes of the row counts on entry.  The MMA's token
-// count is the tile's own (rounded up to 16), as are the boxes copied (32
-// rows each), so a ragged end costs what it holds.  Two forms, by the mean
-// rows per expert:
-//   NT = 192  eight fold warps, two accumulators; the tensor cores bound it
-//   NT = 32   for experts with few rows: eight converter warps and deep rings
-//             (12 weight tiles of 8 KB in flight); the weights' bytes bound it
+// sums that each CTA takes of the row counts on entry.  All rings move by
+// batches of GB groups.  The MMA's token count is the tile's own (rounded up
+// to 16), as are the rows copied, so a ragged end costs what it holds.
 //
-// Warps (16):
-//   0       TMA producer: 128 x 64-byte nibble tiles
-//   2       TMA producer: fp16 token tiles
-//   1, 3    MMA issuers, even and odd groups (one issuer's waits leave the
+// Two forms, by the mean rows of an expert:
+//   NT = 96, GB = 2   24 warps.  17,776 tokens in two experts each of eight:
+//                     up 7680 x 1920 926 us, down 1920 x 7680 453 us, 1.13
+//                     PFLOP/s, 58% of what bf16 GEMMs reach here; 512 rows an
+//                     expert 124 us.  Bound by the round of an accumulator
+//                     (MMAs 700 - 800 cycles, fold 1,000, and some 700 of
+//                     barriers between them, two in flight), not by the tensor
+//                     cores (768 cycles a batch), the converters (850) or
+//                     memory.  Larger tiles spill in the fold (128: 1066 us),
+//                     one fold team leaves the epilogue alone (1070 us), two
+//                     teams that share a tile as well (1295 us).
+//   NT = 32, GB = 4   20 warps.  452 rows over 64 experts of 7680 x 1920 93 us
+//                     (5.0 TB/s of the weights' bytes, 75% of a copy), 32 rows
+//                     over 64 40 us, 16 over 8 17.4 us.  Bound by the weights'
+//                     bytes and, close behind, by the fold.  Its weights are
+//                     v + 8 (no sign to convert: the integer pipe bound it
+//                     before, 102 us), which the fold takes out with the sums of
+//                     the tokens' codes.  Tiles of up to 16 rows take both
+//                     digits in one MMA, as 32 columns that the fold adds (32
+//                     over 64 experts: 52 -> 43 us).
+//
+// Warps:
+//   0       TMA producer: 128 x 128-byte nibble tiles (two groups each); asks
+//           L2 for the scales
+//   2       TMA producer: a batch of tokens in one 3-D box (eight copies a batch
+//           paced the narrow form)
+//   1, 3    MMA issuers, even and odd batches (one issuer's waits leave the
 //           tensor core idle, as measured in the dense GEMM); warp 1 also
 //           allocates tensor memory
-//   4 ..    converters, one warp per 32-lane quarter (narrow form: two such
-//           sets, even and odd groups)
-//   .. 15   fold + epilogue
-// A group's MMAs are followed by two commits: onto the token slot's barrier
-// (the producer may refill it; the converters may refill the group's A slot:
-// that barrier's next phase is group g + SX > g + NA, whose conversion comes
-// after this wait), and onto the accumulator's barrier of the team that folds
-// the tile.  Each team has barriers of its own, so that it sees every phase of
-// the barriers it waits on.
+//   4 ..    converters, one warp per 32-lane quarter and two groups
+//   ..      two fold teams, alternate tiles, so that one team's epilogue runs
+//           beside the other's batches
+// A batch's MMAs are followed by three commits: onto its accumulator's barrier
+// of the team that folds the tile (each team has barriers of its own, so that
+// it sees every phase of those it waits on), its A slot's and its token slot's.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records
 // SIXBIT_ETIMEOUT, raises the abort flag, waits (bounded) for its copies and
@@ -92,7 +111,7 @@ struct Smem {
   static constexpr int kConv = 4 * (C::GB / 2), kFold = C::kTeamWarps * C::kTeams;  // warps
   static constexpr int kWarps = kConvWarp0 + kConv + kFold, kThreads = 32 * kWarps;
   static constexpr int kCols = C::NT / (C::kTeamWarps / 4);  // tokens of a fold thread
-    static constexpr int kBox = token_box(NARROW);
+  static constexpr int kBox = token_box(NARROW);
   static constexpr int kXSlot = C::GB * C::NT * 256, kWSlot = (C::GB / 2) * kPairBytes;
   // a fold warp's row scales, and the narrow form's sums of codes
   static constexpr int kWarpArea = kCols * 4 * (NARROW ? 1 + C::GB : 1);

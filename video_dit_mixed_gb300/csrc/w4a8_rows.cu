@@ -6,8 +6,11 @@
 //   acc_g[m, n] = sum_{k in group g} qa[m, k] * qw[n, k]    (exact integers)
 //
 // With so few rows the call reads each weight byte once and multiplies it a few
-// times: the weights' bytes bound it, so they go straight from global memory
-// to registers as INT4 and are never expanded in memory.
+// times, so they go straight from global memory to registers as INT4 and are
+// never expanded in memory.  Measured, weights cold (a copy of their bytes would
+// take 1.2, 3.0 and 3.1 us): one token, 7680 x 1920 3.9 us and 3072 x 12288
+// 5.8 us, bound by the latencies of a launch, its loads and the join; 32 tokens,
+// 12288 x 3072 17 us, bound by the conversions of codes and nibbles.
 #include <cstdint>
 
 #include "common.cuh"
