@@ -336,6 +336,49 @@ def test_grouped_extreme_codes(ops, counts):
         assert np.array_equal(y[r], (q[r].astype(np.int64) @ _unpack(w4[e]).astype(np.int64).T).astype(np.float32))
 
 
+@pytest.mark.parametrize("counts", [[8], [9], [15, 1], [16, 17], [31, 33], [47], [48], [95, 96, 97], [128, 64, 63],
+                                    [1] * 17, [0] * 40 + [4], [2, 0, 14] * 6])
+@pytest.mark.parametrize("n,k", [(130, 640), (64, 1152)])
+def test_grouped_every_form_and_tile_end(ops, counts, n, k):
+    """Row counts on both sides of each form's limits and of each copied box, with a part of a batch at the end of K."""
+    g = np.random.default_rng(sum(counts) + 3 * n + k)
+    offsets = [0] + [int(o) for o in np.cumsum(counts)]
+    _grouped(ops, g, offsets, offsets[-1], n, k, (len(counts) + n) % 3, f32=n == 64)
+
+
+@pytest.mark.parametrize("counts", [[1, 4], [16, 5], [17, 30], [40, 2, 9], [96, 97], [150, 31]])
+@pytest.mark.parametrize("code,nibble", [(127, 7), (127, -8), (-128, 7), (-128, -8), (None, None)])
+def test_grouped_sums_at_their_limits(ops, counts, code, nibble):
+    """Codes and weights all at one end, or at either end by chance: exact integers in a float32 output."""
+    g = np.random.default_rng(11)
+    n, k, m, e = 136, 384, sum(counts), len(counts)
+    q = np.full((m, k), code, np.int8) if code is not None else (g.integers(0, 2, (m, k)) * 255 - 128).astype(np.int8)
+    v = np.full((e, n, k), nibble) if nibble is not None else g.integers(0, 2, (e, n, k)) * 15 - 8
+    w4 = ((v[..., 0::2] & 15) | ((v[..., 1::2] & 15) << 4)).astype(np.uint8)
+    offsets = [0] + [int(o) for o in np.cumsum(counts)]
+    y = ops.qgemm_grouped(ops.int8_act(torch.from_numpy(q).cuda(), torch.ones(m, device="cuda")),
+                          ops.Int4Weights(torch.from_numpy(w4).cuda(), torch.ones(e, k // 128, n, device="cuda")),
+                          torch.tensor(offsets, dtype=torch.int32, device="cuda"), out_f32=True).cpu().numpy()
+    for i in range(e):
+        r = slice(offsets[i], offsets[i + 1])
+        assert np.array_equal(y[r], (q[r].astype(np.int64) @ v[i].T).astype(np.float32))
+
+
+@pytest.mark.parametrize("m", [16, 17, 25, 32])
+@pytest.mark.parametrize("code,nibble", [(127, -8), (-128, -8), (None, None)])
+def test_qgemv_many_outputs(ops, m, code, nibble):
+    """More weight rows than two tiles of 16 for each of two CTAs an SM, an odd number: exact integers."""
+    g = np.random.default_rng(m)
+    n, k = 64 * torch.cuda.get_device_properties(0).multi_processor_count + 21, 384
+    q = np.full((m, k), code, np.int8) if code is not None else (g.integers(0, 2, (m, k)) * 255 - 128).astype(np.int8)
+    v = np.full((n, k), nibble) if nibble is not None else g.integers(0, 2, (n, k)) * 15 - 8
+    w4 = ((v[:, 0::2] & 15) | ((v[:, 1::2] & 15) << 4)).astype(np.uint8)
+    y = ops.qgemv(ops.int8_act(torch.from_numpy(q).cuda(), torch.ones(m, device="cuda")),
+                  ops.Int4Weights(torch.from_numpy(w4).cuda(), torch.ones(k // 128, n, device="cuda")),
+                  out_f32=True).cpu().numpy()
+    assert np.array_equal(y, (q.astype(np.int64) @ v.T).astype(np.float32))
+
+
 def test_grouped_many_experts(ops):
     g = np.random.default_rng(5)
     counts = g.integers(0, 4, size=300)
