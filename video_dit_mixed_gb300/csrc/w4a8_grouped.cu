@@ -150,6 +150,11 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t& even, uint32_t& od
   }
 }
 
+// The kernel may start while the digits' kernel runs (programmatic dependent
+// launch): what reads its results waits for its end here.  The producer of
+// every CTA does, so that this kernel never ends first.
+__device__ __forceinline__ void digits_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // One lane of the (converged) warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -315,7 +320,10 @@ struct Tile {
 template <bool NARROW, Out OUT>
 __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ TokenMaps tmX, const RowsParams p) {
-  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) {
+    digits_wait();
+    return;
+  }
   using C = Cfg<NARROW>;
   using L = Smem<NARROW>;
   constexpr int NT = C::NT, GB = C::GB, SW = C::SW, SX = C::SX, NA = C::NA, NB = C::NB;
@@ -453,6 +461,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     } else if (warp == 2) {
       if (lane == 0) {
         // --------------------------------------------------- token producer --
+        digits_wait();
         uint32_t it = 0;
         bool ok = true;
         for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x) {
@@ -624,6 +633,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * q) << 16) + cs;
     float* my_rs = reinterpret_cast<float*>(smem + L::kFoldArea + ew * L::kWarpArea);
     uint64_t* full = acc_full + team * NB;
+    if (NARROW) digits_wait();
     uint32_t phases = 0;  // bit b: parity of this team's next wait for buffer b
     uint32_t bi = 0, turn = 0;
     bool ok = true;
@@ -650,7 +660,8 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       auto fetch_less = [&](int left) {
 #pragma unroll
         for (int g = 0; g < GB; ++g, less += p.M)
-          if (g < left) next_less[g] = load_now(less);
+          if (g < left)  // (not .nc: the digits' kernel may write while this one runs)
+            asm volatile("ld.global.f32 %0, [%1];" : "=f"(next_less[g]) : "l"(less));
       };
       if (NARROW) fetch_less(nk);
       __syncwarp();  // every lane is done with the last tile's row scales
@@ -776,6 +787,7 @@ __device__ __forceinline__ uint32_t high_digits(uint32_t q) {
 __global__ void __launch_bounds__(256) digits_kernel(const int8_t* __restrict__ codes, int64_t n16, int M, int groups,
                                                      uint8_t* __restrict__ out, float* __restrict__ less,
                                                      const int32_t* mode_dev) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (mode_dev != nullptr && SIXBIT_MODE_OF(*mode_dev) != SIXBIT_MODE_INT8) return;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
@@ -821,9 +833,22 @@ cudaError_t launch(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p
   const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
   if (tiles_t * tiles_n > INT32_MAX) return cudaErrorInvalidValue;  // tile numbers are 32 bits
   const int grid = static_cast<int>(std::min<int64_t>(tiles_t * tiles_n, sm_count()));
-  grouped_kernel<NARROW, OUT><<<grid, Smem<NARROW>::kThreads, Smem<NARROW>::bytes(p.E), st>>>(w, x, p);
+  // The CTAs' set-up and first weights beside the digits' kernel: 16 rows over 8
+  // experts 17.2 -> 16.5 us, 32 over 64 40.4 -> 38.8, 1024 over 8 49.1 -> 47.4,
+  // 35552 over 8 928 -> 922; but in the narrow form 1024 rows over 32 78 -> 82
+  // and 2560 over 64 173 -> 185 (768 over 64 96.7 -> 95.5).
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Smem<NARROW>::kThreads);
+  cfg.dynamicSmemBytes = Smem<NARROW>::bytes(p.E);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = NARROW && p.M > 768 ? 0 : 1;
   note_launch();
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<NARROW, OUT>, w, x, p);
 }
 
 template <bool NARROW>
