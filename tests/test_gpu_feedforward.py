@@ -520,6 +520,30 @@ def test_offsets_change_between_replays(ops):
         assert torch.equal(out, want)
 
 
+def test_grouped_in_a_switched_branch(ops):
+    """The product in a body of a device-selected branch of a captured graph, beside work outside of it."""
+    x, r, w, _, we, offsets = _setup(ops)
+    a, _ = ops.add_rmsnorm_quant(x, r, w, had_block=64)
+    want = ops.qgemm_grouped(a, we, offsets)
+    out = torch.zeros_like(want)
+    ws = torch.empty(ops.qgemm_grouped_workspace_bytes(a.m, a.k), dtype=torch.uint8, device="cuda")
+    word = torch.tensor([ops.MODE_INT8], dtype=torch.int32, device="cuda")
+    stream, body = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        sw = ops.GraphSwitch(stream, body, word, ops.MODE_INT8, 1)
+        with sw.branch(0):
+            ops.qgemm_grouped(a, we, offsets, out=out, ws=ws)
+        sw.close()
+    for mode, runs in ((ops.MODE_INT8, True), (ops.MODE_BF16, False), (ops.MODE_INT8, True)):
+        word.fill_(mode)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want if runs else torch.zeros_like(want))
+
+
 def test_mode_word(ops):
     x, r, w, wd, we, offsets = _setup(ops)
     want = _all_three(ops, x, r, w, wd, we, offsets)

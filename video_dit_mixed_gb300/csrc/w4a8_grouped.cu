@@ -34,18 +34,18 @@
 //
 // Two forms, by the mean rows of an expert:
 //   NT = 96, GB = 2   24 warps.  17,776 tokens in two experts each of eight:
-//                     up 7680 x 1920 926 us, down 1920 x 7680 453 us, 1.13
+//                     up 7680 x 1920 922 us, down 1920 x 7680 453 us, 1.14
 //                     PFLOP/s, 58% of what bf16 GEMMs reach here; 512 rows an
-//                     expert 124 us.  Bound by the round of an accumulator
+//                     expert 121 us.  Bound by the round of an accumulator
 //                     (MMAs 700 - 800 cycles, fold 1,000, and some 700 of
 //                     barriers between them, two in flight), not by the tensor
 //                     cores (768 cycles a batch), the converters (850) or
 //                     memory.  Larger tiles spill in the fold (128: 1066 us),
 //                     one fold team leaves the epilogue alone (1070 us), two
 //                     teams that share a tile as well (1295 us).
-//   NT = 32, GB = 4   20 warps.  452 rows over 64 experts of 7680 x 1920 93 us
-//                     (5.0 TB/s of the weights' bytes, 75% of a copy), 32 rows
-//                     over 64 40 us, 16 over 8 17.4 us.  Bound by the weights'
+//   NT = 32, GB = 4   20 warps.  452 rows over 64 experts of 7680 x 1920 92 us
+//                     (5.1 TB/s of the weights' bytes, 76% of a copy), 32 rows
+//                     over 64 39 us, 16 over 8 16.5 us.  Bound by the weights'
 //                     bytes and, close behind, by the fold.  Its weights are
 //                     v + 8 (no sign to convert: the integer pipe bound it
 //                     before, 102 us), which the fold takes out with the sums of
