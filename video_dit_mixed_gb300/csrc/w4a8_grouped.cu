@@ -520,15 +520,15 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
           const uint32_t d_tmem = tmem + (bi % NB) * L::kAccCols, a_tmem = tmem + L::kACol0 + (bi % NA) * L::kACols;
           const uint32_t b_base = smem_u32(smem + L::kX) + (bi % SX) * L::kXSlot;
           if (elect_one()) {
-            auto issue = [&](uint32_t chunk, bool apart) {  // (the narrow form's are constants)
+            auto issue = [&](uint32_t step, bool apart) {  // (the narrow form's are constants)
 #pragma unroll
               for (int g = 0; g < GB; ++g) {
                 if (g < groups) {
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {  // 32 k: the high digits, then the low ones
-                    const uint32_t b = b_base + 2 * g * chunk + 32 * k, a = a_tmem + g * 32 + 8 * k;
+                    const uint32_t b = b_base + 2 * g * step + 32 * k, a = a_tmem + g * 32 + 8 * k;
                     mma_e4m3_fill(d_tmem + g * NT, a, sdesc_sw128(b), idesc, k == 0 ? 0u : 1u);
-                    if (apart) mma_e4m3_lastuse(d_tmem + g * NT, a, sdesc_sw128(b + chunk), idesc);
+                    if (apart) mma_e4m3_lastuse(d_tmem + g * NT, a, sdesc_sw128(b + step), idesc);
                   }
                 }
               }
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       // The narrow form's weights stand 8 too high: -8 of the sums of the codes
       // goes onto every accumulator column.  A lane fetches its token's.
       float* my_less = my_rs + kCols;
-      const float* less = p.less + t.row + min(lane, t.rows - 1);
+      const float* less = NARROW ? p.less + t.row + min(lane, t.rows - 1) : nullptr;
       float next_less[GB];
       auto fetch_less = [&](int left) {
 #pragma unroll
