@@ -6,7 +6,9 @@ stream, so that layers chain without a separate addition:
     y, h = layer(x, residual)        # h = x + residual,  y = down(GELU(up(norm(h))))
 
 ``FFN`` is the dense layer (the few-row product for up to 32 tokens, the GEMM above), ``MoEFFN`` a mixture of
-experts whose row counts stay on the device.  Neither synchronises with the host.
+experts whose row counts stay on the device.  Neither synchronises with the host.  Both run on the current stream and
+take their buffers from torch's allocator for the call, so that calls on different streams, from different threads or
+captured into CUDA graphs do not share any.
 """
 from __future__ import annotations
 
@@ -32,8 +34,13 @@ class FFN:
             def product(act, w, epilogue):
                 return ops.qgemv(act, w, epilogue)
         else:
+            # The GEMM expands its weights here first.  A buffer of the call's own: one shared with calls on other
+            # streams, or with a captured graph, would be overwritten while it is read.
+            ws = torch.empty(max(ops.qgemm_workspace_bytes(w.n, w.k) for w in (self.up, self.down)),
+                             dtype=torch.uint8, device=h.device)
+
             def product(act, w, epilogue):
-                return ops.qgemm(act, None, w, ops.MODE_INT8, epilogue)
+                return ops.qgemm(act, None, w, ops.MODE_INT8, epilogue, ws=ws)
         u = product(a, self.up, ops.EPI_GELU)
         q = ops.hadamard_quant(u, self.had_block, ops.MODE_INT8, out=ops.QActTensors(*u.shape, u.device, nvfp4=False))
         return product(q, self.down, ops.EPI_NONE), h
