@@ -43,19 +43,19 @@ def qgemm_workspace_bytes(n: int, k: int) -> int:
     return int(_lib.sixbit_qgemm_workspace_bytes(n, k))
 
 
-_workspaces = {}
+_workspaces = {}  # device -> its buffers, the largest last
 
 
 def workspace(n: int, k: int, device) -> torch.Tensor:
     """A device buffer of at least qgemm_workspace_bytes(n, k) bytes, shared by every call on `device`
-    that passes none of its own (calls that share it must be ordered, e.g. on one stream)."""
+    that passes none of its own (calls that share it must be ordered, e.g. on one stream).  A buffer that a
+    larger one replaces is kept: a captured graph goes on writing to the address it was captured with."""
     dev = torch.device(device)
     need = qgemm_workspace_bytes(n, k)
-    buf = _workspaces.get(dev)
-    if buf is None or buf.numel() < need:
-        buf = torch.empty(need, dtype=torch.uint8, device=dev)
-        _workspaces[dev] = buf
-    return buf
+    bufs = _workspaces.setdefault(dev, [])
+    if not bufs or bufs[-1].numel() < need:
+        bufs.append(torch.empty(need, dtype=torch.uint8, device=dev))
+    return bufs[-1]
 
 
 class QActTensors:
