@@ -200,9 +200,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// How a tile's outputs are written.  kPair*: bf16, N even, Y and residual
-// 4-byte aligned: neighbouring lanes exchange one value of each two tokens, so
-// that a lane holds two outputs of one token and a store writes 4 bytes.  kAny:
+// How a tile's outputs are written.  kPair*: bf16, N even and below 2^30 (two
+// rows' bytes are a 32-bit step there), Y and residual 4-byte aligned:
+// neighbouring lanes exchange one value of each two tokens, so that a lane
+// holds two outputs of one token and a store writes 4 bytes.  kAny:
 // whatever else, one output at a time.  They are forms of the kernel: one code
 // path a kernel, since its instruction fetch (92% hits) paced the epilogue.
 enum Out { kPair, kPairGelu, kPairResidual, kAny };
@@ -854,7 +855,7 @@ cudaError_t launch(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p
 template <bool NARROW>
 cudaError_t launch_form(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p,
                         cudaStream_t st) {
-  const bool pairs = p.Yf == nullptr && (p.N & 1) == 0 &&
+  const bool pairs = p.Yf == nullptr && (p.N & 1) == 0 && p.N < (1 << 30) &&
                      ((reinterpret_cast<uintptr_t>(p.Y) | reinterpret_cast<uintptr_t>(p.residual)) & 3) == 0;
   if (!pairs) return launch<NARROW, kAny>(w, x, p, st);
   if (p.epilogue == SIXBIT_EPI_GELU) return launch<NARROW, kPairGelu>(w, x, p, st);
