@@ -506,8 +506,8 @@ enum { SIXBIT_QGEMV_MAX_ROWS = 32 };
  * other fields are ignored), group sums exact, FP32 from there on, with the
  * same epilogues; the weights are read once, as INT4, and no workspace is
  * needed.  Y [M, N] bf16, or Y_f32 when it is non-NULL; residual [M, N] bf16
- * may be Y.  0 <= M <= SIXBIT_QGEMV_MAX_ROWS (0: nothing is enqueued), any
- * N >= 1, K % 128 == 0; i8_codes and i4_codes 16-byte aligned, the others
+ * may be Y.  0 <= M <= SIXBIT_QGEMV_MAX_ROWS (0: nothing is enqueued),
+ * 1 <= N < 2^31 - 128, K % 128 == 0; i8_codes and i4_codes 16-byte aligned, the others
  * aligned to their type.  With mode_dev, runs only when the mode word is INT8.
  */
 sixbit_status sixbit_qgemv(const sixbit_qact* A, const sixbit_weights* W, int M, int N, int K, const int32_t* mode_dev,

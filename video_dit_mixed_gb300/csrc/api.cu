@@ -585,7 +585,8 @@ static sixbit_status rows_params(const sixbit_qact* A, const sixbit_weights* W, 
   if (A == nullptr || W == nullptr) return SIXBIT_EINVAL;
   if (epilogue != SIXBIT_EPI_NONE && epilogue != SIXBIT_EPI_GELU && epilogue != SIXBIT_EPI_RESIDUAL)
     return SIXBIT_EINVAL;
-  if (M < 0 || N <= 0 || K <= 0 || K % 128 != 0) return SIXBIT_ESHAPE;
+  // (a last tile of up to 128 weight rows ends within 32 bits)
+  if (M < 0 || N <= 0 || N > INT32_MAX - 128 || K <= 0 || K % 128 != 0) return SIXBIT_ESHAPE;
   if (M == 0) {
     *empty = true;
     return SIXBIT_OK;
