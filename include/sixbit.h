@@ -526,8 +526,9 @@ enum { SIXBIT_MAX_EXPERTS = 1024 };
  * may be ragged, an expert may have none, and the host never reads them.  A
  * pair that is not ascending within [0, M] is reported as SIXBIT_EDEVICE in
  * err_dev and read as an expert without rows (a row that two other experts
- * then claim holds either's result); no memory outside the arrays is
- * touched.  Rows outside every expert's range are not written.  M: rows of A
+ * then claim holds either's result, or with Y on the residual's place a sum of
+ * both; rows claimed more often than 2^31 tiles allow may be left out); no
+ * memory outside the arrays is touched.  Rows outside every expert's range are not written.  M: rows of A
  * and Y (0: nothing is enqueued).  Any N >= 1, K % 128 == 0,
  * 1 <= E <= SIXBIT_MAX_EXPERTS, E N < 2^31 - 128.  workspace: device memory of
  * sixbit_qgemm_grouped_workspace_bytes(M, K) bytes, 16-byte aligned; scratch.

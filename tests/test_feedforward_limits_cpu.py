@@ -22,3 +22,46 @@ def test_few_rows_refuse_widths_whose_last_tile_passes_32_bits(lib, n, m):
     before = lib.sixbit_launch_count()
     assert lib.sixbit_qgemv(C.byref(qa), C.byref(qw), m, n, 128, None, 0, None, p, None, None, None) == ESHAPE
     assert lib.sixbit_launch_count() == before
+
+
+def test_grouped_tile_numbers_stay_in_32_bits(tmp_path):
+    """Offsets that do not ascend (0, M, 0, M, ...) let every second of 1024 experts claim all rows: the device's count
+    of tiles is capped, in 64 bits, before it becomes a tile number."""
+    import os
+    import shutil
+    import subprocess
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = r"""
+#include <cstdio>
+#include "internal.h"
+int main() {
+  using sixbit::capped_tiles;
+  const int64_t grid = 152;
+  for (int64_t rows : {1ll, 96ll, 50000ll, 402653184ll, 2147483647ll})
+    for (int64_t n : {1ll, 128ll, 7680ll, 2097151ll, 2147483519ll}) {
+      const uint32_t tiles_n = static_cast<uint32_t>((n + 127) / 128);
+      int64_t before = 0;
+      int last = 0;
+      for (int e = 0; e < 1024; ++e) {
+        before += e % 2 ? 0 : (rows + 95) / 96;
+        const int now = capped_tiles(before, tiles_n);
+        const int64_t all = static_cast<int64_t>(now) * tiles_n;
+        // ascending, a tile number and the next turn's within unsigned 32 bits, nothing left out below the limit
+        if (now < last || all > INT32_MAX || all + grid > UINT32_MAX) return 1;
+        if (before * tiles_n <= INT32_MAX && now != before) return 2;
+        last = now;
+      }
+    }
+  std::puts("ok");
+}
+"""
+    src = tmp_path / "tiles.cc"
+    src.write_text(code)
+    exe = tmp_path / "tiles"
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    subprocess.run([cxx, "-std=c++17", "-I" + os.path.join(root, "include"), "-I" + os.path.join(cuda, "include"),
+                    "-I" + os.path.join(root, "video_dit_mixed_gb300", "csrc"), str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout == "ok\n"

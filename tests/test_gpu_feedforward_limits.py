@@ -49,3 +49,21 @@ def test_grouped_rows_of_two_gigabytes(ops):
         y[:, pick] = 0
     for row in y:
         assert not bool(row.any())
+
+
+@pytest.mark.parametrize("m,e", [(7, 15), (40, 65), (300, 3), (300, 1023)])
+def test_grouped_offsets_that_claim_every_row_many_times(ops, m, e):
+    """0, M, 0, M, ...: reported; with one weight for all experts, every row has its result all the same."""
+    n, k = 136, 384
+    g = np.random.default_rng(m)
+    q, s = g.integers(-127, 128, size=(m, k)).astype(np.int8), (g.random(m) * 0.05 + 0.01).astype(np.float32)
+    w4 = g.integers(0, 256, size=(n, k // 2)).astype(np.uint8)
+    ws = (g.random((k // 128, n)) * 0.02 + 0.001).astype(np.float32)
+    w = ops.Int4Weights(torch.from_numpy(w4).cuda().expand(e, -1, -1).contiguous(),
+                        torch.from_numpy(ws).cuda().expand(e, -1, -1).contiguous())
+    offsets = torch.tensor([0 if i % 2 == 0 else m for i in range(e + 1)], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = ops.qgemm_grouped(ops.int8_act(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()), w, offsets, out_f32=True,
+                          err=err)
+    assert err.item() == 7
+    _check_product(y, *_product(q, s, w4, ws, 0, None))

@@ -144,6 +144,17 @@ constexpr int token_maps(bool narrow) { return narrow ? 2 : 3; }
 struct TokenMaps {
   CUtensorMap map[3];
 };
+// Token tiles of the experts so far, as many as leave the numbers of all tiles
+// (tiles_n weight tiles for each) within 31 bits.  The host checks that
+// ascending offsets need no more; those that are not can let 512 experts claim
+// every row, whose tiles beyond this are left out.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr int capped_tiles(int64_t tiles_t, uint32_t tiles_n) {
+  const int64_t most = INT32_MAX / static_cast<int64_t>(tiles_n);
+  return static_cast<int>(tiles_t < most ? tiles_t : most);
+}
 // w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows, 128-byte
 // swizzle).  narrow: token tiles of 32 instead of 96.
 cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p, bool narrow,

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 2) {  // row counts and the prefix sums of token tiles, 32 experts at a time
-    int before = 0;
+    int64_t before = 0;  // (32 experts' tiles fit in 32 bits, all experts' need not)
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int f = 0, c = 0;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         const int u = __shfl_up_sync(0xFFFFFFFFu, t, o);
         if (lane >= o) t += u;
       }
-      if (e < p.E) prefix[e + 1] = before + t;
+      if (e < p.E) prefix[e + 1] = capped_tiles(before + t, tiles_n);
       before += __shfl_sync(0xFFFFFFFFu, t, 31);
     }
     if (lane == 0) prefix[0] = 0;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t ntiles = static_cast<uint32_t>(prefix[p.E]) * tiles_n;  // (below 2^31: checked on the host)
+  const uint32_t ntiles = static_cast<uint32_t>(prefix[p.E]) * tiles_n;  // (below 2^31)
 
   auto tile_at = [&](uint32_t id) {
     const int q = static_cast<int>(id / tiles_n);
