@@ -247,6 +247,7 @@ def skip_apply_mxfp8(x_in, codes, scales, x_out, stats: torch.Tensor, scratch: t
 
 _BF16, _F32, _I8, _I32, _U8 = torch.bfloat16, torch.float32, torch.int8, torch.int32, torch.uint8
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _ptr(t, name: str, dtype, shape, dev: int) -> int:
@@ -263,6 +264,18 @@ def _word(t, name: str, dev: int):
     if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != dev:
         raise ValueError(f"{name}: an int32 word on GPU {dev} expected")
     return t.data_ptr()
+
+
+def _stream_on(dev: int, stream) -> int:
+    """The handle of `stream` (None: the current one) after checking that it and the calling thread are on GPU `dev`:
+    the library launches on the current device."""
+    if _current_device() != dev:
+        raise ValueError(f"the tensors are on GPU {dev}, the current device is {_current_device()}")
+    if stream is None:
+        return _current_raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the tensors are on GPU {dev}, the stream on {stream.device_index}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -323,6 +336,7 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, wei
     dev = x.get_device()
     if dev < 0:
         raise ValueError(f"x must be on the GPU, not on {x.device}")
+    st = _stream_on(dev, stream)
     px = _ptr(x, "x", _BF16, shape, dev)
     pw = None if weight is None else _ptr(weight, "weight", _F32, (k,), dev)
     pr = ps = None
@@ -345,8 +359,7 @@ def add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, wei
                       _ptr(out.row_scale, "out.row_scale", _F32, (m,), dev))
     status = _lib.sixbit_add_rmsnorm_quant(px, pr, pw, m, k, eps, had_block,
                                            None if mode_dev is None else _word(mode_dev, "mode_dev", dev), ps,
-                                           C.byref(QAct(None, None, None, None, pc, pscale, None)), None,
-                                           _current_raw_stream(dev) if stream is None else stream.cuda_stream)
+                                           C.byref(QAct(None, None, None, None, pc, pscale, None)), None, st)
     if status:
         check(status, "add_rmsnorm_quant")
     return out, (x if residual is None else sum_out)
@@ -365,6 +378,7 @@ def _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, er
     dev = codes.get_device()
     if dev < 0:
         raise ValueError(f"i8_codes must be on the GPU, not on {codes.device}")
+    st = _stream_on(dev, stream)
     if experts is None:
         shape4, shapes = (n, k // 2), (k // 128, n)
     else:
@@ -390,7 +404,6 @@ def _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, er
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
     pm = None if mode_dev is None else _word(mode_dev, "mode_dev", dev)
     pe = None if err is None else _word(err, "err", dev)
-    st = _current_raw_stream(dev) if stream is None else stream.cuda_stream
     if experts is None:
         status = _lib.sixbit_qgemv(C.byref(ca), C.byref(cw), m, n, k, pm, epilogue, pr, py, pf, pe, st)
         if status:
