@@ -14,7 +14,7 @@ def ops():
 
 
 def _dense_layer(n, k):
-    return SimpleNamespace(n=n, k=k)
+    return SimpleNamespace(n=n, k=k, i4_codes=torch.zeros((n, k // 2), dtype=torch.uint8))
 
 
 @pytest.fixture()
@@ -65,3 +65,12 @@ def test_dense_layer_of_few_rows_needs_none(ops, calls):
     layer = ffn.FFN(_dense_layer(640, 256), _dense_layer(256, 640))
     layer(torch.zeros((ops.QGEMV_MAX_ROWS, 256), dtype=torch.bfloat16))
     assert [n for n, _, _ in calls] == ["qgemv"] * 2
+
+
+@pytest.mark.parametrize("t", [1, 32, 33])
+def test_every_product_reports_into_the_layers_word(ops, calls, t):
+    from video_dit_mixed_gb300 import ffn
+    layer = ffn.FFN(_dense_layer(640, 256), _dense_layer(256, 640))
+    layer(torch.zeros((t, 256), dtype=torch.bfloat16))
+    assert layer.err.dtype == torch.int32 and layer.err.numel() == 1
+    assert [kw.get("err") is layer.err for _, _, kw in calls] == [True, True]

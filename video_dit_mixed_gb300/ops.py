@@ -445,6 +445,13 @@ def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogu
     return _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, err, stream, ws)
 
 
+def check_err(err: torch.Tensor, what: str, stream=None) -> None:
+    """Waits for `stream` (None: the current one), clears the error word and raises SixbitError with what the calls that
+    were given it recorded there (sixbit_check)."""
+    dev = err.get_device()
+    check(_lib.sixbit_check(_word(err, "err", dev), _stream_on(dev, stream)), what)
+
+
 def policy_cfg(gamma_thr=0.1, cos_thr=0.99, err_cap=0.05, pdr_ratio=30.0, near_rel=1e-6, refresh_bf16=False):
     return PolicyCfg(gamma_thr, cos_thr, err_cap, pdr_ratio, near_rel, int(refresh_bf16), 0)
 
