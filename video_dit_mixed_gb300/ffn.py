@@ -60,24 +60,31 @@ class FFN(_Layer):
 class MoEFFN(_Layer):
     """router [E, H]; up [E, F, H], down [E, H, F]: ops.pack_experts results with this had_block.
 
-    Each token goes to the top_k experts of softmax(router h); their outputs are summed with the probabilities
-    renormalised over those experts."""
+    Each token goes to the top_k experts of softmax(router h), or with normed_router of softmax(router norm(h)), as
+    a pre-norm block trains it (norm_weight included); their outputs are summed with the probabilities renormalised
+    over those experts.  The router reads the new stream h in bf16, in FP32."""
 
     def __init__(self, router: torch.Tensor, up: ops.Int4Weights, down: ops.Int4Weights, top_k: int, norm_weight=None,
-                 had_block: int = 64, eps: float = 1e-6):
+                 had_block: int = 64, eps: float = 1e-6, normed_router: bool = False):
         if up.experts is None or up.experts != down.experts or (up.n, up.k) != (down.k, down.n):
             raise ValueError("up [E, F, H] and down [E, H, F] of the same experts expected")
         if tuple(router.shape) != (up.experts, up.k) or not 1 <= top_k <= up.experts:
             raise ValueError(f"router [{up.experts}, {up.k}] and 1 <= top_k <= {up.experts} expected")
         self.router, self.up, self.down, self.top_k = router.float(), up, down, top_k
-        self.norm_weight, self.had_block, self.eps = norm_weight, had_block, eps
+        self.norm_weight, self.had_block, self.eps, self.normed_router = norm_weight, had_block, eps, normed_router
+        if normed_router and norm_weight is not None:
+            self.router = self.router * norm_weight
         self.ids = torch.arange(up.experts + 1, device=router.device)
         self.err = torch.zeros(1, dtype=torch.int32, device=up.i4_codes.device)
 
     def route(self, h: torch.Tensor):
         """(row of each token's choices [T, k], weights [T, k], token of each row [T k], offsets int32 [E + 1]): the
         T k rows are sorted by expert, rows of one expert by token."""
-        top = (h.float() @ self.router.mT).topk(self.top_k, dim=1)
+        h = h.float()
+        logits = h @ self.router.mT
+        if self.normed_router:  # (the norm's row factor comes out of the product, its weight stands in the router)
+            logits *= torch.rsqrt(h.square().mean(1, keepdim=True) + self.eps)
+        top = logits.topk(self.top_k, dim=1)
         weights = torch.softmax(top.values, dim=1)
         expert, order = top.indices.flatten().sort(stable=True)
         offsets = torch.searchsorted(expert, self.ids, out_int32=True)
