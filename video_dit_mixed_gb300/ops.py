@@ -309,6 +309,8 @@ def pack_experts(w: torch.Tensor, had_block: int, stream=None) -> Int4Weights:
     """Experts' weights [E, N, K] float32, each packed by pack_weights, INT4 form kept."""
     if w.dim() != 3:
         raise ValueError(f"w: [E, N, K] expected, got {tuple(w.shape)}")
+    if w.dtype is not _F32 or not w.is_contiguous() or w.get_device() < 0:
+        raise ValueError(f"w: dense float32 on the GPU expected, got {w.dtype}, strides {w.stride()}, on {w.device}")
     e, n, k = w.shape
     with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(w.device)):
         codes = torch.empty((e, n, k // 2), dtype=torch.uint8, device=w.device)
