@@ -1,5 +1,5 @@
-// Device helpers of the W4A8 products on the stored operands (w4a8_rows.cu,
-// w4a8_grouped.cu): nibbles and codes to fp16, and an expert's row range.
+// Device helpers of the W4A8 products on the stored operands: nibbles and codes
+// to fp16 (w4a8_rows.cu), and an expert's row range (also w4a8_grouped.cu).
 #pragma once
 
 #include <cstdint>

@@ -186,19 +186,6 @@ __device__ __forceinline__ void mma_e4m3_lastuse(uint32_t d_tmem, uint32_t a_tme
       "r"(a_tmem), "l"(bdesc), "r"(idesc)
       : "memory");
 }
-// Each thread of the warp writes 32 consecutive 32-bit columns of its lane.
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // How a tile's outputs are written.  kPair*: bf16, N even and below 2^30 (two
 // rows' bytes are a 32-bit step there), Y and residual 4-byte aligned:
@@ -282,8 +269,6 @@ __device__ __forceinline__ float load_now(const float* p) {
   return v;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // sum += s * accumulator columns
 __device__ __forceinline__ void fold16(float s, const uint32_t (&r)[16], float* sum) {
   const uint64_t s2 = f2_pack(s, s);
@@ -340,7 +325,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   uint64_t* a_full = x_empty + SX;              // [NA] the converter warps stored a batch's A
   uint64_t* a_empty = a_full + NA;              // [NA] the batch's MMAs are complete
   uint64_t* acc_full = a_empty + NA;            // [team][NB] an accumulator of the team's tile is complete
-  uint64_t* afree = acc_full + C::kTeams * NB;  // [NB] it has been read back by the team's four warps
+  uint64_t* afree = acc_full + C::kTeams * NB;  // [NB] it has been read back by all of the team's warps
   uint64_t* turns = afree + NB;                 // [2] the other issuer has issued its batch
   uint64_t* drain = turns + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -504,7 +489,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
       bool ok = true;
       for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
         const Tile t = tile_at(id);
-        uint64_t* done = acc_full + (C::kTeams > 1 ? (turn & 1) * NB : 0);
+        uint64_t* done = acc_full + (turn & 1) * NB;
         const bool few = NARROW && t.rows <= 16;
         const uint32_t nt = few ? 32 : static_cast<uint32_t>((t.rows + 15) & ~15);
         const uint32_t chunk = ((t.rows - 1) / kBox + 1) * kBox * 128;  // bytes of the tile's digits of a group
@@ -625,8 +610,9 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   } else {
     setmaxnreg_inc<C::kRegsFold>();
     // -------------------------------------------------------- fold + epilogue --
-    // A team takes a whole tile, every kTeams-th of the CTA's; a thread one
+    // A team takes a whole tile, every second one of the CTA's; a thread one
     // weight row and kCols tokens of it.
+    static_assert(C::kTeams == 2, "teams take turns");
     constexpr int kCols = L::kCols, kChunks = kCols / 16;
     const int ew = warp - kFoldWarp0, q = warp & 3;
     const uint32_t team = static_cast<uint32_t>(ew / C::kTeamWarps);
@@ -639,7 +625,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     uint32_t bi = 0, turn = 0;
     bool ok = true;
     for (uint32_t id = blockIdx.x; id < ntiles && ok; id += gridDim.x, ++turn) {
-      if (C::kTeams > 1 && (turn & 1) != team) {
+      if ((turn & 1) != team) {
         bi += np;
         continue;
       }
