@@ -26,7 +26,7 @@ def test_few_rows_refuse_widths_whose_last_tile_passes_32_bits(lib, n, m):
 
 def test_grouped_tile_numbers_stay_in_32_bits(tmp_path):
     """Offsets that do not ascend (0, M, 0, M, ...) let every second of 1024 experts claim all rows: the device's count
-    of tiles is capped, in 64 bits, before it becomes a tile number."""
+    of tiles is capped before it becomes a tile number."""
     import os
     import shutil
     import subprocess
@@ -38,23 +38,26 @@ def test_grouped_tile_numbers_stay_in_32_bits(tmp_path):
 #include <cstdio>
 #include "internal.h"
 int main() {
-  using sixbit::capped_tiles;
   const int64_t grid = 152;
-  for (int64_t rows : {1ll, 96ll, 50000ll, 402653184ll, 2147483647ll})
-    for (int64_t n : {1ll, 128ll, 7680ll, 2097151ll, 2147483519ll}) {
-      const uint32_t tiles_n = static_cast<uint32_t>((n + 127) / 128);
-      int64_t before = 0;
-      int last = 0;
-      for (int e = 0; e < 1024; ++e) {
-        before += e % 2 ? 0 : (rows + 95) / 96;
-        const int now = capped_tiles(before, tiles_n);
-        const int64_t all = static_cast<int64_t>(now) * tiles_n;
-        // ascending, a tile number and the next turn's within unsigned 32 bits, nothing left out below the limit
-        if (now < last || all > INT32_MAX || all + grid > UINT32_MAX) return 1;
-        if (before * tiles_n <= INT32_MAX && now != before) return 2;
-        last = now;
-      }
-    }
+  int refused = 0;
+  for (int tile : {32, 96})
+    for (int64_t rows : {1ll, 96ll, 50000ll, 402653184ll, 805306368ll, 2147483647ll})
+      for (int64_t n : {1ll, 128ll, 7680ll, 2097151ll, 2147483519ll})
+        for (int experts : {1, 2, 7, 1024}) {
+          if (sixbit::most_token_tiles(rows, tile, experts) > UINT32_MAX) {
+            ++refused;
+            continue;
+          }
+          int64_t claimed = 0;
+          for (int e = 0; e < experts; e += 2) claimed += (rows + tile - 1) / tile;
+          if (claimed > sixbit::most_token_tiles(rows, tile, experts)) return 1;  // (so below 2^32)
+          const uint32_t tiles_n = static_cast<uint32_t>((n + 127) / 128);
+          const int64_t all = sixbit::tile_count(static_cast<uint32_t>(claimed), tiles_n);
+          // the next turn's number within unsigned 32 bits, nothing left out below the limit
+          if (all > INT32_MAX || all + grid > UINT32_MAX) return 2;
+          if (claimed * tiles_n <= INT32_MAX && all != claimed * tiles_n) return 3;
+        }
+  if (refused == 0) return 4;
   std::puts("ok");
 }
 """

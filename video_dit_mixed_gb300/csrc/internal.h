@@ -144,16 +144,18 @@ constexpr int token_maps(bool narrow) { return narrow ? 2 : 3; }
 struct TokenMaps {
   CUtensorMap map[3];
 };
-// Token tiles of the experts so far, as many as leave the numbers of all tiles
-// (tiles_n weight tiles for each) within 31 bits.  The host checks that
-// ascending offsets need no more; those that are not can let 512 experts claim
-// every row, whose tiles beyond this are left out.
+// Token tiles that E experts' ranges of M rows can come to: ascending offsets
+// claim each row once, others once for each run of ascending ones, of which a
+// pair that does not ascend ends each but the last.
+constexpr int64_t most_token_tiles(int64_t M, int tile, int E) { return (E + 1) / 2 * (M / tile) + E; }
+// Numbers of all tiles are 31 bits: with offsets that claim rows more than once,
+// tiles beyond them are left out.
 #ifdef __CUDACC__
 __host__ __device__
 #endif
-constexpr int capped_tiles(int64_t tiles_t, uint32_t tiles_n) {
-  const int64_t most = INT32_MAX / static_cast<int64_t>(tiles_n);
-  return static_cast<int>(tiles_t < most ? tiles_t : most);
+constexpr uint32_t tile_count(uint32_t tiles_t, uint32_t tiles_n) {
+  const uint64_t all = static_cast<uint64_t>(tiles_t) * tiles_n;
+  return all < INT32_MAX ? static_cast<uint32_t>(all) : INT32_MAX;
 }
 // w: map of the INT4 codes [E N, K/2] (box 128 bytes x 128 rows, 128-byte
 // swizzle).  narrow: token tiles of 32 instead of 96.

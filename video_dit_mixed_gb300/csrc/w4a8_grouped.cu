@@ -330,9 +330,10 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
   uint64_t* drain = turns + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* prefix = reinterpret_cast<int*>(smem + L::kTables);  // [E + 1] token tiles of the experts before e
-  int* first = prefix + p.E + 1;                            // [E]
-  int* count = first + p.E;                                 // [E]
+  uint32_t* total = tmem_slot + 2;  // tiles of the call
+  uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + L::kTables);  // [E + 1] token tiles of the experts before e
+  int* first = reinterpret_cast<int*>(prefix) + p.E + 1;              // [E]
+  int* count = first + p.E;                                           // [E]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nk = p.K / 128, np = (nk + GB - 1) / GB;  // groups, batches of a tile
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
     tmem_relinquish();
   }
   if (warp == 2) {  // row counts and the prefix sums of token tiles, 32 experts at a time
-    int64_t before = 0;  // (32 experts' tiles fit in 32 bits, all experts' need not)
+    uint32_t before = 0;  // (no sum passes 32 bits, whatever the offsets: checked on the host)
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       int f = 0, c = 0;
@@ -382,19 +383,22 @@ __global__ void __launch_bounds__(Smem<NARROW>::kThreads, 1)
         const int u = __shfl_up_sync(0xFFFFFFFFu, t, o);
         if (lane >= o) t += u;
       }
-      if (e < p.E) prefix[e + 1] = capped_tiles(before + t, tiles_n);
+      if (e < p.E) prefix[e + 1] = before + t;
       before += __shfl_sync(0xFFFFFFFFu, t, 31);
     }
-    if (lane == 0) prefix[0] = 0;
+    if (lane == 0) {
+      prefix[0] = 0;
+      *total = tile_count(before, tiles_n);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t ntiles = static_cast<uint32_t>(prefix[p.E]) * tiles_n;  // (below 2^31)
+  const uint32_t ntiles = *total;
 
   auto tile_at = [&](uint32_t id) {
-    const int q = static_cast<int>(id / tiles_n);
+    const uint32_t q = id / tiles_n;
     int lo = 0, hi = p.E;  // prefix[lo] <= q < prefix[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -818,7 +822,9 @@ cudaError_t launch(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p
   // at most one token tile per row, and one more per expert than rows / NT
   const int64_t tiles_n = (p.N + kBM - 1) / kBM;
   const int64_t tiles_t = std::min<int64_t>(p.M, p.M / Cfg<NARROW>::NT + static_cast<int64_t>(p.E));
-  if (tiles_t * tiles_n > INT32_MAX) return cudaErrorInvalidValue;  // tile numbers are 32 bits
+  // (neither is reached by arrays that fit the GPU's memory)
+  if (tiles_t * tiles_n > INT32_MAX || most_token_tiles(p.M, Cfg<NARROW>::NT, p.E) > UINT32_MAX)
+    return cudaErrorInvalidValue;
   const int grid = static_cast<int>(std::min<int64_t>(tiles_t * tiles_n, sm_count()));
   // The CTAs' set-up and first weights beside the digits' kernel: 16 rows over 8
   // experts 17.2 -> 16.5 us, 32 over 64 40.4 -> 38.8, 1024 over 8 49.1 -> 47.4,
