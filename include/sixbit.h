@@ -191,8 +191,9 @@ sixbit_status sixbit_pack_weights(const float* W, int N, int K, int had_block,
  * by a fixed-order FP32 butterfly, then NVFP4 (mode 1) or INT8 (mode 2).
  * X: [M, K] bf16; K % 128 == 0; b in {16, 64, 256}.  In NVFP4 mode the tensor
  * amax is taken from `tamax_in` (a device float, e.g. from the producer of X)
- * or, when it is NULL, computed by a first pass into out->tensor_amax.  Other
- * modes (BF16, SKIP) enqueue nothing when mode_dev is NULL and return at once
+ * or, when it is NULL, computed by a first pass into out->tensor_amax.  In INT8
+ * mode a row whose rotation holds a NaN gets a NaN scale (its codes are
+ * unspecified), so that every product of that row is NaN.  Other modes (BF16, SKIP) enqueue nothing when mode_dev is NULL and return at once
  * on the device otherwise.
  */
 sixbit_status sixbit_hadamard_quant(const uint16_t* X, int M, int K, int had_block, int mode,

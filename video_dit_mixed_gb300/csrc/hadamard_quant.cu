@@ -132,6 +132,24 @@ __device__ __forceinline__ float warp_max(float m) {
   return m;
 }
 
+// The same maxima with a NaN kept: an INT8 row that holds one gets a NaN scale,
+// so that every product of the row is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float warp_max_nan(float m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
 // Loads up to 4 chunks of a bf16 row (chunks c0..c0+3) into registers.
 __device__ __forceinline__ void load_chunks_bf16(const uint16_t* row, int K, int c0, int nch, int lane,
                                                  uint4 (&raw)[4]) {
@@ -283,8 +301,8 @@ __device__ __forceinline__ void int8_chunk_store(const float (&v)[8], int r, int
   for (int i = 0; i < 8; ++i) {
     // With s = RN(amax / 127) normal, |RN(y / s)| <= 127 (1 + 2^-24): the clamp
     // cannot bind, and is only applied on the IEEE-division path (s subnormal
-    // or huge, where s carries less precision).  (A NaN y gives an unspecified
-    // code on the fast path.)
+    // or huge, where s carries less precision; or not a number, as the row's
+    // products then are whatever its codes).
     const float d = fast ? div_by_recip(v[i], s, rs) : fminf(fmaxf(__fdiv_rn(v[i], s), -127.f), 127.f);
     t[i] = __float_as_uint(__fadd_rn(d, kRound));  // 0x4B400000 + q
   }
@@ -321,10 +339,10 @@ __global__ void __launch_bounds__(kHqWarps * 32) hq_int8_kernel(const uint16_t* 
         bf16x8_to_f32(raw[u], v);
         fwht8<B>(v, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v[i]));
       }
     }
-    m = warp_max(m);
+    m = warp_max_nan(m);
     const float s = __fdiv_rn(m, 127.0f);
     const bool fast = recip_ok(s) || s == 0.f;
     const float rs = s != 0.f ? __frcp_rn(s) : 0.f;
@@ -424,13 +442,13 @@ __global__ void __launch_bounds__(kHqRowWarps * 32, 2) hq_int8_rows_kernel(const
     for (int i = 0; i < 8; ++i) v[p][i] = f2_pack(a[i], b[i]);
     if (t + 2 * p * R < nch) fwht8x2<B>(v[p], lane);  // warp-uniform; an absent chunk holds zeros
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(f2_lo(v[p][i])), fabsf(f2_hi(v[p][i]))));
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f2_lo(v[p][i])), fabsf(f2_hi(v[p][i])));
   }
-  m = warp_max(m);
+  m = warp_max_nan(m);
   if (lane == 0) red[warp] = m;
   __syncthreads();
   m = red[team << lr];
-  for (int i = 1; i < R; ++i) m = fmaxf(m, red[(team << lr) + i]);
+  for (int i = 1; i < R; ++i) m = max_nan(m, red[(team << lr) + i]);
   if (!row_ok) return;
   // max |y| = RN(max |v| / sqrt(B)): rounding is monotone, so this is the
   // maximum of the rounded rotated values.
@@ -576,14 +594,14 @@ __global__ void __launch_bounds__(W * 32, MINB) hq_int8_half_kernel(const uint16
     }
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fmaxf(fabsf(f2_lo(P[i])), fabsf(f2_hi(P[i]))));
-    m = warp_max(m);
+    for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(f2_lo(P[i])), fabsf(f2_hi(P[i])));
+    m = warp_max_nan(m);
     // one barrier a group: red[par] is rewritten two groups later, after
     // every warp has passed the next group's barrier (and so read it)
     if (lane == 0) red[par][warp] = m;
     __syncthreads();
     m = red[par][team << lr];
-    for (int i = 1; i < R; ++i) m = fmaxf(m, red[par][(team << lr) + i]);
+    for (int i = 1; i < R; ++i) m = max_nan(m, red[par][(team << lr) + i]);
     if (!have) continue;
     const float s = __fdiv_rn(__fmul_rn(m, kScale), 127.0f);
     const bool fast = recip_ok(s) || s == 0.f;
