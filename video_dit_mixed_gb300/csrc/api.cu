@@ -656,7 +656,8 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   // two at a time, an empty expert's CTAs in vain (7680 x 1920, against the
   // tensor cores: 1 row over 8 experts 5.8 us / 10.2, 8 rows 14.4 / 15.1, over
   // 16 18.9 / 18.6, over 32 23.9 / 18.7; 1920 x 7680, 8 rows over 8 14.1 / 18.4;
-  // but 16 skewed rows over 8 20.2 / 16.5, 16 of one expert 17.6 / 10.0).
+  // but 16 skewed rows over 8 20.2 / 16.5, 16 of one expert 17.6 / 10.0).  How the
+  // rows fall is known on the device only: eight rows of one expert take 10.4 us.
   // Above: token tiles of 32 up to 48 rows an expert on average, else of 96
   // (8 experts: 256 rows 26.4 us against 31.1, 384 rows 32.5 against 31.9, 1024
   // rows 58.4 against 49.6).

@@ -23,8 +23,11 @@
 // stages for b = 64, 4 for b = 256).
 //
 // The floor is bytes: 7 an element with a residual, 3 without.  17,776 rows of
-// 1920 with a residual 40.3 us (5.9 TB/s, 89% of a copy), of 12288 69 us (4,444
-// rows); one row 1.9 us, 226 rows 2.7 us (a launch and two round trips).
+// 1920 with a residual 40.5 us (5.9 TB/s, 88% of a copy), of 12288 69 us (4,444
+// rows); one row 2.0 us, 226 rows 2.7 us (a launch and two round trips); 1,003
+// rows of 7680 without a residual 7.4 us (floor 3.5: registers hold the one row
+// in flight of each of two CTAs an SM); 2,000 of 16640, computed twice, 91 us
+// (floor 35).
 #include <cstdint>
 
 #include "common.cuh"

@@ -34,7 +34,7 @@
 //
 // Two forms, by the mean rows of an expert:
 //   NT = 96, GB = 2   24 warps.  17,776 tokens in two experts each of eight:
-//                     up 7680 x 1920 922 us, down 1920 x 7680 453 us, 1.14
+//                     up 7680 x 1920 920 us, down 1920 x 7680 450 us, 1.14
 //                     PFLOP/s, 58% of what bf16 GEMMs reach here; 512 rows an
 //                     expert 121 us.  Bound by the round of an accumulator
 //                     (MMAs 700 - 800 cycles, fold 1,000, and some 700 of
@@ -829,7 +829,8 @@ cudaError_t launch(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p
   // The CTAs' set-up and first weights beside the digits' kernel: 16 rows over 8
   // experts 17.2 -> 16.5 us, 32 over 64 40.4 -> 38.8, 1024 over 8 49.1 -> 47.4,
   // 35552 over 8 928 -> 922; but in the narrow form 1024 rows over 32 78 -> 82
-  // and 2560 over 64 173 -> 185 (768 over 64 96.7 -> 95.5).
+  // and 2560 over 64 173 -> 185 (768 over 64 96.7 -> 95.5).  (The limit lies
+  // between these sizes; why the narrow form loses above it is not known.)
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;

@@ -8,9 +8,11 @@
 // With so few rows the call reads each weight byte once and multiplies it a few
 // times, so they go straight from global memory to registers as INT4 and are
 // never expanded in memory.  Measured, weights cold (a copy of their bytes would
-// take 1.2, 3.0 and 3.1 us): one token, 7680 x 1920 3.9 us and 3072 x 12288
-// 5.8 us, bound by the latencies of a launch, its loads and the join; 32 tokens,
-// 12288 x 3072 17 us, bound by the conversions of codes and nibbles.
+// take 1.2, 3.0 and 3.1 us): one token, 7680 x 1920 4.3 us and 3072 x 12288
+// 6.2 us, bound by the latencies of a launch, its loads and the join; 32 tokens,
+// 12288 x 3072 17 us, bound by the conversions of codes and nibbles (the grouped
+// product with one expert, whose CTAs convert weights only, takes 11.3 us there,
+// but 24.6 against 22.4 for 3072 x 12288).
 #include <cstdint>
 
 #include "common.cuh"
@@ -326,7 +328,8 @@ cudaError_t launch_tile(const RowsParams& p, cudaStream_t st) {
 // 5760 x 1920 4.7 -> 5.6 and 16 tokens, 3072 x 12288 17.1 -> 18.8.  Above 16
 // tokens and with more 16-row tiles than four an SM, a warp takes two of them
 // for each conversion of the codes, four warps a CTA: 32 tokens, 12288 x 3072
-// 19.6 -> 16.5 us, but 5760 x 1920 9.4 -> 10.6 and 3072 x 12288 22 -> 44.
+// 19.6 -> 16.5 us, though that form spills 76 bytes a thread, but 5760 x 1920
+// 9.4 -> 10.6 and 3072 x 12288 22 -> 44.
 cudaError_t launch_tiles(const RowsParams& p, cudaStream_t st) {
   const int tiles = (p.N + 15) / 16;
   const bool deep = p.K > 16 * 128;
@@ -339,8 +342,8 @@ cudaError_t launch_tiles(const RowsParams& p, cudaStream_t st) {
 }  // namespace rows
 
 // One weight (up to 32 rows): dot products up to two rows, MMAs above (two
-// tokens, 7680 x 1920: 4.7 us against 4.8 for any three to eight; 3072 x 12288
-// 6.9 against 10.8).  Experts: any rows, one or two at a time.
+// tokens, 7680 x 1920: 4.7 us, where MMAs take 5.1 for three and 5.3 for eight;
+// 3072 x 12288 6.9 against 10.6).  Experts: any rows, one or two at a time.
 cudaError_t launch_w4a8_rows(const RowsParams& p, cudaStream_t st) {
   return p.offsets != nullptr || p.M <= 2 ? rows::launch_dot(p, st) : rows::launch_tiles(p, st);
 }
