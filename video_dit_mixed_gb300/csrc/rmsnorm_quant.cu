@@ -33,6 +33,7 @@
 #include "common.cuh"
 #include "ctx_cache.h"
 #include "internal.h"
+#include "row_norm.cuh"
 
 namespace sixbit {
 namespace arq {
@@ -51,66 +52,7 @@ struct Params {
   int team_log;          // warp form: lanes of one row = 1 << team_log
 };
 
-constexpr int kE = 16;             // elements of a chunk
 constexpr int kWarpThreads = 128;  // CTA of the warp form
-
-__device__ __forceinline__ void load32(const uint16_t* p, bool wide, uint32_t (&r)[8]) {
-  if (wide) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-    r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
-  }
-}
-__device__ __forceinline__ void store32(uint16_t* p, bool wide, const uint32_t (&r)[8]) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
-  }
-}
-
-// Unscaled fixed-order butterfly (ascending strides) over blocks of B; u holds
-// elements 16 t .. 16 t + 15 of lane t's chunk as pairs.  Every lane of the
-// warp takes part.
-template <int B>
-__device__ __forceinline__ void fwht(uint64_t (&u)[8]) {
-  if constexpr (B >= 16) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = f2_lo(u[i]), b = f2_hi(u[i]);
-      u[i] = f2_pack(__fadd_rn(a, b), __fsub_rn(a, b));
-    }
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if ((i & h) == 0) {
-          const uint64_t a = u[i], b = u[i | h];
-          u[i] = f2_add(a, b);
-          u[i | h] = f2_sub(a, b);
-        }
-      }
-    }
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int h = 1; h < B / kE; h <<= 1) {
-      const float sg = (lane & h) ? -1.f : 1.f;  // upper lane: other - mine
-      const uint64_t s2 = f2_pack(sg, sg);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, static_cast<unsigned long long>(u[i]), h);
-        u[i] = f2_fma(u[i], s2, o);
-      }
-    }
-  }
-}
 
 // h = x + r of one chunk (into u) and its contribution to the sum of squares;
 // the bf16 sum is stored when `put`.
@@ -131,65 +73,6 @@ __device__ __forceinline__ void add(const Params& p, size_t at, bool live, bool 
   for (int i = 0; i < 8; ++i) ss = f2_fma(u[i], u[i], ss);
 }
 
-// 16 weights from channel k on, as pairs (1 without weights, or beyond the row).
-__device__ __forceinline__ void load_weights(const Params& p, int k, bool live, uint64_t (&w)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = f2_pack(1.f, 1.f);
-  if (p.w != nullptr && live) {
-    const float4* w4 = reinterpret_cast<const float4*>(p.w + k);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(w4 + i);
-      w[2 * i] = f2_pack(v.x, v.y);
-      w[2 * i + 1] = f2_pack(v.z, v.w);
-    }
-  }
-}
-
-// max over |u| as bit patterns: a NaN compares above infinity, so it is kept
-__device__ __forceinline__ uint32_t max_bits(const uint64_t (&u)[8], uint32_t m) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t a = f2_abs(u[i]);
-    m = max(m, max(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32)));
-  }
-  return m;
-}
-
-// The row's scale, and the multiplier of u that gives codes (pre: applied to u
-// first, so that the multiplier is finite for the smallest maxima).  A row
-// whose sum or maximum is not finite gets a NaN scale and zero codes.
-struct RowOut {
-  float scale, mul, pre;
-};
-__device__ __forceinline__ RowOut row_out(const Params& p, float ss, uint32_t mbits) {
-  const float a = __uint_as_float(mbits);
-  const float rinv = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(p.K)), p.eps)));
-  RowOut o;
-  o.pre = a < 1e-30f ? 0x1p100f : 1.f;
-  const bool bad = mbits >= 0x7F800000u || !(ss < __uint_as_float(0x7F800000u));
-  o.mul = (bad || mbits == 0) ? 0.f : __fdiv_rn(127.f, a * o.pre);
-  o.scale = bad ? __uint_as_float(0x7FC00000u) : __fdiv_rn(a * (rinv * p.inv_sqrt_b), 127.f);
-  return o;
-}
-
-__device__ __forceinline__ void store_codes(const Params& p, size_t at, const RowOut& o, uint64_t (&u)[8]) {
-  if (o.pre != 1.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = f2_mul(u[i], f2_pack(o.pre, o.pre));
-  }
-  const uint64_t mul = f2_pack(o.mul, o.mul), magic = f2_pack(12582912.f, 12582912.f);
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t a = f2_fma(u[2 * i], mul, magic), b = f2_fma(u[2 * i + 1], mul, magic);
-    const uint32_t lo = __byte_perm(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), 0x0040);
-    const uint32_t hi = __byte_perm(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32), 0x0040);
-    q[i] = o.mul == 0.f ? 0u : __byte_perm(lo, hi, 0x5410);  // (a NaN times 0 is not a code)
-  }
-  *reinterpret_cast<uint4*>(p.codes + at) = make_uint4(q[0], q[1], q[2], q[3]);
-}
-
 // A CTA takes whole rows, every gridDim-th one, V chunks a thread, kept in
 // registers; the thread's weights stay there too, and the next row's loads are
 // in flight while this one is rotated, reduced and stored.  (One CTA per row,
@@ -203,12 +86,12 @@ __global__ void __launch_bounds__(512) row_kernel(const Params p) {
   __shared__ uint32_t s_mx[2][16];
   constexpr int R = V > 0 ? V : 1;
   constexpr bool kKeep = V > 0;  // weights in registers
-  const int chunks = p.K / kE;
+  const int chunks = p.K / kChunk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
   const int loops = V > 0 ? 1 : (chunks + blockDim.x - 1) / blockDim.x;
   uint64_t w[kKeep ? R : 1][8];
   uint32_t xr[R][8], rr[R][8];
-  auto at_of = [&](int row, int c) { return static_cast<size_t>(row) * p.K + static_cast<size_t>(c) * kE; };
+  auto at_of = [&](int row, int c) { return static_cast<size_t>(row) * p.K + static_cast<size_t>(c) * kChunk; };
   auto load = [&](int row, int it) {
 #pragma unroll
     for (int v = 0; v < R; ++v) {
@@ -225,11 +108,11 @@ __global__ void __launch_bounds__(512) row_kernel(const Params p) {
 #pragma unroll
     for (int v = 0; v < R; ++v) {
       const int c = threadIdx.x + v * blockDim.x;
-      load_weights(p, c * kE, c < chunks, w[v]);
+      load_weights(p.w, c * kChunk, c < chunks, w[v]);
     }
   }
   auto rotate = [&](int v, int c, uint64_t (&u)[8]) {
-    if constexpr (!kKeep) load_weights(p, c * kE, c < chunks, w[0]);
+    if constexpr (!kKeep) load_weights(p.w, c * kChunk, c < chunks, w[0]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = f2_mul(u[i], w[kKeep ? v : 0][i]);
     fwht<B>(u);
@@ -270,7 +153,7 @@ __global__ void __launch_bounds__(512) row_kernel(const Params p) {
         mb = max(mb, s_mx[buf][i]);
       }
     }
-    const RowOut o = row_out(p, ss, mb);
+    const RowOut o = row_out(rms_inv(ss, p.K, p.eps) * p.inv_sqrt_b, finite_sum(ss), mb);
     if (threadIdx.x == 0) p.row_scale[row] = o.scale;
     for (int it = 0; it < loops; ++it) {
 #pragma unroll
@@ -282,7 +165,7 @@ __global__ void __launch_bounds__(512) row_kernel(const Params p) {
           add(p, at_of(row, c), c < chunks, true, xr[v], rr[v], unused, u[v]);
           rotate(v, c, u[v]);
         }
-        if (c < chunks) store_codes(p, at_of(row, c), o, u[v]);
+        if (c < chunks) store_codes(p.codes + at_of(row, c), o, u[v]);
       }
     }
   }
@@ -295,8 +178,8 @@ __global__ void __launch_bounds__(kWarpThreads) team_kernel(const Params p) {
   const int team = 1 << p.team_log;
   const int t = threadIdx.x & (team - 1);
   const int64_t row = blockIdx.x * static_cast<int64_t>(kWarpThreads >> p.team_log) + (threadIdx.x >> p.team_log);
-  const bool live = row < p.M && t < p.K / kE;
-  const size_t at = static_cast<size_t>(row) * p.K + t * kE;
+  const bool live = row < p.M && t < p.K / kChunk;
+  const size_t at = static_cast<size_t>(row) * p.K + t * kChunk;
   uint32_t xr[8], rr[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) xr[i] = rr[i] = 0;
@@ -306,7 +189,7 @@ __global__ void __launch_bounds__(kWarpThreads) team_kernel(const Params p) {
   }
   uint64_t u[8], w[8], ss2 = 0;
   add(p, at, live, true, xr, rr, ss2, u);
-  load_weights(p, t * kE, live, w);
+  load_weights(p.w, t * kChunk, live, w);
 #pragma unroll
   for (int i = 0; i < 8; ++i) u[i] = f2_mul(u[i], w[i]);
   fwht<B>(u);
@@ -316,9 +199,9 @@ __global__ void __launch_bounds__(kWarpThreads) team_kernel(const Params p) {
     ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     mb = max(mb, __shfl_xor_sync(0xFFFFFFFFu, mb, o));
   }
-  const RowOut o = row_out(p, ss, mb);
+  const RowOut o = row_out(rms_inv(ss, p.K, p.eps) * p.inv_sqrt_b, finite_sum(ss), mb);
   if (live && t == 0) p.row_scale[row] = o.scale;
-  if (live) store_codes(p, at, o, u);
+  if (live) store_codes(p.codes + at, o, u);
 }
 
 template <int B, int V>
@@ -336,7 +219,7 @@ cudaError_t launch_rows(const Params& p, int threads, cudaStream_t st) {
 
 template <int B>
 cudaError_t launch(Params& p, cudaStream_t st) {
-  const int chunks = p.K / kE;
+  const int chunks = p.K / kChunk;
   note_launch();
   if (chunks <= 32) {
     p.team_log = chunks <= 8 ? 3 : chunks <= 16 ? 4 : 5;
