@@ -542,6 +542,121 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
 /* Bytes of the workspace sixbit_qgemm_grouped needs for M rows of K. */
 size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K);
 
+/* ---- what stands around those products ---------------------------------- */
+
+/*
+ * The norms before and after a block's branch, its gate and the scaled residual
+ * in one call (the transformer block's own; the pages leave them out):
+ *   u = X                                              (post_weight NULL)
+ *     | X / sqrt(mean_k X^2 + eps) * post_weight       (a norm of the branch's output)
+ *   h = residual_scale * residual + gate[s] * u        (residual NULL: no such term; gate NULL: 1)
+ *   sum_out = bf16(h)
+ *   y = h / sqrt(mean_k h^2 + eps) * weight * (1 + scale[s]) + shift[s]
+ *   z = y . blockdiag(H_b / sqrt b)                    (had_block 0: z = y)
+ *   out->row_scale[m] = max_k |z| / 127,  out->i8_codes = rint(z / row_scale)
+ * or, with Y non-NULL (out may be NULL then, had_block must be 0), Y = bf16(y).
+ * All in FP32 from the bf16 inputs; the second norm takes h before its rounding.
+ * weight, post_weight [K] float (NULL: 1, and no norm of the branch); gate, scale,
+ * shift [S][K] float or NULL, each apart from the others.  s is the row's segment:
+ * segment[m], a DEVICE array of int32 in [0, S), or with segment NULL the run of
+ * M / S consecutive rows that m lies in (S must divide M).  A segment outside
+ * [0, S) is reported as SIXBIT_EDEVICE in err_dev and gives that row's outputs NaN
+ * (scale NaN, codes 0).
+ * X, residual, sum_out, Y [M, K] bf16; sum_out may be NULL, X or residual (in
+ * place).  Zero rows and rows that hold infinities or NaN, or whose squares'
+ * sums overflow FP32, as for sixbit_add_rmsnorm_quant.  M >= 0 (0: nothing is
+ * enqueued), K % 128 == 0, K <= 16384, S >= 1, b in {0, 16, 64, 256},
+ * K % b == 0, eps > 0 and finite, residual_scale finite.  X, residual, sum_out, Y,
+ * i8_codes and the float arrays but row_scale 16-byte aligned.  With mode_dev, runs only when the mode
+ * word is INT8.
+ */
+sixbit_status sixbit_gated_rmsnorm_quant(const uint16_t* X, const uint16_t* residual, float residual_scale,
+                                         const float* weight, const float* post_weight, const float* gate,
+                                         const float* scale, const float* shift, const int32_t* segment, int S, int M,
+                                         int K, float eps, int had_block, const int32_t* mode_dev, uint16_t* sum_out,
+                                         uint16_t* Y, const sixbit_qact* out, int32_t* err_dev, void* stream);
+
+/* Scores of sixbit_moe_route. */
+enum { SIXBIT_SCORE_SOFTMAX = 0, SIXBIT_SCORE_SIGMOID = 1 };
+/* Experts a token can go to, and groups of experts, at most. */
+enum { SIXBIT_MAX_TOP_K = 32, SIXBIT_MAX_GROUPS = 32 };
+
+/*
+ * Routing of T tokens to k of E experts, and the order in which
+ * sixbit_qgemm_grouped takes their rows:
+ *   p = softmax(logits) or sigmoid(logits),  key = p + bias     (bias NULL: 0)
+ *   with groups > 1: the E / groups consecutive experts of a group; a group's
+ *     score is the sum of its group_best (1 or 2) largest keys, and only the
+ *     top_groups groups of the largest scores take part
+ *   experts[t] = the k experts of the largest keys, largest first
+ *   weights[t] = p of those, divided by their sum if renormalize (0 where all
+ *     of them are 0), times factor
+ *   offsets[e] = choices of experts below e;  rows[t][j] = the place of token t's
+ *     j-th choice among the T k choices sorted by expert, then by token;
+ *   token[rows[t][j]] = t
+ * Equal keys (and groups) go to the lower number; without a bias experts compare
+ * by their logits.  Keys and scores are compared as FP64 computes them.  A NaN
+ * compares above everything; with softmax, a NaN or +infinity among a row's logits
+ * makes its weights NaN.  A logit of -infinity is a probability of 0; such an
+ * expert is chosen after all others that may be, with a weight of 0.
+ * logits [T, E] float, or with logits_bf16 non-NULL that, bf16 (logits is ignored);
+ * experts, rows [T, k], token [T k], offsets [E + 1] int32; weights [T, k] float.
+ * T >= 0 (0: offsets are zeroed), 1 <= E <= SIXBIT_MAX_EXPERTS,
+ * 1 <= k <= SIXBIT_MAX_TOP_K, T k < 2^31, groups in [1, SIXBIT_MAX_GROUPS] divides
+ * E, 1 <= top_groups <= groups, k <= top_groups E / groups, factor finite.
+ * workspace: device memory of sixbit_moe_route_workspace_bytes(T, E) bytes (NULL
+ * where that is 0), scratch.
+ */
+sixbit_status sixbit_moe_route(const float* logits, const uint16_t* logits_bf16, const float* bias, int T, int E, int k,
+                               int score, int groups, int top_groups, int group_best, int renormalize, float factor,
+                               int32_t* experts, float* weights, int32_t* rows, int32_t* token, int32_t* offsets,
+                               void* workspace, void* stream);
+
+/* Bytes of the workspace sixbit_moe_route needs. */
+size_t sixbit_moe_route_workspace_bytes(int T, int E);
+
+/*
+ * The sum that ends a routed layer: out[t] = sum_j weights[t][j] * d[rows[t][j]],
+ * j = 0 .. k - 1, in FP32 and in an order that depends on k alone.  d [R, H] bf16,
+ * or float in d_f32 when that is non-NULL; rows [T, k] int32 on the device: -1
+ * adds nothing, and any other number outside [0, R) is reported as SIXBIT_EDEVICE
+ * in err_dev and adds nothing.  weights [T, k] float.  Y [T, H] bf16, or Y_f32 when
+ * it is non-NULL.  T >= 0 (0: nothing is enqueued), 1 <= k <= SIXBIT_MAX_TOP_K,
+ * R >= 0, 1 <= H <= 2^20; tensors aligned to their type.
+ */
+sixbit_status sixbit_moe_combine(const uint16_t* d, const float* d_f32, const int32_t* rows, const float* weights,
+                                 int T, int k, int R, int H, uint16_t* Y, float* Y_f32, int32_t* err_dev, void* stream);
+
+/* Ranks of an adapter sixbit_lowrank_add takes at most. */
+enum { SIXBIT_MAX_RANK = 128 };
+
+/*
+ * Low-rank adapters of many requests beside a projection they share:
+ *   out[m] = epilogue(base[m] + alpha[l] * B_l (A_l x[m])),   l = ids[m]
+ * ids [M] int32 on the device in [-1, L), -1 for the base alone (any other number
+ * is reported as SIXBIT_EDEVICE in err_dev and read as -1).  x: A's i8_codes times
+ * row_scale (its other fields are ignored), or with x_bf16 non-NULL that, bf16
+ * [M, K] (A is ignored).  Codes are those of rotated rows, so the adapters' A has
+ * to be rotated by the same blocks.  lr_a [L][R][K], lr_b [L][N][R] bf16, alpha [L]
+ * float or NULL (1).  base [M, N] bf16, or base_f32, or neither (0).  Products are
+ * summed in FP32; A_l x enters the second product to 2^-16 of itself (2^-24 with Y_f32).
+ * Epilogues as for sixbit_qgemm: NONE, GELU, RESIDUAL (+ residual [M, N] bf16).
+ * Y [M, N] bf16, or Y_f32 when it is non-NULL; Y may be base or residual, Y_f32
+ * base_f32 (in place).  M >= 0 (0: nothing is enqueued), 1 <= N <= 2^20,
+ * K % 128 == 0, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, L >= 1.  Codes, x_bf16,
+ * lr_a, lr_b and the workspace 16-byte aligned, the others to their type.
+ * workspace: device memory of sixbit_lowrank_workspace_bytes(M, K, R) bytes,
+ * scratch.  With mode_dev, runs only when the mode word is INT8.
+ */
+sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, const uint16_t* lr_a,
+                                 const uint16_t* lr_b, const float* alpha, const int32_t* ids, int L, int M, int N,
+                                 int K, int R, const uint16_t* base, const float* base_f32, const int32_t* mode_dev,
+                                 int epilogue, const uint16_t* residual, uint16_t* Y, float* Y_f32, void* workspace,
+                                 int32_t* err_dev, void* stream);
+
+/* Bytes of the workspace sixbit_lowrank_add needs. */
+size_t sixbit_lowrank_workspace_bytes(int M, int K, int R);
+
 /* ---- device-decided branches in a captured CUDA graph ------------------- */
 
 /*

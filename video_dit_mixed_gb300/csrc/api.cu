@@ -675,4 +675,186 @@ sixbit_status sixbit_qgemm_grouped(const sixbit_qact* A, const sixbit_weights* W
   return cuda_status(launch_w4a8_grouped(mw, mx, p, narrow, st));
 }
 
+sixbit_status sixbit_gated_rmsnorm_quant(const uint16_t* X, const uint16_t* residual, float residual_scale,
+                                         const float* weight, const float* post_weight, const float* gate,
+                                         const float* scale, const float* shift, const int32_t* segment, int S, int M,
+                                         int K, float eps, int had_block, const int32_t* mode_dev, uint16_t* sum_out,
+                                         uint16_t* Y, const sixbit_qact* out, int32_t* err_dev, void* stream) {
+  if (M < 0 || K <= 0 || K % 128 != 0 || K > 16384 || S < 1 ||
+      (had_block != 0 && (!valid_block(had_block) || K % had_block != 0)) || (segment == nullptr && M % S != 0))
+    return SIXBIT_ESHAPE;
+  if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(residual_scale) || (Y == nullptr && out == nullptr) ||
+      (Y != nullptr && had_block != 0))
+    return SIXBIT_EINVAL;
+  if (M == 0) return SIXBIT_OK;
+  if (X == nullptr || (Y == nullptr && (out->i8_codes == nullptr || out->row_scale == nullptr))) return SIXBIT_EINVAL;
+  for (const void* q : {static_cast<const void*>(X), static_cast<const void*>(residual),
+                        static_cast<const void*>(sum_out), static_cast<const void*>(Y),
+                        static_cast<const void*>(weight), static_cast<const void*>(post_weight),
+                        static_cast<const void*>(gate), static_cast<const void*>(scale),
+                        static_cast<const void*>(shift)})
+    if (!aligned16(q)) return SIXBIT_EALIGN;
+  if (!aligned_to(segment, 4) || (Y == nullptr && (!aligned16(out->i8_codes) || !aligned_to(out->row_scale, 4))))
+    return SIXBIT_EALIGN;
+  const sixbit_status s = check_device();
+  if (s != SIXBIT_OK) return s;
+  GatedNormParams g{};
+  g.x = X;
+  g.res = residual;
+  g.w = weight;
+  g.post_w = post_weight;
+  g.gate = gate;
+  g.scale = scale;
+  g.shift = shift;
+  g.segment = segment;
+  g.res_scale = residual_scale;
+  g.eps = eps;
+  g.M = M;
+  g.K = K;
+  g.S = S;
+  g.rows_per_seg = M / S > 0 ? M / S : 1;
+  g.mode_dev = mode_dev;
+  g.sum_out = sum_out;
+  g.y = Y;
+  if (Y == nullptr) {
+    g.codes = out->i8_codes;
+    g.row_scale = out->row_scale;
+  }
+  g.err = err_dev;
+  return cuda_status(launch_gated_norm(g, had_block, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sixbit_moe_route_workspace_bytes(int T, int E) {
+  if (T <= kRouteTurn || E <= 0) return 0;
+  return static_cast<size_t>(kRouteRuns) * static_cast<size_t>(E) * 4;
+}
+
+sixbit_status sixbit_moe_route(const float* logits, const uint16_t* logits_bf16, const float* bias, int T, int E, int k,
+                               int score, int groups, int top_groups, int group_best, int renormalize, float factor,
+                               int32_t* experts, float* weights, int32_t* rows, int32_t* token, int32_t* offsets,
+                               void* workspace, void* stream) {
+  if (T < 0 || E < 1 || E > SIXBIT_MAX_EXPERTS || k < 1 || k > SIXBIT_MAX_TOP_K ||
+      static_cast<int64_t>(T) * k > INT32_MAX || groups < 1 || groups > SIXBIT_MAX_GROUPS || E % groups != 0 ||
+      top_groups < 1 || top_groups > groups || k > top_groups * (E / groups))
+    return SIXBIT_ESHAPE;
+  if ((score != SIXBIT_SCORE_SOFTMAX && score != SIXBIT_SCORE_SIGMOID) || group_best < 1 || group_best > 2 ||
+      !std::isfinite(factor) || offsets == nullptr)
+    return SIXBIT_EINVAL;
+  if (T > 0 && ((logits == nullptr && logits_bf16 == nullptr) || experts == nullptr || weights == nullptr ||
+                rows == nullptr || token == nullptr ||
+                (workspace == nullptr && sixbit_moe_route_workspace_bytes(T, E) > 0)))
+    return SIXBIT_EINVAL;
+  for (const void* q : {static_cast<const void*>(logits), static_cast<const void*>(bias),
+                        static_cast<const void*>(experts), static_cast<const void*>(weights),
+                        static_cast<const void*>(rows), static_cast<const void*>(token),
+                        static_cast<const void*>(offsets), static_cast<const void*>(workspace)})
+    if (!aligned_to(q, 4)) return SIXBIT_EALIGN;
+  if (!aligned_to(logits_bf16, 2)) return SIXBIT_EALIGN;
+  const sixbit_status s = check_device();
+  if (s != SIXBIT_OK) return s;
+  RouteParams p{};
+  p.logits = logits;
+  p.logits_bf16 = logits_bf16;
+  p.bias = bias;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.score = score;
+  p.groups = groups;
+  p.top_groups = top_groups;
+  p.best = group_best;
+  p.renorm = renormalize != 0;
+  p.factor = factor;
+  p.experts = experts;
+  p.weights = weights;
+  p.rows = rows;
+  p.token = token;
+  p.offsets = offsets;
+  p.counts = static_cast<int32_t*>(workspace);
+  return cuda_status(launch_moe_route(p, static_cast<cudaStream_t>(stream)));
+}
+
+sixbit_status sixbit_moe_combine(const uint16_t* d, const float* d_f32, const int32_t* rows, const float* weights,
+                                 int T, int k, int R, int H, uint16_t* Y, float* Y_f32, int32_t* err_dev,
+                                 void* stream) {
+  if (T < 0 || k < 1 || k > SIXBIT_MAX_TOP_K || R < 0 || H < 1 || H > 1 << 20) return SIXBIT_ESHAPE;
+  if (T == 0) return SIXBIT_OK;
+  if ((R > 0 && d == nullptr && d_f32 == nullptr) || rows == nullptr || weights == nullptr ||
+      (Y == nullptr && Y_f32 == nullptr))
+    return SIXBIT_EINVAL;
+  if (!aligned_to(d, 2) || !aligned_to(d_f32, 4) || !aligned_to(rows, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(Y, 2) || !aligned_to(Y_f32, 4))
+    return SIXBIT_EALIGN;
+  const sixbit_status s = check_device();
+  if (s != SIXBIT_OK) return s;
+  CombineParams p{};
+  p.f32 = d_f32 != nullptr;
+  p.d = p.f32 ? static_cast<const void*>(d_f32) : d;
+  p.rows = rows;
+  p.weights = weights;
+  p.T = T;
+  p.k = k;
+  p.H = H;
+  p.R = R;
+  p.Y = Y_f32 != nullptr ? nullptr : Y;
+  p.Yf = Y_f32;
+  p.err = err_dev;
+  return cuda_status(launch_moe_combine(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sixbit_lowrank_workspace_bytes(int M, int K, int R) {
+  if (M <= 0 || K <= 0 || R <= 0) return 0;
+  return static_cast<size_t>(lowrank_splits(M, K)) * static_cast<size_t>(M) * static_cast<size_t>(R) * 4;
+}
+
+sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, const uint16_t* lr_a,
+                                 const uint16_t* lr_b, const float* alpha, const int32_t* ids, int L, int M, int N,
+                                 int K, int R, const uint16_t* base, const float* base_f32, const int32_t* mode_dev,
+                                 int epilogue, const uint16_t* residual, uint16_t* Y, float* Y_f32, void* workspace,
+                                 int32_t* err_dev, void* stream) {
+  if (epilogue != SIXBIT_EPI_NONE && epilogue != SIXBIT_EPI_GELU && epilogue != SIXBIT_EPI_RESIDUAL)
+    return SIXBIT_EINVAL;
+  if (M < 0 || M > INT32_MAX - 32 || N < 1 || N > 1 << 20 || K <= 0 || K % 128 != 0 || R < 16 ||
+      R > SIXBIT_MAX_RANK || R % 16 != 0 || L < 1)
+    return SIXBIT_ESHAPE;
+  if (base != nullptr && base_f32 != nullptr) return SIXBIT_EINVAL;
+  if (M == 0) return SIXBIT_OK;
+  if ((x_bf16 == nullptr && (A == nullptr || A->i8_codes == nullptr || A->row_scale == nullptr)) || lr_a == nullptr ||
+      lr_b == nullptr || ids == nullptr || (Y == nullptr && Y_f32 == nullptr) || workspace == nullptr ||
+      (epilogue == SIXBIT_EPI_RESIDUAL && residual == nullptr))
+    return SIXBIT_EINVAL;
+  if (!aligned16(x_bf16) || !aligned16(lr_a) || !aligned16(lr_b) || !aligned16(workspace) || !aligned_to(alpha, 4) ||
+      !aligned_to(ids, 4) || !aligned_to(base, 2) || !aligned_to(base_f32, 4) || !aligned_to(residual, 2) ||
+      !aligned_to(Y, 2) || !aligned_to(Y_f32, 4) ||
+      (x_bf16 == nullptr && (!aligned16(A->i8_codes) || !aligned_to(A->row_scale, 4))))
+    return SIXBIT_EALIGN;
+  const sixbit_status s = check_device();
+  if (s != SIXBIT_OK) return s;
+  LowRankParams p{};
+  p.x = x_bf16;
+  if (x_bf16 == nullptr) {
+    p.codes = A->i8_codes;
+    p.row_scale = A->row_scale;
+  }
+  p.a = lr_a;
+  p.b = lr_b;
+  p.alpha = alpha;
+  p.ids = ids;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.R = R;
+  p.L = L;
+  p.base = base;
+  p.base_f32 = base_f32;
+  p.epilogue = epilogue;
+  p.residual = epilogue == SIXBIT_EPI_RESIDUAL ? residual : nullptr;
+  p.Y = Y_f32 != nullptr ? nullptr : Y;
+  p.Yf = Y_f32;
+  p.v = static_cast<float*>(workspace);
+  p.mode_dev = mode_dev;
+  p.err = err_dev;
+  return cuda_status(launch_lowrank(p, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

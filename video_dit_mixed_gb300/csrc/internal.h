@@ -162,4 +162,82 @@ constexpr uint32_t tile_count(uint32_t tiles_t, uint32_t tiles_n) {
 cudaError_t launch_w4a8_grouped(const CUtensorMap& w, const TokenMaps& x, const RowsParams& p, bool narrow,
                                 cudaStream_t st);
 
+// The norms around a block's branch (sixbit_gated_rmsnorm_quant): y non-NULL
+// takes bf16 rows in place of codes and row_scale.
+struct GatedNormParams {
+  const uint16_t* x;
+  const uint16_t* res;   // or NULL
+  const float* w;        // [K], or NULL
+  const float* post_w;   // [K], or NULL: no norm of the branch
+  const float* gate;     // [S][K], or NULL
+  const float* scale;    // [S][K], or NULL
+  const float* shift;    // [S][K], or NULL
+  const int32_t* segment;  // [M], or NULL: runs of rows_per_seg rows
+  float res_scale, eps;
+  int M, K, S, rows_per_seg;
+  const int32_t* mode_dev;
+  uint16_t* sum_out;     // or NULL
+  uint16_t* y;
+  int8_t* codes;
+  float* row_scale;
+  int32_t* err;
+};
+cudaError_t launch_gated_norm(const GatedNormParams& g, int b, cudaStream_t st);
+
+// Routing (sixbit_moe_route).  counts: workspace, [kRouteRuns][E].
+constexpr int kRouteTurn = 32;   // tokens of a turn; up to these one CTA does all and needs no workspace
+constexpr int kRouteRuns = 152;  // runs of tokens, a CTA each: one an SM
+struct RouteParams {
+  const float* logits;           // [T][E], or
+  const uint16_t* logits_bf16;
+  const float* bias;             // [E], or NULL
+  int T, E, k, score, groups, top_groups, best, renorm;
+  float factor;
+  int32_t* experts;              // [T][k]
+  float* weights;                // [T][k]
+  int32_t* rows;                 // [T][k]
+  int32_t* token;                // [T k]
+  int32_t* offsets;              // [E + 1]
+  int32_t* counts;
+  int tokens_per_cta;            // set by the launch
+};
+cudaError_t launch_moe_route(RouteParams p, cudaStream_t st);
+
+// The experts' weighted sum (sixbit_moe_combine).
+struct CombineParams {
+  const void* d;                 // [R][H] bf16, or FP32
+  int f32;
+  const int32_t* rows;           // [T][k]
+  const float* weights;          // [T][k]
+  int T, k, H, R;
+  uint16_t* Y;
+  float* Yf;
+  int32_t* err;
+};
+cudaError_t launch_moe_combine(const CombineParams& p, cudaStream_t st);
+
+// Low-rank adapters (sixbit_lowrank_add).
+struct LowRankParams {
+  const int8_t* codes;           // [M][K] with row_scale [M], or
+  const float* row_scale;
+  const uint16_t* x;             // bf16 [M][K]
+  const uint16_t* a;             // [L][R][K]
+  const uint16_t* b;             // [L][N][R]
+  const float* alpha;            // [L], or NULL
+  const int32_t* ids;            // [M]
+  int M, N, K, R, L;
+  const float* base_f32;         // [M][N], or
+  const uint16_t* base;          // bf16, or neither
+  int epilogue;
+  const uint16_t* residual;
+  uint16_t* Y;
+  float* Yf;
+  float* v;                      // workspace: [splits][M][R]
+  const int32_t* mode_dev;
+  int32_t* err;
+  int splits, tiles_per_cta;     // set by the launch
+};
+int lowrank_splits(int M, int K);
+cudaError_t launch_lowrank(LowRankParams p, cudaStream_t st);
+
 }  // namespace sixbit

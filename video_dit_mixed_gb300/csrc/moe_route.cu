@@ -1,0 +1,454 @@
+// Routing of tokens to experts: each token's top-k experts by score, their
+// weights, and the counting sort of the T k choices by expert that the grouped
+// product's offsets describe.
+//
+//   p = softmax(l) or sigmoid(l),  key = p + bias
+//   groups of consecutive experts are ranked by the sum of their one or two
+//   largest keys, and only experts of the best ones can be chosen
+//   the k largest keys, the lower number first among equals
+//   w = p of the chosen, divided by their sum or not, times a factor
+//
+// Both scores rise with the logit, so without a bias the experts are compared by
+// their logits, exactly.  Keys and groups' sums are compared in FP32 where they
+// are further apart than FP32 can be wrong, and the row is done again in FP64
+// where two that matter are not (about one row in a thousand), so that a choice
+// is that of FP64 without its rate (GB300 issues an FP64 instruction of a warp
+// every 16 cycles an SM).  A NaN compares above everything.
+//
+// A warp takes a token, expert e in lane e % 32.  A CTA takes a run of tokens, 32
+// at a time: the choices set one bit for each token in a word for each expert, so
+// that a choice's rank among the run's is a count of bits below its own, whatever
+// order the warps came in.  The runs' counts go to the workspace, and a second
+// kernel adds what lies before each run (a single run needs none).
+#include <cstdint>
+
+#include "common.cuh"
+#include "ctx_cache.h"
+#include "internal.h"
+
+namespace sixbit {
+namespace route {
+
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kBlock = kRouteTurn;  // tokens of a turn: bits of a word
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// Bits in the order of the values; a NaN above all, an absent expert (0) below.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  if (v != v) return 0xFFFFFFFFu;
+  const uint32_t b = __float_as_uint(v + 0.f);  // (-0 is 0)
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+  if (v != v) return ~0ull;
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return b ^ ((b >> 63) ? ~0ull : 0x8000000000000000ull);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float((o >> 31) ? o ^ 0x80000000u : ~o);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+template <typename F>
+struct OrdOf;
+template <>
+struct OrdOf<float> {
+  using type = uint32_t;
+};
+template <>
+struct OrdOf<double> {
+  using type = uint64_t;
+};
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+
+// The k largest of the warp's keys (N a lane, 0: absent), lower numbers first
+// among equals: lane j's `mine` is the j-th expert.  CHECK: true if no two
+// consecutive ones, the last chosen and the next included, are within `tol` +
+// `rel` |key|.
+template <int N, bool CHECK, typename O>
+__device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, int* mine) {
+  const int lane = threadIdx.x & 31;
+  O best = 0;
+  int slot = 0;
+  auto refresh = [&] {
+    best = 0;
+    slot = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        slot = i;
+      }
+  };
+  refresh();
+  bool clear = true;
+  float last = 0.f;
+  const int turns = CHECK ? k + 1 : k;
+  for (int j = 0; j < turns; ++j) {
+    const O top = warp_max(best);
+    if (CHECK) {
+      if (top == 0) break;  // (nothing is left beyond the last)
+      const float v = value_of(static_cast<uint32_t>(top));
+      if (j > 0 && !(last - v > tol + rel * fabsf(last))) clear = false;
+      last = v;
+      if (j == k) break;
+    }
+    const unsigned who = best == top ? static_cast<unsigned>(lane + 32 * slot) : kAll;
+    const int e = static_cast<int>(__reduce_min_sync(kAll, who));
+    if (lane == j) *mine = e;
+    if ((e & 31) == lane) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i == (e >> 5)) key[i] = 0;
+      refresh();
+    }
+  }
+  return clear;
+}
+
+// Bits of the groups that are kept.  keys: the warp's E keys in shared memory.
+template <bool CHECK, typename F>
+__device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys, float tol, float rel, uint32_t* kept) {
+  using O = typename OrdOf<F>::type;
+  const int lane = threadIdx.x & 31, size = p.E / p.groups;
+  O score = 0;
+  __syncwarp();
+  if (lane < p.groups) {
+    O a = 0, b = 0;  // the two largest; a lane starts at its own number, so that lanes read different banks
+    F fa = 0, fb = 0;
+    int i = lane % size;
+    for (int n = 0; n < size; ++n) {
+      const F v = keys[lane * size + i];
+      const O o = ordered(v);
+      if (o > a) {
+        b = a, fb = fa;
+        a = o, fa = v;
+      } else if (o > b) {
+        b = o, fb = v;
+      }
+      i = i + 1 == size ? 0 : i + 1;
+    }
+    score = ordered(p.best > 1 && size > 1 ? fa + fb : fa);
+  }
+  uint32_t bits = 0;
+  O top = 0;
+  for (int j = 0; j < p.top_groups; ++j) {
+    top = warp_max(score);
+    const int g = __ffs(__ballot_sync(kAll, score == top)) - 1;
+    bits |= 1u << g;
+    if (lane == g) score = 0;
+  }
+  bool clear = true;
+  if (CHECK && p.top_groups < p.groups) {  // (which of the kept comes first does not matter)
+    const float v = value_of(static_cast<uint32_t>(top)), next = value_of(static_cast<uint32_t>(warp_max(score)));
+    clear = v - next > 2.f * tol + rel * fabsf(v);
+  }
+  __syncwarp();
+  *kept = bits;
+  return clear;
+}
+
+// One token's experts (lane j: the j-th), from its logits l.  F: the type that
+// keys are computed in; CHECK: false is returned where F is too narrow.
+template <int N, bool CHECK, typename F>
+__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], float lmax, F* keys, int* mine) {
+  using O = typename OrdOf<F>::type;
+  const int lane = threadIdx.x & 31;
+  const bool by_logit = p.bias == nullptr;
+  O key[N];
+  F v[N];
+  float tol = 0.f;
+  if (!by_logit || p.groups > 1) {
+    if (p.score == SIXBIT_SCORE_SOFTMAX) {
+      F sum = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[i] = lane + 32 * i < p.E && l[i] != -INFINITY ? exp_of(static_cast<F>(l[i]) - static_cast<F>(lmax)) : F(0);
+        sum += v[i];
+      }
+      sum = warp_sum(sum);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = sum == F(0) ? F(0) : v[i] / sum;
+      // a term is 4 units off by its exponential and 0.4 by its argument, the sum by that and its N + 5 additions
+      tol = 0x1p-24f * 2.f * (N + 18);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = F(1) / (F(1) + exp_of(-static_cast<F>(l[i])));
+      tol = 0x1p-24f * 2.f * 8;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = lane + 32 * i;
+      if (p.bias != nullptr && e < p.E) v[i] += static_cast<F>(__ldg(p.bias + e));
+    }
+  }
+  const float rel = 0x1p-24f * 8;
+  bool clear = true;
+  uint32_t kept = kAll;
+  if (p.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 32 * i < p.E) keys[lane + 32 * i] = v[i];
+    clear = keep_groups<CHECK>(p, keys, tol, rel, &kept);
+  }
+  const int size = p.E / p.groups;
+  if (by_logit) {
+    uint32_t lk[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = lane + 32 * i;
+      lk[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(l[i]) : 0u;
+    }
+    top_k<N, false>(lk, p.k, 0.f, 0.f, mine);
+    return clear;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(v[i]) : O(0);
+  }
+  return top_k<N, CHECK>(key, p.k, tol, rel, mine) && clear;
+}
+
+__device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e) {
+  const size_t at = static_cast<size_t>(t) * p.E + e;
+  return p.logits_bf16 != nullptr ? __uint_as_float(static_cast<uint32_t>(__ldg(p.logits_bf16 + at)) << 16)
+                                  : __ldg(p.logits + at);
+}
+
+// A call of its own: its registers (two a key) are not the fast path's.
+template <int N>
+__device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax, double* keys) {
+  float l[N];
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i) l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
+  int mine = 0;
+  choose<N, false, double>(p, l, lmax, keys, &mine);
+  return mine;
+}
+
+// Lane j's weight of the j-th expert.
+template <int N>
+__device__ __forceinline__ float weight_of(const RouteParams& p, const float (&l)[N], float lmax, float mine, bool live) {
+  const int lane = threadIdx.x & 31;
+  float w;
+  if (p.renorm) {  // relative to the largest chosen, so that small scores keep their ratio
+    float m = live ? mine : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    if (p.score == SIXBIT_SCORE_SIGMOID) {
+      m = fminf(m, 0.f);
+      // e^(l - m) / (1 + e^l); above 0 (m is 0 then) without the large exponential
+      w = mine > 0.f ? 1.f / (1.f + expf(-mine)) : expf(mine - m) / (1.f + expf(mine));
+    } else {
+      w = expf(mine - m);
+    }
+    if (mine == -INFINITY || !live) w = 0.f;
+    const float sum = warp_sum(w);
+    w = sum == 0.f ? 0.f : w / sum;
+  } else if (p.score == SIXBIT_SCORE_SIGMOID) {
+    w = 1.f / (1.f + expf(-mine));
+  } else {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += lane + 32 * i < p.E && l[i] != -INFINITY ? expf(l[i] - lmax) : 0.f;
+    sum = warp_sum(sum);
+    w = mine == -INFINITY ? 0.f * sum : expf(mine - lmax) / sum;
+  }
+  // (a NaN or an infinite logit makes every probability of its row NaN)
+  if (p.score == SIXBIT_SCORE_SOFTMAX && !(lmax < INFINITY)) w = __uint_as_float(0x7FC00000u);
+  return w * p.factor;
+}
+
+// Exclusive prefix sums of v[0 .. n) in shared memory, n <= 2 kThreads; v[n]
+// becomes the total.
+__device__ __forceinline__ void scan(int* v, int n, int* part) {
+  const int i = 2 * threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int a = i < n ? v[i] : 0, b = i + 1 < n ? v[i + 1] : 0;
+  int s = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(kAll, s, o);
+    if (lane >= o) s += up;
+  }
+  if (lane == 31) part[warp] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  s += before - a - b;
+  if (i < n) v[i] = s;
+  if (i + 1 < n) v[i + 1] = s + a;
+  if (threadIdx.x == 0) v[n] = all;
+  __syncthreads();
+}
+
+// Shared memory: run [E + 1], mask [E], chosen [kBlock k], then with groups the
+// warps' keys, E doubles each.
+__host__ __device__ constexpr size_t keys_at(int E, int k) {
+  return ((static_cast<size_t>(E) * 2 + 1 + kBlock * k) * 4 + 7) / 8 * 8;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ RouteParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int part[kWarps];
+  int* run = reinterpret_cast<int*>(smem);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(run + p.E + 1);
+  int* chosen = reinterpret_cast<int*>(mask + p.E);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double* keys = reinterpret_cast<double*>(smem + keys_at(p.E, p.k)) + static_cast<size_t>(p.groups > 1 ? warp : 0) * p.E;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    run[e] = 0;
+    mask[e] = 0;
+  }
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tokens_per_cta;
+  const int64_t t1 = min(t0 + p.tokens_per_cta, static_cast<int64_t>(p.T));
+  for (int64_t tb = t0; tb < t1; tb += kBlock) {
+    for (int j = warp; j < kBlock && tb + j < t1; j += kWarps) {
+      const int64_t t = tb + j;
+      float l[N];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
+        top = max(top, ordered(l[i]));
+      }
+      const float lmax = value_of(warp_max(top));
+      int mine = 0;
+      if (!choose<N, true, float>(p, l, lmax, reinterpret_cast<float*>(keys), &mine))
+        mine = choose64<N>(p, t, lmax, keys);
+      const bool live = lane < p.k;
+      const float w = weight_of<N>(p, l, lmax, live ? logit_at(p, t, mine) : -INFINITY, live);
+      if (live) {
+        const size_t at = static_cast<size_t>(t) * p.k + lane;
+        p.experts[at] = mine;
+        p.weights[at] = w;
+        chosen[j * p.k + lane] = mine;
+        atomicOr(&mask[mine], 1u << j);
+      }
+    }
+    __syncthreads();
+    const int live = static_cast<int>(min(static_cast<int64_t>(kBlock), t1 - tb)) * p.k;
+    for (int i = threadIdx.x; i < live; i += kThreads) {
+      const int e = chosen[i];
+      p.rows[static_cast<size_t>(tb) * p.k + i] = run[e] + __popc(mask[e] & ((1u << (i / p.k)) - 1));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+      run[e] += __popc(mask[e]);
+      mask[e] = 0;
+    }
+    __syncthreads();
+  }
+  if (gridDim.x > 1) {
+    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.E + e] = run[e];
+    return;
+  }
+  scan(run, p.E, part);
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = run[e];
+  for (int i = threadIdx.x; i < p.T * p.k; i += kThreads) {  // (this thread wrote rows[i]: one turn of 32 tokens)
+    const int r = p.rows[i] + run[p.experts[i]];
+    p.rows[i] = r;
+    p.token[r] = i / p.k;
+  }
+}
+
+// Adds what lies before each run: the experts' offsets and the earlier runs' counts.
+__global__ void __launch_bounds__(kThreads) place_kernel(const RouteParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int part[kWarps];
+  int* all = reinterpret_cast<int*>(smem);  // [E + 1]
+  int* before = all + p.E + 1;              // [E]
+  for (int e = threadIdx.x; e < p.E; e += kThreads) all[e] = before[e] = 0;
+  __syncthreads();
+  const int runs = gridDim.x, me = blockIdx.x;
+  const int lanes = p.E < kThreads ? kThreads / p.E : 1;  // threads of an expert
+  for (int i = threadIdx.x; i < p.E * lanes; i += kThreads) {
+    const int e = i % p.E, first = i / p.E;
+    int a = 0, b = 0;
+    for (int c = first; c < runs; c += lanes) {
+      const int n = p.counts[static_cast<size_t>(c) * p.E + e];
+      a += n;
+      if (c < me) b += n;
+    }
+    atomicAdd(&all[e], a);
+    atomicAdd(&before[e], b);
+  }
+  __syncthreads();
+  scan(all, p.E, part);
+  if (me == 0)
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = all[e];
+  const int64_t t0 = static_cast<int64_t>(me) * p.tokens_per_cta;
+  const int64_t t1 = min(t0 + p.tokens_per_cta, static_cast<int64_t>(p.T));
+  for (int64_t i = t0 * p.k + threadIdx.x; i < t1 * p.k; i += kThreads) {
+    const int e = p.experts[i], r = p.rows[i] + all[e] + before[e];
+    p.rows[i] = r;
+    p.token[r] = static_cast<int>(i / p.k);
+  }
+}
+
+template <int N>
+cudaError_t launch(const RouteParams& p, int ctas, cudaStream_t st) {
+  size_t smem = keys_at(p.E, p.k) + (p.groups > 1 ? static_cast<size_t>(kWarps) * p.E * 8 : 0);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = set_smem_once<choose_kernel<N>>(200 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  note_launch();
+  choose_kernel<N><<<ctas, kThreads, smem, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (static_cast<size_t>(p.E) * 2 + 1) * 4;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, place_kernel, p);
+}
+
+}  // namespace route
+
+cudaError_t launch_moe_route(RouteParams p, cudaStream_t st) {
+  // one run up to a turn of 32 tokens, else up to kRouteRuns equal ones of whole rounds of the warps
+  int ctas = 1;
+  p.tokens_per_cta = p.T;
+  if (p.T > route::kBlock) {
+    const int64_t per = (static_cast<int64_t>(p.T) + kRouteRuns - 1) / kRouteRuns;
+    p.tokens_per_cta = static_cast<int>((per + route::kWarps - 1) / route::kWarps * route::kWarps);
+    ctas = static_cast<int>((static_cast<int64_t>(p.T) + p.tokens_per_cta - 1) / p.tokens_per_cta);
+  }
+  if (p.E <= 32) return route::launch<1>(p, ctas, st);
+  if (p.E <= 64) return route::launch<2>(p, ctas, st);
+  if (p.E <= 128) return route::launch<4>(p, ctas, st);
+  if (p.E <= 256) return route::launch<8>(p, ctas, st);
+  if (p.E <= 512) return route::launch<16>(p, ctas, st);
+  return route::launch<32>(p, ctas, st);
+}
+
+}  // namespace sixbit

@@ -8,12 +8,13 @@ CUDA kernels; there is no CPU path.
 from __future__ import annotations
 
 import ctypes as C
+from typing import NamedTuple
 
 import torch
 
 from . import abi
-from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MAX_EXPERTS, MODE_BF16, MODE_INT8, MODE_NVFP4,  # noqa: F401
-                  MODE_SKIP, QGEMV_MAX_ROWS, DitBlocks, PolicyCfg, PolicyState, QAct, Stats, Weights, check, lib)
+from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MAX_EXPERTS, MAX_GROUPS, MAX_RANK, MAX_TOP_K,  # noqa: F401
+                  MODE_BF16, MODE_INT8, MODE_NVFP4, MODE_SKIP, QGEMV_MAX_ROWS, SCORE_SIGMOID, SCORE_SOFTMAX, DitBlocks, PolicyCfg, PolicyState, QAct, Stats, Weights, check, lib)
 
 _lib = lib()
 
@@ -445,6 +446,277 @@ def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogu
     if experts is None:
         raise ValueError("experts' weights expected (Int4Weights with [E, N, K/2] codes)")
     return _w4a8(a, w, experts, offsets, epilogue, residual, out, out_f32, mode_dev, err, stream, ws)
+
+
+# ---- what stands around those products --------------------------------------
+
+def _gpu(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on the GPU, not on {t.device}")
+    return dev
+
+
+def gated_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                        post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None, shift: torch.Tensor | None = None,
+                        segment: torch.Tensor | None = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                        had_block: int = 0, quantize: bool = True, out=None, sum_out=None, mode_dev=None, err=None,
+                        stream=None):
+    """h = residual_scale residual + gate u, u = x or (with post_weight) its RMS norm times post_weight; then
+    y = norm(h) weight (1 + scale) + shift, rotation by had_block (0: none), INT8 codes and row scales
+    (sixbit_gated_rmsnorm_quant); with quantize=False bf16 y instead (had_block 0).
+
+    x, residual: bf16 [M, K]; weight, post_weight: float32 [K]; gate, scale, shift: float32 [K], or [S, K] for S
+    segments of rows: segment int32 [M] names each row's, by default they are S equal runs of rows.  Returns (result,
+    h): QActTensors or bf16 [M, K] (in `out`), and bf16(h) (in sum_out, which may be x or residual)."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: [M, K] expected, got {tuple(shape)}")
+    m, k = shape
+    dev = _gpu(x, "x")
+    st = _stream_on(dev, stream)
+    px = _ptr(x, "x", _BF16, shape, dev)
+    pr = None if residual is None else _ptr(residual, "residual", _BF16, shape, dev)
+    pw = None if weight is None else _ptr(weight, "weight", _F32, (k,), dev)
+    pp = None if post_weight is None else _ptr(post_weight, "post_weight", _F32, (k,), dev)
+    s, mods = None, [None, None, None]
+    for i, v in enumerate((gate, scale, shift)):
+        if v is not None:
+            if s is None:
+                s = v.shape[0] if v.dim() == 2 else 1
+            mods[i] = _ptr(v, ("gate", "scale", "shift")[i], _F32, (s, k) if v.dim() == 2 else (k,), dev)
+            if v.dim() != 2 and s != 1:
+                raise ValueError(f"gate, scale and shift of {s} segments or of one")
+    pseg = None
+    if segment is not None:
+        pseg = _ptr(segment, "segment", _I32, (m,), dev)
+        if s is None:
+            pseg = None  # (nothing is modulated)
+    elif s is not None and s > 1 and m % s:
+        raise ValueError(f"{m} rows are not {s} equal segments: segment expected")
+    if sum_out is None:
+        sum_out = _empty(shape, _BF16, x.device, stream)
+        ps = sum_out.data_ptr()
+    else:
+        ps = _ptr(sum_out, "sum_out", _BF16, shape, dev)
+    py = None
+    qa = None
+    if not quantize:
+        if out is None:
+            out = _empty(shape, _BF16, x.device, stream)
+            py = out.data_ptr()
+        else:
+            py = _ptr(out, "out", _BF16, shape, dev)
+    elif out is None:
+        codes, rs = _empty(shape, _I8, x.device, stream), _empty((m,), _F32, x.device, stream)
+        out = int8_act(codes, rs)
+        qa = QAct(None, None, None, None, codes.data_ptr(), rs.data_ptr(), None)
+    else:
+        qa = QAct(None, None, None, None, _ptr(out.i8_codes, "out.i8_codes", _I8, shape, dev),
+                  _ptr(out.row_scale, "out.row_scale", _F32, (m,), dev), None)
+    if m == 0:
+        return out, sum_out
+    status = _lib.sixbit_gated_rmsnorm_quant(px, pr, residual_scale, pw, pp, mods[0], mods[1], mods[2], pseg,
+                                             s if s is not None else 1, m, k, eps, had_block,
+                                             None if mode_dev is None else _word(mode_dev, "mode_dev", dev), ps, py,
+                                             None if qa is None else C.byref(qa),
+                                             None if err is None else _word(err, "err", dev), st)
+    if status:
+        check(status, "gated_rmsnorm_quant")
+    return out, sum_out
+
+
+class Routing(NamedTuple):
+    """moe_route's result: each token's experts int32 [T, k] and weights float32 [T, k], the row of each choice int32
+    [T, k] in the order that qgemm_grouped takes, the token of each row int32 [T k], and the experts' offsets int32
+    [E + 1]."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    rows: torch.Tensor
+    token: torch.Tensor
+    offsets: torch.Tensor
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
+              groups: int = 1, top_groups: int = 1, group_best: int = 2, renormalize: bool = True, scale: float = 1.0,
+              stream=None) -> Routing:
+    """Routing of T tokens to top_k of E experts (sixbit_moe_route).
+
+    logits: float32 or bf16 [T, E].  score: SCORE_SOFTMAX or SCORE_SIGMOID; bias: float32 [E], added for the choice and
+    not to the weights.  With groups > 1 only experts of the top_groups groups are chosen, by the sum of a group's
+    group_best (1 or 2) largest keys.  Equal keys go to the lower number.  The weights are the chosen experts' scores,
+    divided by their sum (renormalize), times scale."""
+    shape = logits.shape
+    if len(shape) != 2:
+        raise ValueError(f"logits: [T, E] expected, got {tuple(shape)}")
+    t, e = shape
+    dev = _gpu(logits, "logits")
+    st = _stream_on(dev, stream)
+    if not 1 <= top_k <= min(MAX_TOP_K, e):
+        raise ValueError(f"1 <= top_k <= {min(MAX_TOP_K, e)} expected, got {top_k}")
+    pl = ph = None
+    if logits.dtype is _BF16:
+        ph = _ptr(logits, "logits", _BF16, shape, dev)
+    else:
+        pl = _ptr(logits, "logits", _F32, shape, dev)
+    pb = None if bias is None else _ptr(bias, "bias", _F32, (e,), dev)
+    n = t * top_k
+    # one allocation: experts, weights, rows, token, offsets, and the workspace behind them
+    need = (int(_lib.sixbit_moe_route_workspace_bytes(t, e)) + 3) // 4
+    buf = _empty((4 * n + e + 1 + need,), _I32, logits.device, stream)
+    at = buf.data_ptr()
+    status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, bool(renormalize),
+                                   scale, at, at + 4 * n, at + 8 * n, at + 12 * n, at + 16 * n,
+                                   at + 16 * n + 4 * (e + 1) if need else None, st)
+    if status:
+        check(status, "moe_route")
+    experts, weights, rows, token, offsets = buf[:4 * n + e + 1].split((n, n, n, n, e + 1))
+    return Routing(experts.view(t, top_k), weights.view(_F32).view(t, top_k), rows.view(t, top_k), token, offsets)
+
+
+def moe_combine(d: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None, out_f32: bool = False, err=None,
+                stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] d[rows[t, j]] in FP32 (sixbit_moe_combine).  d: float32 or bf16 [R, H]; rows: int32
+    [T, k] (-1: none); weights: float32 [T, k].  Returns bf16 [T, H], or float32 with out_f32 or a float32 `out`."""
+    if d.dim() != 2 or rows.dim() != 2:
+        raise ValueError(f"d [R, H] and rows [T, k] expected, got {tuple(d.shape)} and {tuple(rows.shape)}")
+    r, h = d.shape
+    t, k = shape = rows.shape
+    dev = _gpu(d, "d")
+    st = _stream_on(dev, stream)
+    pd = pf = None
+    if d.dtype is _F32:
+        pf = _ptr(d, "d", _F32, d.shape, dev)
+    else:
+        pd = _ptr(d, "d", _BF16, d.shape, dev)
+    pr, pw = _ptr(rows, "rows", _I32, shape, dev), _ptr(weights, "weights", _F32, shape, dev)
+    py = pyf = None
+    if out is None:
+        out = _empty((t, h), _F32 if out_f32 else _BF16, d.device, stream)
+        if out_f32:
+            pyf = out.data_ptr()
+        else:
+            py = out.data_ptr()
+    elif out.dtype is _F32:
+        pyf = _ptr(out, "out", _F32, (t, h), dev)
+    else:
+        py = _ptr(out, "out", _BF16, (t, h), dev)
+    status = _lib.sixbit_moe_combine(pd, pf, pr, pw, t, k, r, h, py, pyf,
+                                     None if err is None else _word(err, "err", dev), st)
+    if status:
+        check(status, "moe_combine")
+    return out
+
+
+class LowRank:
+    """L adapters of one projection [N, K]: a bf16 [L, R, K], b bf16 [L, N, R], alpha float32 [L] or None (1).  R is a
+    multiple of 16 up to MAX_RANK.  Beside INT8 codes, a is in the codes' rotated basis (pack_lowrank)."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, alpha: torch.Tensor | None = None):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError(f"a [L, R, K] and b [L, N, R] expected, got {tuple(a.shape)} and {tuple(b.shape)}")
+        self.a, self.b, self.alpha = a, b, alpha
+        self.count, self.rank, self.k = a.shape
+        self.n = b.shape[1]
+
+
+def pack_lowrank(a: torch.Tensor, b: torch.Tensor, alpha: torch.Tensor | None, had_block: int, stream=None) -> LowRank:
+    """Adapters as they were trained (a bf16 [L, R, K], b bf16 [L, N, R], any R up to MAX_RANK) for a projection whose
+    activations are rotated by had_block (0: not rotated): a is rotated in FP32 and rounded to bf16, the ranks are
+    padded with zeros to a multiple of 16."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"a [L, R, K] and b [L, N, R] expected, got {tuple(a.shape)} and {tuple(b.shape)}")
+    count, rank, k = a.shape
+    n = b.shape[1]
+    dev = _gpu(a, "a")
+    _ptr(a, "a", _BF16, a.shape, dev)
+    _ptr(b, "b", _BF16, b.shape, dev)
+    if not 1 <= rank <= MAX_RANK:
+        raise ValueError(f"1 <= R <= {MAX_RANK} expected, got {rank}")
+    st = _stream_on(dev, stream)
+    padded = (rank + 15) // 16 * 16
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(a.device)):
+        pa = torch.zeros((count, padded, k), dtype=_BF16, device=a.device)
+        pb = torch.zeros((count, n, padded), dtype=_BF16, device=a.device)
+        pb[:, :, :rank] = b
+        if had_block:
+            rows = a.view(count * rank, k)
+            q = QActTensors(count * rank, k, a.device, nvfp4=False, rotated=True)
+            ca = q.c()
+            check(_lib.sixbit_hadamard_quant(_p(rows), count * rank, k, had_block, MODE_INT8, None, None, C.byref(ca),
+                                             None, C.c_void_p(st)), "pack_lowrank")
+            pa[:, :rank] = q.rotated.view(count, rank, k)
+        else:
+            pa[:, :rank] = a
+    return LowRank(pa, pb, alpha)
+
+
+def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = None, epilogue: int = EPI_NONE,
+                residual=None, out=None, out_f32: bool = False, mode_dev=None, err=None, stream=None, ws=None):
+    """out[m] = epilogue(base[m] + alpha[l] B_l (A_l x[m])), l = ids[m] (sixbit_lowrank_add).
+
+    x: INT8 QActTensors or bf16 [M, K]; ids: int32 [M] on the GPU, -1 for rows without an adapter; base: the shared
+    projection's result, float32 or bf16 [M, N], or None.  `out` may be base or residual.  ws:
+    lowrank_workspace_bytes(M, K, R) bytes, allocated for the call by default.  Returns bf16 [M, N], or float32 with
+    out_f32 or a float32 `out`."""
+    if isinstance(x, torch.Tensor):
+        dev = _gpu(x, "x")
+        shape, device = x.shape, x.device
+        if len(shape) != 2:
+            raise ValueError(f"x: [M, K] expected, got {tuple(shape)}")
+        ca, px = None, _ptr(x, "x", _BF16, shape, dev)
+    else:
+        codes = x.i8_codes
+        if codes is None or codes.dim() != 2:
+            raise ValueError("INT8 activations [M, K] expected")
+        dev = _gpu(codes, "i8_codes")
+        shape, device, px = codes.shape, codes.device, None
+        ca = C.byref(QAct(None, None, None, None, _ptr(codes, "i8_codes", _I8, shape, dev),
+                          _ptr(x.row_scale, "row_scale", _F32, (shape[0],), dev), None))
+    m, k = shape
+    n, r, count = w.n, w.rank, w.count
+    if w.k != k:
+        raise ValueError(f"activations have {k} inputs, the adapters {w.k}")
+    st = _stream_on(dev, stream)
+    pa, pb = _ptr(w.a, "a", _BF16, (count, r, k), dev), _ptr(w.b, "b", _BF16, (count, n, r), dev)
+    pal = None if w.alpha is None else _ptr(w.alpha, "alpha", _F32, (count,), dev)
+    pi = _ptr(ids, "ids", _I32, (m,), dev)
+    p0 = p0f = py = pf = pr = None
+    if base is not None:
+        if base.dtype is _F32:
+            p0f = _ptr(base, "base", _F32, (m, n), dev)
+        else:
+            p0 = _ptr(base, "base", _BF16, (m, n), dev)
+    if out is None:
+        out = _empty((m, n), _F32 if out_f32 else _BF16, device, stream)
+        if out_f32:
+            pf = out.data_ptr()
+        else:
+            py = out.data_ptr()
+    elif out.dtype is _F32:
+        pf = _ptr(out, "out", _F32, (m, n), dev)
+    else:
+        py = _ptr(out, "out", _BF16, (m, n), dev)
+    if residual is not None:
+        if epilogue != EPI_RESIDUAL:
+            raise ValueError("a residual without the residual epilogue")
+        pr = _ptr(residual, "residual", _BF16, (m, n), dev)
+    need = int(_lib.sixbit_lowrank_workspace_bytes(m, k, r))
+    if ws is None:
+        ws = _empty((need,), _U8, device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
+    status = _lib.sixbit_lowrank_add(ca, px, pa, pb, pal, pi, count, m, n, k, r, p0, p0f,
+                                     None if mode_dev is None else _word(mode_dev, "mode_dev", dev), epilogue, pr, py,
+                                     pf, ws.data_ptr(), None if err is None else _word(err, "err", dev), st)
+    if status:
+        check(status, "lowrank_add")
+    return out
+
+
+def lowrank_workspace_bytes(m: int, k: int, r: int) -> int:
+    return int(_lib.sixbit_lowrank_workspace_bytes(m, k, r))
 
 
 def check_err(err: torch.Tensor, what: str, stream=None) -> None:
