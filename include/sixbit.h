@@ -627,8 +627,8 @@ size_t sixbit_moe_route_workspace_bytes(int T, int E);
 sixbit_status sixbit_moe_combine(const uint16_t* d, const float* d_f32, const int32_t* rows, const float* weights,
                                  int T, int k, int R, int H, uint16_t* Y, float* Y_f32, int32_t* err_dev, void* stream);
 
-/* Ranks of an adapter sixbit_lowrank_add takes at most. */
-enum { SIXBIT_MAX_RANK = 128 };
+/* Ranks of an adapter, and adapters, sixbit_lowrank_add takes at most. */
+enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 32768 };
 
 /*
  * Low-rank adapters of many requests beside a projection they share:
@@ -643,9 +643,9 @@ enum { SIXBIT_MAX_RANK = 128 };
  * Epilogues as for sixbit_qgemm: NONE, GELU, RESIDUAL (+ residual [M, N] bf16).
  * Y [M, N] bf16, or Y_f32 when it is non-NULL; Y may be base or residual, Y_f32
  * base_f32 (in place).  M >= 0 (0: nothing is enqueued), 1 <= N <= 2^20,
- * K % 128 == 0, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, L >= 1.  Codes, x_bf16,
+ * K % 128 == 0, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, 1 <= L <= SIXBIT_MAX_ADAPTERS.  Codes, x_bf16,
  * lr_a, lr_b and the workspace 16-byte aligned, the others to their type.
- * workspace: device memory of sixbit_lowrank_workspace_bytes(M, K, R) bytes,
+ * workspace: device memory of sixbit_lowrank_workspace_bytes(M, R) bytes,
  * scratch.  With mode_dev, runs only when the mode word is INT8.
  */
 sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, const uint16_t* lr_a,
@@ -655,7 +655,7 @@ sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, c
                                  int32_t* err_dev, void* stream);
 
 /* Bytes of the workspace sixbit_lowrank_add needs. */
-size_t sixbit_lowrank_workspace_bytes(int M, int K, int R);
+size_t sixbit_lowrank_workspace_bytes(int M, int R);
 
 /* ---- device-decided branches in a captured CUDA graph ------------------- */
 

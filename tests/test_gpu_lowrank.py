@@ -206,7 +206,7 @@ def test_in_place_alignment_streams_modes(ops):
         mode.fill_(ops.MODE_INT8)
         c.call(ops, out=out, mode_dev=mode)
         assert torch.equal(out, want)
-        ws = torch.full((ops.lowrank_workspace_bytes(m, 256, 32),), 255, dtype=torch.uint8, device="cuda")
+        ws = torch.full((ops.lowrank_workspace_bytes(m, 32),), 255, dtype=torch.uint8, device="cuda")
         assert torch.equal(c.call(ops, ws=ws), want)
 
 

@@ -13,7 +13,7 @@ FLAG_REFRESH, FLAG_PDR, FLAG_POSTSKIP, FLAG_NEAR = 1 << 8, 1 << 9, 1 << 10, 1 <<
 EPI_NONE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 QGEMV_MAX_ROWS, MAX_EXPERTS = 32, 1024
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
-MAX_TOP_K, MAX_GROUPS, MAX_RANK = 32, 32, 128
+MAX_TOP_K, MAX_GROUPS, MAX_RANK, MAX_ADAPTERS = 32, 32, 128, 32768
 MODE_NAMES = {MODE_NVFP4: "NVFP4", MODE_INT8: "INT8", MODE_BF16: "BF16", MODE_SKIP: "SKIP"}
 
 
@@ -89,7 +89,7 @@ EXPORTS = {
     "sixbit_moe_combine": (C.c_int, [c_p, c_p, c_p, c_p, C.c_int, C.c_int, C.c_int, C.c_int, c_p, c_p, c_p, c_p]),
     "sixbit_lowrank_add": (C.c_int, [C.POINTER(QAct), c_p, c_p, c_p, c_p, c_p, C.c_int, C.c_int, C.c_int, C.c_int,
                                      C.c_int, c_p, c_p, c_p, C.c_int, c_p, c_p, c_p, c_p, c_p, c_p]),
-    "sixbit_lowrank_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int]),
+    "sixbit_lowrank_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int]),
     "sixbit_block_stats_noalloc": (C.c_int, [c_p, c_p, c_p, C.c_int64, c_p, c_p, c_p, c_p]),
     "sixbit_block_stats_noalloc_max_elems": (C.c_int64, []),
     "sixbit_dit_begin": (C.c_int, [C.POINTER(PolicyCfg), C.POINTER(DitBlocks), c_p, c_p, c_p]),

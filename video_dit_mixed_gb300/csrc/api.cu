@@ -802,10 +802,7 @@ sixbit_status sixbit_moe_combine(const uint16_t* d, const float* d_f32, const in
   return cuda_status(launch_moe_combine(p, static_cast<cudaStream_t>(stream)));
 }
 
-size_t sixbit_lowrank_workspace_bytes(int M, int K, int R) {
-  if (M <= 0 || K <= 0 || R <= 0) return 0;
-  return static_cast<size_t>(lowrank_splits(M, K)) * static_cast<size_t>(M) * static_cast<size_t>(R) * 4;
-}
+size_t sixbit_lowrank_workspace_bytes(int M, int R) { return M <= 0 || R <= 0 ? 0 : lowrank_workspace(M, R); }
 
 sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, const uint16_t* lr_a,
                                  const uint16_t* lr_b, const float* alpha, const int32_t* ids, int L, int M, int N,
@@ -815,7 +812,7 @@ sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, c
   if (epilogue != SIXBIT_EPI_NONE && epilogue != SIXBIT_EPI_GELU && epilogue != SIXBIT_EPI_RESIDUAL)
     return SIXBIT_EINVAL;
   if (M < 0 || M > INT32_MAX - 32 || N < 1 || N > 1 << 20 || K <= 0 || K % 128 != 0 || R < 16 ||
-      R > SIXBIT_MAX_RANK || R % 16 != 0 || L < 1)
+      R > SIXBIT_MAX_RANK || R % 16 != 0 || L < 1 || L > SIXBIT_MAX_ADAPTERS)
     return SIXBIT_ESHAPE;
   if (base != nullptr && base_f32 != nullptr) return SIXBIT_EINVAL;
   if (M == 0) return SIXBIT_OK;
@@ -851,10 +848,9 @@ sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, c
   p.residual = epilogue == SIXBIT_EPI_RESIDUAL ? residual : nullptr;
   p.Y = Y_f32 != nullptr ? nullptr : Y;
   p.Yf = Y_f32;
-  p.v = static_cast<float*>(workspace);
   p.mode_dev = mode_dev;
   p.err = err_dev;
-  return cuda_status(launch_lowrank(p, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_lowrank(p, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -232,12 +232,14 @@ struct LowRankParams {
   const uint16_t* residual;
   uint16_t* Y;
   float* Yf;
-  float* v;                      // workspace: [splits][M][R]
   const int32_t* mode_dev;
   int32_t* err;
-  int splits, tiles_per_cta;     // set by the launch
+  void* v;                       // in the workspace, as are the rows' order and their adapters
+  int32_t* perm;
+  int32_t* sid;
+  int tiles_per_cta;             // set by the launch
 };
-int lowrank_splits(int M, int K);
-cudaError_t launch_lowrank(LowRankParams p, cudaStream_t st);
+size_t lowrank_workspace(int M, int R);
+cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st);
 
 }  // namespace sixbit

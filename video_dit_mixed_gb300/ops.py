@@ -13,7 +13,7 @@ from typing import NamedTuple
 import torch
 
 from . import abi
-from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MAX_EXPERTS, MAX_GROUPS, MAX_RANK, MAX_TOP_K,  # noqa: F401
+from .abi import (EPI_GELU, EPI_NONE, EPI_RESIDUAL, MAX_ADAPTERS, MAX_EXPERTS, MAX_GROUPS, MAX_RANK, MAX_TOP_K,  # noqa: F401
                   MODE_BF16, MODE_INT8, MODE_NVFP4, MODE_SKIP, QGEMV_MAX_ROWS, SCORE_SIGMOID, SCORE_SOFTMAX, DitBlocks, PolicyCfg, PolicyState, QAct, Stats, Weights, check, lib)
 
 _lib = lib()
@@ -658,7 +658,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
 
     x: INT8 QActTensors or bf16 [M, K]; ids: int32 [M] on the GPU, -1 for rows without an adapter; base: the shared
     projection's result, float32 or bf16 [M, N], or None.  `out` may be base or residual.  ws:
-    lowrank_workspace_bytes(M, K, R) bytes, allocated for the call by default.  Returns bf16 [M, N], or float32 with
+    lowrank_workspace_bytes(M, R) bytes, allocated for the call by default.  Returns bf16 [M, N], or float32 with
     out_f32 or a float32 `out`."""
     if isinstance(x, torch.Tensor):
         dev = _gpu(x, "x")
@@ -702,7 +702,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    need = int(_lib.sixbit_lowrank_workspace_bytes(m, k, r))
+    need = int(_lib.sixbit_lowrank_workspace_bytes(m, r))
     if ws is None:
         ws = _empty((need,), _U8, device, stream)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
@@ -715,8 +715,8 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
     return out
 
 
-def lowrank_workspace_bytes(m: int, k: int, r: int) -> int:
-    return int(_lib.sixbit_lowrank_workspace_bytes(m, k, r))
+def lowrank_workspace_bytes(m: int, r: int) -> int:
+    return int(_lib.sixbit_lowrank_workspace_bytes(m, r))
 
 
 def check_err(err: torch.Tensor, what: str, stream=None) -> None:
