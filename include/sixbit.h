@@ -628,7 +628,7 @@ sixbit_status sixbit_moe_combine(const uint16_t* d, const float* d_f32, const in
                                  int T, int k, int R, int H, uint16_t* Y, float* Y_f32, int32_t* err_dev, void* stream);
 
 /* Ranks of an adapter, and adapters, sixbit_lowrank_add takes at most. */
-enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 32768 };
+enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 16384 };
 
 /*
  * Low-rank adapters of many requests beside a projection they share:

@@ -125,7 +125,20 @@ def test_widths_and_epilogues(ops, n, epilogue):
         c.check(c.call(ops, out_f32=True))
 
 
-@pytest.mark.parametrize("m", [32, 200, 1003])
+@pytest.mark.parametrize("r", [16, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("m,count", [(2047, 3), (2048, 1), (2500, 300), (5001, 6)])
+@pytest.mark.parametrize("int8", [True, False])
+def test_many_rows(ops, m, count, r, int8):
+    """Mixed rows, and the same rows with their requests side by side."""
+    ids = _mixed(m, count, r)
+    for order in (ids, ids.sort().values):
+        c = Case(m, 136, 384, r, count, order, int8=int8, base="bf16")
+        c.check(c.call(ops))
+    c = Case(m, 33, 1920, r, count, ids, int8=int8)
+    c.check(c.call(ops, out_f32=True))
+
+
+@pytest.mark.parametrize("m", [32, 200, 1003, 4100])
 def test_runs_of_requests(ops, m):
     ids = torch.full((m,), -1, dtype=torch.int32)
     cuts = [0, m // 7, m // 7 + 1, m // 2, m - 3, m]
@@ -210,7 +223,7 @@ def test_in_place_alignment_streams_modes(ops):
         assert torch.equal(c.call(ops, ws=ws), want)
 
 
-@pytest.mark.parametrize("m", [1, 20, 300])
+@pytest.mark.parametrize("m", [1, 20, 300, 4200])
 def test_streams_and_graphs(ops, m):
     c = Case(m, 256, 1920, 16, 4, _mixed(m, 4, 3), epilogue="gelu")
     want = c.call(ops)

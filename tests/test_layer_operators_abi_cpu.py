@@ -87,7 +87,7 @@ def test_lowrank_add(lib, p):
 
     _expect(lib, call,
             (ESHAPE, [dict(m=-1), dict(m=2**31 - 16), dict(n=0), dict(n=(1 << 20) + 1), dict(k=0), dict(k=64), dict(r=0),
-                      dict(r=8), dict(r=24), dict(r=144), dict(l=0), dict(l=32769)]),
+                      dict(r=8), dict(r=24), dict(r=144), dict(l=0), dict(l=16385)]),
             (EINVAL, [dict(act=False), dict(codes=None), dict(scale=None), dict(a=None), dict(b=None), dict(ids=None),
                       dict(y=None), dict(ws=None), dict(epi=2), dict(epi=3), dict(epi=-1), dict(base=p, bf=p)]),
             (EALIGN, [dict(codes=p + 8), dict(scale=p + 2), dict(x=p + 8), dict(a=p + 8), dict(b=p + 4), dict(al=p + 2),

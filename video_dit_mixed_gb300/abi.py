@@ -13,7 +13,7 @@ FLAG_REFRESH, FLAG_PDR, FLAG_POSTSKIP, FLAG_NEAR = 1 << 8, 1 << 9, 1 << 10, 1 <<
 EPI_NONE, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
 QGEMV_MAX_ROWS, MAX_EXPERTS = 32, 1024
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
-MAX_TOP_K, MAX_GROUPS, MAX_RANK, MAX_ADAPTERS = 32, 32, 128, 32768
+MAX_TOP_K, MAX_GROUPS, MAX_RANK, MAX_ADAPTERS = 32, 32, 128, 16384
 MODE_NAMES = {MODE_NVFP4: "NVFP4", MODE_INT8: "INT8", MODE_BF16: "BF16", MODE_SKIP: "SKIP"}
 
 

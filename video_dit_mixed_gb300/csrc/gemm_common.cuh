@@ -64,6 +64,31 @@ __device__ __forceinline__ uint64_t gelu_pair(uint64_t v) {
   return f2_fma(h, f2_mul(xc, q), h);  // h (1 + erf)
 }
 
+// gelu_pair of N pairs step by step, so that a coefficient is brought into registers
+// once for all of them.
+template <int N>
+__device__ __forceinline__ void gelu_pairs(uint64_t (&v)[N]) {
+  uint64_t xc[N], s[N], q[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint64_t x = f2_mul(v[n], f2_pack(0.7071067811865475244f, 0.7071067811865475244f));
+    xc[n] = f2_pack(clamp_erf_arg(f2_lo(x)), clamp_erf_arg(f2_hi(x)));
+    s[n] = f2_fma(f2_mul(xc[n], xc[n]), f2_pack(kGeluS, kGeluS), f2_pack(-1.0f, -1.0f));
+    q[n] = f2_pack(gelu_q(15), gelu_q(15));
+  }
+#pragma unroll
+  for (int i = 14; i >= 0; --i) {
+    const uint64_t c = f2_pack(gelu_q(i), gelu_q(i));
+#pragma unroll
+    for (int n = 0; n < N; ++n) q[n] = f2_fma(q[n], s[n], c);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint64_t h = f2_mul(v[n], f2_pack(0.5f, 0.5f));
+    v[n] = f2_fma(h, f2_mul(xc[n], q[n]), h);
+  }
+}
+
 // 16-byte global -> shared copy without a register round trip (zero-fill when
 // !valid; src must still be a valid address).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {

@@ -237,7 +237,7 @@ struct LowRankParams {
   void* v;                       // in the workspace, as are the rows' order and their adapters
   int32_t* perm;
   int32_t* sid;
-  int tiles_per_cta;             // set by the launch
+  int chunk, chunks_per_cta;     // set by the launch
 };
 size_t lowrank_workspace(int M, int R);
 cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st);

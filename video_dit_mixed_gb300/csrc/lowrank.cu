@@ -34,6 +34,9 @@ constexpr int kTile = 32;        // positions of a tile
 constexpr int kWarps = 8;
 constexpr int kUnit = 64;        // k of a warp's turn
 constexpr int kFew = kTile;      // rows that need no sorting kernel
+constexpr int kFewWarps = 4;
+constexpr int kChunk = 256;      // positions of a CTA that applies B
+constexpr int kStagedRows = 2048;  // from these rows on x and A pass through shared memory
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -72,40 +75,69 @@ __device__ __forceinline__ int adapter_of(const LowRankParams& p, int row, bool 
   return -1;
 }
 
-// Counting sort of the rows by adapter: perm[pos] = row, sid[pos] = its adapter.
-constexpr int kPlanThreads = 1024;
+// Counting sort of the rows by adapter: perm[pos] = row, sid[pos] = its adapter.  One
+// CTA, or a cluster of them that each count a part of the rows and read each
+// other's counts (17776 rows: 19 us by one).
+constexpr int kPlanThreads = 1024, kPlanAtOnce = 4, kPlanCluster = 8;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LowRankParams p) {
+  namespace cg = cooperative_groups;
   next_may_start();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
-  extern __shared__ int at[];  // [L + 1]: rows of adapter i - 1, then where they go
+  extern __shared__ int count[];  // [L + 1] rows of adapter i - 1 in this CTA's part, [L + 1] where they go
   __shared__ int part[kPlanThreads / 32];
   const int bins = p.L + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < bins; i += kPlanThreads) at[i] = 0;
+  int* at = count + bins;
+  const auto cluster = cg::this_cluster();
+  const int ctas = gridDim.x, me = blockIdx.x;
+  for (int i = threadIdx.x; i < bins; i += kPlanThreads) count[i] = 0;
   __syncthreads();
-  auto walk = [&](bool place) {
-    for (int64_t r0 = threadIdx.x - lane; r0 < p.M; r0 += kPlanThreads) {
-      const int64_t row = r0 + lane;
-      const int id = row < p.M ? adapter_of(p, static_cast<int>(row), !place) : INT_MAX;
-      const uint32_t same = __match_any_sync(kAll, id);
-      const int leader = __ffs(same) - 1;
-      int first = 0;
-      if (id != INT_MAX && lane == leader) first = atomicAdd(&at[id + 1], __popc(same));
+  const int64_t per = (static_cast<int64_t>(p.M) + ctas - 1) / ctas, end = min(static_cast<int64_t>(p.M), per * (me + 1));
+  auto walk = [&](int* to, bool place) {
+    for (int64_t r0 = per * me + threadIdx.x - lane; r0 < end; r0 += kPlanThreads * kPlanAtOnce) {
+      int id[kPlanAtOnce], first[kPlanAtOnce];
+      uint32_t same[kPlanAtOnce];
+#pragma unroll
+      for (int u = 0; u < kPlanAtOnce; ++u) {
+        const int64_t row = r0 + u * kPlanThreads + lane;
+        id[u] = row < end ? adapter_of(p, static_cast<int>(row), !place) : INT_MAX;
+      }
+#pragma unroll
+      for (int u = 0; u < kPlanAtOnce; ++u) {
+        same[u] = __match_any_sync(kAll, id[u]);
+        first[u] = 0;
+        if (id[u] != INT_MAX && lane == __ffs(same[u]) - 1) first[u] = atomicAdd(&to[id[u] + 1], __popc(same[u]));
+      }
       if (place) {
-        first = __shfl_sync(kAll, first, leader);
-        if (id != INT_MAX) {
-          const int pos = first + __popc(same & ((1u << lane) - 1));
-          p.perm[pos] = static_cast<int>(row);
-          p.sid[pos] = id;
+#pragma unroll
+        for (int u = 0; u < kPlanAtOnce; ++u) {
+          const int pos = __shfl_sync(kAll, first[u], __ffs(same[u]) - 1) + __popc(same[u] & ((1u << lane) - 1));
+          if (id[u] != INT_MAX) {
+            p.perm[pos] = static_cast<int>(r0 + u * kPlanThreads + lane);
+            p.sid[pos] = id[u];
+          }
         }
       }
     }
   };
-  walk(false);
-  __syncthreads();
-  // exclusive sums of the bins, each thread a run of them
-  const int run = (bins + kPlanThreads - 1) / kPlanThreads, i0 = threadIdx.x * run, i1 = min(i0 + run, bins);
+  walk(count, false);
+  if (ctas > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  // exclusive sums over the bins, each thread a run of them, and the earlier CTAs' share of each
+  const int run = (bins + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(static_cast<int>(threadIdx.x) * run, bins), i1 = min(i0 + run, bins);
   int sum = 0;
-  for (int i = i0; i < i1; ++i) sum += at[i];
+  for (int i = i0; i < i1; ++i) {
+    int before = 0, all = 0;
+    for (int c = 0; c < ctas; ++c) {
+      const int n = ctas > 1 ? cluster.map_shared_rank(count, c)[i] : count[i];
+      if (c < me) before += n;
+      all += n;
+    }
+    at[i] = sum + before;
+    sum += all;
+  }
   int up = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -113,16 +145,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const LowRankParams 
     if (lane >= o) up += v;
   }
   if (lane == 31) part[warp] = up;
-  __syncthreads();
+  if (ctas > 1)
+    cluster.sync();  // (no CTA leaves while another reads its counts)
+  else
+    __syncthreads();
   int first = up - sum;
   for (int w = 0; w < warp; ++w) first += part[w];
-  for (int i = i0; i < i1; ++i) {
-    const int n = at[i];
-    at[i] = first;
-    first += n;
-  }
+  for (int i = i0; i < i1; ++i) at[i] += first;
   __syncthreads();
-  walk(true);
+  walk(at, true);
 }
 
 // A tile's positions, one a lane: the row and its adapter (INT_MAX beyond the
@@ -288,182 +319,452 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
   }
 }
 
-// Eight consecutive values of one row of a bf16 or FP32 matrix.
-struct Eight {
-  uint4 a, b;
-};
-__device__ __forceinline__ void add_bf16(const uint4& w, float (&v)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] += __uint_as_float(u[i] << 16);
-    v[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+// 16 bytes from global to shared memory without a register round trip; zeros
+// where !valid (src must still be an address).
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
 }
-__device__ __forceinline__ Eight load_base(const LowRankParams& p, size_t at) {
-  Eight e;
-  e.a = e.b = make_uint4(0, 0, 0, 0);
-  if (p.base_f32 != nullptr) {
-    e.a = *reinterpret_cast<const uint4*>(p.base_f32 + at);
-    e.b = *reinterpret_cast<const uint4*>(p.base_f32 + at + 4);
-  } else if (p.base != nullptr) {
-    e.a = *reinterpret_cast<const uint4*>(p.base + at);
-  }
-  return e;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Eight consecutive outputs of one row from column n on: base, epilogue, store.
-// `base` holds the base's where VEC.
-template <bool VEC>
-__device__ __forceinline__ void finish(const LowRankParams& p, size_t at, int n, const Eight& base, float (&v)[8]) {
-  if constexpr (VEC) {
-    if (p.base_f32 != nullptr) {
-      const uint32_t u[8] = {base.a.x, base.a.y, base.a.z, base.a.w, base.b.x, base.b.y, base.b.z, base.b.w};
+// v of 128 positions, for many rows: x and A_l pass through shared memory, 128 k a
+// stage, and are read there by four teams of warps, 32 rows a warp, a team for each
+// quarter of the stage's k.  A run of one adapter within the block is a pass over
+// K.  Grid: blocks of positions x blocks of 8 RT ranks.
+constexpr int kBlock = 128, kStages = 4, kStageK = 128, kStagedThreads = 512;
+template <bool INT8, int RT>
+struct Staged {
+  static constexpr int kXRow = INT8 ? 128 : 256;  // bytes of a row's stage
+  static constexpr int kX = kBlock * kXRow, kA = 8 * RT * 256, kStage = kX + kA;
+  static constexpr int kP = 8 * RT + 4;           // floats of a row's sums
+  static constexpr int kSums = kBlock * kP * 4;
+  static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
+};
+// Where chunk `ch` (16 bytes) of a row lies.  A quarter warp's 16-byte reads take
+// four neighbouring chunks of two rows, a half warp's 8-byte ones two of four.
+__device__ __forceinline__ int chunk256(int row, int ch) { return row * 256 + ((ch ^ ((row & 1) << 2)) << 4); }
+__device__ __forceinline__ int chunk128(int row, int ch) { return row * 128 + ((ch ^ ((row & 3) << 1)) << 4); }
+template <bool INT8, int RT, int PARTS>
+__global__ void __launch_bounds__(kStagedThreads, 1) staged_kernel(const LowRankParams p) {
+  using S = Staged<INT8, RT>;
+  next_may_start();
+  before_done();
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int rows[kBlock], ids[kBlock];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, q = lane & 3;
+  const int wr = warp & 3, wk = warp >> 2;
+  const int64_t pos0 = static_cast<int64_t>(blockIdx.x) * kBlock;
+  const int r0 = blockIdx.y * 8 * RT, tiles = min(RT, (p.R - r0) / 8);
+  if (tid < kBlock) {
+    const bool in = pos0 + tid < p.M;
+    rows[tid] = in ? p.perm[pos0 + tid] : 0;
+    ids[tid] = in ? p.sid[pos0 + tid] : INT_MAX;
+  }
+  __syncthreads();
+  const int stages = p.K / kStageK;
+  for (int first = 0; first < kBlock;) {
+    const int id = ids[first];
+    if (id == INT_MAX) break;
+    int end = kBlock;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(u[i]);
-    } else {
-      add_bf16(base.a, v);
+    for (int b = kBlock / 32 - 1; b >= 0; --b) {
+      const uint32_t other = __ballot_sync(kAll, 32 * b + lane > first && ids[32 * b + lane] != id);
+      if (other != 0) end = 32 * b + __ffs(other) - 1;
     }
-    if (p.epilogue == SIXBIT_EPI_GELU) {
+    if (id < 0) {
+      first = end;
+      continue;
+    }
+    // this thread's chunks of a stage: of x, then of A
+    constexpr int kXC = S::kXRow / 16, kNX = kBlock * kXC / kStagedThreads;
+    constexpr int kNA = (8 * RT * 16 + kStagedThreads - 1) / kStagedThreads;
+    const unsigned char* from[kNX + kNA];
+    int to[kNX + kNA];
+    bool in[kNX + kNA];
+#pragma unroll
+    for (int i = 0; i < kNX; ++i) {
+      const int c = tid + i * kStagedThreads, row = c / kXC, ch = c % kXC;
+      in[i] = row >= first && row < end;
+      const size_t at = static_cast<size_t>(rows[row]) * p.K;
+      from[i] = (INT8 ? reinterpret_cast<const unsigned char*>(p.codes + at) : reinterpret_cast<const unsigned char*>(p.x + at)) + ch * 16;
+      to[i] = INT8 ? chunk128(row, ch) : chunk256(row, ch);
+    }
+#pragma unroll
+    for (int i = 0; i < kNA; ++i) {
+      const int c = tid + i * kStagedThreads, row = c >> 4, ch = c & 15;
+      in[kNX + i] = row < 8 * tiles;
+      from[kNX + i] = reinterpret_cast<const unsigned char*>(
+          p.a + (static_cast<size_t>(id) * p.R + r0 + (row < 8 * tiles ? row : 0)) * p.K + ch * 8);
+      to[kNX + i] = S::kX + chunk256(row, ch);
+    }
+    auto fetch = [&](int st) {
+      unsigned char* base = smem + (st % kStages) * S::kStage;
+#pragma unroll
+      for (int i = 0; i < kNX; ++i) {
+        copy16(base + to[i], from[i], in[i]);
+        from[i] += S::kXRow;
+      }
+#pragma unroll
+      for (int i = kNX; i < kNX + kNA; ++i) {
+        if (in[i]) copy16(base + to[i], from[i], true);
+        from[i] += 256;
+      }
+    };
+    for (int st = 0; st < kStages - 1; ++st) {
+      if (st < stages) fetch(st);
+      copies_commit();
+    }
+    const bool mine = wr * 32 < end && wr * 32 + 32 > first;
+    float acc[2][RT][4] = {};
+    for (int st = 0; st < stages; ++st) {
+      copies_wait<kStages - 2>();
+      __syncthreads();  // (the stage is here, and the one before it is free)
+      if (st + kStages - 1 < stages) fetch(st + kStages - 1);
+      copies_commit();
+      if (!mine) continue;
+      const unsigned char* xs = smem + (st % kStages) * S::kStage;
+      const unsigned char* as = xs + S::kX;
+      uint4 b[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        if (j < tiles) b[j] = *reinterpret_cast<const uint4*>(as + chunk256(8 * j + g8, 4 * wk + q));
+      uint32_t x[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t g = gelu_pair(f2_pack(v[2 * i], v[2 * i + 1]));
-        v[2 * i] = f2_lo(g);
-        v[2 * i + 1] = f2_hi(g);
+        const int row = wr * 32 + g8 + 8 * i;
+        if constexpr (INT8) {
+          const uint2 w = *reinterpret_cast<const uint2*>(xs + chunk128(row, 2 * wk + (q >> 1)) + (q & 1) * 8);
+          x[i][0] = codes_bf16(__byte_perm(w.x, 0, 0x4140));
+          x[i][1] = codes_bf16(__byte_perm(w.x, 0, 0x4342));
+          x[i][2] = codes_bf16(__byte_perm(w.y, 0, 0x4140));
+          x[i][3] = codes_bf16(__byte_perm(w.y, 0, 0x4342));
+        } else {
+          const uint4 w = *reinterpret_cast<const uint4*>(xs + chunk256(row, 4 * wk + q));
+          x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
+        }
       }
-    } else if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
-      add_bf16(*reinterpret_cast<const uint4*>(p.residual + at), v);
-    }
-    if (p.Yf != nullptr) {
-      reinterpret_cast<float4*>(p.Yf + at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p.Yf + at)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4*>(p.Y + at) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    }
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (n + i >= p.N) return;
-      float y = v[i];
-      if (p.base_f32 != nullptr) y += p.base_f32[at + i];
-      if (p.base != nullptr) y += __uint_as_float(static_cast<uint32_t>(p.base[at + i]) << 16);
-      if (p.epilogue == SIXBIT_EPI_GELU) y = f2_lo(gelu_pair(f2_pack(y, y)));
-      if (p.epilogue == SIXBIT_EPI_RESIDUAL) y += __uint_as_float(static_cast<uint32_t>(p.residual[at + i]) << 16);
-      if (p.Yf != nullptr)
-        p.Yf[at + i] = y;
-      else
-        p.Y[at + i] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t a[4] = {x[2 * m][2 * h], x[2 * m + 1][2 * h], x[2 * m][2 * h + 1], x[2 * m + 1][2 * h + 1]};
+            if (j < tiles) mma(acc[m][j], a, h == 0 ? b[j].x : b[j].z, h == 0 ? b[j].y : b[j].w);
+          }
     }
+    // the quarters of k, joined in the stages' place
+    copies_wait<0>();
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int quarter = 3; quarter >= 0; --quarter) {
+      if (wk == quarter && mine) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              float2* at = reinterpret_cast<float2*>(&sums[(wr * 32 + 16 * m + 4 * i + g8) * S::kP + 8 * j + 2 * q]);
+              const float2 v = make_float2(acc[m][j][i], acc[m][j][i + 1]);
+              *at = quarter == 3 ? v : make_float2(v.x + at->x, v.y + at->y);
+            }
+      }
+      __syncthreads();
+    }
+    const int quads = 2 * tiles;
+    const float alpha = p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f;
+    for (int i = tid; i < (end - first) * quads; i += kStagedThreads) {
+      const int n = first + i / quads, r = i % quads * 4;
+      const float4 f = *reinterpret_cast<const float4*>(&sums[n * S::kP + r]);
+      const float by = (INT8 ? __ldg(p.row_scale + rows[n]) : 1.f) * alpha;
+      float v[4] = {f.x * by, f.y * by, f.z * by, f.w * by};
+      store_parts<PARTS>(p, pos0 + n, r0 + r, v);
+    }
+    __syncthreads();
+    first = end;
   }
 }
 
-// base + B_l v and the epilogue.  Grid: strips of 32 columns, one a warp, x chunks
-// of tiles_per_cta tiles x slots (of a tile's runs, as above).  Ranks and columns
-// may stand in any order as long as the operands agree: a lane keeps four
+// Eight consecutive values of the base, which is FP32 (F32) or bf16.
+template <bool F32>
+struct Eight {
+  uint4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const LowRankParams& p, size_t at) {
+    if constexpr (F32) {
+      w[0] = *reinterpret_cast<const uint4*>(p.base_f32 + at);
+      w[1] = *reinterpret_cast<const uint4*>(p.base_f32 + at + 4);
+    } else {
+      w[0] = p.base != nullptr ? *reinterpret_cast<const uint4*>(p.base + at) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+__device__ __forceinline__ void add_bf16(const uint4& w, uint64_t* v) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2_add(v[i], f2_from_bf16x2(u[i]));
+}
+__device__ __forceinline__ void add_f32(const uint4& w, uint64_t* v) {
+  v[0] = f2_add(v[0], f2_pack(__uint_as_float(w.x), __uint_as_float(w.y)));
+  v[1] = f2_add(v[1], f2_pack(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
+// Eight consecutive outputs of one row, 16-byte aligned, behind base and GELU.
+__device__ __forceinline__ void store8(const LowRankParams& p, size_t at, uint64_t* v) {
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL) add_bf16(*reinterpret_cast<const uint4*>(p.residual + at), v);
+  if (p.Yf != nullptr) {
+    reinterpret_cast<float4*>(p.Yf + at)[0] = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
+    reinterpret_cast<float4*>(p.Yf + at)[1] = make_float4(f2_lo(v[2]), f2_hi(v[2]), f2_lo(v[3]), f2_hi(v[3]));
+  } else {
+    *reinterpret_cast<uint4*>(p.Y + at) =
+        make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
+  }
+}
+// One output.
+__device__ __forceinline__ void finish1(const LowRankParams& p, size_t at, float y) {
+  if (p.base_f32 != nullptr) y += p.base_f32[at];
+  if (p.base != nullptr) y += __uint_as_float(static_cast<uint32_t>(p.base[at]) << 16);
+  if (p.epilogue == SIXBIT_EPI_GELU) y = f2_lo(gelu_pair(f2_pack(y, y)));
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL) y += __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16);
+  if (p.Yf != nullptr)
+    p.Yf[at] = y;
+  else
+    p.Y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+}
+
+// base + B_l v and the epilogue, a warp a strip of 32 columns from n0 on.  Ranks and
+// columns may stand in any order as long as the operands agree: a lane keeps four
 // consecutive ranks of an MMA's 16, and column c of MMA j stands for
 // n0 + 8 (c / 2) + 2 j + c % 2, so that a lane ends up with eight consecutive
-// outputs of each of its rows.  B_l's strip stays in registers from run to run of
-// one adapter (KS: 16-rank steps of them).
-template <bool FEW, bool VEC, int PARTS, int KS>
-__global__ void __launch_bounds__(kWarps * 32, 2) expand_kernel(const LowRankParams p) {
-  __shared__ int scratch[kWarps][32];
+// outputs of each of its two rows of a 16-row tile.  KS: 16-rank steps that are
+// held in registers; of a larger R as many at a time.
+template <int KS>
+struct Strip {
+  uint2 b[KS][4];
+  __device__ __forceinline__ void load(const LowRankParams& p, int id, int n0, int s0) {
+    const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3, steps = p.R / 16;
+    const int c0 = n0 + 8 * (g8 >> 1) + (g8 & 1);
+    const uint16_t* bl = p.b + (static_cast<size_t>(id) * p.N + c0) * p.R + s0 * 16 + 4 * q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j, bl += 2 * p.R)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        b[s][j] = make_uint2(0, 0);
+        if (c0 + 2 * j < p.N && s0 + s < steps) b[s][j] = __ldg(reinterpret_cast<const uint2*>(bl + s * 16));
+      }
+  }
+};
+// acc += the strip times a step of v: lo, hi: this lane's parts of rows g8 and g8 + 8.
+template <int PARTS>
+__device__ __forceinline__ void step_mma(float (&acc)[4][4], const uint2 (&lo)[PARTS], const uint2 (&hi)[PARTS],
+                                         const uint2 (&b)[4]) {
+#pragma unroll
+  for (int w = PARTS - 1; w >= 0; --w) {
+    const uint32_t a[4] = {lo[w].x, hi[w].x, lo[w].y, hi[w].y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mma(acc[j], a, b[j].x, b[j].y);
+  }
+}
+template <int PARTS>
+__device__ __forceinline__ void load_v(const unsigned char* from, bool live, uint2 (&v)[PARTS]) {
+  const uint2* u = reinterpret_cast<const uint2*>(from);
+#pragma unroll
+  for (int w = 0; w < PARTS; ++w) v[w] = make_uint2(0, 0);
+  if (!live) return;
+  if constexpr (PARTS == 2) {
+    const uint4 f = *reinterpret_cast<const uint4*>(u);
+    v[0] = make_uint2(f.x, f.y);
+    v[1] = make_uint2(f.z, f.w);
+  } else {
+#pragma unroll
+    for (int w = 0; w < PARTS; ++w) v[w] = u[w];
+  }
+}
+// The outputs of a tile of 16 rows.  VEC: 16-byte accesses; else through the warp's
+// `turn` [16][33], a row's 32 columns a lane each.
+template <bool VEC, bool F32>
+__device__ __forceinline__ void finish_tile(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
+                                            const bool (&live)[2], int n0, const Eight<F32> (&base)[2], float* turn) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+  if constexpr (VEC) {
+    uint64_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = f2_pack(acc[i & 3][2 * (i >> 2)], acc[i & 3][2 * (i >> 2) + 1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (F32) {
+        add_f32(base[h].w[0], y + 4 * h);
+        add_f32(base[h].w[1], y + 4 * h + 2);
+      } else {
+        add_bf16(base[h].w[0], y + 4 * h);
+      }
+    }
+    if (p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (live[h] && n0 + 8 * q < p.N) store8(p, row[h] * p.N + n0 + 8 * q, y + 4 * h);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j] = acc[j][2 * h];
+        turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j + 1] = acc[j][2 * h + 1];
+      }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const size_t r = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4);
+      const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4);
+      if (in && n0 + lane < p.N) finish1(p, r * p.N + n0 + lane, turn[i * 33 + lane]);
+    }
+    __syncwarp();
+  }
+}
+
+// Up to 32 rows.  Grid: groups of strips x 1 x slots (of the tile's runs).
+template <bool VEC, bool F32, int PARTS, int KS>
+__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams p) {
+  __shared__ int scratch[kFewWarps][32];
+  __shared__ float turns[VEC ? 1 : kFewWarps][16 * 33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-  const int n0 = (blockIdx.x * (blockDim.x >> 5) + warp) * 32, n = n0 + 8 * q;
+  const int n0 = (blockIdx.x * kFewWarps + warp) * 32;
   before_done();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   if (n0 >= p.N) return;
-  const int steps = p.R / 16;
-  int held = -1;  // the adapter whose strip is in b
-  uint2 b[KS][4];
-  for (int i = 0; i < p.tiles_per_cta; ++i) {
-    const int64_t pos0 = (static_cast<int64_t>(blockIdx.y) * p.tiles_per_cta + i) * kTile;
-    if (pos0 >= p.M) return;
-    const Tile t = tile_at<FEW>(p, pos0, scratch[warp], false);
-    uint32_t left = t.heads;
-    for (int turn = 0; left != 0; ++turn, left &= left - 1) {
-      if (turn % gridDim.z != blockIdx.z) continue;
-      const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
-      for (int m = 0; m < count; m += 16) {
-        size_t at[2];
-        bool live[2];
-        Eight base[2];
+  const Tile t = tile_at<true>(p, 0, scratch[warp], false);
+  uint32_t left = t.heads;
+  for (int turn = 0; left != 0; ++turn, left &= left - 1) {
+    if (turn % gridDim.z != blockIdx.z) continue;
+    const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
+    for (int m = 0; m < count; m += 16) {
+      size_t row[2];
+      bool live[2];
+      Eight<F32> base[2] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          live[h] = g8 + 8 * h < count - m;
-          at[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31)) * p.N + n;
-          if constexpr (VEC) {
-            live[h] = live[h] && n < p.N;
-            if (live[h]) base[h] = load_base(p, at[h]);
+      for (int h = 0; h < 2; ++h) {
+        live[h] = g8 + 8 * h < count - m;
+        row[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31));
+        if (VEC && live[h] && n0 + 8 * q < p.N) base[h].load(p, row[h] * p.N + n0 + 8 * q);
+      }
+      float acc[4][4] = {};
+      if (id >= 0) {
+        const unsigned char* v = static_cast<const unsigned char*>(p.v) + ((first + m + g8) * (p.R / 4) + q) * (8 * PARTS);
+        for (int s0 = 0; s0 < p.R / 16; s0 += KS) {
+          Strip<KS> strip;
+          strip.load(p, id, n0, s0);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if (s0 + s >= p.R / 16) break;
+            uint2 lo[PARTS], hi[PARTS];
+            load_v<PARTS>(v + (s0 + s) * 32 * PARTS, live[0], lo);
+            load_v<PARTS>(v + (s0 + s) * 32 * PARTS + 8 * (p.R / 4) * 8 * PARTS, live[1], hi);
+            step_mma<PARTS>(acc, lo, hi, strip.b[s]);
           }
-        }
-        float acc[4][4] = {};
-        if (id >= 0) {
-          const int64_t pos = pos0 + first + m + g8;
-          for (int s0 = 0; s0 < steps; s0 += KS) {
-            if (held != id || steps > KS) {
-              const uint16_t* bl = p.b + static_cast<size_t>(id) * p.N * p.R;
-#pragma unroll
-              for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int c = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
-                  b[s][j] = make_uint2(0, 0);
-                  if (c < p.N && s0 + s < steps)
-                    b[s][j] = __ldg(reinterpret_cast<const uint2*>(bl + static_cast<size_t>(c) * p.R + (s0 + s) * 16 + 4 * q));
-                }
-              held = id;
-            }
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              if (s0 + s >= steps) break;
-              uint2 v[2][PARTS];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int w = 0; w < PARTS; ++w) v[h][w] = make_uint2(0, 0);
-                if (g8 + 8 * h < count - m) {
-                  const uint2* from = reinterpret_cast<const uint2*>(p.v) + ((pos + 8 * h) * (p.R / 4) + (s0 + s) * 4 + q) * PARTS;
-                  if constexpr (PARTS == 2) {
-                    const uint4 f = *reinterpret_cast<const uint4*>(from);
-                    v[h][0] = make_uint2(f.x, f.y);
-                    v[h][1] = make_uint2(f.z, f.w);
-                  } else {
-#pragma unroll
-                    for (int w = 0; w < PARTS; ++w) v[h][w] = from[w];
-                  }
-                }
-              }
-#pragma unroll
-              for (int w = PARTS - 1; w >= 0; --w) {
-                const uint32_t a[4] = {v[0][w].x, v[1][w].x, v[0][w].y, v[1][w].y};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma(acc[j], a, b[s][j].x, b[s][j].y);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!live[h]) continue;
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            y[2 * j] = acc[j][2 * h];
-            y[2 * j + 1] = acc[j][2 * h + 1];
-          }
-          finish<VEC>(p, at[h], n, base[h], y);
         }
       }
+      finish_tile<VEC, F32>(p, acc, row, live, n0, base, turns[VEC ? 0 : warp]);
     }
   }
 }
 
-// A launch that may start while the one before it on the stream runs.
-struct Early {
+// More rows.  Grid: groups of eight strips x chunks of positions, whose v, rows and
+// adapters the CTA keeps in shared memory; the next tile's base is asked for
+// before this one is multiplied.
+template <int PARTS>
+__host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 more than a multiple of 128 spares conflicts
+  const int bytes = R * 2 * PARTS;
+  return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
+}
+template <bool VEC, bool F32, int PARTS, int KS>
+__global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
+  int* rows = reinterpret_cast<int*>(smem);
+  int* ids = rows + p.chunk;  // [chunk + 16]
+  unsigned char* vs = smem + (2 * p.chunk + 16) * 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+  const int n0 = (blockIdx.x * kWarps + warp) * 32;
+  const int stride = v_stride<PARTS>(p.R);
+  before_done();
+  if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
+  for (int chunk = 0; chunk < p.chunks_per_cta; ++chunk) {
+    const int64_t pos0 = (static_cast<int64_t>(blockIdx.y) * p.chunks_per_cta + chunk) * p.chunk;
+    if (pos0 >= p.M) break;
+    const int live_rows = static_cast<int>(min(static_cast<int64_t>(p.chunk), p.M - pos0));
+    if (chunk > 0) __syncthreads();
+    const int pieces = p.R * PARTS / 8;  // 16 bytes each, of a row's v
+    const unsigned char* v = static_cast<const unsigned char*>(p.v) + pos0 * (static_cast<size_t>(p.R) * 2 * PARTS);
+    for (int i = threadIdx.x; i < live_rows * pieces; i += kWarps * 32)
+      copy16(vs + (i / pieces) * stride + (i % pieces) * 16, v + static_cast<size_t>(i) * 16, true);
+    copies_commit();
+    for (int i = threadIdx.x; i < p.chunk + 16; i += kWarps * 32) {
+      if (i < p.chunk) rows[i] = i < live_rows ? p.perm[pos0 + i] : 0;
+      ids[i] = i < live_rows ? p.sid[pos0 + i] : INT_MAX;
+    }
+    copies_wait<0>();
+    __syncthreads();
+    if (n0 >= p.N) continue;
+    Strip<KS> strip;
+    int held = -1;
+    // a tile: up to 16 positions of one adapter from `at` on
+    auto length = [&](int at) {
+      const int id = ids[at];
+      const uint32_t other = __ballot_sync(kAll, lane < 16 && ids[at + (lane & 15)] != id);
+      return other != 0 ? __ffs(other) - 1 : 16;
+    };
+    size_t row[2];
+    Eight<F32> base[2] = {};
+    auto ask = [&](int at, int count) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        row[h] = static_cast<size_t>(rows[min(at + g8 + 8 * h, p.chunk - 1)]);
+        if (VEC && g8 + 8 * h < count && n0 + 8 * q < p.N) base[h].load(p, row[h] * p.N + n0 + 8 * q);
+      }
+    };
+    int at = 0, count = length(0);
+    ask(at, count);
+    while (count > 0) {
+      const size_t row_now[2] = {row[0], row[1]};
+      const Eight<F32> base_now[2] = {base[0], base[1]};
+      const bool live[2] = {g8 < count, g8 + 8 < count};
+      const int at_now = at, id = ids[at];
+      at += count;
+      count = at < live_rows ? length(at) : 0;
+      if (count > 0) ask(at, count);
+      float acc[4][4] = {};
+      if (id >= 0) {
+        const unsigned char* from = vs + (at_now + g8) * stride + q * 8 * PARTS;
+        for (int s0 = 0; s0 < p.R / 16; s0 += KS) {
+          if (p.R / 16 > KS || held != id) strip.load(p, id, n0, s0);
+          held = id;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if (s0 + s >= p.R / 16) break;
+            uint2 lo[PARTS], hi[PARTS];
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
+            step_mma<PARTS>(acc, lo, hi, strip.b[s]);
+          }
+        }
+      }
+      finish_tile<VEC, F32>(p, acc, row_now, live, n0, base_now, turns[VEC ? 0 : warp]);
+    }
+  }
+}
+
+// A launch that may start while the one before it on the stream runs (early), of
+// clusters of this shape.
+struct Launch {
   cudaLaunchAttribute attrs[2];
   cudaLaunchConfig_t cfg;
-  Early(dim3 grid, int threads, int smem, cudaStream_t st, bool early, int cluster_z = 1) : cfg{} {
+  Launch(dim3 grid, int threads, int smem, cudaStream_t st, bool early, dim3 cluster = dim3(1)) : cfg{} {
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
@@ -473,73 +774,94 @@ struct Early {
       attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    if (cluster_z > 1) {
+    if (cluster.x * cluster.y * cluster.z > 1) {
       attrs[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-      attrs[cfg.numAttrs].val.clusterDim.x = 1;
-      attrs[cfg.numAttrs].val.clusterDim.y = 1;
-      attrs[cfg.numAttrs++].val.clusterDim.z = cluster_z;
+      attrs[cfg.numAttrs].val.clusterDim.x = cluster.x;
+      attrs[cfg.numAttrs].val.clusterDim.y = cluster.y;
+      attrs[cfg.numAttrs++].val.clusterDim.z = cluster.z;
     }
   }
 };
 
 template <bool FEW, bool INT8, int RT, int PARTS>
-cudaError_t launch_shrink(const LowRankParams& p, int tiles, cudaStream_t st) {
+cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
+  if constexpr (!FEW) {
+    if (p.M >= kStagedRows) {
+      constexpr int smem = Staged<INT8, RT>::kBytes;
+      const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
+      if (e != cudaSuccess) return e;
+      Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT)), kStagedThreads, smem, st, true);
+      note_launch();
+      return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT, PARTS>, p);
+    }
+  }
   constexpr int smem = kWarps * kTile * (8 * RT + 4) * 4;
   if (smem > 48 * 1024) {
     const cudaError_t e = set_smem_once<shrink_kernel<FEW, INT8, RT, PARTS>>(smem);
     if (e != cudaSuccess) return e;
   }
   // about two CTAs an SM: first a CTA for each of a tile's runs, then K over clusters
-  const int rows = p.M < 32 ? p.M : FEW ? 32 : 4;
+  const int tiles = (p.M + kTile - 1) / kTile, rows = p.M < 32 ? p.M : FEW ? 32 : 4;
   const int most = 304 / tiles > 0 ? 304 / tiles : 1, slots = most < rows ? most : rows;
   const int turns = (p.K / kUnit + kWarps - 1) / kWarps, left = most / slots > 0 ? most / slots : 1;
   int splits = turns < left ? turns : left;
   if (splits > 8) splits = 8;
-  Early l(dim3(tiles, slots, splits), kWarps * 32, smem, st, !FEW, splits);
+  Launch l(dim3(tiles, slots, splits), kWarps * 32, smem, st, !FEW, dim3(1, 1, splits));
   note_launch();
   return cudaLaunchKernelEx(&l.cfg, shrink_kernel<FEW, INT8, RT, PARTS>, p);
 }
 
 template <bool FEW, bool INT8, int PARTS>
-cudaError_t launch_shrink(const LowRankParams& p, int tiles, cudaStream_t st) {
-  if (p.R <= 16) return launch_shrink<FEW, INT8, 2, PARTS>(p, tiles, st);
-  if (p.R <= 32) return launch_shrink<FEW, INT8, 4, PARTS>(p, tiles, st);
-  return launch_shrink<FEW, INT8, 8, PARTS>(p, tiles, st);
+cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
+  if (p.R <= 16) return launch_shrink<FEW, INT8, 2, PARTS>(p, st);
+  if (p.R <= 32) return launch_shrink<FEW, INT8, 4, PARTS>(p, st);
+  return launch_shrink<FEW, INT8, 8, PARTS>(p, st);
 }
 
-template <bool FEW, bool VEC, int PARTS, int KS>
-cudaError_t launch_expand(LowRankParams p, int tiles, cudaStream_t st) {
+template <bool FEW, bool VEC, bool F32, int PARTS, int KS>
+cudaError_t launch_expand(LowRankParams p, cudaStream_t st) {
   const int strips = (p.N + 31) / 32;
-  int warps = kWarps, slots = 1;
-  p.tiles_per_cta = 1;
-  if (FEW) {
-    warps = 4;
-    slots = p.M;
-  } else {
-    p.tiles_per_cta = tiles > 4 * 65535 ? (tiles + 65534) / 65535 : 4;
-  }
-  const dim3 grid((strips + warps - 1) / warps, (tiles + p.tiles_per_cta - 1) / p.tiles_per_cta, slots);
-  Early l(grid, warps * 32, 0, st, true);
   note_launch();
-  return cudaLaunchKernelEx(&l.cfg, expand_kernel<FEW, VEC, PARTS, KS>, p);
+  if constexpr (FEW) {
+    Launch l(dim3((strips + kFewWarps - 1) / kFewWarps, 1, p.M), kFewWarps * 32, 0, st, true);
+    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, PARTS, KS>, p);
+  } else {
+    // chunks of kChunk positions, smaller ones where they would leave SMs idle
+    const int groups = (strips + kWarps - 1) / kWarps;
+    p.chunk = kChunk;
+    while (p.chunk > kTile && static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304) p.chunk /= 2;
+    const int chunks = (p.M + p.chunk - 1) / p.chunk;
+    p.chunks_per_cta = (chunks + 65534) / 65535;
+    const auto bytes = [](int chunk, int R) { return (2 * chunk + 16) * 4 + chunk * v_stride<PARTS>(R); };
+    const cudaError_t e =
+        set_smem_once<many_kernel<VEC, F32, PARTS, KS>>(bytes(kChunk, KS < 4 ? 16 * KS : SIXBIT_MAX_RANK));
+    if (e != cudaSuccess) return e;
+    Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32, bytes(p.chunk, p.R), st, true);
+    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, PARTS, KS>, p);
+  }
 }
 
-template <bool FEW, bool VEC, int PARTS>
-cudaError_t launch_both(const LowRankParams& p, int tiles, cudaStream_t st) {
-  const cudaError_t e = p.codes != nullptr ? launch_shrink<FEW, true, PARTS>(p, tiles, st)
-                                           : launch_shrink<FEW, false, PARTS>(p, tiles, st);
+template <bool FEW, bool VEC, bool F32, int PARTS>
+cudaError_t launch_expand(const LowRankParams& p, cudaStream_t st) {
+  if (p.R <= 16) return launch_expand<FEW, VEC, F32, PARTS, 1>(p, st);
+  if (p.R <= 32) return launch_expand<FEW, VEC, F32, PARTS, 2>(p, st);
+  return launch_expand<FEW, VEC, F32, PARTS, 4>(p, st);
+}
+
+template <bool FEW, int PARTS>
+cudaError_t launch_both(const LowRankParams& p, cudaStream_t st) {
+  const cudaError_t e = p.codes != nullptr ? launch_shrink<FEW, true, PARTS>(p, st)
+                                           : launch_shrink<FEW, false, PARTS>(p, st);
   if (e != cudaSuccess) return e;
-  if (p.R <= 16) return launch_expand<FEW, VEC, PARTS, 1>(p, tiles, st);
-  if (p.R <= 32) return launch_expand<FEW, VEC, PARTS, 2>(p, tiles, st);
-  return launch_expand<FEW, VEC, PARTS, 4>(p, tiles, st);
+  const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+  if (p.N % 8 != 0 || !a16(p.base) || !a16(p.base_f32) || !a16(p.residual) || !a16(p.Y) || !a16(p.Yf))
+    return launch_expand<FEW, false, false, PARTS>(p, st);
+  return p.base_f32 != nullptr ? launch_expand<FEW, true, true, PARTS>(p, st) : launch_expand<FEW, true, false, PARTS>(p, st);
 }
 
 template <bool FEW>
-cudaError_t launch_form(const LowRankParams& p, int tiles, cudaStream_t st) {
-  const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
-  const bool vec = p.N % 8 == 0 && a16(p.base) && a16(p.base_f32) && a16(p.residual) && a16(p.Y) && a16(p.Yf);
-  if (p.Yf != nullptr) return vec ? launch_both<FEW, true, 3>(p, tiles, st) : launch_both<FEW, false, 3>(p, tiles, st);
-  return vec ? launch_both<FEW, true, 2>(p, tiles, st) : launch_both<FEW, false, 2>(p, tiles, st);
+cudaError_t launch_form(const LowRankParams& p, cudaStream_t st) {
+  return p.Yf != nullptr ? launch_both<FEW, 3>(p, st) : launch_both<FEW, 2>(p, st);
 }
 
 }  // namespace lowrank
@@ -551,24 +873,24 @@ size_t lowrank_workspace(int M, int R) {
 }
 
 cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
-  const int tiles = (p.M + lowrank::kTile - 1) / lowrank::kTile;
   if (p.M <= lowrank::kFew) {
     p.v = workspace;
-    return lowrank::launch_form<true>(p, tiles, st);
+    return lowrank::launch_form<true>(p, st);
   }
   const size_t order = (static_cast<size_t>(p.M) * 4 + 15) / 16 * 16;
   p.perm = static_cast<int32_t*>(workspace);
   p.sid = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + order);
   p.v = static_cast<uint8_t*>(workspace) + 2 * order;
-  const int smem = (p.L + 1) * 4;
+  const int smem = 2 * (p.L + 1) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<lowrank::plan_kernel>((SIXBIT_MAX_ADAPTERS + 1) * 4);
+    const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
     if (e != cudaSuccess) return e;
   }
+  const int ctas = p.M > 4 * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
+  lowrank::Launch l(dim3(ctas), lowrank::kPlanThreads, smem, st, false, dim3(ctas));
   note_launch();
-  lowrank::plan_kernel<<<1, lowrank::kPlanThreads, smem, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : lowrank::launch_form<false>(p, tiles, st);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
+  return e != cudaSuccess ? e : lowrank::launch_form<false>(p, st);
 }
 
 }  // namespace sixbit
