@@ -47,11 +47,12 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 
 // Two s8 codes (bytes 0 and 2 of w) as bf16, exact: 128 + the low seven bits, less
-// 128, or 256 where the sign bit is set.
+// 128, or 256 where the sign bit is set.  (A bf16 FMA is one instruction here, a
+// bf16 subtraction some ten.)
 __device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, b = (w & 0x00800080u) | 0x43004300u;
+  const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, b = (w & 0x00800080u) | 0xC300C300u;
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x3F803F80u), "r"(b));
   return d;
 }
 
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
           uint4 b[RT];
 #pragma unroll
           for (int j = 0; j < RT; ++j)
-            if (j < tiles) b[j] = __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(8 * j) * p.K + k));
+            b[j] = j < tiles ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(8 * j) * p.K + k))
+                             : make_uint4(0, 0, 0, 0);
           uint32_t x[4][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -272,11 +274,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
             const uint32_t a0[4] = {x[2 * m][0], x[2 * m + 1][0], x[2 * m][1], x[2 * m + 1][1]};
             const uint32_t a1[4] = {x[2 * m][2], x[2 * m + 1][2], x[2 * m][3], x[2 * m + 1][3]};
 #pragma unroll
-            for (int j = 0; j < RT; ++j)
-              if (j < tiles) {
-                mma(acc[m][j], a0, b[j].x, b[j].y);
-                mma(acc[m][j], a1, b[j].z, b[j].w);
-              }
+            for (int j = 0; j < RT; ++j) {
+              mma(acc[m][j], a0, b[j].x, b[j].y);
+              mma(acc[m][j], a1, b[j].z, b[j].w);
+            }
           }
         }
       }
@@ -331,15 +332,17 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// v of 128 positions, for many rows: x and A_l pass through shared memory, 128 k a
-// stage, and are read there by four teams of warps, 32 rows a warp, a team for each
+// v of 64 positions, for many rows: x and A_l pass through shared memory, 128 k a
+// stage, and are read there by four pairs of warps, 32 rows a warp, a pair for each
 // quarter of the stage's k.  A run of one adapter within the block is a pass over
-// K.  Grid: blocks of positions x blocks of 8 RT ranks.
-constexpr int kBlock = 128, kStages = 4, kStageK = 128, kStagedThreads = 512;
+// K.  Grid: blocks of positions x blocks of 8 RT ranks.  (Two CTAs an SM, so that
+// one's MMAs run while the other waits at its stage's barrier.)
+constexpr int kBlock = 64, kStageK = 128, kStagedThreads = 256;
 template <bool INT8, int RT>
 struct Staged {
   static constexpr int kXRow = INT8 ? 128 : 256;  // bytes of a row's stage
   static constexpr int kX = kBlock * kXRow, kA = 8 * RT * 256, kStage = kX + kA;
+  static constexpr int kStages = INT8 ? 4 : 3;
   static constexpr int kP = 8 * RT + 4;           // floats of a row's sums
   static constexpr int kSums = kBlock * kP * 4;
   static constexpr int kBytes = kStages * kStage > kSums ? kStages * kStage : kSums;
@@ -349,15 +352,16 @@ struct Staged {
 __device__ __forceinline__ int chunk256(int row, int ch) { return row * 256 + ((ch ^ ((row & 1) << 2)) << 4); }
 __device__ __forceinline__ int chunk128(int row, int ch) { return row * 128 + ((ch ^ ((row & 3) << 1)) << 4); }
 template <bool INT8, int RT, int PARTS>
-__global__ void __launch_bounds__(kStagedThreads, 1) staged_kernel(const LowRankParams p) {
+__global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRankParams p) {
   using S = Staged<INT8, RT>;
+  constexpr int kStages = S::kStages;
   next_may_start();
   before_done();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int rows[kBlock], ids[kBlock];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, q = lane & 3;
-  const int wr = warp & 3, wk = warp >> 2;
+  const int wr = warp & 1, wk = warp >> 1;
   const int64_t pos0 = static_cast<int64_t>(blockIdx.x) * kBlock;
   const int r0 = blockIdx.y * 8 * RT, tiles = min(RT, (p.R - r0) / 8);
   if (tid < kBlock) {
@@ -380,39 +384,38 @@ __global__ void __launch_bounds__(kStagedThreads, 1) staged_kernel(const LowRank
       first = end;
       continue;
     }
-    // this thread's chunks of a stage: of x, then of A
+    // this thread's chunks of a stage: of x, and of A (bytes from the adapter's first)
     constexpr int kXC = S::kXRow / 16, kNX = kBlock * kXC / kStagedThreads;
     constexpr int kNA = (8 * RT * 16 + kStagedThreads - 1) / kStagedThreads;
-    const unsigned char* from[kNX + kNA];
-    int to[kNX + kNA];
-    bool in[kNX + kNA];
+    const unsigned char* x_from[kNX];
+    const unsigned char* a_from = reinterpret_cast<const unsigned char*>(p.a + (static_cast<size_t>(id) * p.R + r0) * p.K);
+    int a_at[kNA];
+    unsigned live = 0;  // bit i: x chunk i; ranks beyond R are zeros too
 #pragma unroll
     for (int i = 0; i < kNX; ++i) {
       const int c = tid + i * kStagedThreads, row = c / kXC, ch = c % kXC;
-      in[i] = row >= first && row < end;
+      if (row >= first && row < end) live |= 1u << i;
       const size_t at = static_cast<size_t>(rows[row]) * p.K;
-      from[i] = (INT8 ? reinterpret_cast<const unsigned char*>(p.codes + at) : reinterpret_cast<const unsigned char*>(p.x + at)) + ch * 16;
-      to[i] = INT8 ? chunk128(row, ch) : chunk256(row, ch);
+      x_from[i] = (INT8 ? reinterpret_cast<const unsigned char*>(p.codes + at) : reinterpret_cast<const unsigned char*>(p.x + at)) + ch * 16;
     }
 #pragma unroll
     for (int i = 0; i < kNA; ++i) {
       const int c = tid + i * kStagedThreads, row = c >> 4, ch = c & 15;
-      in[kNX + i] = row < 8 * tiles;
-      from[kNX + i] = reinterpret_cast<const unsigned char*>(
-          p.a + (static_cast<size_t>(id) * p.R + r0 + (row < 8 * tiles ? row : 0)) * p.K + ch * 8);
-      to[kNX + i] = S::kX + chunk256(row, ch);
+      if (row < 8 * tiles) live |= 1u << (kNX + i);
+      a_at[i] = row < 8 * tiles ? row * p.K * 2 + ch * 16 : 0;
     }
     auto fetch = [&](int st) {
-      unsigned char* base = smem + (st % kStages) * S::kStage;
+      unsigned char* to = smem + (st % kStages) * S::kStage;
 #pragma unroll
       for (int i = 0; i < kNX; ++i) {
-        copy16(base + to[i], from[i], in[i]);
-        from[i] += S::kXRow;
+        const int c = tid + i * kStagedThreads, row = c / kXC, ch = c % kXC;
+        copy16(to + (INT8 ? chunk128(row, ch) : chunk256(row, ch)), x_from[i] + st * S::kXRow, (live >> i) & 1);
       }
 #pragma unroll
-      for (int i = kNX; i < kNX + kNA; ++i) {
-        if (in[i]) copy16(base + to[i], from[i], true);
-        from[i] += 256;
+      for (int i = 0; i < kNA; ++i) {
+        const int c = tid + i * kStagedThreads;
+        if (8 * RT * 16 % kStagedThreads == 0 || c < 8 * RT * 16)
+          copy16(to + S::kX + chunk256(c >> 4, c & 15), a_from + a_at[i] + st * 256, (live >> (kNX + i)) & 1);
       }
     };
     for (int st = 0; st < kStages - 1; ++st) {
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1) staged_kernel(const LowRank
       uint4 b[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j)
-        if (j < tiles) b[j] = *reinterpret_cast<const uint4*>(as + chunk256(8 * j + g8, 4 * wk + q));
+        b[j] = *reinterpret_cast<const uint4*>(as + chunk256(8 * j + g8, 4 * wk + q));
       uint32_t x[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(kStagedThreads, 1) staged_kernel(const LowRank
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             const uint32_t a[4] = {x[2 * m][2 * h], x[2 * m + 1][2 * h], x[2 * m][2 * h + 1], x[2 * m + 1][2 * h + 1]};
-            if (j < tiles) mma(acc[m][j], a, h == 0 ? b[j].x : b[j].z, h == 0 ? b[j].y : b[j].w);
+            mma(acc[m][j], a, h == 0 ? b[j].x : b[j].z, h == 0 ? b[j].y : b[j].w);
           }
     }
     // the quarters of k, joined in the stages' place
@@ -543,7 +546,7 @@ __device__ __forceinline__ void finish1(const LowRankParams& p, size_t at, float
 // consecutive ranks of an MMA's 16, and column c of MMA j stands for
 // n0 + 8 (c / 2) + 2 j + c % 2, so that a lane ends up with eight consecutive
 // outputs of each of its two rows of a 16-row tile.  KS: 16-rank steps that are
-// held in registers; of a larger R as many at a time.
+// held in registers; R is 16 KS, or with BIG taken KS steps at a time.
 template <int KS>
 struct Strip {
   uint2 b[KS][4];
@@ -629,7 +632,7 @@ __device__ __forceinline__ void finish_tile(const LowRankParams& p, const float 
 }
 
 // Up to 32 rows.  Grid: groups of strips x 1 x slots (of the tile's runs).
-template <bool VEC, bool F32, int PARTS, int KS>
+template <bool VEC, bool F32, int PARTS, int KS, bool BIG>
 __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams p) {
   __shared__ int scratch[kFewWarps][32];
   __shared__ float turns[VEC ? 1 : kFewWarps][16 * 33];
@@ -656,12 +659,12 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams
       float acc[4][4] = {};
       if (id >= 0) {
         const unsigned char* v = static_cast<const unsigned char*>(p.v) + ((first + m + g8) * (p.R / 4) + q) * (8 * PARTS);
-        for (int s0 = 0; s0 < p.R / 16; s0 += KS) {
+        for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
           Strip<KS> strip;
           strip.load(p, id, n0, s0);
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
-            if (s0 + s >= p.R / 16) break;
+            if (BIG && s0 + s >= p.R / 16) break;
             uint2 lo[PARTS], hi[PARTS];
             load_v<PARTS>(v + (s0 + s) * 32 * PARTS, live[0], lo);
             load_v<PARTS>(v + (s0 + s) * 32 * PARTS + 8 * (p.R / 4) * 8 * PARTS, live[1], hi);
@@ -682,7 +685,7 @@ __host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 m
   const int bytes = R * 2 * PARTS;
   return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
 }
-template <bool VEC, bool F32, int PARTS, int KS>
+template <bool VEC, bool F32, int PARTS, int KS, bool BIG>
 __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
@@ -741,12 +744,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
       float acc[4][4] = {};
       if (id >= 0) {
         const unsigned char* from = vs + (at_now + g8) * stride + q * 8 * PARTS;
-        for (int s0 = 0; s0 < p.R / 16; s0 += KS) {
-          if (p.R / 16 > KS || held != id) strip.load(p, id, n0, s0);
+        for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
+          if (BIG || held != id) strip.load(p, id, n0, s0);
           held = id;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
-            if (s0 + s >= p.R / 16) break;
+            if (BIG && s0 + s >= p.R / 16) break;
             uint2 lo[PARTS], hi[PARTS];
             load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
             load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
@@ -815,16 +818,17 @@ template <bool FEW, bool INT8, int PARTS>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   if (p.R <= 16) return launch_shrink<FEW, INT8, 2, PARTS>(p, st);
   if (p.R <= 32) return launch_shrink<FEW, INT8, 4, PARTS>(p, st);
+  if (p.R == 48 || p.R == 96) return launch_shrink<FEW, INT8, 6, PARTS>(p, st);
   return launch_shrink<FEW, INT8, 8, PARTS>(p, st);
 }
 
-template <bool FEW, bool VEC, bool F32, int PARTS, int KS>
+template <bool FEW, bool VEC, bool F32, int PARTS, int KS, bool BIG>
 cudaError_t launch_expand(LowRankParams p, cudaStream_t st) {
   const int strips = (p.N + 31) / 32;
   note_launch();
   if constexpr (FEW) {
     Launch l(dim3((strips + kFewWarps - 1) / kFewWarps, 1, p.M), kFewWarps * 32, 0, st, true);
-    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, PARTS, KS>, p);
+    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, PARTS, KS, BIG>, p);
   } else {
     // chunks of kChunk positions, smaller ones where they would leave SMs idle
     const int groups = (strips + kWarps - 1) / kWarps;
@@ -834,18 +838,22 @@ cudaError_t launch_expand(LowRankParams p, cudaStream_t st) {
     p.chunks_per_cta = (chunks + 65534) / 65535;
     const auto bytes = [](int chunk, int R) { return (2 * chunk + 16) * 4 + chunk * v_stride<PARTS>(R); };
     const cudaError_t e =
-        set_smem_once<many_kernel<VEC, F32, PARTS, KS>>(bytes(kChunk, KS < 4 ? 16 * KS : SIXBIT_MAX_RANK));
+        set_smem_once<many_kernel<VEC, F32, PARTS, KS, BIG>>(bytes(kChunk, BIG ? SIXBIT_MAX_RANK : 16 * KS));
     if (e != cudaSuccess) return e;
     Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32, bytes(p.chunk, p.R), st, true);
-    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, PARTS, KS>, p);
+    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, PARTS, KS, BIG>, p);
   }
 }
 
 template <bool FEW, bool VEC, bool F32, int PARTS>
 cudaError_t launch_expand(const LowRankParams& p, cudaStream_t st) {
-  if (p.R <= 16) return launch_expand<FEW, VEC, F32, PARTS, 1>(p, st);
-  if (p.R <= 32) return launch_expand<FEW, VEC, F32, PARTS, 2>(p, st);
-  return launch_expand<FEW, VEC, F32, PARTS, 4>(p, st);
+  switch (p.R) {
+    case 16: return launch_expand<FEW, VEC, F32, PARTS, 1, false>(p, st);
+    case 32: return launch_expand<FEW, VEC, F32, PARTS, 2, false>(p, st);
+    case 48: return launch_expand<FEW, VEC, F32, PARTS, 3, false>(p, st);
+    case 64: return launch_expand<FEW, VEC, F32, PARTS, 4, false>(p, st);
+    default: return launch_expand<FEW, VEC, F32, PARTS, 4, true>(p, st);
+  }
 }
 
 template <bool FEW, int PARTS>
