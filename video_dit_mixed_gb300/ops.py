@@ -561,18 +561,17 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     else:
         pl = _ptr(logits, "logits", _F32, shape, dev)
     pb = None if bias is None else _ptr(bias, "bias", _F32, (e,), dev)
-    n = t * top_k
-    # one allocation: experts, weights, rows, token, offsets, and the workspace behind them
-    need = (int(_lib.sixbit_moe_route_workspace_bytes(t, e)) + 3) // 4
-    buf = _empty((4 * n + e + 1 + need,), _I32, logits.device, stream)
-    at = buf.data_ptr()
-    status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, bool(renormalize),
-                                   scale, at, at + 4 * n, at + 8 * n, at + 12 * n, at + 16 * n,
-                                   at + 16 * n + 4 * (e + 1) if need else None, st)
+    # experts, weights, rows and token in one allocation, offsets and the workspace (above a turn of 32 tokens) in another
+    buf = _empty((4, t, top_k), _I32, logits.device, stream)
+    need = 0 if t <= 32 else 152 * e  # sixbit_moe_route_workspace_bytes / 4
+    offsets = _empty((e + 1 + need,), _I32, logits.device, stream)
+    at, n4, po = buf.data_ptr(), 4 * t * top_k, offsets.data_ptr()
+    status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, renormalize, scale,
+                                   at, at + n4, at + 2 * n4, at + 3 * n4, po, po + 4 * (e + 1) if need else None, st)
     if status:
         check(status, "moe_route")
-    experts, weights, rows, token, offsets = buf[:4 * n + e + 1].split((n, n, n, n, e + 1))
-    return Routing(experts.view(t, top_k), weights.view(_F32).view(t, top_k), rows.view(t, top_k), token, offsets)
+    experts, weights, rows, token = buf.unbind()
+    return Routing(experts, weights.view(_F32), rows, token.view(-1), offsets[:e + 1] if need else offsets)
 
 
 def moe_combine(d: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None, out_f32: bool = False, err=None,
@@ -702,7 +701,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    need = int(_lib.sixbit_lowrank_workspace_bytes(m, r))
+    need = m * r * 6 + (0 if m <= 32 else 2 * ((4 * m + 15) // 16 * 16))  # sixbit_lowrank_workspace_bytes
     if ws is None:
         ws = _empty((need,), _U8, device, stream)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
