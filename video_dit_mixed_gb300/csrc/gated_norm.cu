@@ -8,7 +8,20 @@
 //   z = y . blockdiag(H_b / sqrt b),  s = max|z| / 127,  q = rint(z / s)
 //
 // s is the row's segment (text or frames, or a sample of the batch).
+//
+// A team of W warps takes a row, V chunks of 16 elements a lane, which stay in
+// registers from the load to the store; each warp's part of the next row is copied
+// to shared memory in the meantime.  (A warp has what it does for a row as such
+// -- three reductions, the factors, the addresses -- once for 512 V elements; with
+// four warps of one chunk a lane that was a third of all instructions.)  Up to
+// three factors a channel remain when those of the same place are joined: post_w .
+// gate, w . (1 + scale) and shift.  A CTA takes neighbouring rows and keeps those of
+// a window of segments, as many as fit, in shared memory; where its rows leave the
+// window it is filled anew, unless few rows would use it: they join them as they go.
+// An absent operand is a factor of 1 or a shift of 0, so that nothing branches.
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ctx_cache.h"
@@ -18,28 +31,61 @@
 namespace sixbit {
 namespace gnorm {
 
+constexpr int kWarps = 16;                // of a CTA
+constexpr int kFewRows = 600;
+constexpr int kSmemBytes = 224 * 1024;  // copies and factors
+
 struct Params {
   GatedNormParams g;
-  float inv_sqrt_b;
+  float inv_sqrt_b, inv_k;
+  int b;     // of the rotation
   int wide;  // x, res, sum_out, y are 32-byte aligned
+  int held;  // segments whose factors are in shared memory
+  int rows;  // of a CTA
 };
 
-// Sum (and maximum) over the CTA; two buffers, so that a later call's writes
-// need no barrier of their own.
-struct Joint {
-  float ss[2][16];
-  uint32_t mx[2][16];
-};
-__device__ __forceinline__ float cta_sum(float v, Joint& j, int buf, int nwarps) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (nwarps == 1) return v;
-  if ((threadIdx.x & 31) == 0) j.ss[buf][threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int i = 0; i < nwarps; ++i) v += j.ss[buf][i];
   return v;
 }
+
+// Sums and maxima of a team's warps; two buffers, so that the next row's writes need
+// no barrier of their own.
+template <int W>
+struct Joint {
+  float ss[2][W];
+  uint32_t mx[2][W];
+};
+template <int W>
+__device__ __forceinline__ void team_sync(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory");
+}
+template <int W>
+__device__ __forceinline__ float team_sum(float v, Joint<W>& j, int buf, int team, int rank) {
+  v = warp_sum(v);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) j.ss[buf][rank] = v;
+    team_sync<W>(team);
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += j.ss[buf][i];
+  }
+  return v;
+}
+// 1 / sqrt(ss / K + eps); NaN for a sum that is not finite.
+__device__ __forceinline__ float row_factor(float ss, float inv_k, float eps) {
+  const float r = rsqrtf(fmaf(ss, inv_k, eps));
+  return finite_sum(ss) ? r : __uint_as_float(0x7FC00000u);
+}
+// max over |u|, a NaN above all
+__device__ __forceinline__ float max_abs(const uint64_t (&u)[8], float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(f2_lo(u[i])), "f"(f2_hi(u[i])));
+  return m;
+}
+
 __device__ __forceinline__ void load16f(const float* v, float fill, uint64_t (&o)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = f2_pack(fill, fill);
@@ -54,241 +100,303 @@ __device__ __forceinline__ void load16f(const float* v, float fill, uint64_t (&o
   }
 }
 
-// Up to three factors a channel remain when those of the same place are joined:
-// post_w . gate, w . (1 + scale) and shift.  Each thread keeps those of its own
-// channels in shared memory (four 16-byte pieces a chunk, side by side across the
-// threads) and joins them anew when a row's segment differs from the last one's.
-struct Vectors {
-  float4* at;  // [3][V][4][threads]
-  int threads;
-  template <int V>
-  __device__ __forceinline__ float4* place(int which, int v) const {
-    return at + (static_cast<size_t>(which) * V + v) * 4 * threads + threadIdx.x;
+// The joined factors of segment `seg`, channels k .. k + 15: 0 the branch's, 1 the
+// norm's, 2 the shift.
+__device__ __forceinline__ void join(const GatedNormParams& g, int which, int seg, int k, uint64_t (&a)[8]) {
+  const size_t at = static_cast<size_t>(seg) * g.K + k;
+  if (which == 2) {
+    load16f(g.shift != nullptr ? g.shift + at : nullptr, 0.f, a);
+    return;
   }
-  template <int V>
-  __device__ __forceinline__ void put(int which, int v, const uint64_t (&w)[8]) const {
-    float4* o = place<V>(which, v);
+  uint64_t b[8];
+  if (which == 0) {
+    load16f(g.post_w != nullptr ? g.post_w + k : nullptr, 1.f, a);
+    load16f(g.gate != nullptr ? g.gate + at : nullptr, 1.f, b);
+  } else {
+    load16f(g.w != nullptr ? g.w + k : nullptr, 1.f, a);
+    load16f(g.scale != nullptr ? g.scale + at : nullptr, 0.f, b);
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i * threads] = make_float4(f2_lo(w[2 * i]), f2_hi(w[2 * i]), f2_lo(w[2 * i + 1]), f2_hi(w[2 * i + 1]));
-  }
-  template <int V>
-  __device__ __forceinline__ void get(int which, int v, uint64_t (&w)[8]) const {
-    const float4* o = place<V>(which, v);
+  for (int i = 0; i < 8; ++i) a[i] = which == 0 ? f2_mul(a[i], b[i]) : f2_fma(a[i], b[i], a[i]);
+}
+// They lie in shared memory as [segment][3][4][chunks] pieces of 16 bytes.
+__device__ __forceinline__ void put(float4* to, int chunks, const uint64_t (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = o[i * threads];
-      w[2 * i] = f2_pack(f.x, f.y);
-      w[2 * i + 1] = f2_pack(f.z, f.w);
-    }
+  for (int i = 0; i < 4; ++i)
+    to[i * chunks] = make_float4(f2_lo(w[2 * i]), f2_hi(w[2 * i]), f2_lo(w[2 * i + 1]), f2_hi(w[2 * i + 1]));
+}
+__device__ __forceinline__ void get(const float4* from, int chunks, uint64_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = from[i * chunks];
+    w[2 * i] = f2_pack(f.x, f.y);
+    w[2 * i + 1] = f2_pack(f.z, f.w);
   }
-};
+}
 
-// A CTA takes whole rows, every gridDim-th one, V chunks of 16 elements a thread,
-// with the next row's loads in flight while this one is reduced and stored.  The
-// row's second factor multiplies every y but the shift: without one it drops out
-// of the codes, and the sum and the maximum are one reduction.
-template <int B, int V>
-__global__ void __launch_bounds__(512) row_kernel(const Params p) {
-  const GatedNormParams& g = p.g;
-  if (g.mode_dev != nullptr && SIXBIT_MODE_OF(*g.mode_dev) != SIXBIT_MODE_INT8) return;
-  extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Joint post, pre, top;
-  const Vectors vec{reinterpret_cast<float4*>(smem), static_cast<int>(blockDim.x)};
-  const int chunks = g.K / kChunk, nwarps = blockDim.x >> 5;
-  const bool has_p = g.post_w != nullptr || g.gate != nullptr, has_w = g.w != nullptr || g.scale != nullptr;
-  const bool has_t = g.shift != nullptr, late = !has_t && g.y == nullptr;  // late: the factor goes to the scale
-  const float nan = __uint_as_float(0x7FC00000u);
-  uint32_t xr[V][8], rr[V][8];
-  int seg_next = 0;
-  auto load = [&](int row) {
-    seg_next = g.segment != nullptr ? __ldg(g.segment + row) : g.S > 1 ? row / g.rows_per_seg : 0;
-    const size_t base = static_cast<size_t>(row) * g.K;
+// The unscaled butterfly of blocks of b (0: none) across a warp's chunks.
+template <int V>
+__device__ __forceinline__ void rotate(uint64_t (&u)[V][8], int b) {
+  if (b == 0) return;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xr[v][i] = rr[v][i] = 0;
-      if (c < chunks) {
-        load32(g.x + base + static_cast<size_t>(c) * kChunk, p.wide, xr[v]);
-        if (g.res != nullptr) load32(g.res + base + static_cast<size_t>(c) * kChunk, p.wide, rr[v]);
-      }
-    }
-  };
-  auto join = [&](int seg) {
-    const size_t mod = static_cast<size_t>(seg) * g.K;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x, k = c * kChunk;
-      if (c >= chunks) continue;
-      uint64_t a[8], b[8];
-      if (has_p) {
-        load16f(g.post_w != nullptr ? g.post_w + k : nullptr, 1.f, a);
-        load16f(g.gate != nullptr ? g.gate + mod + k : nullptr, 1.f, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = f2_mul(a[i], b[i]);
-        vec.put<V>(0, v, a);
-      }
-      if (has_w) {
-        load16f(g.w != nullptr ? g.w + k : nullptr, 1.f, a);
-        load16f(g.scale != nullptr ? g.scale + mod + k : nullptr, 0.f, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = f2_fma(a[i], b[i], a[i]);
-        vec.put<V>(1, v, a);
-      }
-      if (has_t) {
-        load16f(g.shift + mod + k, 0.f, a);
-        vec.put<V>(2, v, a);
-      }
-    }
-  };
-  if (blockIdx.x < static_cast<unsigned>(g.M)) load(blockIdx.x);
-  int buf = 0, held = -1;
-  for (int row = blockIdx.x; row < g.M; row += gridDim.x, buf ^= 1) {
-    const size_t base = static_cast<size_t>(row) * g.K;
-    int seg = seg_next;
-    const bool bad = seg < 0 || seg >= g.S;
-    if (bad) {
-      seg = 0;
-      if (threadIdx.x == 0) set_error(g.err, SIXBIT_EDEVICE);
-    }
-    if (seg != held) join(seg);  // (a thread reads back what it wrote itself)
-    held = seg;
-    uint64_t u[V][8];
-    float rpost = 1.f;
-    uint64_t ss = 0;
+  for (int v = 0; v < V; ++v) fwht<16>(u[v]);
+  const int lane = threadIdx.x & 31;
+  for (int h = 1; h < b / kChunk; h <<= 1) {
+    const float sg = (lane & h) ? -1.f : 1.f;  // upper lane: other - mine
+    const uint64_t s2 = f2_pack(sg, sg);
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[v][i] = bad ? f2_pack(nan, nan) : f2_from_bf16x2(xr[v][i]);
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, static_cast<unsigned long long>(u[v][i]), h);
+        u[v][i] = f2_fma(u[v][i], s2, o);
+      }
+  }
+}
+
+template <int V, int W, bool STAGE>
+__global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
+  const GatedNormParams& g = p.g;
+  if (g.mode_dev != nullptr && SIXBIT_MODE_OF(*g.mode_dev) != SIXBIT_MODE_INT8) return;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ Joint<W> post[kWarps / W], pre[kWarps / W], top[kWarps / W];
+  __shared__ uint64_t arrived[kWarps];
+  constexpr int kPart = V * 32 * 32;  // bytes of a warp's part of a row
+  constexpr int kTeams = kWarps / W;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, rank = warp % W;
+  const int chunks = g.K / kChunk, c0 = rank * 32 * V + lane;  // this lane's: c0 + 32 v
+  unsigned char* part = smem + warp * (2 * kPart);             // x, then the residual
+  float4* vec = reinterpret_cast<float4*>(smem + (STAGE ? kWarps * 2 * kPart : 0));
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+  const int64_t row1 = min(row0 + p.rows, static_cast<int64_t>(g.M));
+  auto segment_of = [&](int64_t row) {
+    return g.segment != nullptr ? __ldg(g.segment + row) : g.S > 1 ? static_cast<int>(row) / g.rows_per_seg : 0;
+  };
+  // this warp's part of a row on its way to shared memory (one lane; the others are past their last reads of it)
+  auto fetch = [&](int64_t row) {
+    const int bytes = min(32 * V, chunks - rank * 32 * V) * 32;
+    const size_t at = static_cast<size_t>(row) * g.K + static_cast<size_t>(rank) * 32 * V * kChunk;
+    mbar_expect_tx(&arrived[warp], g.res != nullptr ? 2 * bytes : bytes);
+    bulk_load(part, g.x + at, bytes, &arrived[warp]);
+    if (g.res != nullptr) bulk_load(part + kPart, g.res + at, bytes, &arrived[warp]);
+  };
+  const bool copies = STAGE && rank * 32 * V < chunks;
+  if (STAGE) {
+    if (g.res == nullptr)
+      for (int i = lane; i < kPart / 16; i += 32) reinterpret_cast<uint4*>(part + kPart)[i] = make_uint4(0, 0, 0, 0);
+    if (lane == 0) {
+      mbar_init(&arrived[warp], 1);
+      fence_barrier_init();
+      if (copies && row0 + team < row1) fetch(row0 + team);
+    }
+    __syncwarp();
+  }
+  uint32_t buf = 0;
+  bool dead = false;  // a copy did not arrive in time: reported, and waited for no more
+
+  // One row; HELD: its factors are in shared memory from `mine` on.
+  auto process = [&](auto held, int64_t row, int seg, const float4* mine) {
+    constexpr bool HELD = decltype(held)::value;
+    auto factors = [&](int which, int v, uint64_t (&w)[8]) {
+      if constexpr (HELD)
+        get(mine + which * 4 * chunks + 32 * v, chunks, w);
+      else
+        join(g, which, seg, (c0 + 32 * v) * kChunk, w);
+    };
+    const size_t base = static_cast<size_t>(row) * g.K;
+    uint32_t xr[V][8], rr[V][8];
+    if (STAGE) {
+      if (copies && !dead && !mbar_wait(&arrived[warp], buf, nullptr)) {
+        dead = true;
+        set_error(g.err, SIXBIT_ETIMEOUT);
+      }
+    }
+    auto part_of = [&](const unsigned char* from, int v, uint32_t (&r)[8]) {
+      const uint4* q = reinterpret_cast<const uint4*>(from + (v * 32 + lane) * 32);
+      const uint4 a = q[0], b = q[1];
+      r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = c0 + 32 * v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xr[v][i] = rr[v][i] = 0;
+      if (c < chunks) {
+        if (STAGE)
+          part_of(part, v, xr[v]);
+        else
+          load32(g.x + base + static_cast<size_t>(c) * kChunk, p.wide, xr[v]);
+      }
+    }
+    if (!STAGE && g.res != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (c0 + 32 * v < chunks) load32(g.res + base + static_cast<size_t>(c0 + 32 * v) * kChunk, p.wide, rr[v]);
+    }
+    if (seg < 0 || seg >= g.S) {
+      seg = 0;
+      if (lane == 0) set_error(g.err, SIXBIT_EDEVICE);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xr[v][i] = 0x7FC07FC0u;  // (NaN)
+    }
+    uint64_t u[V][8], ss = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[v][i] = f2_from_bf16x2(xr[v][i]);
+    float rpost = 1.f;
     if (g.post_w != nullptr) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = f2_fma(u[v][i], u[v][i], ss);
-      const float sum = cta_sum(f2_lo(ss) + f2_hi(ss), post, buf, nwarps);
-      rpost = finite_sum(sum) ? rms_inv(sum, g.K, g.eps) : nan;
+      rpost = row_factor(team_sum<W>(f2_lo(ss) + f2_hi(ss), post[team], buf, team, rank), p.inv_k, g.eps);
       ss = 0;
     }
     const uint64_t rp = f2_pack(rpost, rpost), rs = f2_pack(g.res_scale, g.res_scale);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x;
-      if (c >= chunks) {
+      const int c = c0 + 32 * v;
+      if (c >= chunks) continue;  // (u is 0)
+      uint64_t w[8];
+      factors(0, v, w);
+      if (STAGE) part_of(part + kPart, v, rr[v]);
+      uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = 0;
-        continue;
+      for (int i = 0; i < 8; ++i) {
+        u[v][i] = f2_fma(f2_from_bf16x2(rr[v][i]), rs, f2_mul(f2_mul(u[v][i], rp), w[i]));
+        o[i] = f2_to_bf16x2(u[v][i]);
+        ss = f2_fma(u[v][i], u[v][i], ss);
       }
-      if (has_p) {
-        uint64_t w[8];
-        vec.get<V>(0, v, w);
+      if (g.sum_out != nullptr) store32(g.sum_out + base + static_cast<size_t>(c) * kChunk, p.wide, o);
+    }
+    if (STAGE) {
+      __syncwarp();
+      if (lane == 0 && copies && !dead && row + kTeams < row1) fetch(row + kTeams);
+    }
+    const float rpre = row_factor(team_sum<W>(f2_lo(ss) + f2_hi(ss), pre[team], buf, team, rank), p.inv_k, g.eps);
+    const uint64_t r2 = f2_pack(rpre, rpre);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = f2_mul(f2_mul(u[v][i], rp), w[i]);
-      }
-      if (g.res != nullptr) {
+    for (int v = 0; v < V; ++v) {
+      if (c0 + 32 * v >= chunks) continue;
+      uint64_t w[8], t[8];
+      factors(1, v, w);
+      factors(2, v, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[v][i] = f2_fma(f2_from_bf16x2(rr[v][i]), rs, u[v][i]);
-      }
-      if (g.sum_out != nullptr) {
+      for (int i = 0; i < 8; ++i) u[v][i] = f2_fma(f2_mul(u[v][i], r2), w[i], t[i]);
+    }
+    if (g.y != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = c0 + 32 * v;
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = f2_to_bf16x2(u[v][i]);
-        store32(g.sum_out + base + static_cast<size_t>(c) * kChunk, p.wide, o);
+        if (c < chunks) store32(g.y + base + static_cast<size_t>(c) * kChunk, p.wide, o);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = f2_fma(u[v][i], u[v][i], ss);
+      return;
     }
-    if (row + static_cast<int64_t>(gridDim.x) < g.M) load(row + gridDim.x);
-    float sum = f2_lo(ss) + f2_hi(ss), rpre = 1.f;
-    if (!late) {
-      sum = cta_sum(sum, pre, buf, nwarps);
-      rpre = finite_sum(sum) ? rms_inv(sum, g.K, g.eps) : nan;
-    }
-    const uint64_t r2 = f2_pack(rpre, rpre);
-    uint32_t mb = 0;
+    float m = 0.f;
+    rotate<V>(u, p.b);  // (every lane of the warp takes part)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x;
-      if (c < chunks) {
-        uint64_t w[8];
-        if (!late) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[v][i] = f2_mul(u[v][i], r2);
-        }
-        if (has_w) {
-          vec.get<V>(1, v, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[v][i] = f2_mul(u[v][i], w[i]);
-        }
-        if (has_t) {
-          vec.get<V>(2, v, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[v][i] = f2_add(u[v][i], w[i]);
-        }
-        if (g.y != nullptr) {
-          uint32_t o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = f2_to_bf16x2(u[v][i]);
-          store32(g.y + base + static_cast<size_t>(c) * kChunk, p.wide, o);
-        }
-      }
-      if (g.y == nullptr) {  // (every lane of the warp takes part)
-        fwht<B>(u[v]);
-        mb = max_bits(u[v], mb);
-      }
-    }
-    if (g.y != nullptr) continue;
-    mb = __reduce_max_sync(0xFFFFFFFFu, mb);
-    if (late) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    }
-    if (nwarps > 1) {
-      if ((threadIdx.x & 31) == 0) {
-        top.ss[buf][threadIdx.x >> 5] = sum;
-        top.mx[buf][threadIdx.x >> 5] = mb;
-      }
-      __syncthreads();
+    for (int v = 0; v < V; ++v) m = max_abs(u[v], m);
+    uint32_t mb = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m) & 0x7FFFFFFFu);
+    if constexpr (W > 1) {
+      if (lane == 0) top[team].mx[buf][rank] = mb;
+      team_sync<W>(team);
       mb = 0;
-      for (int i = 0; i < nwarps; ++i) mb = max(mb, top.mx[buf][i]);
-      if (late) {
-        sum = 0.f;
-        for (int i = 0; i < nwarps; ++i) sum += top.ss[buf][i];
-      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) mb = max(mb, top[team].mx[buf][i]);
     }
-    const RowOut o = late ? row_out(rms_inv(sum, g.K, g.eps) * p.inv_sqrt_b, finite_sum(sum), mb)
-                          : row_out(p.inv_sqrt_b, true, mb);
-    if (threadIdx.x == 0) g.row_scale[row] = o.scale;
+    const RowOut o = row_out(p.inv_sqrt_b, true, mb);
+    if (lane == 0 && rank == 0) g.row_scale[row] = o.scale;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = threadIdx.x + v * blockDim.x;
+      const int c = c0 + 32 * v;
       if (c < chunks) store_codes(g.codes + base + static_cast<size_t>(c) * kChunk, o, u[v]);
     }
+  };
+
+  int64_t row = row0 + team;
+  for (int64_t from = row0; from < row1;) {  // (the same windows in every warp)
+    int64_t to = row1;
+    int seg0 = 0;
+    bool fill = p.held > 0;
+    if (p.held > 0 && p.held < g.S) {
+      seg0 = min(max(segment_of(from), 0), g.S - p.held);
+      for (int64_t r = from; r < row1; r += 32) {
+        const int s = r + lane < row1 ? segment_of(r + lane) : seg0;
+        const uint32_t out = __ballot_sync(0xFFFFFFFFu, s >= 0 && s < g.S && (s < seg0 || s >= seg0 + p.held));
+        if (out != 0) {
+          to = r + __ffs(out) - 1;
+          break;
+        }
+      }
+      fill = to - from >= 2 * kTeams;
+    }
+    if (fill) {
+      __syncthreads();  // (the last window's rows are done)
+      for (int i = threadIdx.x; i < p.held * chunks; i += blockDim.x) {
+        const int seg = i / chunks, c = i % chunks;
+        uint64_t a[8];
+#pragma unroll
+        for (int which = 0; which < 3; ++which) {
+          join(g, which, seg0 + seg, c * kChunk, a);
+          put(vec + (static_cast<size_t>(seg) * 3 + which) * 4 * chunks + c, chunks, a);
+        }
+      }
+      __syncthreads();
+    }
+    for (; row < to; row += kTeams, buf ^= 1) {
+      const int seg = segment_of(row);
+      if (fill && seg >= seg0 && seg < seg0 + p.held)
+        process(std::true_type{}, row, seg, vec + static_cast<size_t>(seg - seg0) * 12 * chunks + c0);
+      else
+        process(std::false_type{}, row, seg, vec);
+    }
+    from = to;
   }
+  if (STAGE && dead) mbar_wait(&arrived[warp], buf, nullptr);  // (the copy in flight, once more with a limit)
 }
 
-template <int B, int V>
-cudaError_t launch_rows(const Params& p, int threads, cudaStream_t st) {
-  static ContextCache<int> cache[17];  // resident CTAs an SM, by warps
-  const int smem = 3 * V * 64 * threads;
-  int per_sm = 0;
-  cudaError_t e = set_smem_once<row_kernel<B, V>>(3 * V * 64 * 512);
+template <int V, int W, bool STAGE>
+cudaError_t launch_rows(Params& p, int64_t grid, cudaStream_t st) {
+  static_assert(kWarps % W == 0 && (W == 1 || kWarps / W <= 15), "a named barrier a team");
+  const cudaError_t e = set_smem_once<row_kernel<V, W, STAGE>>(kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = cache[threads / 32].get(&per_sm, [&](int* o) {
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(o, row_kernel<B, V>, threads, smem);
-  });
-  if (e != cudaSuccess) return e;
-  const int most = sm_count() * (per_sm > 0 ? per_sm : 1);
+  const GatedNormParams& g = p.g;
+  p.rows = static_cast<int>((static_cast<int64_t>(g.M) + grid - 1) / grid);
+  int smem = STAGE ? kWarps * 2 * V * 1024 : 0;
+  const int of_segment = 3 * g.K * 4;
+  p.held = 0;
+  if (p.rows > kWarps / W) {  // (with a row a team nothing is shared)
+    p.held = std::min(g.S, (kSmemBytes - smem) / of_segment);
+    smem += p.held * of_segment;
+  }
   note_launch();
-  row_kernel<B, V><<<p.g.M < most ? p.g.M : most, threads, smem, st>>>(p);
+  const int threads = p.rows == 1 ? 32 * W : 32 * kWarps;  // (one team has nothing to share a CTA with)
+  row_kernel<V, W, STAGE><<<static_cast<unsigned>((g.M + p.rows - 1) / p.rows), threads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <int B>
-cudaError_t launch(const Params& p, cudaStream_t st) {
-  const int chunks = p.g.K / kChunk;
-  const int v = chunks <= 256 ? 1 : 2;
-  const int threads = ((chunks + v - 1) / v + 31) / 32 * 32;
-  return v == 1 ? launch_rows<B, 1>(p, threads, st) : launch_rows<B, 2>(p, threads, st);
+cudaError_t launch(Params& p, cudaStream_t st) {
+  const int chunks = p.g.K / kChunk, sms = sm_count();
+  if (p.g.M < kFewRows) {  // one chunk a lane, a row a CTA: the shortest way through one row
+    if (chunks <= 32) return launch_rows<1, 1, false>(p, p.g.M, st);
+    if (chunks <= 64) return launch_rows<1, 2, false>(p, p.g.M, st);
+    if (chunks <= 128) return launch_rows<1, 4, false>(p, p.g.M, st);
+    if (chunks <= 256) return launch_rows<1, 8, false>(p, p.g.M, st);
+    if (chunks <= 512) return launch_rows<1, 16, false>(p, p.g.M, st);
+    return launch_rows<2, 16, false>(p, p.g.M, st);
+  }
+  if (chunks <= 32) return launch_rows<1, 1, true>(p, sms, st);
+  if (chunks <= 64) return launch_rows<2, 1, true>(p, sms, st);
+  if (chunks <= 128) return launch_rows<4, 1, true>(p, sms, st);
+  if (chunks <= 256) return launch_rows<4, 2, true>(p, sms, st);
+  if (chunks <= 512) return launch_rows<4, 4, true>(p, sms, st);
+  return launch_rows<4, 8, false>(p, sms, st);
 }
 
 }  // namespace gnorm
@@ -296,15 +404,12 @@ cudaError_t launch(const Params& p, cudaStream_t st) {
 cudaError_t launch_gated_norm(const GatedNormParams& g, int b, cudaStream_t st) {
   gnorm::Params p{};
   p.g = g;
+  p.inv_k = 1.f / static_cast<float>(g.K);
   p.inv_sqrt_b = b == 16 ? 0.25f : b == 64 ? 0.125f : b == 256 ? 0.0625f : 1.f;
   const auto a32 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31u) == 0; };
   p.wide = a32(g.x) && a32(g.res) && a32(g.sum_out) && a32(g.y);
-  switch (b) {
-    case 16: return gnorm::launch<16>(p, st);
-    case 64: return gnorm::launch<64>(p, st);
-    case 256: return gnorm::launch<256>(p, st);
-    default: return gnorm::launch<0>(p, st);
-  }
+  p.b = b;
+  return gnorm::launch(p, st);
 }
 
 }  // namespace sixbit
