@@ -213,8 +213,9 @@ struct CombineParams {
   uint16_t* Y;
   float* Yf;
   int32_t* err;
+  int wide;                      // set by the launch: rows are 32-byte aligned
 };
-cudaError_t launch_moe_combine(const CombineParams& p, cudaStream_t st);
+cudaError_t launch_moe_combine(CombineParams p, cudaStream_t st);
 
 // Low-rank adapters (sixbit_lowrank_add).
 struct LowRankParams {
