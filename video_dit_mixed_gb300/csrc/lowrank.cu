@@ -35,7 +35,8 @@ constexpr int kWarps = 8;
 constexpr int kUnit = 64;        // k of a warp's turn
 constexpr int kFew = kTile;      // rows that need no sorting kernel
 constexpr int kFewWarps = 4;
-constexpr int kChunk = 256;      // positions of a CTA that applies B
+constexpr int kChunk = 256;      // positions of a CTA that applies B, at most
+constexpr int kManyBytes = 112 * 1024;  // its shared memory: two on an SM
 constexpr int kStagedRows = 2048;  // from these rows on x and A pass through shared memory
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -518,9 +519,8 @@ __device__ __forceinline__ void add_f32(const uint4& w, uint64_t* v) {
   v[1] = f2_add(v[1], f2_pack(__uint_as_float(w.z), __uint_as_float(w.w)));
 }
 
-// Eight consecutive outputs of one row, 16-byte aligned, behind base and GELU.
-__device__ __forceinline__ void store8(const LowRankParams& p, size_t at, uint64_t* v) {
-  if (p.epilogue == SIXBIT_EPI_RESIDUAL) add_bf16(*reinterpret_cast<const uint4*>(p.residual + at), v);
+// Eight consecutive outputs of one row, 16-byte aligned.
+__device__ __forceinline__ void store8(const LowRankParams& p, size_t at, const uint64_t* v) {
   if (p.Yf != nullptr) {
     reinterpret_cast<float4*>(p.Yf + at)[0] = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
     reinterpret_cast<float4*>(p.Yf + at)[1] = make_float4(f2_lo(v[2]), f2_hi(v[2]), f2_lo(v[3]), f2_hi(v[3]));
@@ -529,18 +529,6 @@ __device__ __forceinline__ void store8(const LowRankParams& p, size_t at, uint64
         make_uint4(f2_to_bf16x2(v[0]), f2_to_bf16x2(v[1]), f2_to_bf16x2(v[2]), f2_to_bf16x2(v[3]));
   }
 }
-// One output.
-__device__ __forceinline__ void finish1(const LowRankParams& p, size_t at, float y) {
-  if (p.base_f32 != nullptr) y += p.base_f32[at];
-  if (p.base != nullptr) y += __uint_as_float(static_cast<uint32_t>(p.base[at]) << 16);
-  if (p.epilogue == SIXBIT_EPI_GELU) y = f2_lo(gelu_pair(f2_pack(y, y)));
-  if (p.epilogue == SIXBIT_EPI_RESIDUAL) y += __uint_as_float(static_cast<uint32_t>(p.residual[at]) << 16);
-  if (p.Yf != nullptr)
-    p.Yf[at] = y;
-  else
-    p.Y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-}
-
 // base + B_l v and the epilogue, a warp a strip of 32 columns from n0 on.  Ranks and
 // columns may stand in any order as long as the operands agree: a lane keeps four
 // consecutive ranks of an MMA's 16, and column c of MMA j stands for
@@ -589,50 +577,79 @@ __device__ __forceinline__ void load_v(const unsigned char* from, bool live, uin
     for (int w = 0; w < PARTS; ++w) v[w] = u[w];
   }
 }
-// The outputs of a tile of 16 rows.  VEC: 16-byte accesses; else through the warp's
-// `turn` [16][33], a row's 32 columns a lane each.
-template <bool VEC, bool F32>
-__device__ __forceinline__ void finish_tile(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
-                                            const bool (&live)[2], int n0, const Eight<F32> (&base)[2], float* turn) {
+// The outputs of a tile of 16 rows, columns n .. n + 7 of this lane's two.
+template <bool F32, bool RES>
+__device__ __forceinline__ void finish_rows(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
+                                            const bool (&live)[2], int n, const Eight<F32> (&base)[2],
+                                            const uint4 (&res)[2]) {
+  uint64_t y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = f2_pack(acc[i & 3][2 * (i >> 2)], acc[i & 3][2 * (i >> 2) + 1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (F32) {
+      add_f32(base[h].w[0], y + 4 * h);
+      add_f32(base[h].w[1], y + 4 * h + 2);
+    } else {
+      add_bf16(base[h].w[0], y + 4 * h);
+    }
+    if constexpr (RES) add_bf16(res[h], y + 4 * h);
+  }
+  if (!RES && p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (live[h] && n < p.N) store8(p, row[h] * p.N + n, y + 4 * h);
+}
+// The same for rows that are not 16-byte aligned, through the warp's `turn` [16][33]:
+// a lane has a column of all 16 rows, eight of them loaded before they are used.
+__device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
+                                          const bool (&live)[2], int n0, float* turn) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-  if constexpr (VEC) {
-    uint64_t y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = f2_pack(acc[i & 3][2 * (i >> 2)], acc[i & 3][2 * (i >> 2) + 1]);
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (F32) {
-        add_f32(base[h].w[0], y + 4 * h);
-        add_f32(base[h].w[1], y + 4 * h + 2);
-      } else {
-        add_bf16(base[h].w[0], y + 4 * h);
-      }
+    for (int j = 0; j < 4; ++j) {
+      turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j] = acc[j][2 * h];
+      turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j + 1] = acc[j][2 * h + 1];
+    }
+  __syncwarp();
+  const int n = n0 + lane;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    size_t at[8];
+    bool in[8];
+    float add[8] = {}, res[8] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at[i] = __shfl_sync(kAll, row[h], i * 4) * p.N + n;
+      in[i] = __shfl_sync(kAll, static_cast<int>(live[h]), i * 4) != 0 && n < p.N;
+      if (!in[i]) continue;
+      if (p.base_f32 != nullptr) add[i] = p.base_f32[at[i]];
+      if (p.base != nullptr) add[i] = __uint_as_float(static_cast<uint32_t>(p.base[at[i]]) << 16);
+      if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[i] = __uint_as_float(static_cast<uint32_t>(p.residual[at[i]]) << 16);
+    }
+    uint64_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = turn[(8 * h + 2 * i) * 33 + lane] + add[2 * i], b = turn[(8 * h + 2 * i + 1) * 33 + lane] + add[2 * i + 1];
+      y[i] = f2_pack(a + res[2 * i], b + res[2 * i + 1]);
     }
     if (p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (live[h] && n0 + 8 * q < p.N) store8(p, row[h] * p.N + n0 + 8 * q, y + 4 * h);
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j] = acc[j][2 * h];
-        turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j + 1] = acc[j][2 * h + 1];
-      }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const size_t r = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4);
-      const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4);
-      if (in && n0 + lane < p.N) finish1(p, r * p.N + n0 + lane, turn[i * 33 + lane]);
+    for (int i = 0; i < 8; ++i) {
+      if (!in[i]) continue;
+      const float o = (i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2]);
+      if (p.Yf != nullptr)
+        p.Yf[at[i]] = o;
+      else
+        p.Y[at[i]] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
     }
-    __syncwarp();
   }
+  __syncwarp();
 }
 
 // Up to 32 rows.  Grid: groups of strips x 1 x slots (of the tile's runs).
-template <bool VEC, bool F32, int PARTS, int KS, bool BIG>
+template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
 __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams p) {
   __shared__ int scratch[kFewWarps][32];
   __shared__ float turns[VEC ? 1 : kFewWarps][16 * 33];
@@ -650,11 +667,15 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams
       size_t row[2];
       bool live[2];
       Eight<F32> base[2] = {};
+      uint4 res[2] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         live[h] = g8 + 8 * h < count - m;
         row[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31));
-        if (VEC && live[h] && n0 + 8 * q < p.N) base[h].load(p, row[h] * p.N + n0 + 8 * q);
+        if (VEC && live[h] && n0 + 8 * q < p.N) {
+          base[h].load(p, row[h] * p.N + n0 + 8 * q);
+          if constexpr (RES) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n0 + 8 * q);
+        }
       }
       float acc[4][4] = {};
       if (id >= 0) {
@@ -672,29 +693,48 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams
           }
         }
       }
-      finish_tile<VEC, F32>(p, acc, row, live, n0, base, turns[VEC ? 0 : warp]);
+      if constexpr (VEC)
+        finish_rows<F32, RES>(p, acc, row, live, n0 + 8 * q, base, res);
+      else
+        turn_rows(p, acc, row, live, n0, turns[warp]);
     }
   }
 }
 
 // More rows.  Grid: groups of eight strips x chunks of positions, whose v, rows and
-// adapters the CTA keeps in shared memory; the next tile's base is asked for
-// before this one is multiplied.
+// tiles (up to 16 positions of one adapter) the CTA keeps in shared memory.  Each
+// lane copies the base, and the residual, of its outputs kAhead tiles ahead into
+// pieces of its own: with one tile ahead, in registers, 16 KB an SM were on their
+// way, a quarter of what it takes.
+constexpr int kAhead = 4;
 template <int PARTS>
 __host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 more than a multiple of 128 spares conflicts
   const int bytes = R * 2 * PARTS;
   return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
 }
-template <bool VEC, bool F32, int PARTS, int KS, bool BIG>
+// Pieces of 16 bytes a lane has of each row: base, residual.
+template <bool VEC, bool F32>
+__host__ __device__ constexpr int pieces_of(bool residual) {
+  return !VEC ? 0 : (F32 ? 2 : 1) + (residual ? 1 : 0);
+}
+template <bool VEC, bool F32, int PARTS>
+int many_bytes(int chunk, int R, bool residual) {
+  return (3 * chunk + 48) * 4 + (chunk + 16) * v_stride<PARTS>(R) + kWarps * kAhead * 1024 * pieces_of<VEC, F32>(residual);
+}
+template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
 __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
+  __shared__ int counts[kWarps];
+  constexpr int kPieces = pieces_of<VEC, F32>(RES);
+  const int padded = p.chunk + 16, stride = v_stride<PARTS>(p.R);
   int* rows = reinterpret_cast<int*>(smem);
-  int* ids = rows + p.chunk;  // [chunk + 16]
-  unsigned char* vs = smem + (2 * p.chunk + 16) * 4;
+  int* ids = rows + padded;
+  int* tiles = ids + padded;  // where each begins, and the last ends
+  unsigned char* vs = smem + (3 * p.chunk + 48) * 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-  const int n0 = (blockIdx.x * kWarps + warp) * 32;
-  const int stride = v_stride<PARTS>(p.R);
+  const int n0 = (blockIdx.x * kWarps + warp) * 32, n = n0 + 8 * q;
+  unsigned char* ring = vs + padded * stride + warp * kAhead * 1024 * kPieces + lane * 16;
   before_done();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   for (int chunk = 0; chunk < p.chunks_per_cta; ++chunk) {
@@ -707,43 +747,73 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
     for (int i = threadIdx.x; i < live_rows * pieces; i += kWarps * 32)
       copy16(vs + (i / pieces) * stride + (i % pieces) * 16, v + static_cast<size_t>(i) * 16, true);
     copies_commit();
-    for (int i = threadIdx.x; i < p.chunk + 16; i += kWarps * 32) {
-      if (i < p.chunk) rows[i] = i < live_rows ? p.perm[pos0 + i] : 0;
+    for (int i = threadIdx.x; i < padded; i += kWarps * 32) {
+      rows[i] = i < live_rows ? p.perm[pos0 + i] : 0;
       ids[i] = i < live_rows ? p.sid[pos0 + i] : INT_MAX;
+    }
+    __syncthreads();
+    {
+      const int i = threadIdx.x;  // (a chunk has no more positions than the CTA threads)
+      bool begins = false;
+      if (i < live_rows) {
+        int lo = 0, hi = i;  // the first position of this one's adapter: they ascend
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (ids[mid] < ids[i])
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        begins = ((i - lo) & 15) == 0;
+      }
+      const uint32_t mask = __ballot_sync(kAll, begins);
+      if (lane == 0) counts[warp] = __popc(mask);
+      __syncthreads();
+      int at = __popc(mask & ((1u << lane) - 1));
+      for (int w = 0; w < warp; ++w) at += counts[w];
+      if (begins) tiles[at] = i;
+      if (i == kWarps * 32 - 1) tiles[at + (begins ? 1 : 0)] = live_rows;
     }
     copies_wait<0>();
     __syncthreads();
     if (n0 >= p.N) continue;
-    Strip<KS> strip;
-    int held = -1;
-    // a tile: up to 16 positions of one adapter from `at` on
-    auto length = [&](int at) {
-      const int id = ids[at];
-      const uint32_t other = __ballot_sync(kAll, lane < 16 && ids[at + (lane & 15)] != id);
-      return other != 0 ? __ffs(other) - 1 : 16;
-    };
-    size_t row[2];
-    Eight<F32> base[2] = {};
-    auto ask = [&](int at, int count) {
+    int many = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        row[h] = static_cast<size_t>(rows[min(at + g8 + 8 * h, p.chunk - 1)]);
-        if (VEC && g8 + 8 * h < count && n0 + 8 * q < p.N) base[h].load(p, row[h] * p.N + n0 + 8 * q);
+    for (int w = 0; w < kWarps; ++w) many += counts[w];
+    auto ask = [&](int t) {
+      if constexpr (VEC) {
+        if (t < many && n < p.N) {
+          const int at = tiles[t], end = tiles[t + 1];
+          unsigned char* to = ring + (t % kAhead) * 1024 * kPieces;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int pos = at + g8 + 8 * h;
+            if (pos >= end) continue;
+            const size_t from = static_cast<size_t>(rows[pos]) * p.N + n;
+            if constexpr (F32) {
+              copy16(to + h * 512 * kPieces, p.base_f32 + from, true);
+              copy16(to + h * 512 * kPieces + 512, p.base_f32 + from + 4, true);
+            } else {
+              if (p.base != nullptr) copy16(to + h * 512 * kPieces, p.base + from, true);
+            }
+            if constexpr (RES) copy16(to + h * 512 * kPieces + 512 * (kPieces - 1), p.residual + from, true);
+          }
+        }
+        copies_commit();
       }
     };
-    int at = 0, count = length(0);
-    ask(at, count);
-    while (count > 0) {
-      const size_t row_now[2] = {row[0], row[1]};
-      const Eight<F32> base_now[2] = {base[0], base[1]};
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) ask(t);
+    Strip<KS> strip;
+    int held = -1;
+    for (int t = 0; t < many; ++t) {
+      const int at = tiles[t], count = tiles[t + 1] - at, id = ids[at];
       const bool live[2] = {g8 < count, g8 + 8 < count};
-      const int at_now = at, id = ids[at];
-      at += count;
-      count = at < live_rows ? length(at) : 0;
-      if (count > 0) ask(at, count);
+      size_t row[2] = {static_cast<size_t>(rows[at + g8]), static_cast<size_t>(rows[at + g8 + 8])};
       float acc[4][4] = {};
       if (id >= 0) {
-        const unsigned char* from = vs + (at_now + g8) * stride + q * 8 * PARTS;
+        // (rows of the MMA that are not live hold anything: they stay apart)
+        const unsigned char* from = vs + (at + g8) * stride + q * 8 * PARTS;
         for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
           if (BIG || held != id) strip.load(p, id, n0, s0);
           held = id;
@@ -751,14 +821,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
           for (int s = 0; s < KS; ++s) {
             if (BIG && s0 + s >= p.R / 16) break;
             uint2 lo[PARTS], hi[PARTS];
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, true, lo);
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, true, hi);
             step_mma<PARTS>(acc, lo, hi, strip.b[s]);
           }
         }
       }
-      finish_tile<VEC, F32>(p, acc, row_now, live, n0, base_now, turns[VEC ? 0 : warp]);
+      if constexpr (VEC) {
+        copies_wait<kAhead - 1>();
+        const unsigned char* mine = ring + (t % kAhead) * 1024 * kPieces;
+        Eight<F32> base[2] = {};
+        uint4 res[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (F32 || p.base != nullptr) {
+#pragma unroll
+            for (int i = 0; i < (F32 ? 2 : 1); ++i)
+              base[h].w[i] = *reinterpret_cast<const uint4*>(mine + h * 512 * kPieces + i * 512);
+          }
+          if constexpr (RES) res[h] = *reinterpret_cast<const uint4*>(mine + h * 512 * kPieces + 512 * (kPieces - 1));
+        }
+        ask(t + kAhead);
+        finish_rows<F32, RES>(p, acc, row, live, n, base, res);
+      } else {
+        turn_rows(p, acc, row, live, n0, turns[warp]);
+      }
     }
+    copies_wait<0>();
   }
 }
 
@@ -822,37 +911,38 @@ cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   return launch_shrink<FEW, INT8, 8, PARTS>(p, st);
 }
 
-template <bool FEW, bool VEC, bool F32, int PARTS, int KS, bool BIG>
+template <bool FEW, bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
 cudaError_t launch_expand(LowRankParams p, cudaStream_t st) {
   const int strips = (p.N + 31) / 32;
   note_launch();
   if constexpr (FEW) {
     Launch l(dim3((strips + kFewWarps - 1) / kFewWarps, 1, p.M), kFewWarps * 32, 0, st, true);
-    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, PARTS, KS, BIG>, p);
+    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
   } else {
-    // chunks of kChunk positions, smaller ones where they would leave SMs idle
+    // the largest chunks that let two CTAs share an SM, smaller ones where they would leave SMs idle
     const int groups = (strips + kWarps - 1) / kWarps;
     p.chunk = kChunk;
-    while (p.chunk > kTile && static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304) p.chunk /= 2;
+    while (p.chunk > kTile && (many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES) > kManyBytes ||
+                               static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304))
+      p.chunk /= 2;
     const int chunks = (p.M + p.chunk - 1) / p.chunk;
     p.chunks_per_cta = (chunks + 65534) / 65535;
-    const auto bytes = [](int chunk, int R) { return (2 * chunk + 16) * 4 + chunk * v_stride<PARTS>(R); };
-    const cudaError_t e =
-        set_smem_once<many_kernel<VEC, F32, PARTS, KS, BIG>>(bytes(kChunk, BIG ? SIXBIT_MAX_RANK : 16 * KS));
+    const cudaError_t e = set_smem_once<many_kernel<VEC, F32, RES, PARTS, KS, BIG>>(kManyBytes);
     if (e != cudaSuccess) return e;
-    Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32, bytes(p.chunk, p.R), st, true);
-    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, PARTS, KS, BIG>, p);
+    Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32,
+             many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES), st, true);
+    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
   }
 }
 
-template <bool FEW, bool VEC, bool F32, int PARTS>
+template <bool FEW, bool VEC, bool F32, bool RES, int PARTS>
 cudaError_t launch_expand(const LowRankParams& p, cudaStream_t st) {
   switch (p.R) {
-    case 16: return launch_expand<FEW, VEC, F32, PARTS, 1, false>(p, st);
-    case 32: return launch_expand<FEW, VEC, F32, PARTS, 2, false>(p, st);
-    case 48: return launch_expand<FEW, VEC, F32, PARTS, 3, false>(p, st);
-    case 64: return launch_expand<FEW, VEC, F32, PARTS, 4, false>(p, st);
-    default: return launch_expand<FEW, VEC, F32, PARTS, 4, true>(p, st);
+    case 16: return launch_expand<FEW, VEC, F32, RES, PARTS, 1, false>(p, st);
+    case 32: return launch_expand<FEW, VEC, F32, RES, PARTS, 2, false>(p, st);
+    case 48: return launch_expand<FEW, VEC, F32, RES, PARTS, 3, false>(p, st);
+    case 64: return launch_expand<FEW, VEC, F32, RES, PARTS, 4, false>(p, st);
+    default: return launch_expand<FEW, VEC, F32, RES, PARTS, 4, true>(p, st);
   }
 }
 
@@ -863,8 +953,11 @@ cudaError_t launch_both(const LowRankParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
   if (p.N % 8 != 0 || !a16(p.base) || !a16(p.base_f32) || !a16(p.residual) || !a16(p.Y) || !a16(p.Yf))
-    return launch_expand<FEW, false, false, PARTS>(p, st);
-  return p.base_f32 != nullptr ? launch_expand<FEW, true, true, PARTS>(p, st) : launch_expand<FEW, true, false, PARTS>(p, st);
+    return launch_expand<FEW, false, false, false, PARTS>(p, st);
+  const bool f32 = p.base_f32 != nullptr;
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL)
+    return f32 ? launch_expand<FEW, true, true, true, PARTS>(p, st) : launch_expand<FEW, true, false, true, PARTS>(p, st);
+  return f32 ? launch_expand<FEW, true, true, false, PARTS>(p, st) : launch_expand<FEW, true, false, false, PARTS>(p, st);
 }
 
 template <bool FEW>
