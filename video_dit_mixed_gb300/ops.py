@@ -561,17 +561,17 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     else:
         pl = _ptr(logits, "logits", _F32, shape, dev)
     pb = None if bias is None else _ptr(bias, "bias", _F32, (e,), dev)
-    # experts, weights, rows and token in one allocation, offsets and the workspace (above a turn of 32 tokens) in another
-    buf = _empty((4, t, top_k), _I32, logits.device, stream)
-    need = 0 if t <= 32 else 152 * e  # sixbit_moe_route_workspace_bytes / 4
-    offsets = _empty((e + 1 + need,), _I32, logits.device, stream)
-    at, n4, po = buf.data_ptr(), 4 * t * top_k, offsets.data_ptr()
+    # (tensors of their own: views into one allocation take twice the time on the host)
+    device, tk = logits.device, (t, top_k)
+    experts, weights, rows = _empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream)
+    token, offsets = _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream)
+    ws = None if t <= 32 else _empty((152 * e,), _I32, device, stream)  # sixbit_moe_route_workspace_bytes
     status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, renormalize, scale,
-                                   at, at + n4, at + 2 * n4, at + 3 * n4, po, po + 4 * (e + 1) if need else None, st)
+                                   experts.data_ptr(), weights.data_ptr(), rows.data_ptr(), token.data_ptr(),
+                                   offsets.data_ptr(), None if ws is None else ws.data_ptr(), st)
     if status:
         check(status, "moe_route")
-    experts, weights, rows, token = buf.unbind()
-    return Routing(experts, weights.view(_F32), rows, token.view(-1), offsets[:e + 1] if need else offsets)
+    return Routing(experts, weights, rows, token, offsets)
 
 
 def moe_combine(d: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None, out_f32: bool = False, err=None,
