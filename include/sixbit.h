@@ -645,8 +645,8 @@ enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 16384 };
  * base_f32 (in place).  M >= 0 (0: nothing is enqueued), 1 <= N <= 2^20,
  * K % 128 == 0, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, 1 <= L <= SIXBIT_MAX_ADAPTERS.  Codes, x_bf16,
  * lr_a, lr_b and the workspace 16-byte aligned, the others to their type.
- * workspace: device memory of sixbit_lowrank_workspace_bytes(M, R) bytes,
- * scratch.  With mode_dev, runs only when the mode word is INT8.
+ * workspace: device memory of sixbit_lowrank_workspace_bytes(M, R) bytes (NULL
+ * where that is 0), scratch.  With mode_dev, runs only when the mode word is INT8.
  */
 sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, const uint16_t* lr_a,
                                  const uint16_t* lr_b, const float* alpha, const int32_t* ids, int L, int M, int N,

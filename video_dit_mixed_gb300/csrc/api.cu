@@ -817,7 +817,8 @@ sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, c
   if (base != nullptr && base_f32 != nullptr) return SIXBIT_EINVAL;
   if (M == 0) return SIXBIT_OK;
   if ((x_bf16 == nullptr && (A == nullptr || A->i8_codes == nullptr || A->row_scale == nullptr)) || lr_a == nullptr ||
-      lr_b == nullptr || ids == nullptr || (Y == nullptr && Y_f32 == nullptr) || workspace == nullptr ||
+      lr_b == nullptr || ids == nullptr || (Y == nullptr && Y_f32 == nullptr) ||
+      (workspace == nullptr && lowrank_workspace(M, R) > 0) ||
       (epilogue == SIXBIT_EPI_RESIDUAL && residual == nullptr))
     return SIXBIT_EINVAL;
   if (!aligned16(x_bf16) || !aligned16(lr_a) || !aligned16(lr_b) || !aligned16(workspace) || !aligned_to(alpha, 4) ||

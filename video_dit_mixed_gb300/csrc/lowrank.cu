@@ -15,7 +15,8 @@
 //
 // Rows are taken in the order of their adapters, 32 positions a tile, so that an
 // MMA's rows share one however requests are mixed.  Up to 32 rows every warp sorts
-// them by itself; above, a counting sort by one CTA goes first.  The order of rows
+// them by itself, and one launch does both products; above, a counting sort by one
+// CTA goes first.  The order of rows
 // of one adapter is not fixed (atomics), and does not matter: a row's sums do not
 // depend on its place.
 #include <climits>
@@ -34,7 +35,6 @@ constexpr int kTile = 32;        // positions of a tile
 constexpr int kWarps = 8;
 constexpr int kUnit = 64;        // k of a warp's turn
 constexpr int kFew = kTile;      // rows that need no sorting kernel
-constexpr int kFewWarps = 4;
 constexpr int kChunk = 256;      // positions of a CTA that applies B, at most
 constexpr int kManyBytes = 112 * 1024;  // its shared memory: two on an SM
 constexpr int kStagedRows = 2048;  // from these rows on x and A pass through shared memory
@@ -164,31 +164,34 @@ struct Tile {
   int id, row;
   uint32_t heads;
 };
-template <bool FEW>
-__device__ __forceinline__ Tile tile_at(const LowRankParams& p, int64_t pos0, int* scratch, bool report) {
-  const int lane = threadIdx.x & 31;
-  Tile t;
-  t.id = INT_MAX;
-  t.row = 0;
-  if constexpr (FEW) {
-    const int id = lane < p.M ? adapter_of(p, lane, report) : INT_MAX;
-    int rank = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int o = __shfl_sync(kAll, id, i);
-      rank += o < id || (o == id && i < lane);
-    }
-    scratch[rank] = lane;
-    __syncwarp();
-    t.row = scratch[lane];
-    t.id = __shfl_sync(kAll, id, t.row);
-    if (t.id == INT_MAX) t.row = 0;
-  } else if (pos0 + lane < p.M) {
-    t.id = p.sid[pos0 + lane];
-    t.row = p.perm[pos0 + lane];
-  }
-  const int before = __shfl_up_sync(kAll, t.id, 1);
+__device__ __forceinline__ void mark_heads(Tile& t) {
+  const int lane = threadIdx.x & 31, before = __shfl_up_sync(kAll, t.id, 1);
   t.heads = __ballot_sync(kAll, t.id != INT_MAX && (lane == 0 || before != t.id));
+}
+__device__ __forceinline__ Tile tile_at(const LowRankParams& p, int64_t pos0) {
+  const int64_t pos = pos0 + (threadIdx.x & 31);
+  Tile t;
+  t.id = pos < p.M ? p.sid[pos] : INT_MAX;
+  t.row = pos < p.M ? p.perm[pos] : 0;
+  mark_heads(t);
+  return t;
+}
+// All rows, up to 32, sorted by the warp; scratch: 32 words of its own.
+__device__ __forceinline__ Tile tile_of_few(const LowRankParams& p, int* scratch, bool report) {
+  const int lane = threadIdx.x & 31, id = lane < p.M ? adapter_of(p, lane, report) : INT_MAX;
+  int rank = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int o = __shfl_sync(kAll, id, i);
+    rank += o < id || (o == id && i < lane);
+  }
+  scratch[rank] = lane;
+  __syncwarp();
+  Tile t;
+  t.row = scratch[lane];
+  t.id = __shfl_sync(kAll, id, t.row);
+  if (t.id == INT_MAX) t.row = 0;
+  mark_heads(t);
   return t;
 }
 // The run that begins at bit `first` of a tile: its length.
@@ -201,8 +204,8 @@ __device__ __forceinline__ int run_length(const Tile& t, int first) {
 // v as the second product takes it: for each position and four ranks PARTS times
 // four bf16.
 template <int PARTS>
-__device__ __forceinline__ void store_parts(const LowRankParams& p, int64_t pos, int r, float (&v)[4]) {
-  uint2* o = reinterpret_cast<uint2*>(p.v) + (pos * (p.R / 4) + r / 4) * PARTS;
+__device__ __forceinline__ void store_parts(unsigned char* to, float (&v)[4]) {
+  uint2* o = reinterpret_cast<uint2*>(to);
 #pragma unroll
   for (int s = 0; s < PARTS; ++s) {
     const uint2 w = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -212,21 +215,83 @@ __device__ __forceinline__ void store_parts(const LowRankParams& p, int64_t pos,
   }
 }
 
+template <int PARTS>
+__device__ __forceinline__ unsigned char* v_at(const LowRankParams& p, int64_t pos, int r) {
+  return static_cast<unsigned char*>(p.v) + (pos * (p.R / 4) + r / 4) * (8 * PARTS);
+}
+
+// One warp's share of A_l x for up to 32 rows: k units first, first + step, ..., 8 RT
+// ranks from `a` (rank g8 of them) on, of which `tiles` times eight exist.  The sums
+// go to `to` [kTile][8 RT + 4].
+template <bool INT8, int RT>
+__device__ __forceinline__ void sums_of(const LowRankParams& p, const uint16_t* a, int tiles, const size_t (&at)[4],
+                                        const bool (&live)[4], int count, int first, int step, float* to) {
+  constexpr int kP = 8 * RT + 4;
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+  float acc[2][RT][4] = {};
+  for (int u = first; u < p.K / kUnit; u += step) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 32 k; a lane keeps eight of them, four for each MMA
+      const int k = u * kUnit + 32 * h + 8 * q;
+      uint4 b[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        b[j] = j < tiles ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(8 * j) * p.K + k))
+                         : make_uint4(0, 0, 0, 0);
+      uint32_t x[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+        if (live[i]) {
+          if constexpr (INT8) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.codes + at[i] + k));
+            x[i][0] = codes_bf16(__byte_perm(w.x, 0, 0x4140));
+            x[i][1] = codes_bf16(__byte_perm(w.x, 0, 0x4342));
+            x[i][2] = codes_bf16(__byte_perm(w.y, 0, 0x4140));
+            x[i][3] = codes_bf16(__byte_perm(w.y, 0, 0x4342));
+          } else {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + at[i] + k));
+            x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (m == 1 && count <= 16) break;
+        const uint32_t a0[4] = {x[2 * m][0], x[2 * m + 1][0], x[2 * m][1], x[2 * m + 1][1]};
+        const uint32_t a1[4] = {x[2 * m][2], x[2 * m + 1][2], x[2 * m][3], x[2 * m + 1][3]};
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          mma(acc[m][j], a0, b[j].x, b[j].y);
+          mma(acc[m][j], a1, b[j].z, b[j].w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+        *reinterpret_cast<float2*>(&to[(16 * m + 4 * i + g8) * kP + 8 * j + 2 * q]) =
+            make_float2(acc[m][j][i], acc[m][j][i + 1]);
+}
+
 // v of one tile.  Grid: tiles x slots x splits; slot s takes the tile's runs s,
 // s + slots, ...; a cluster of `splits` CTAs and their warps share K, and their
 // sums meet in shared memory in a fixed order.  RT: tiles of eight ranks at a time.
-template <bool FEW, bool INT8, int RT, int PARTS>
+template <bool INT8, int RT, int PARTS>
 __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankParams p) {
   namespace cg = cooperative_groups;
   next_may_start();
-  if (!FEW) before_done();
+  before_done();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   extern __shared__ float part[];  // [kWarps][kTile][kP]
-  __shared__ int scratch[kWarps][32];
   constexpr int kP = 8 * RT + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
   const int64_t pos0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const Tile t = tile_at<FEW>(p, pos0, scratch[warp], blockIdx.y == 0 && blockIdx.z == 0 && warp == 0);
+  const Tile t = tile_at(p, pos0);
   uint32_t left = t.heads;
   for (int turn = 0; left != 0; ++turn, left &= left - 1) {
     const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first);
@@ -242,54 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
     for (int r0 = 0; r0 < p.R; r0 += 8 * RT) {
       const int tiles = min(RT, (p.R - r0) / 8);
       const uint16_t* a = p.a + (static_cast<size_t>(id) * p.R + r0 + g8) * p.K;
-      float acc[2][RT][4] = {};
-      for (int u = blockIdx.z * kWarps + warp; u < p.K / kUnit; u += gridDim.z * kWarps) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 32 k; a lane keeps eight of them, four for each MMA
-          const int k = u * kUnit + 32 * h + 8 * q;
-          uint4 b[RT];
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-            b[j] = j < tiles ? __ldg(reinterpret_cast<const uint4*>(a + static_cast<size_t>(8 * j) * p.K + k))
-                             : make_uint4(0, 0, 0, 0);
-          uint32_t x[4][4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
-            if (live[i]) {
-              if constexpr (INT8) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.codes + at[i] + k));
-                x[i][0] = codes_bf16(__byte_perm(w.x, 0, 0x4140));
-                x[i][1] = codes_bf16(__byte_perm(w.x, 0, 0x4342));
-                x[i][2] = codes_bf16(__byte_perm(w.y, 0, 0x4140));
-                x[i][3] = codes_bf16(__byte_perm(w.y, 0, 0x4342));
-              } else {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + at[i] + k));
-                x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
-              }
-            }
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (m == 1 && count <= 16) break;
-            const uint32_t a0[4] = {x[2 * m][0], x[2 * m + 1][0], x[2 * m][1], x[2 * m + 1][1]};
-            const uint32_t a1[4] = {x[2 * m][2], x[2 * m + 1][2], x[2 * m][3], x[2 * m + 1][3]};
-#pragma unroll
-            for (int j = 0; j < RT; ++j) {
-              mma(acc[m][j], a0, b[j].x, b[j].y);
-              mma(acc[m][j], a1, b[j].z, b[j].w);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; i += 2)
-            *reinterpret_cast<float2*>(&part[(warp * kTile + 16 * m + 4 * i + g8) * kP + 8 * j + 2 * q]) =
-                make_float2(acc[m][j][i], acc[m][j][i + 1]);
+      sums_of<INT8, RT>(p, a, tiles, at, live, count, blockIdx.z * kWarps + warp, gridDim.z * kWarps, part + warp * kTile * kP);
       const auto cluster = cg::this_cluster();
       if (gridDim.z > 1)
         cluster.sync();
@@ -307,11 +325,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
             v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
           }
         }
-        const int row = FEW ? scratch[0][first + n] : p.perm[pos0 + first + n];
+        const int row = p.perm[pos0 + first + n];
         const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * (p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] *= f;
-        store_parts<PARTS>(p, pos0 + first + n, r0 + r, v);
+        store_parts<PARTS>(v_at<PARTS>(p, pos0 + first + n, r0 + r), v);
       }
       if (gridDim.z > 1)
         cluster.sync();
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRank
       const float4 f = *reinterpret_cast<const float4*>(&sums[n * S::kP + r]);
       const float by = (INT8 ? __ldg(p.row_scale + rows[n]) : 1.f) * alpha;
       float v[4] = {f.x * by, f.y * by, f.z * by, f.w * by};
-      store_parts<PARTS>(p, pos0 + n, r0 + r, v);
+      store_parts<PARTS>(v_at<PARTS>(p, pos0 + n, r0 + r), v);
     }
     __syncthreads();
     first = end;
@@ -648,38 +666,102 @@ __device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&
   __syncwarp();
 }
 
-// Up to 32 rows.  Grid: groups of strips x 1 x slots (of the tile's runs).
-template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
-__global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams p) {
-  __shared__ int scratch[kFewWarps][32];
-  __shared__ float turns[VEC ? 1 : kFewWarps][16 * 33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-  const int n0 = (blockIdx.x * kFewWarps + warp) * 32;
-  before_done();
+template <int PARTS>
+__host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 more than a multiple of 128 spares conflicts
+  const int bytes = R * 2 * PARTS;
+  return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
+}
+// Up to 32 rows: everything in one launch.  A cluster of eight CTAs takes one of the
+// batch's runs and a share of the columns: its 64 warps split K, their sums meet in
+// shared memory (the warps' of a CTA, then the CTAs' through the cluster), every CTA
+// keeps v in parts, and its warps go through their strips.  Grid: 8 shares of the
+// columns x runs (a cluster without one ends).
+constexpr int kCluster = 8;
+template <int PARTS, int RT>
+constexpr int few_bytes(int R) {
+  return kWarps * kTile * (8 * RT + 4) * 4 + kTile * v_stride<PARTS>(R);
+}
+template <bool VEC, bool INT8, int PARTS, int KS, bool BIG>
+__global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p) {
+  namespace cg = cooperative_groups;
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
-  if (n0 >= p.N) return;
-  const Tile t = tile_at<true>(p, 0, scratch[warp], false);
+  extern __shared__ __align__(16) float part[];  // [kWarps][kTile][kP], then v's parts
+  __shared__ int scratch[kWarps][32];
+  __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
+  constexpr int RT = 2 * KS, kP = 8 * RT + 4;
+  unsigned char* vs = reinterpret_cast<unsigned char*>(part + kWarps * kTile * kP);
+  const auto cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+  const int rank = blockIdx.x % kCluster, stride = v_stride<PARTS>(p.R);
+  const Tile t = tile_of_few(p, scratch[warp], blockIdx.x == 0 && blockIdx.y == 0 && warp == 0);
   uint32_t left = t.heads;
-  for (int turn = 0; left != 0; ++turn, left &= left - 1) {
-    if (turn % gridDim.z != blockIdx.z) continue;
-    const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
+  for (unsigned turn = 0; turn < blockIdx.y; ++turn) left &= left - 1;
+  if (left == 0) return;  // (the same in the whole cluster)
+  const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
+  if (id >= 0) {
+    size_t at[4];
+    bool live[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      live[i] = g8 + 8 * i < count;
+      at[i] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + g8 + 8 * i) & 31)) * p.K;
+    }
+    const float alpha = p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f;
+    for (int r0 = 0; r0 < p.R; r0 += 8 * RT) {
+      const int tiles = min(RT, (p.R - r0) / 8), quads = 2 * tiles;
+      sums_of<INT8, RT>(p, p.a + (static_cast<size_t>(id) * p.R + r0 + g8) * p.K, tiles, at, live, count,
+                        rank * kWarps + warp, kCluster * kWarps, part + warp * kTile * kP);
+      __syncthreads();
+      for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
+        float4* mine = reinterpret_cast<float4*>(&part[(i / quads) * kP + i % quads * 4]);
+        float4 v = *mine;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 f = mine[w * kTile * kP / 4];
+          v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+        }
+        *mine = v;
+      }
+      cluster.sync();
+      for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
+        const int n = i / quads, r = i % quads * 4, row = scratch[0][first + n];
+        float v[4] = {};
+#pragma unroll
+        for (int z = 0; z < kCluster; ++z) {
+          const float4 f = *reinterpret_cast<const float4*>(&cluster.map_shared_rank(part, z)[n * kP + r]);
+          v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+        }
+        const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * alpha;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] *= f;
+        store_parts<PARTS>(vs + n * stride + (r0 + r) * (2 * PARTS), v);
+      }
+      cluster.sync();  // (no CTA writes its sums again, or leaves, while another reads them)
+    }
+  }
+  for (int n0 = (blockIdx.x * kWarps + warp) * 32; n0 < p.N; n0 += gridDim.x * kWarps * 32) {
+    const int n = n0 + 8 * q;
     for (int m = 0; m < count; m += 16) {
       size_t row[2];
       bool live[2];
-      Eight<F32> base[2] = {};
+      Eight<true> wide[2] = {};
+      Eight<false> base[2] = {};
       uint4 res[2] = {};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         live[h] = g8 + 8 * h < count - m;
         row[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31));
-        if (VEC && live[h] && n0 + 8 * q < p.N) {
-          base[h].load(p, row[h] * p.N + n0 + 8 * q);
-          if constexpr (RES) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n0 + 8 * q);
+        if (VEC && live[h] && n < p.N) {
+          if (p.base_f32 != nullptr)
+            wide[h].load(p, row[h] * p.N + n);
+          else
+            base[h].load(p, row[h] * p.N + n);
+          if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n);
         }
       }
       float acc[4][4] = {};
       if (id >= 0) {
-        const unsigned char* v = static_cast<const unsigned char*>(p.v) + ((first + m + g8) * (p.R / 4) + q) * (8 * PARTS);
+        const unsigned char* from = vs + (m + g8) * stride + q * 8 * PARTS;
         for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
           Strip<KS> strip;
           strip.load(p, id, n0, s0);
@@ -687,16 +769,26 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams
           for (int s = 0; s < KS; ++s) {
             if (BIG && s0 + s >= p.R / 16) break;
             uint2 lo[PARTS], hi[PARTS];
-            load_v<PARTS>(v + (s0 + s) * 32 * PARTS, live[0], lo);
-            load_v<PARTS>(v + (s0 + s) * 32 * PARTS + 8 * (p.R / 4) * 8 * PARTS, live[1], hi);
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
+            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
             step_mma<PARTS>(acc, lo, hi, strip.b[s]);
           }
         }
       }
-      if constexpr (VEC)
-        finish_rows<F32, RES>(p, acc, row, live, n0 + 8 * q, base, res);
-      else
+      if constexpr (VEC) {
+        if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
+          if (p.base_f32 != nullptr)
+            finish_rows<true, true>(p, acc, row, live, n, wide, res);
+          else
+            finish_rows<false, true>(p, acc, row, live, n, base, res);
+        } else if (p.base_f32 != nullptr) {
+          finish_rows<true, false>(p, acc, row, live, n, wide, res);
+        } else {
+          finish_rows<false, false>(p, acc, row, live, n, base, res);
+        }
+      } else {
         turn_rows(p, acc, row, live, n0, turns[warp]);
+      }
     }
   }
 }
@@ -707,11 +799,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const LowRankParams
 // pieces of its own: with one tile ahead, in registers, 16 KB an SM were on their
 // way, a quarter of what it takes.
 constexpr int kAhead = 4;
-template <int PARTS>
-__host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 more than a multiple of 128 spares conflicts
-  const int bytes = R * 2 * PARTS;
-  return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
-}
 // Pieces of 16 bytes a lane has of each row: base, residual.
 template <bool VEC, bool F32>
 __host__ __device__ constexpr int pieces_of(bool residual) {
@@ -875,123 +962,136 @@ struct Launch {
   }
 };
 
-template <bool FEW, bool INT8, int RT, int PARTS>
+template <bool VEC, bool INT8, int PARTS, int KS, bool BIG>
+cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
+  const int smem = few_bytes<PARTS, 2 * KS>(p.R);
+  const cudaError_t e =
+      set_smem_once<few_kernel<VEC, INT8, PARTS, KS, BIG>>(few_bytes<PARTS, 2 * KS>(BIG ? SIXBIT_MAX_RANK : 16 * KS));
+  if (e != cudaSuccess) return e;
+  // a strip a warp, as far as all runs' clusters together come to about two CTAs an SM
+  const int strips = (p.N + 31) / 32, most = 304 / kCluster / p.M > 0 ? 304 / kCluster / p.M : 1;
+  const int shares = (strips + kCluster * kWarps - 1) / (kCluster * kWarps);
+  Launch l(dim3(kCluster * (shares < most ? shares : most), p.M), kWarps * 32, smem, st, false, dim3(kCluster));
+  note_launch();
+  return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, INT8, PARTS, KS, BIG>, p);
+}
+
+template <bool VEC, bool INT8, int PARTS>
+cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
+  switch (p.R) {
+    case 16: return launch_few<VEC, INT8, PARTS, 1, false>(p, st);
+    case 32: return launch_few<VEC, INT8, PARTS, 2, false>(p, st);
+    case 48: return launch_few<VEC, INT8, PARTS, 3, false>(p, st);
+    case 64: return launch_few<VEC, INT8, PARTS, 4, false>(p, st);
+    default: return launch_few<VEC, INT8, PARTS, 4, true>(p, st);
+  }
+}
+
+template <bool INT8, int RT, int PARTS>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
-  if constexpr (!FEW) {
-    if (p.M >= kStagedRows) {
-      constexpr int smem = Staged<INT8, RT>::kBytes;
-      const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
-      if (e != cudaSuccess) return e;
-      Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT)), kStagedThreads, smem, st, true);
-      note_launch();
-      return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT, PARTS>, p);
-    }
+  if (p.M >= kStagedRows) {
+    constexpr int smem = Staged<INT8, RT>::kBytes;
+    const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
+    if (e != cudaSuccess) return e;
+    Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT)), kStagedThreads, smem, st, true);
+    note_launch();
+    return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT, PARTS>, p);
   }
   constexpr int smem = kWarps * kTile * (8 * RT + 4) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<shrink_kernel<FEW, INT8, RT, PARTS>>(smem);
+    const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT, PARTS>>(smem);
     if (e != cudaSuccess) return e;
   }
-  // about two CTAs an SM: first a CTA for each of a tile's runs, then K over clusters
-  const int tiles = (p.M + kTile - 1) / kTile, rows = p.M < 32 ? p.M : FEW ? 32 : 4;
-  const int most = 304 / tiles > 0 ? 304 / tiles : 1, slots = most < rows ? most : rows;
+  // about two CTAs an SM: first up to four for a tile's runs, then K over clusters
+  const int tiles = (p.M + kTile - 1) / kTile, most = 304 / tiles > 0 ? 304 / tiles : 1, slots = most < 4 ? most : 4;
   const int turns = (p.K / kUnit + kWarps - 1) / kWarps, left = most / slots > 0 ? most / slots : 1;
   int splits = turns < left ? turns : left;
-  if (splits > 8) splits = 8;
-  Launch l(dim3(tiles, slots, splits), kWarps * 32, smem, st, !FEW, dim3(1, 1, splits));
+  if (splits > kCluster) splits = kCluster;
+  Launch l(dim3(tiles, slots, splits), kWarps * 32, smem, st, true, dim3(1, 1, splits));
   note_launch();
-  return cudaLaunchKernelEx(&l.cfg, shrink_kernel<FEW, INT8, RT, PARTS>, p);
+  return cudaLaunchKernelEx(&l.cfg, shrink_kernel<INT8, RT, PARTS>, p);
 }
 
-template <bool FEW, bool INT8, int PARTS>
+template <bool INT8, int PARTS>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
-  if (p.R <= 16) return launch_shrink<FEW, INT8, 2, PARTS>(p, st);
-  if (p.R <= 32) return launch_shrink<FEW, INT8, 4, PARTS>(p, st);
-  if (p.R == 48 || p.R == 96) return launch_shrink<FEW, INT8, 6, PARTS>(p, st);
-  return launch_shrink<FEW, INT8, 8, PARTS>(p, st);
+  if (p.R <= 16) return launch_shrink<INT8, 2, PARTS>(p, st);
+  if (p.R <= 32) return launch_shrink<INT8, 4, PARTS>(p, st);
+  if (p.R == 48 || p.R == 96) return launch_shrink<INT8, 6, PARTS>(p, st);
+  return launch_shrink<INT8, 8, PARTS>(p, st);
 }
 
-template <bool FEW, bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
-cudaError_t launch_expand(LowRankParams p, cudaStream_t st) {
-  const int strips = (p.N + 31) / 32;
-  note_launch();
-  if constexpr (FEW) {
-    Launch l(dim3((strips + kFewWarps - 1) / kFewWarps, 1, p.M), kFewWarps * 32, 0, st, true);
-    return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
-  } else {
-    // the largest chunks that let two CTAs share an SM, smaller ones where they would leave SMs idle
-    const int groups = (strips + kWarps - 1) / kWarps;
-    p.chunk = kChunk;
-    while (p.chunk > kTile && (many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES) > kManyBytes ||
-                               static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304))
-      p.chunk /= 2;
-    const int chunks = (p.M + p.chunk - 1) / p.chunk;
-    p.chunks_per_cta = (chunks + 65534) / 65535;
-    const cudaError_t e = set_smem_once<many_kernel<VEC, F32, RES, PARTS, KS, BIG>>(kManyBytes);
-    if (e != cudaSuccess) return e;
-    Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32,
-             many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES), st, true);
-    return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
-  }
-}
-
-template <bool FEW, bool VEC, bool F32, bool RES, int PARTS>
-cudaError_t launch_expand(const LowRankParams& p, cudaStream_t st) {
-  switch (p.R) {
-    case 16: return launch_expand<FEW, VEC, F32, RES, PARTS, 1, false>(p, st);
-    case 32: return launch_expand<FEW, VEC, F32, RES, PARTS, 2, false>(p, st);
-    case 48: return launch_expand<FEW, VEC, F32, RES, PARTS, 3, false>(p, st);
-    case 64: return launch_expand<FEW, VEC, F32, RES, PARTS, 4, false>(p, st);
-    default: return launch_expand<FEW, VEC, F32, RES, PARTS, 4, true>(p, st);
-  }
-}
-
-template <bool FEW, int PARTS>
-cudaError_t launch_both(const LowRankParams& p, cudaStream_t st) {
-  const cudaError_t e = p.codes != nullptr ? launch_shrink<FEW, true, PARTS>(p, st)
-                                           : launch_shrink<FEW, false, PARTS>(p, st);
+template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
+cudaError_t launch_many(LowRankParams p, cudaStream_t st) {
+  // the largest chunks that let two CTAs share an SM, smaller ones where they would leave SMs idle
+  const int groups = ((p.N + 31) / 32 + kWarps - 1) / kWarps;
+  p.chunk = kChunk;
+  while (p.chunk > kTile && (many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES) > kManyBytes ||
+                             static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304))
+    p.chunk /= 2;
+  const int chunks = (p.M + p.chunk - 1) / p.chunk;
+  p.chunks_per_cta = (chunks + 65534) / 65535;
+  const cudaError_t e = set_smem_once<many_kernel<VEC, F32, RES, PARTS, KS, BIG>>(kManyBytes);
   if (e != cudaSuccess) return e;
-  const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
-  if (p.N % 8 != 0 || !a16(p.base) || !a16(p.base_f32) || !a16(p.residual) || !a16(p.Y) || !a16(p.Yf))
-    return launch_expand<FEW, false, false, false, PARTS>(p, st);
-  const bool f32 = p.base_f32 != nullptr;
-  if (p.epilogue == SIXBIT_EPI_RESIDUAL)
-    return f32 ? launch_expand<FEW, true, true, true, PARTS>(p, st) : launch_expand<FEW, true, false, true, PARTS>(p, st);
-  return f32 ? launch_expand<FEW, true, true, false, PARTS>(p, st) : launch_expand<FEW, true, false, false, PARTS>(p, st);
+  Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32,
+           many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES), st, true);
+  note_launch();
+  return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
 }
 
-template <bool FEW>
-cudaError_t launch_form(const LowRankParams& p, cudaStream_t st) {
-  return p.Yf != nullptr ? launch_both<FEW, 3>(p, st) : launch_both<FEW, 2>(p, st);
+template <bool VEC, bool F32, bool RES, int PARTS>
+cudaError_t launch_many(const LowRankParams& p, cudaStream_t st) {
+  switch (p.R) {
+    case 16: return launch_many<VEC, F32, RES, PARTS, 1, false>(p, st);
+    case 32: return launch_many<VEC, F32, RES, PARTS, 2, false>(p, st);
+    case 48: return launch_many<VEC, F32, RES, PARTS, 3, false>(p, st);
+    case 64: return launch_many<VEC, F32, RES, PARTS, 4, false>(p, st);
+    default: return launch_many<VEC, F32, RES, PARTS, 4, true>(p, st);
+  }
+}
+
+template <int PARTS>
+cudaError_t launch(const LowRankParams& p, cudaStream_t st) {
+  const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+  const bool vec = p.N % 8 == 0 && a16(p.base) && a16(p.base_f32) && a16(p.residual) && a16(p.Y) && a16(p.Yf);
+  const bool int8 = p.codes != nullptr, f32 = p.base_f32 != nullptr;
+  if (p.M <= kFew) {
+    if (vec) return int8 ? launch_few<true, true, PARTS>(p, st) : launch_few<true, false, PARTS>(p, st);
+    return int8 ? launch_few<false, true, PARTS>(p, st) : launch_few<false, false, PARTS>(p, st);
+  }
+  const cudaError_t e = int8 ? launch_shrink<true, PARTS>(p, st) : launch_shrink<false, PARTS>(p, st);
+  if (e != cudaSuccess) return e;
+  if (!vec) return launch_many<false, false, false, PARTS>(p, st);
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL)
+    return f32 ? launch_many<true, true, true, PARTS>(p, st) : launch_many<true, false, true, PARTS>(p, st);
+  return f32 ? launch_many<true, true, false, PARTS>(p, st) : launch_many<true, false, false, PARTS>(p, st);
 }
 
 }  // namespace lowrank
 
 size_t lowrank_workspace(int M, int R) {
-  // v in up to three parts; above kFew rows the rows' order and their adapters
+  // v in up to three parts, the rows' order and their adapters
   const size_t rows = static_cast<size_t>(M), order = (rows * 4 + 15) / 16 * 16;
-  return rows * R * 6 + (M > lowrank::kFew ? 2 * order : 0);
+  return M > lowrank::kFew ? rows * R * 6 + 2 * order : 0;
 }
 
 cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
-  if (p.M <= lowrank::kFew) {
-    p.v = workspace;
-    return lowrank::launch_form<true>(p, st);
-  }
-  const size_t order = (static_cast<size_t>(p.M) * 4 + 15) / 16 * 16;
-  p.perm = static_cast<int32_t*>(workspace);
-  p.sid = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + order);
-  p.v = static_cast<uint8_t*>(workspace) + 2 * order;
-  const int smem = 2 * (p.L + 1) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
+  if (p.M > lowrank::kFew) {
+    const size_t order = (static_cast<size_t>(p.M) * 4 + 15) / 16 * 16;
+    p.perm = static_cast<int32_t*>(workspace);
+    p.sid = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + order);
+    p.v = static_cast<uint8_t*>(workspace) + 2 * order;
+    const int smem = 2 * (p.L + 1) * 4;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
+      if (e != cudaSuccess) return e;
+    }
+    const int ctas = p.M > 4 * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
+    lowrank::Launch l(dim3(ctas), lowrank::kPlanThreads, smem, st, false, dim3(ctas));
+    note_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
     if (e != cudaSuccess) return e;
   }
-  const int ctas = p.M > 4 * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
-  lowrank::Launch l(dim3(ctas), lowrank::kPlanThreads, smem, st, false, dim3(ctas));
-  note_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
-  return e != cudaSuccess ? e : lowrank::launch_form<false>(p, st);
+  return p.Yf != nullptr ? lowrank::launch<3>(p, st) : lowrank::launch<2>(p, st);
 }
 
 }  // namespace sixbit

@@ -701,14 +701,15 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    need = m * r * 6 + (0 if m <= 32 else 2 * ((4 * m + 15) // 16 * 16))  # sixbit_lowrank_workspace_bytes
+    need = 0 if m <= 32 else m * r * 6 + 2 * ((4 * m + 15) // 16 * 16)  # sixbit_lowrank_workspace_bytes
     if ws is None:
-        ws = _empty((need,), _U8, device, stream)
+        if need:
+            ws = _empty((need,), _U8, device, stream)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
     status = _lib.sixbit_lowrank_add(ca, px, pa, pb, pal, pi, count, m, n, k, r, p0, p0f,
                                      None if mode_dev is None else _word(mode_dev, "mode_dev", dev), epilogue, pr, py,
-                                     pf, ws.data_ptr(), None if err is None else _word(err, "err", dev), st)
+                                     pf, None if ws is None else ws.data_ptr(), None if err is None else _word(err, "err", dev), st)
     if status:
         check(status, "lowrank_add")
     return out
