@@ -604,8 +604,8 @@ enum { SIXBIT_MAX_TOP_K = 32, SIXBIT_MAX_GROUPS = 32 };
  * T >= 0 (0: offsets are zeroed), 1 <= E <= SIXBIT_MAX_EXPERTS,
  * 1 <= k <= SIXBIT_MAX_TOP_K, T k < 2^31, groups in [1, SIXBIT_MAX_GROUPS] divides
  * E, 1 <= top_groups <= groups, k <= top_groups E / groups, factor finite.
- * workspace: device memory of sixbit_moe_route_workspace_bytes(T, E) bytes (NULL
- * where that is 0), scratch.
+ * workspace: device memory of sixbit_moe_route_workspace_bytes(T, E) bytes, 16-byte
+ * aligned (NULL where that is 0), scratch.
  */
 sixbit_status sixbit_moe_route(const float* logits, const uint16_t* logits_bf16, const float* bias, int T, int E, int k,
                                int score, int groups, int top_groups, int group_best, int renormalize, float factor,

@@ -60,9 +60,9 @@ def test_moe_route(lib, p):
                       dict(experts=None), dict(w=None), dict(rows=None), dict(token=None), dict(off=None),
                       dict(t=33, ws=None), dict(t=0, off=None)]),
             (EALIGN, [dict(l=p + 2), dict(lb=p + 1), dict(bias=p + 2), dict(experts=p + 1), dict(w=p + 2),
-                      dict(rows=p + 2), dict(token=p + 2), dict(off=p + 2), dict(ws=p + 2)]))
+                      dict(rows=p + 2), dict(token=p + 2), dict(off=p + 2), dict(ws=p + 8)]))
     assert lib.sixbit_moe_route_workspace_bytes(1, 8) == 0 and lib.sixbit_moe_route_workspace_bytes(0, 8) == 0
-    assert lib.sixbit_moe_route_workspace_bytes(32, 8) == 0 and lib.sixbit_moe_route_workspace_bytes(33, 8) == 152 * 8 * 4
+    assert lib.sixbit_moe_route_workspace_bytes(32, 8) == 0 and lib.sixbit_moe_route_workspace_bytes(33, 9) == 304 * 12 * 4
 
 
 def test_moe_combine(lib, p):

@@ -726,7 +726,7 @@ sixbit_status sixbit_gated_rmsnorm_quant(const uint16_t* X, const uint16_t* resi
 
 size_t sixbit_moe_route_workspace_bytes(int T, int E) {
   if (T <= kRouteTurn || E <= 0) return 0;
-  return static_cast<size_t>(kRouteRuns) * static_cast<size_t>(E) * 4;
+  return static_cast<size_t>(kRouteRuns) * ((static_cast<size_t>(E) + 3) / 4 * 4) * 4;
 }
 
 sixbit_status sixbit_moe_route(const float* logits, const uint16_t* logits_bf16, const float* bias, int T, int E, int k,
@@ -747,8 +747,9 @@ sixbit_status sixbit_moe_route(const float* logits, const uint16_t* logits_bf16,
   for (const void* q : {static_cast<const void*>(logits), static_cast<const void*>(bias),
                         static_cast<const void*>(experts), static_cast<const void*>(weights),
                         static_cast<const void*>(rows), static_cast<const void*>(token),
-                        static_cast<const void*>(offsets), static_cast<const void*>(workspace)})
+                        static_cast<const void*>(offsets)})
     if (!aligned_to(q, 4)) return SIXBIT_EALIGN;
+  if (!aligned16(workspace)) return SIXBIT_EALIGN;
   if (!aligned_to(logits_bf16, 2)) return SIXBIT_EALIGN;
   const sixbit_status s = check_device();
   if (s != SIXBIT_OK) return s;

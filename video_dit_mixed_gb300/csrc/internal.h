@@ -184,9 +184,9 @@ struct GatedNormParams {
 };
 cudaError_t launch_gated_norm(const GatedNormParams& g, int b, cudaStream_t st);
 
-// Routing (sixbit_moe_route).  counts: workspace, [kRouteRuns][E].
+// Routing (sixbit_moe_route).  counts: workspace, [kRouteRuns][pitch].
 constexpr int kRouteTurn = 32;   // tokens of a turn; up to these one CTA does all and needs no workspace
-constexpr int kRouteRuns = 152;  // runs of tokens, a CTA each: one an SM
+constexpr int kRouteRuns = 304;  // runs of tokens, a CTA each: two an SM
 struct RouteParams {
   const float* logits;           // [T][E], or
   const uint16_t* logits_bf16;
@@ -199,7 +199,8 @@ struct RouteParams {
   int32_t* token;                // [T k]
   int32_t* offsets;              // [E + 1]
   int32_t* counts;
-  int tokens_per_cta;            // set by the launch
+  int tokens_per_cta;            // set by the launch, as are log2 of the lanes that look through a group
+  int team, pitch;               // and E rounded up to four
 };
 cudaError_t launch_moe_route(RouteParams p, cudaStream_t st);
 

@@ -77,9 +77,9 @@ __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 // The k largest of the warp's keys (N a lane, 0: absent), lower numbers first
 // among equals: lane j's `mine` is the j-th expert.  CHECK: true if no two
 // consecutive ones, the last chosen and the next included, are within `tol` +
-// `rel` |key|.
+// `rel` |key|, and the last chosen in `least`.
 template <int N, bool CHECK, typename O>
-__device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, int* mine) {
+__device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, int* mine, float* least) {
   const int lane = threadIdx.x & 31;
   O best = 0;
   int slot = 0;
@@ -103,8 +103,8 @@ __device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, 
       if (top == 0) break;  // (nothing is left beyond the last)
       const float v = value_of(static_cast<uint32_t>(top));
       if (j > 0 && !(last - v > tol + rel * fabsf(last))) clear = false;
-      last = v;
       if (j == k) break;
+      last = v;
     }
     const unsigned who = best == top ? static_cast<unsigned>(lane + 32 * slot) : kAll;
     const int e = static_cast<int>(__reduce_min_sync(kAll, who));
@@ -116,6 +116,7 @@ __device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, 
       refresh();
     }
   }
+  *least = last;
   return clear;
 }
 
@@ -124,14 +125,14 @@ template <bool CHECK, typename F>
 __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys, float tol, float rel, uint32_t* kept) {
   using O = typename OrdOf<F>::type;
   const int lane = threadIdx.x & 31, size = p.E / p.groups;
-  O score = 0;
   __syncwarp();
-  if (lane < p.groups) {
-    O a = 0, b = 0;  // the two largest; a lane starts at its own number, so that lanes read different banks
-    F fa = 0, fb = 0;
-    int i = lane % size;
-    for (int n = 0; n < size; ++n) {
-      const F v = keys[lane * size + i];
+  // 1 << p.team lanes a group, each every so many keys of it; their two largest are joined in a tree
+  const int team = 1 << p.team, g = lane >> p.team, sub = lane & (team - 1);
+  O a = 0, b = 0;
+  F fa = 0, fb = 0;
+  if (g < p.groups) {
+    for (int i = sub; i < size; i += team) {
+      const F v = keys[g * size + i];
       const O o = ordered(v);
       if (o > a) {
         b = a, fb = fa;
@@ -139,10 +140,23 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys,
       } else if (o > b) {
         b = o, fb = v;
       }
-      i = i + 1 == size ? 0 : i + 1;
     }
-    score = ordered(p.best > 1 && size > 1 ? fa + fb : fa);
   }
+  for (int h = team >> 1; h > 0; h >>= 1) {
+    const F xa = __shfl_xor_sync(kAll, fa, h), xb = __shfl_xor_sync(kAll, fb, h);
+    const O oa = __shfl_xor_sync(kAll, a, h), ob = __shfl_xor_sync(kAll, b, h);
+    if (oa > a) {
+      const bool mine = a > ob;
+      b = mine ? a : ob, fb = mine ? fa : xb;
+      a = oa, fa = xa;
+    } else if (oa > b) {
+      b = oa, fb = xa;
+    }
+  }
+  // lane g: group g's
+  const int from = (lane << p.team) & 31;
+  a = __shfl_sync(kAll, a, from), fa = __shfl_sync(kAll, fa, from), fb = __shfl_sync(kAll, fb, from);
+  O score = lane < p.groups ? ordered(p.best > 1 && size > 1 ? fa + fb : fa) : O(0);
   uint32_t bits = 0;
   O top = 0;
   for (int j = 0; j < p.top_groups; ++j) {
@@ -161,14 +175,21 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys,
   return clear;
 }
 
+// What FP32 left open of a token: everything (all), or the order of the experts
+// whose keys are not clearly below the last chosen (bit i: expert lane + 32 i).
+struct Open {
+  bool all;
+  uint32_t listed;
+};
+
 // One token's experts (lane j: the j-th), from its logits l.  F: the type that
 // keys are computed in; CHECK: false is returned where F is too narrow.
 template <int N, bool CHECK, typename F>
-__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], float lmax, F* keys, int* mine) {
+__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], float lmax, F* keys, int* mine,
+                                       Open* open) {
   using O = typename OrdOf<F>::type;
   const int lane = threadIdx.x & 31;
   const bool by_logit = p.bias == nullptr;
-  O key[N];
   F v[N];
   float tol = 0.f;
   if (!by_logit || p.groups > 1) {
@@ -182,12 +203,13 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
       sum = warp_sum(sum);
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = sum == F(0) ? F(0) : v[i] / sum;
-      // a term is 4 units off by its exponential and 0.4 by its argument, the sum by that and its N + 5 additions
-      tol = 0x1p-24f * 2.f * (N + 18);
+      // units of 2^-24: a term is 2 off by its exponential and 0.4 by its argument, the sum by that and its N + 5
+      // additions, the quotient 1
+      tol = 0x1p-24f * 2.f * (N + 12);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] = F(1) / (F(1) + exp_of(-static_cast<F>(l[i])));
-      tol = 0x1p-24f * 2.f * 8;
+      tol = 0x1p-24f * 6.f;  // (0.5 by the exponential, two roundings)
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -195,7 +217,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
       if (p.bias != nullptr && e < p.E) v[i] += static_cast<F>(__ldg(p.bias + e));
     }
   }
-  const float rel = 0x1p-24f * 8;
+  const float rel = 0x1p-24f * 3;  // (the bias joins with half a unit of the key)
   bool clear = true;
   uint32_t kept = kAll;
   if (p.groups > 1) {
@@ -205,6 +227,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
     clear = keep_groups<CHECK>(p, keys, tol, rel, &kept);
   }
   const int size = p.E / p.groups;
+  float least = 0.f;
   if (by_logit) {
     uint32_t lk[N];
 #pragma unroll
@@ -212,15 +235,28 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
       const int e = lane + 32 * i;
       lk[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(l[i]) : 0u;
     }
-    top_k<N, false>(lk, p.k, 0.f, 0.f, mine);
+    top_k<N, false>(lk, p.k, 0.f, 0.f, mine, &least);
+    if (CHECK) open->all = true;
     return clear;
   }
+  O key[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = lane + 32 * i;
     key[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(v[i]) : O(0);
   }
-  return top_k<N, CHECK>(key, p.k, tol, rel, mine) && clear;
+  const bool order = top_k<N, CHECK>(key, p.k, tol, rel, mine, &least);
+  if (CHECK && !(order && clear)) {
+    const float below = least - (tol + rel * fabsf(least));
+    open->all = !clear || p.score == SIXBIT_SCORE_SOFTMAX || !(fabsf(below) < INFINITY);
+    open->listed = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = lane + 32 * i;
+      if (e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) && !(v[i] < F(below))) open->listed |= 1u << i;
+    }
+  }
+  return order && clear;
 }
 
 __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e) {
@@ -229,15 +265,52 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e
                                   : __ldg(p.logits + at);
 }
 
-// A call of its own: its registers (two a key) are not the fast path's.
+// A token again in FP64, a call of its own: its registers (two a key) are not the
+// fast path's.  With sigmoid scores only the listed experts, up to four a lane (an
+// exponential is some 60 FP64 instructions).
 template <int N>
-__device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax, double* keys) {
-  float l[N];
+__device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax, double* keys, bool all, uint32_t listed) {
   const int lane = threadIdx.x & 31;
+  int mine = 0;
+  if (!all && !__any_sync(kAll, __popc(listed) > 4)) {
+    uint64_t key[4] = {};
+    int number[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (__all_sync(kAll, listed == 0)) break;
+      if (listed != 0) {
+        const int e = lane + 32 * (__ffs(listed) - 1);
+        listed &= listed - 1;
+        number[j] = e;
+        key[j] = ordered(1.0 / (1.0 + exp(-static_cast<double>(logit_at(p, t, e)))) + static_cast<double>(__ldg(p.bias + e)));
+      }
+    }
+    for (int j = 0; j < p.k; ++j) {
+      uint64_t best = 0;
+      int slot = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          slot = i;
+        }
+      const uint64_t top = warp_max(best);
+      int e = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i == slot) e = number[i];
+      const int first = static_cast<int>(__reduce_min_sync(kAll, best == top ? static_cast<unsigned>(e) : kAll));
+      if (lane == j) mine = first;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (best == top && e == first && i == slot) key[i] = 0;
+    }
+    return mine;
+  }
+  float l[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
-  int mine = 0;
-  choose<N, false, double>(p, l, lmax, keys, &mine);
+  choose<N, false, double>(p, l, lmax, keys, &mine, nullptr);
   return mine;
 }
 
@@ -334,8 +407,9 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
       }
       const float lmax = value_of(warp_max(top));
       int mine = 0;
-      if (!choose<N, true, float>(p, l, lmax, reinterpret_cast<float*>(keys), &mine))
-        mine = choose64<N>(p, t, lmax, keys);
+      Open open;
+      if (!choose<N, true, float>(p, l, lmax, reinterpret_cast<float*>(keys), &mine, &open))
+        mine = choose64<N>(p, t, lmax, keys, open.all, open.listed);
       const bool live = lane < p.k;
       const float w = weight_of<N>(p, l, lmax, live ? logit_at(p, t, mine) : -INFINITY, live);
       if (live) {
@@ -360,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
     __syncthreads();
   }
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.E + e] = run[e];
+    for (int e = threadIdx.x; e < p.pitch; e += kThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.pitch + e] = e < p.E ? run[e] : 0;
     return;
   }
   scan(run, p.E, part);
@@ -381,18 +455,34 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteParams p) {
   int* before = all + p.E + 1;              // [E]
   for (int e = threadIdx.x; e < p.E; e += kThreads) all[e] = before[e] = 0;
   __syncthreads();
-  const int runs = gridDim.x, me = blockIdx.x;
-  const int lanes = p.E < kThreads ? kThreads / p.E : 1;  // threads of an expert
-  for (int i = threadIdx.x; i < p.E * lanes; i += kThreads) {
-    const int e = i % p.E, first = i / p.E;
-    int a = 0, b = 0;
-    for (int c = first; c < runs; c += lanes) {
-      const int n = p.counts[static_cast<size_t>(c) * p.E + e];
-      a += n;
-      if (c < me) b += n;
+  // four experts a thread and every so many runs of them, eight loads at once
+  const int runs = gridDim.x, me = blockIdx.x, quads = p.pitch / 4;
+  const int teams = min(kThreads / quads, 16), team = threadIdx.x / quads, q = threadIdx.x % quads;
+  if (team < teams) {
+    int a[4] = {}, b[4] = {};
+    for (int c0 = team; c0 < runs; c0 += 8 * teams) {
+      int4 n[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[i] = make_int4(0, 0, 0, 0);
+        if (c0 + i * teams < runs) n[i] = *reinterpret_cast<const int4*>(p.counts + static_cast<size_t>(c0 + i * teams) * p.pitch + 4 * q);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int v[4] = {n[i].x, n[i].y, n[i].z, n[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j] += v[j];
+          if (c0 + i * teams < me) b[j] += v[j];
+        }
+      }
     }
-    atomicAdd(&all[e], a);
-    atomicAdd(&before[e], b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * q + j < p.E) {
+        atomicAdd(&all[4 * q + j], a[j]);
+        atomicAdd(&before[4 * q + j], b[j]);
+      }
   }
   __syncthreads();
   scan(all, p.E, part);
@@ -443,6 +533,9 @@ cudaError_t launch_moe_route(RouteParams p, cudaStream_t st) {
     p.tokens_per_cta = static_cast<int>((per + route::kWarps - 1) / route::kWarps * route::kWarps);
     ctas = static_cast<int>((static_cast<int64_t>(p.T) + p.tokens_per_cta - 1) / p.tokens_per_cta);
   }
+  p.pitch = (p.E + 3) / 4 * 4;
+  p.team = 0;
+  while (p.groups << (p.team + 1) <= 32) ++p.team;
   if (p.E <= 32) return route::launch<1>(p, ctas, st);
   if (p.E <= 64) return route::launch<2>(p, ctas, st);
   if (p.E <= 128) return route::launch<4>(p, ctas, st);

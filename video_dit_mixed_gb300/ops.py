@@ -565,7 +565,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     device, tk = logits.device, (t, top_k)
     experts, weights, rows = _empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream)
     token, offsets = _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream)
-    ws = None if t <= 32 else _empty((152 * e,), _I32, device, stream)  # sixbit_moe_route_workspace_bytes
+    ws = None if t <= 32 else _empty((304 * ((e + 3) // 4 * 4),), _I32, device, stream)  # sixbit_moe_route_workspace_bytes
     status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, renormalize, scale,
                                    experts.data_ptr(), weights.data_ptr(), rows.data_ptr(), token.data_ptr(),
                                    offsets.data_ptr(), None if ws is None else ws.data_ptr(), st)
