@@ -618,11 +618,41 @@ __device__ __forceinline__ void finish_rows(const LowRankParams& p, const float 
   for (int h = 0; h < 2; ++h)
     if (live[h] && n < p.N) store8(p, row[h] * p.N + n, y + 4 * h);
 }
-// The same for rows that are not 16-byte aligned, through the warp's `turn` [16][33]:
-// a lane has a column of all 16 rows, eight of them loaded before they are used.
+// The same for rows that are not 16-byte aligned: through the warp's `turn` [16][33],
+// so that a lane has one column of all 16 rows.  What is added to them, the base and
+// the residual, is loaded in front of the products.
+__device__ __forceinline__ void turn_load(const LowRankParams& p, const size_t (&row)[2], const bool (&live)[2], int n,
+                                          float (&add)[16]) {
+  // (dead rows read the first one's place: loads under a condition would wait for each other)
+  size_t at[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4) != 0 && n < p.N;
+    const size_t from = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4) * p.N + n;
+    at[i] = in ? from : 0;
+    add[i] = 0.f;
+  }
+  if (p.base_f32 != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add[i] = p.base_f32[at[i]];
+  } else if (p.base != nullptr) {
+    uint16_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = p.base[at[i]];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add[i] = __uint_as_float(static_cast<uint32_t>(w[i]) << 16);
+  }
+  if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
+    uint16_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = p.residual[at[i]];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) add[i] += __uint_as_float(static_cast<uint32_t>(w[i]) << 16);
+  }
+}
 __device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
-                                          const bool (&live)[2], int n0, float* turn) {
-  const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
+                                          const bool (&live)[2], int n0, const float (&add)[16], float* turn) {
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3, n = n0 + lane;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -631,37 +661,21 @@ __device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&
       turn[(g8 + 8 * h) * 33 + 8 * q + 2 * j + 1] = acc[j][2 * h + 1];
     }
   __syncwarp();
-  const int n = n0 + lane;
+  uint64_t y[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    size_t at[8];
-    bool in[8];
-    float add[8] = {}, res[8] = {};
+  for (int i = 0; i < 8; ++i)
+    y[i] = f2_pack(turn[2 * i * 33 + lane] + add[2 * i], turn[(2 * i + 1) * 33 + lane] + add[2 * i + 1]);
+  if (p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      at[i] = __shfl_sync(kAll, row[h], i * 4) * p.N + n;
-      in[i] = __shfl_sync(kAll, static_cast<int>(live[h]), i * 4) != 0 && n < p.N;
-      if (!in[i]) continue;
-      if (p.base_f32 != nullptr) add[i] = p.base_f32[at[i]];
-      if (p.base != nullptr) add[i] = __uint_as_float(static_cast<uint32_t>(p.base[at[i]]) << 16);
-      if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[i] = __uint_as_float(static_cast<uint32_t>(p.residual[at[i]]) << 16);
-    }
-    uint64_t y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = turn[(8 * h + 2 * i) * 33 + lane] + add[2 * i], b = turn[(8 * h + 2 * i + 1) * 33 + lane] + add[2 * i + 1];
-      y[i] = f2_pack(a + res[2 * i], b + res[2 * i + 1]);
-    }
-    if (p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!in[i]) continue;
-      const float o = (i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2]);
-      if (p.Yf != nullptr)
-        p.Yf[at[i]] = o;
-      else
-        p.Y[at[i]] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-    }
+  for (int i = 0; i < 16; ++i) {
+    const size_t at = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4) * p.N + n;
+    const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4) != 0 && n < p.N;
+    if (!in) continue;
+    const float o = (i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2]);
+    if (p.Yf != nullptr)
+      p.Yf[at] = o;
+    else
+      p.Y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
   }
   __syncwarp();
 }
@@ -759,6 +773,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
           if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n);
         }
       }
+      float add[16];
+      if constexpr (!VEC) turn_load(p, row, live, n0 + lane, add);
       float acc[4][4] = {};
       if (id >= 0) {
         const unsigned char* from = vs + (m + g8) * stride + q * 8 * PARTS;
@@ -787,7 +803,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
           finish_rows<false, false>(p, acc, row, live, n, base, res);
         }
       } else {
-        turn_rows(p, acc, row, live, n0, turns[warp]);
+        turn_rows(p, acc, row, live, n0, add, turns[warp]);
       }
     }
   }
@@ -896,7 +912,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
     for (int t = 0; t < many; ++t) {
       const int at = tiles[t], count = tiles[t + 1] - at, id = ids[at];
       const bool live[2] = {g8 < count, g8 + 8 < count};
-      size_t row[2] = {static_cast<size_t>(rows[at + g8]), static_cast<size_t>(rows[at + g8 + 8])};
+      const size_t row[2] = {static_cast<size_t>(rows[at + g8]), static_cast<size_t>(rows[at + g8 + 8])};
+      float add[16];
+      if constexpr (!VEC) turn_load(p, row, live, n0 + lane, add);
       float acc[4][4] = {};
       if (id >= 0) {
         // (rows of the MMA that are not live hold anything: they stay apart)
@@ -931,7 +949,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
         ask(t + kAhead);
         finish_rows<F32, RES>(p, acc, row, live, n, base, res);
       } else {
-        turn_rows(p, acc, row, live, n0, turns[warp]);
+        turn_rows(p, acc, row, live, n0, add, turns[warp]);
       }
     }
     copies_wait<0>();
