@@ -36,7 +36,7 @@ constexpr int kWarps = 8;
 constexpr int kUnit = 64;        // k of a warp's turn
 constexpr int kFew = kTile;      // rows that need no sorting kernel
 constexpr int kChunk = 256;      // positions of a CTA that applies B, at most
-constexpr int kManyBytes = 112 * 1024;  // its shared memory: two on an SM
+constexpr int kManyBytes = 113 * 1024;  // its shared memory: two on an SM
 constexpr int kStagedRows = 2048;  // from these rows on x and A pass through shared memory
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
@@ -47,14 +47,19 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two s8 codes (bytes 0 and 2 of w) as bf16, exact: 128 + the low seven bits, less
-// 128, or 256 where the sign bit is set.  (A bf16 FMA is one instruction here, a
-// bf16 subtraction some ten.)
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
-  const uint32_t a = (w & 0x007F007Fu) | 0x43004300u, b = (w & 0x00800080u) | 0xC300C300u;
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0x3F803F80u), "r"(b));
-  return d;
+// Four s8 codes as bf16, exact: under the exponent of 2^23 a byte is 2^23 + 128 + the
+// code in FP32, and the high half of an integer below 256 is its bf16.  (bf16
+// arithmetic on pairs is three or more instructions here.)
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const uint64_t less = f2_pack(-8388736.f, -8388736.f);
+  const auto pair = [&](uint32_t first) {
+    const uint64_t f = f2_add(f2_pack(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + first)),
+                                      __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441u + first))), less);
+    return __byte_perm(static_cast<uint32_t>(f), static_cast<uint32_t>(f >> 32), 0x7632);
+  };
+  lo = pair(0);
+  hi = pair(2);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) { return f2_to_bf16x2(f2_pack(lo, hi)); }
@@ -245,10 +250,8 @@ __device__ __forceinline__ void sums_of(const LowRankParams& p, const uint16_t* 
         if (live[i]) {
           if constexpr (INT8) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.codes + at[i] + k));
-            x[i][0] = codes_bf16(__byte_perm(w.x, 0, 0x4140));
-            x[i][1] = codes_bf16(__byte_perm(w.x, 0, 0x4342));
-            x[i][2] = codes_bf16(__byte_perm(w.y, 0, 0x4140));
-            x[i][3] = codes_bf16(__byte_perm(w.y, 0, 0x4342));
+            codes_bf16(w.x, x[i][0], x[i][1]);
+            codes_bf16(w.y, x[i][2], x[i][3]);
           } else {
             const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.x + at[i] + k));
             x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
@@ -354,7 +357,8 @@ __device__ __forceinline__ void copies_wait() {
 // v of 64 positions, for many rows: x and A_l pass through shared memory, 128 k a
 // stage, and are read there by four pairs of warps, 32 rows a warp, a pair for each
 // quarter of the stage's k.  A run of one adapter within the block is a pass over
-// K.  Grid: blocks of positions x blocks of 8 RT ranks.  (Two CTAs an SM, so that
+// K.  Grid: blocks of positions x blocks of 8 RT ranks x 2 (the block's runs in
+// turn).  (Two CTAs an SM, so that
 // one's MMAs run while the other waits at its stage's barrier.)
 constexpr int kBlock = 64, kStageK = 128, kStagedThreads = 256;
 template <bool INT8, int RT>
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRank
   }
   __syncthreads();
   const int stages = p.K / kStageK;
-  for (int first = 0; first < kBlock;) {
+  for (int first = 0, turn = 0; first < kBlock; ) {
     const int id = ids[first];
     if (id == INT_MAX) break;
     int end = kBlock;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRank
       const uint32_t other = __ballot_sync(kAll, 32 * b + lane > first && ids[32 * b + lane] != id);
       if (other != 0) end = 32 * b + __ffs(other) - 1;
     }
-    if (id < 0) {
+    if (id < 0 || turn++ % gridDim.z != blockIdx.z) {
       first = end;
       continue;
     }
@@ -461,10 +465,8 @@ __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRank
         const int row = wr * 32 + g8 + 8 * i;
         if constexpr (INT8) {
           const uint2 w = *reinterpret_cast<const uint2*>(xs + chunk128(row, 2 * wk + (q >> 1)) + (q & 1) * 8);
-          x[i][0] = codes_bf16(__byte_perm(w.x, 0, 0x4140));
-          x[i][1] = codes_bf16(__byte_perm(w.x, 0, 0x4342));
-          x[i][2] = codes_bf16(__byte_perm(w.y, 0, 0x4140));
-          x[i][3] = codes_bf16(__byte_perm(w.y, 0, 0x4342));
+          codes_bf16(w.x, x[i][0], x[i][1]);
+          codes_bf16(w.y, x[i][2], x[i][3]);
         } else {
           const uint4 w = *reinterpret_cast<const uint4*>(xs + chunk256(row, 4 * wk + q));
           x[i][0] = w.x, x[i][1] = w.y, x[i][2] = w.z, x[i][3] = w.w;
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
 // lane copies the base, and the residual, of its outputs kAhead tiles ahead into
 // pieces of its own: with one tile ahead, in registers, 16 KB an SM were on their
 // way, a quarter of what it takes.
-constexpr int kAhead = 4;
+constexpr int kAhead = 3;
 // Pieces of 16 bytes a lane has of each row: base, residual.
 template <bool VEC, bool F32>
 __host__ __device__ constexpr int pieces_of(bool residual) {
@@ -1011,7 +1013,7 @@ cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
     constexpr int smem = Staged<INT8, RT>::kBytes;
     const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
     if (e != cudaSuccess) return e;
-    Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT)), kStagedThreads, smem, st, true);
+    Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT), 2), kStagedThreads, smem, st, true);
     note_launch();
     return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT, PARTS>, p);
   }
