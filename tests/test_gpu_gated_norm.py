@@ -133,9 +133,63 @@ def test_segments(ops, m, segments, indexed):
         _check(ops, _inputs(m, 384, m, mod=mod, segments=segments, indexed=indexed), 64)
 
 
+@pytest.mark.parametrize("k", [128, 640, 1024, 1920, 2048, 2176, 4096, 5120, 7680, 8192, 8320, 16384])
+@pytest.mark.parametrize("m,b", [(600, 64), (1217, 0), (2500, 16)])
+def test_many_rows(ops, m, k, b):
+    """Rows whose parts are copied ahead, teams of every size, windows of segments that do not all fit."""
+    for segments, indexed in ((1, False), (11, True)):
+        _check(ops, _inputs(m, k, m + k, segments=segments, indexed=indexed), b)
+    c = _inputs(m, k, k, segments=5)
+    c["segment"] = np.sort(np.random.default_rng(m).integers(0, 5, m)).astype(np.int32)  # runs
+    _check(ops, c, b)
+    c["res"] = None
+    c["post"] = None
+    _check(ops, c, b)
+
+
+@pytest.mark.parametrize("k", [256, 1920, 7680, 16384])
+def test_many_rows_in_place_and_bf16(ops, k):
+    m = 777
+    c = _inputs(m, k, k, segments=3)
+    want, hw = _call(ops, c, 64)
+    f = {n: torch.from_numpy(c[n]).cuda() for n in ("w", "post", "gate", "scale", "shift")}
+    for i in range(2):
+        v = [torch.from_numpy(c[n]).to(torch.bfloat16).cuda() for n in ("x", "res")]
+        a, h = ops.gated_rmsnorm_quant(*v, f["w"], f["post"], f["gate"], f["scale"], f["shift"], None, 0.75, EPS, 64,
+                                       sum_out=v[i])
+        assert h is v[i] and torch.equal(h, hw)
+        assert torch.equal(a.i8_codes, want.i8_codes) and torch.equal(a.row_scale, want.row_scale)
+    y, h = _call(ops, c, 0, quantize=False)
+    _, _, z, ez = _ref(c, 0)
+    assert torch.equal(h, hw)
+    assert np.all(np.abs(y.double().cpu().numpy() - z) <= ez + _half_ulp(np.abs(z) + ez))
+
+
+def test_many_special_rows(ops):
+    m, k = 700, 1920
+    c = _inputs(m, k, 2, segments=2, indexed=True)
+    bad = [3, 77, 333, 699]
+    c["x"][3, 5], c["res"][77, 9], c["x"][333, 0] = np.inf, np.nan, -np.inf
+    c["segment"][699] = 2
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, h = _call(ops, c, 64, err=err)
+    with pytest.raises(RuntimeError):
+        ops.check_err(err, "norm")
+    s = a.row_scale.cpu().numpy()
+    assert np.isnan(s[bad]).all() and not a.i8_codes[bad].any()
+    for i in bad:
+        c["x"][i], c["res"][i], c["segment"][i] = 1, 1, 0
+    _check(ops, c, 64, rows=[i for i in range(m) if i not in bad], got=(a, h))
+
+
 @pytest.mark.parametrize("one", ["gate", "scale", "shift"])
 def test_one_modulation_alone(ops, one):
     c = _inputs(41, 640, 3, segments=3, indexed=True)
+    for n in ("gate", "scale", "shift"):
+        if n != one:
+            c[n] = None
+    _check(ops, c, 64)
+    c = _inputs(900, 1280, 3, residual=False, post=False, weight=False, segments=3, indexed=True)
     for n in ("gate", "scale", "shift"):
         if n != one:
             c[n] = None

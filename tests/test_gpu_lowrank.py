@@ -148,6 +148,25 @@ def test_runs_of_requests(ops, m):
     c.check(c.call(ops))
 
 
+def test_as_many_adapters_as_there_may_be(ops):
+    count, k, n = ops.MAX_ADAPTERS, 128, 8
+    for m in (20, 700, 5000):
+        g = torch.Generator().manual_seed(m)
+        ids = torch.randint(0, count, (m,), generator=g, dtype=torch.int32)
+        ids[:3] = torch.tensor([0, count - 1, -1], dtype=torch.int32)
+        a = torch.zeros((count, 16, k), dtype=torch.bfloat16, device="cuda")
+        a[:, 0, 0] = 1.0
+        b = torch.zeros((count, n, 16), dtype=torch.bfloat16, device="cuda")
+        b[:, :, 0] = (torch.arange(count, device="cuda") % 251).to(torch.bfloat16)[:, None]  # whole numbers below 256
+        x = torch.ones((m, k), dtype=torch.bfloat16, device="cuda")
+        y = ops.lowrank_add(x, ops.LowRank(a, b), ids.cuda(), out_f32=True)
+        want = torch.where(ids >= 0, ids % 251, 0).float()
+        assert torch.equal(y.cpu(), want[:, None].expand(m, n))
+    with pytest.raises(RuntimeError):
+        ops.lowrank_add(x, ops.LowRank(torch.zeros((count + 1, 16, k), dtype=torch.bfloat16, device="cuda"),
+                                       torch.zeros((count + 1, n, 16), dtype=torch.bfloat16, device="cuda")), ids.cuda())
+
+
 def test_every_row_its_own_adapter_and_one_for_all(ops):
     for ids in (torch.randperm(64, generator=torch.Generator().manual_seed(1)).int(), torch.full((64,), 9).int(),
                 torch.full((64,), -1).int()):

@@ -540,13 +540,14 @@ class Routing(NamedTuple):
 
 def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
               groups: int = 1, top_groups: int = 1, group_best: int = 2, renormalize: bool = True, scale: float = 1.0,
-              stream=None) -> Routing:
+              out: Routing | None = None, stream=None, ws=None) -> Routing:
     """Routing of T tokens to top_k of E experts (sixbit_moe_route).
 
     logits: float32 or bf16 [T, E].  score: SCORE_SOFTMAX or SCORE_SIGMOID; bias: float32 [E], added for the choice and
     not to the weights.  With groups > 1 only experts of the top_groups groups are chosen, by the sum of a group's
     group_best (1 or 2) largest keys.  Equal keys go to the lower number.  The weights are the chosen experts' scores,
-    divided by their sum (renormalize), times scale."""
+    divided by their sum (renormalize), times scale.  out: an earlier result of these sizes to write into; ws:
+    moe_route_workspace_bytes(T, E) bytes, allocated for the call by default."""
     shape = logits.shape
     if len(shape) != 2:
         raise ValueError(f"logits: [T, E] expected, got {tuple(shape)}")
@@ -561,17 +562,30 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     else:
         pl = _ptr(logits, "logits", _F32, shape, dev)
     pb = None if bias is None else _ptr(bias, "bias", _F32, (e,), dev)
-    # (tensors of their own: views into one allocation take twice the time on the host)
-    device, tk = logits.device, (t, top_k)
-    experts, weights, rows = _empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream)
-    token, offsets = _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream)
-    ws = None if t <= 32 else _empty((304 * ((e + 3) // 4 * 4),), _I32, device, stream)  # sixbit_moe_route_workspace_bytes
+    tk = (t, top_k)
+    if out is None:
+        # (tensors of their own: views into one allocation take twice the time on the host)
+        device = logits.device
+        out = Routing(_empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream),
+                      _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream))
+    experts, weights, rows, token, offsets = out
+    need = 0 if t <= 32 else 304 * ((e + 3) // 4 * 4) * 4  # sixbit_moe_route_workspace_bytes
+    if ws is None:
+        if need:
+            ws = _empty((need,), _U8, logits.device, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
     status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, renormalize, scale,
-                                   experts.data_ptr(), weights.data_ptr(), rows.data_ptr(), token.data_ptr(),
-                                   offsets.data_ptr(), None if ws is None else ws.data_ptr(), st)
+                                   _ptr(experts, "experts", _I32, tk, dev), _ptr(weights, "weights", _F32, tk, dev),
+                                   _ptr(rows, "rows", _I32, tk, dev), _ptr(token, "token", _I32, (t * top_k,), dev),
+                                   _ptr(offsets, "offsets", _I32, (e + 1,), dev), None if ws is None else ws.data_ptr(), st)
     if status:
         check(status, "moe_route")
-    return Routing(experts, weights, rows, token, offsets)
+    return out
+
+
+def moe_route_workspace_bytes(t: int, e: int) -> int:
+    return int(_lib.sixbit_moe_route_workspace_bytes(t, e))
 
 
 def moe_combine(d: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None, out_f32: bool = False, err=None,
