@@ -126,7 +126,7 @@ def test_widths_and_epilogues(ops, n, epilogue):
 
 
 @pytest.mark.parametrize("r", [16, 32, 48, 64, 96, 128])
-@pytest.mark.parametrize("m,count", [(2047, 3), (2048, 1), (2500, 300), (5001, 6)])
+@pytest.mark.parametrize("m,count", [(1535, 3), (1536, 1), (2500, 300), (4095, 2), (5001, 6)])
 @pytest.mark.parametrize("int8", [True, False])
 def test_many_rows(ops, m, count, r, int8):
     """Mixed rows, and the same rows with their requests side by side."""

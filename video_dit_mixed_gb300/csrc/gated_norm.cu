@@ -19,6 +19,13 @@
 // a window of segments, as many as fit, in shared memory; where its rows leave the
 // window it is filled anew, unless few rows would use it: they join them as they go.
 // An absent operand is a factor of 1 or a shift of 0, so that nothing branches.
+//
+// The floor is bytes: 7 an element, 8 with bf16 rows.  17,776 x 1920 with every
+// operand 51 us (4.7 TB/s, 69% of a copy; 47 without gate, scale and shift), 4,444
+// x 7680 67, 2,777 x 12288 79; 1,003 x 7680 gated, to bf16, 23 (floor 9); one row
+// 3.5, 226 rows 4.8.  It is bound by issue and dependence: some 385 instructions a
+// warp for 512 elements, which issue in half of the cycles.  (A CTA a row, one chunk
+// a lane: 66 us, 730 instructions; two rows a CTA at once spilled and took 74.)
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -31,8 +38,7 @@
 namespace sixbit {
 namespace gnorm {
 
-constexpr int kWarps = 16;                // of a CTA
-constexpr int kFewRows = 600;
+constexpr int kWarps = 16;              // of a CTA
 constexpr int kSmemBytes = 224 * 1024;  // copies and factors
 
 struct Params {
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
   __shared__ Joint<W> post[kWarps / W], pre[kWarps / W], top[kWarps / W];
   __shared__ uint64_t arrived[kWarps];
   constexpr int kPart = V * 32 * 32;  // bytes of a warp's part of a row
-  constexpr int kTeams = kWarps / W;
+  constexpr int kTeams = kWarps / W, kFillRows = kTeams > 4 ? kTeams / 2 : 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / W, rank = warp % W;
   const int chunks = g.K / kChunk, c0 = rank * 32 * V + lane;  // this lane's: c0 + 32 v
   unsigned char* part = smem + warp * (2 * kPart);             // x, then the residual
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
   for (int64_t from = row0; from < row1;) {  // (the same windows in every warp)
     int64_t to = row1;
     int seg0 = 0;
-    bool fill = p.held > 0;
+    bool fill = p.held > 0 && to - from >= kFillRows;
     if (p.held > 0 && p.held < g.S) {
       seg0 = min(max(segment_of(from), 0), g.S - p.held);
       for (int64_t r = from; r < row1; r += 32) {
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
           break;
         }
       }
-      fill = to - from >= 2 * kTeams;
+      fill = to - from >= kFillRows;
     }
     if (fill) {
       __syncthreads();  // (the last window's rows are done)
@@ -371,7 +377,7 @@ cudaError_t launch_rows(Params& p, int64_t grid, cudaStream_t st) {
   int smem = STAGE ? kWarps * 2 * V * 1024 : 0;
   const int of_segment = 3 * g.K * 4;
   p.held = 0;
-  if (p.rows > kWarps / W) {  // (with a row a team nothing is shared)
+  if (p.rows > 1) {
     p.held = std::min(g.S, (kSmemBytes - smem) / of_segment);
     smem += p.held * of_segment;
   }
@@ -381,22 +387,26 @@ cudaError_t launch_rows(Params& p, int64_t grid, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// One chunk a lane and a row a CTA, the shortest way through a row, while all rows are
+// resident at once, four CTAs an SM at most (1920: 304 rows 5.1 us against 10.3, 599
+// 6.8 against 10.6, but 1200 12.3 against 9.6; 7680, a CTA an SM: 152 rows 7.2 against
+// 11.0, 304 14.0 against 12.6).  Else teams of warps with four chunks a lane.
 cudaError_t launch(Params& p, cudaStream_t st) {
-  const int chunks = p.g.K / kChunk, sms = sm_count();
-  if (p.g.M < kFewRows) {  // one chunk a lane, a row a CTA: the shortest way through one row
-    if (chunks <= 32) return launch_rows<1, 1, false>(p, p.g.M, st);
-    if (chunks <= 64) return launch_rows<1, 2, false>(p, p.g.M, st);
-    if (chunks <= 128) return launch_rows<1, 4, false>(p, p.g.M, st);
-    if (chunks <= 256) return launch_rows<1, 8, false>(p, p.g.M, st);
-    if (chunks <= 512) return launch_rows<1, 16, false>(p, p.g.M, st);
+  const int chunks = p.g.K / kChunk, sms = sm_count(), warps = (chunks + 31) / 32;
+  if (p.g.M <= sms * (warps <= 4 ? 4 : warps <= 8 ? 2 : 1)) {
+    if (warps == 1) return launch_rows<1, 1, false>(p, p.g.M, st);
+    if (warps == 2) return launch_rows<1, 2, false>(p, p.g.M, st);
+    if (warps <= 4) return launch_rows<1, 4, false>(p, p.g.M, st);
+    if (warps <= 8) return launch_rows<1, 8, false>(p, p.g.M, st);
+    if (warps <= 16) return launch_rows<1, 16, false>(p, p.g.M, st);
     return launch_rows<2, 16, false>(p, p.g.M, st);
   }
-  if (chunks <= 32) return launch_rows<1, 1, true>(p, sms, st);
-  if (chunks <= 64) return launch_rows<2, 1, true>(p, sms, st);
-  if (chunks <= 128) return launch_rows<4, 1, true>(p, sms, st);
-  if (chunks <= 256) return launch_rows<4, 2, true>(p, sms, st);
-  if (chunks <= 512) return launch_rows<4, 4, true>(p, sms, st);
-  return launch_rows<4, 8, false>(p, sms, st);
+  if (warps == 1) return launch_rows<1, 1, true>(p, sms, st);
+  if (warps == 2) return launch_rows<2, 1, true>(p, sms, st);
+  if (warps <= 4) return launch_rows<4, 1, true>(p, sms, st);
+  if (warps <= 8) return launch_rows<4, 2, true>(p, sms, st);
+  if (warps <= 16) return launch_rows<4, 4, true>(p, sms, st);
+  return launch_rows<4, 8, false>(p, sms, st);  // (copies and three factors of a row do not fit)
 }
 
 }  // namespace gnorm

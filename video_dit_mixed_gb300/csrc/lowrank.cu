@@ -15,10 +15,16 @@
 //
 // Rows are taken in the order of their adapters, 32 positions a tile, so that an
 // MMA's rows share one however requests are mixed.  Up to 32 rows every warp sorts
-// them by itself, and one launch does both products; above, a counting sort by one
-// CTA goes first.  The order of rows
-// of one adapter is not fixed (atomics), and does not matter: a row's sums do not
-// depend on its place.
+// them by itself, and one launch does both products; above, a counting sort goes
+// first.  The order of rows of one adapter is not fixed (atomics), and does not
+// matter: a row's sums do not depend on its place.
+//
+// The floor is bytes, of which base and result are nearly all for many rows.
+// 17,776 x 7680 outputs, bf16 base and result: rank 16 118 us (floor 84), rank 64
+// with GELU 222 (GELU is 337 of a tile's some 530 instructions' worth of the FP32
+// pipe, 80 us by itself); 1920 outputs of K 7680, rank 64, residual: 120 (A's product
+// 70 of it).  One row beside 7680 x 1920 5.3 us, 32 rows of 32 requests beside 1920 x
+// 7680 8.9, 226 rows 19, 2000 mixed rows of 32 adapters 46.
 #include <climits>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -37,7 +43,6 @@ constexpr int kUnit = 64;        // k of a warp's turn
 constexpr int kFew = kTile;      // rows that need no sorting kernel
 constexpr int kChunk = 256;      // positions of a CTA that applies B, at most
 constexpr int kManyBytes = 113 * 1024;  // its shared memory: two on an SM
-constexpr int kStagedRows = 2048;  // from these rows on x and A pass through shared memory
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -1009,7 +1014,10 @@ cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
 
 template <bool INT8, int RT, int PARTS>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
-  if (p.M >= kStagedRows) {
+  // For many rows x and A pass through shared memory: K 1920, rank 64, 2047 rows 44 us
+  // against 56, but 1024 mixed ones 50 against 42; rank 16, 2047 rows 30.6 against 30.2,
+  // 4096 44.1 against 44.0, 8192 69 against 70.
+  if (p.M >= (p.R > 32 ? 1536 : 4096)) {
     constexpr int smem = Staged<INT8, RT>::kBytes;
     const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
     if (e != cudaSuccess) return e;
@@ -1105,7 +1113,8 @@ cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
       const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
       if (e != cudaSuccess) return e;
     }
-    const int ctas = p.M > 4 * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
+    // (a cluster where one CTA would go around more than once)
+    const int ctas = p.M > lowrank::kPlanAtOnce * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
     lowrank::Launch l(dim3(ctas), lowrank::kPlanThreads, smem, st, false, dim3(ctas));
     note_launch();
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);

@@ -4,6 +4,10 @@
 //
 // in FP32, rounded once to bf16 (or kept).  Term j joins partial sum j % 4 and the
 // partial sums are added in their order, whatever the launch.
+//
+// Bytes bound it: 17,776 tokens of two rows of 1920 floats 54 us (6.3 TB/s, 93% of a
+// copy), of bf16 35 (85%); 8 tokens 1.7 us, 226 of eight rows of bf16 4.5.  (A token
+// a CTA, its rows' numbers loaded when they are needed: 78 and 60 us.)
 #include <cstdint>
 
 #include "common.cuh"

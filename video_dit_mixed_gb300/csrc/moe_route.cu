@@ -20,6 +20,11 @@
 // that a choice's rank among the run's is a count of bits below its own, whatever
 // order the warps came in.  The runs' counts go to the workspace, and a second
 // kernel adds what lies before each run (a single run needs none).
+//
+// Bytes are next to nothing (4 an expert and token): it is bound by the chain of a
+// token's steps, a warp's maximum and the lowest lane that has it for each choice.
+// One token 3.3 us; 226 over 256 experts, 4 of 8 groups, top 8: 13; 17,776 over 64,
+// top 2: 17; 4,444 over 256 in groups 37.
 #include <cstdint>
 
 #include "common.cuh"
@@ -182,11 +187,12 @@ struct Open {
   uint32_t listed;
 };
 
-// One token's experts (lane j: the j-th), from its logits l.  F: the type that
-// keys are computed in; CHECK: false is returned where F is too narrow.
+// One token's experts (lane j: the j-th), from its logits l and the experts' biases.
+// F: the type that keys are computed in; CHECK: false is returned where F is too
+// narrow.
 template <int N, bool CHECK, typename F>
-__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], float lmax, F* keys, int* mine,
-                                       Open* open) {
+__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], const float (&bias)[N], float lmax,
+                                       F* keys, int* mine, Open* open) {
   using O = typename OrdOf<F>::type;
   const int lane = threadIdx.x & 31;
   const bool by_logit = p.bias == nullptr;
@@ -211,10 +217,9 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
       for (int i = 0; i < N; ++i) v[i] = F(1) / (F(1) + exp_of(-static_cast<F>(l[i])));
       tol = 0x1p-24f * 6.f;  // (0.5 by the exponential, two roundings)
     }
+    if (!by_logit) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      if (p.bias != nullptr && e < p.E) v[i] += static_cast<F>(__ldg(p.bias + e));
+      for (int i = 0; i < N; ++i) v[i] += static_cast<F>(bias[i]);
     }
   }
   const float rel = 0x1p-24f * 3;  // (the bias joins with half a unit of the key)
@@ -265,6 +270,13 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int64_t t, int e
                                   : __ldg(p.logits + at);
 }
 
+template <int N>
+__device__ __forceinline__ void load_bias(const RouteParams& p, float (&bias)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < N; ++i) bias[i] = p.bias != nullptr && lane + 32 * i < p.E ? __ldg(p.bias + lane + 32 * i) : 0.f;
+}
+
 // A token again in FP64, a call of its own: its registers (two a key) are not the
 // fast path's.  With sigmoid scores only the listed experts, up to four a lane (an
 // exponential is some 60 FP64 instructions).
@@ -310,7 +322,9 @@ __device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax
   float l[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
-  choose<N, false, double>(p, l, lmax, keys, &mine, nullptr);
+  float bias[N];
+  load_bias(p, bias);
+  choose<N, false, double>(p, l, bias, lmax, keys, &mine, nullptr);
   return mine;
 }
 
@@ -388,6 +402,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
   int* chosen = reinterpret_cast<int*>(mask + p.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double* keys = reinterpret_cast<double*>(smem + keys_at(p.E, p.k)) + static_cast<size_t>(p.groups > 1 ? warp : 0) * p.E;
+  float bias[N];
+  load_bias(p, bias);
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     run[e] = 0;
     mask[e] = 0;
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
       const float lmax = value_of(warp_max(top));
       int mine = 0;
       Open open;
-      if (!choose<N, true, float>(p, l, lmax, reinterpret_cast<float*>(keys), &mine, &open))
+      if (!choose<N, true, float>(p, l, bias, lmax, reinterpret_cast<float*>(keys), &mine, &open))
         mine = choose64<N>(p, t, lmax, keys, open.all, open.listed);
       const bool live = lane < p.k;
       const float w = weight_of<N>(p, l, lmax, live ? logit_at(p, t, mine) : -INFINITY, live);

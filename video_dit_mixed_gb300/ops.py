@@ -566,9 +566,14 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     if out is None:
         # (tensors of their own: views into one allocation take twice the time on the host)
         device = logits.device
-        out = Routing(_empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream),
-                      _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream))
-    experts, weights, rows, token, offsets = out
+        out = experts, weights, rows, token, offsets = Routing(
+            _empty(tk, _I32, device, stream), _empty(tk, _F32, device, stream), _empty(tk, _I32, device, stream),
+            _empty((t * top_k,), _I32, device, stream), _empty((e + 1,), _I32, device, stream))
+        pe, pw, pr, pt, po = (experts.data_ptr(), weights.data_ptr(), rows.data_ptr(), token.data_ptr(), offsets.data_ptr())
+    else:
+        pe, pw, pr = (_ptr(out.experts, "experts", _I32, tk, dev), _ptr(out.weights, "weights", _F32, tk, dev),
+                      _ptr(out.rows, "rows", _I32, tk, dev))
+        pt, po = _ptr(out.token, "token", _I32, (t * top_k,), dev), _ptr(out.offsets, "offsets", _I32, (e + 1,), dev)
     need = 0 if t <= 32 else 304 * ((e + 3) // 4 * 4) * 4  # sixbit_moe_route_workspace_bytes
     if ws is None:
         if need:
@@ -576,9 +581,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
         raise ValueError(f"ws: {need} dense bytes on GPU {dev} expected")
     status = _lib.sixbit_moe_route(pl, ph, pb, t, e, top_k, score, groups, top_groups, group_best, renormalize, scale,
-                                   _ptr(experts, "experts", _I32, tk, dev), _ptr(weights, "weights", _F32, tk, dev),
-                                   _ptr(rows, "rows", _I32, tk, dev), _ptr(token, "token", _I32, (t * top_k,), dev),
-                                   _ptr(offsets, "offsets", _I32, (e + 1,), dev), None if ws is None else ws.data_ptr(), st)
+                                   pe, pw, pr, pt, po, None if ws is None else ws.data_ptr(), st)
     if status:
         check(status, "moe_route")
     return out
