@@ -199,8 +199,10 @@ struct RouteParams {
   int32_t* token;                // [T k]
   int32_t* offsets;              // [E + 1]
   int32_t* counts;
-  int tokens_per_cta;            // set by the launch, as are log2 of the lanes that look through a group
-  int team, pitch;               // and E rounded up to four
+  // set by the launch: tokens of a run, log2 of the lanes that look through a group, E rounded up to four, and 2^20
+  // over a group's size
+  int tokens_per_cta, team, pitch;
+  uint32_t per;
 };
 cudaError_t launch_moe_route(RouteParams p, cudaStream_t st);
 

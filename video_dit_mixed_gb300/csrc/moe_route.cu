@@ -53,6 +53,10 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float((o >> 31) ? o ^ 0x80000000u : ~o);
 }
 
+__device__ __forceinline__ double value_of(uint64_t o) {
+  return __longlong_as_double(static_cast<long long>((o >> 63) ? o ^ 0x8000000000000000ull : ~o));
+}
+
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(v >> 32));
@@ -78,13 +82,19 @@ struct OrdOf<double> {
 };
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float inverse(float v) {  // to 2^-23
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ double inverse(double v) { return 1.0 / v; }
 
 // The k largest of the warp's keys (N a lane, 0: absent), lower numbers first
 // among equals: lane j's `mine` is the j-th expert.  CHECK: true if no two
 // consecutive ones, the last chosen and the next included, are within `tol` +
 // `rel` |key|, and the last chosen in `least`.
 template <int N, bool CHECK, typename O>
-__device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, int* mine, float* least) {
+__device__ __forceinline__ bool top_k_in_turn(O (&key)[N], int k, float tol, float rel, int* mine, float* least) {
   const int lane = threadIdx.x & 31;
   O best = 0;
   int slot = 0;
@@ -125,43 +135,101 @@ __device__ __forceinline__ bool top_k(O (&key)[N], int k, float tol, float rel, 
   return clear;
 }
 
+// Lanes sorted by v, the largest first.
+template <typename V>
+__device__ __forceinline__ V sorted(V v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int h = size >> 1; h > 0; h >>= 1) {
+      const V o = __shfl_xor_sync(kAll, v, h);
+      const bool larger = ((lane & size) == 0) == ((lane & h) == 0);  // this lane keeps the larger of the two
+      v = (v > o) == larger ? v : o;
+    }
+  return v;
+}
+// The same by sorting: keys that are not clearly below the k-th largest of the
+// lanes' own largest are nearly all of the k largest; up to 32 of them are put side
+// by side and sorted.  Up to four in turn: 17776 tokens over 64, k = 2, 17 us where
+// sorting takes 20; over 256 in groups, k = 8, 100 and 90.  list: the warp's [32].
+template <int N, bool CHECK>
+__device__ __forceinline__ bool top_k(const uint32_t (&key)[N], int k, float tol, float rel, int* mine, float* least, uint2* list) {
+  const int lane = threadIdx.x & 31;
+  uint64_t pair;
+  if (k <= 4) {
+    uint32_t left[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) left[i] = key[i];
+    return top_k_in_turn<N, CHECK>(left, k, tol, rel, mine, least);
+  }
+  if constexpr (N == 1) {
+    pair = key[0] == 0 ? 0 : (static_cast<uint64_t>(key[0]) << 32) | (kAll - lane);
+  } else {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) best = max(best, key[i]);
+    uint32_t from = __shfl_sync(kAll, sorted(best), k - 1);
+    if (CHECK && from != 0) {
+      const float v = value_of(from);
+      from = ordered(v - (tol + rel * fabsf(v)));
+    }
+    if (from == 0) from = 1;
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in = key[i] >= from;
+      const uint32_t all = __ballot_sync(kAll, in);
+      const int at = total + __popc(all & ((1u << lane) - 1));
+      if (in && at < 32) list[at] = make_uint2(key[i], kAll - (lane + 32 * i));
+      total += __popc(all);
+    }
+    if (total > 32) {
+      uint32_t left[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) left[i] = key[i];
+      return top_k_in_turn<N, CHECK>(left, k, tol, rel, mine, least);
+    }
+    __syncwarp();
+    const uint2 l = list[lane];
+    pair = lane < total ? (static_cast<uint64_t>(l.x) << 32) | l.y : 0;
+    __syncwarp();
+  }
+  pair = sorted(pair);
+  *mine = static_cast<int>(kAll - static_cast<uint32_t>(pair));
+  if (!CHECK) return true;
+  const uint32_t o = static_cast<uint32_t>(pair >> 32), next = __shfl_down_sync(kAll, o, 1);
+  const float v = value_of(o);
+  *least = __shfl_sync(kAll, v, k - 1);
+  // (what is not on the list is further away; lane 31 has no next)
+  return __all_sync(kAll, lane >= k || lane == 31 || next == 0 || v - value_of(next) > tol + rel * fabsf(v));
+}
+
 // Bits of the groups that are kept.  keys: the warp's E keys in shared memory.
-template <bool CHECK, typename F>
-__device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys, float tol, float rel, uint32_t* kept) {
-  using O = typename OrdOf<F>::type;
+template <bool CHECK, typename O>
+__device__ __forceinline__ bool keep_groups(const RouteParams& p, const O* keys, float tol, float rel, uint32_t* kept) {
   const int lane = threadIdx.x & 31, size = p.E / p.groups;
   __syncwarp();
   // 1 << p.team lanes a group, each every so many keys of it; their two largest are joined in a tree
   const int team = 1 << p.team, g = lane >> p.team, sub = lane & (team - 1);
   O a = 0, b = 0;
-  F fa = 0, fb = 0;
   if (g < p.groups) {
+#pragma unroll 4
     for (int i = sub; i < size; i += team) {
-      const F v = keys[g * size + i];
-      const O o = ordered(v);
-      if (o > a) {
-        b = a, fb = fa;
-        a = o, fa = v;
-      } else if (o > b) {
-        b = o, fb = v;
-      }
+      const O o = keys[g * size + i];
+      b = max(b, min(a, o));
+      a = max(a, o);
     }
   }
   for (int h = team >> 1; h > 0; h >>= 1) {
-    const F xa = __shfl_xor_sync(kAll, fa, h), xb = __shfl_xor_sync(kAll, fb, h);
     const O oa = __shfl_xor_sync(kAll, a, h), ob = __shfl_xor_sync(kAll, b, h);
-    if (oa > a) {
-      const bool mine = a > ob;
-      b = mine ? a : ob, fb = mine ? fa : xb;
-      a = oa, fa = xa;
-    } else if (oa > b) {
-      b = oa, fb = xa;
-    }
+    b = max(max(b, ob), min(a, oa));
+    a = max(a, oa);
   }
   // lane g: group g's
   const int from = (lane << p.team) & 31;
-  a = __shfl_sync(kAll, a, from), fa = __shfl_sync(kAll, fa, from), fb = __shfl_sync(kAll, fb, from);
-  O score = lane < p.groups ? ordered(p.best > 1 && size > 1 ? fa + fb : fa) : O(0);
+  a = __shfl_sync(kAll, a, from), b = __shfl_sync(kAll, b, from);
+  O score = lane < p.groups ? (p.best > 1 && size > 1 ? ordered(value_of(a) + value_of(b)) : a) : O(0);
   uint32_t bits = 0;
   O top = 0;
   for (int j = 0; j < p.top_groups; ++j) {
@@ -172,12 +240,36 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F* keys,
   }
   bool clear = true;
   if (CHECK && p.top_groups < p.groups) {  // (which of the kept comes first does not matter)
-    const float v = value_of(static_cast<uint32_t>(top)), next = value_of(static_cast<uint32_t>(warp_max(score)));
+    const float v = static_cast<float>(value_of(top)), next = static_cast<float>(value_of(warp_max(score)));
     clear = v - next > 2.f * tol + rel * fabsf(v);
   }
   __syncwarp();
   *kept = bits;
   return clear;
+}
+
+// e / (E / groups): p.per is 2^20 over the group's size, rounded up, and e times the
+// size is below 2^20.
+__device__ __forceinline__ uint32_t group_of(const RouteParams& p, int e) { return (static_cast<uint32_t>(e) * p.per) >> 20; }
+
+// A token's logits, expert lane + 32 i's in l[i]; -infinity beyond the last.
+template <int N>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, float (&l)[N]) {
+  const int lane = threadIdx.x & 31;
+  const size_t at = static_cast<size_t>(t) * p.E;  // (loads under no condition, so that they are on their way at once)
+  if (p.logits_bf16 != nullptr) {
+    uint16_t w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __ldg(p.logits_bf16 + at + min(lane + 32 * i, p.E - 1));
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = __uint_as_float(static_cast<uint32_t>(w[i]) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = __ldg(p.logits + at + min(lane + 32 * i, p.E - 1));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane + 32 * i >= p.E) l[i] = -INFINITY;
 }
 
 // What FP32 left open of a token: everything (all), or the order of the experts
@@ -192,7 +284,7 @@ struct Open {
 // narrow.
 template <int N, bool CHECK, typename F>
 __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N], const float (&bias)[N], float lmax,
-                                       F* keys, int* mine, Open* open) {
+                                       typename OrdOf<F>::type* keys, uint2* list, int* mine, Open* open) {
   using O = typename OrdOf<F>::type;
   const int lane = threadIdx.x & 31;
   const bool by_logit = p.bias == nullptr;
@@ -207,15 +299,16 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
         sum += v[i];
       }
       sum = warp_sum(sum);
+      const F by = sum == F(0) ? F(0) : inverse(sum);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = sum == F(0) ? F(0) : v[i] / sum;
+      for (int i = 0; i < N; ++i) v[i] *= by;
       // units of 2^-24: a term is 2 off by its exponential and 0.4 by its argument, the sum by that and its N + 5
-      // additions, the quotient 1
-      tol = 0x1p-24f * 2.f * (N + 12);
+      // additions, its reciprocal 2 and the product 1
+      tol = 0x1p-24f * 2.f * (N + 14);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = F(1) / (F(1) + exp_of(-static_cast<F>(l[i])));
-      tol = 0x1p-24f * 6.f;  // (0.5 by the exponential, two roundings)
+      for (int i = 0; i < N; ++i) v[i] = inverse(F(1) + exp_of(-static_cast<F>(l[i])));
+      tol = 0x1p-24f * 8.f;  // (0.5 by the exponential, 1 by the sum, 2 by the reciprocal)
     }
     if (!by_logit) {
 #pragma unroll
@@ -225,40 +318,46 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
   const float rel = 0x1p-24f * 3;  // (the bias joins with half a unit of the key)
   bool clear = true;
   uint32_t kept = kAll;
+  O key[N];
+  if (!by_logit || p.groups > 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = lane + 32 * i < p.E ? ordered(v[i]) : O(0);
+  }
   if (p.groups > 1) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (lane + 32 * i < p.E) keys[lane + 32 * i] = v[i];
+      if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
     clear = keep_groups<CHECK>(p, keys, tol, rel, &kept);
   }
-  const int size = p.E / p.groups;
   float least = 0.f;
   if (by_logit) {
     uint32_t lk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = lane + 32 * i;
-      lk[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(l[i]) : 0u;
+      lk[i] = e < p.E && (p.groups == 1 || ((kept >> group_of(p, e)) & 1)) ? ordered(l[i]) : 0u;
     }
-    top_k<N, false>(lk, p.k, 0.f, 0.f, mine, &least);
+    top_k<N, false>(lk, p.k, 0.f, 0.f, mine, &least, list);
     if (CHECK) open->all = true;
     return clear;
   }
-  O key[N];
+  if (p.groups > 1) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) ? ordered(v[i]) : O(0);
+    for (int i = 0; i < N; ++i)
+      if (!((kept >> group_of(p, lane + 32 * i)) & 1)) key[i] = 0;
   }
-  const bool order = top_k<N, CHECK>(key, p.k, tol, rel, mine, &least);
+  bool order;
+  if constexpr (CHECK)
+    order = top_k<N, true>(key, p.k, tol, rel, mine, &least, list);
+  else
+    order = top_k_in_turn<N, false>(key, p.k, tol, rel, mine, &least);
   if (CHECK && !(order && clear)) {
     const float below = least - (tol + rel * fabsf(least));
     open->all = !clear || p.score == SIXBIT_SCORE_SOFTMAX || !(fabsf(below) < INFINITY);
     open->listed = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      if (e < p.E && (p.groups == 1 || ((kept >> (e / size)) & 1)) && !(v[i] < F(below))) open->listed |= 1u << i;
+      if (key[i] != 0 && !(v[i] < F(below))) open->listed |= 1u << i;
     }
   }
   return order && clear;
@@ -274,14 +373,18 @@ template <int N>
 __device__ __forceinline__ void load_bias(const RouteParams& p, float (&bias)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < N; ++i) bias[i] = p.bias != nullptr && lane + 32 * i < p.E ? __ldg(p.bias + lane + 32 * i) : 0.f;
+  for (int i = 0; i < N; ++i) bias[i] = 0.f;
+  if (p.bias == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) bias[i] = __ldg(p.bias + min(lane + 32 * i, p.E - 1));
 }
 
 // A token again in FP64, a call of its own: its registers (two a key) are not the
 // fast path's.  With sigmoid scores only the listed experts, up to four a lane (an
 // exponential is some 60 FP64 instructions).
 template <int N>
-__device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax, double* keys, bool all, uint32_t listed) {
+__device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax, uint64_t* keys, uint2* list, bool all,
+                                     uint32_t listed) {
   const int lane = threadIdx.x & 31;
   int mine = 0;
   if (!all && !__any_sync(kAll, __popc(listed) > 4)) {
@@ -320,11 +423,10 @@ __device__ __noinline__ int choose64(const RouteParams& p, int64_t t, float lmax
     return mine;
   }
   float l[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
+  load_logits(p, t, l);
   float bias[N];
   load_bias(p, bias);
-  choose<N, false, double>(p, l, bias, lmax, keys, &mine, nullptr);
+  choose<N, false, double>(p, l, bias, lmax, keys, list, &mine, nullptr);
   return mine;
 }
 
@@ -387,7 +489,7 @@ __device__ __forceinline__ void scan(int* v, int n, int* part) {
 }
 
 // Shared memory: run [E + 1], mask [E], chosen [kBlock k], then with groups the
-// warps' keys, E doubles each.
+// warps' keys, E of 64 bits each.
 __host__ __device__ constexpr size_t keys_at(int E, int k) {
   return ((static_cast<size_t>(E) * 2 + 1 + kBlock * k) * 4 + 7) / 8 * 8;
 }
@@ -397,11 +499,12 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int part[kWarps];
+  __shared__ uint2 lists[kWarps][32];
   int* run = reinterpret_cast<int*>(smem);
   uint32_t* mask = reinterpret_cast<uint32_t*>(run + p.E + 1);
   int* chosen = reinterpret_cast<int*>(mask + p.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  double* keys = reinterpret_cast<double*>(smem + keys_at(p.E, p.k)) + static_cast<size_t>(p.groups > 1 ? warp : 0) * p.E;
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem + keys_at(p.E, p.k)) + static_cast<size_t>(p.groups > 1 ? warp : 0) * p.E;
   float bias[N];
   load_bias(p, bias);
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -415,17 +518,15 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
     for (int j = warp; j < kBlock && tb + j < t1; j += kWarps) {
       const int64_t t = tb + j;
       float l[N];
+      load_logits(p, t, l);
       uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        l[i] = lane + 32 * i < p.E ? logit_at(p, t, lane + 32 * i) : -INFINITY;
-        top = max(top, ordered(l[i]));
-      }
+      for (int i = 0; i < N; ++i) top = max(top, ordered(l[i]));
       const float lmax = value_of(warp_max(top));
       int mine = 0;
       Open open;
-      if (!choose<N, true, float>(p, l, bias, lmax, reinterpret_cast<float*>(keys), &mine, &open))
-        mine = choose64<N>(p, t, lmax, keys, open.all, open.listed);
+      if (!choose<N, true, float>(p, l, bias, lmax, reinterpret_cast<uint32_t*>(keys), lists[warp], &mine, &open))
+        mine = choose64<N>(p, t, lmax, keys, lists[warp], open.all, open.listed);
       const bool live = lane < p.k;
       const float w = weight_of<N>(p, l, lmax, live ? logit_at(p, t, mine) : -INFINITY, live);
       if (live) {
@@ -550,6 +651,8 @@ cudaError_t launch_moe_route(RouteParams p, cudaStream_t st) {
     ctas = static_cast<int>((static_cast<int64_t>(p.T) + p.tokens_per_cta - 1) / p.tokens_per_cta);
   }
   p.pitch = (p.E + 3) / 4 * 4;
+  const int size = p.E / p.groups;
+  p.per = ((1u << 20) + size - 1) / size;
   p.team = 0;
   while (p.groups << (p.team + 1) <= 32) ++p.team;
   if (p.E <= 32) return route::launch<1>(p, ctas, st);
