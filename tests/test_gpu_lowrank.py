@@ -99,7 +99,7 @@ def _mixed(m, count, seed=1):
     return torch.randint(-1, count, (m,), generator=g, dtype=torch.int32)
 
 
-@pytest.mark.parametrize("m", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 100, 257, 300, 1000])
+@pytest.mark.parametrize("m", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 100, 127, 128, 129, 257, 300, 1000])
 @pytest.mark.parametrize("int8", [True, False])
 def test_rows(ops, m, int8):
     for count in (1, 5, 40):
@@ -322,7 +322,7 @@ def test_empty_and_refusals(ops):
                 lambda: ops.lowrank_add(z(3, 256), w, ids), lambda: ops.lowrank_add(x, w, ids.long()),
                 lambda: ops.lowrank_add(x, w, ids[:2]), lambda: ops.lowrank_add(x, w, ids, z(3, 41)),
                 lambda: ops.lowrank_add(act, w, ids, residual=z(3, 40)), lambda: ops.lowrank_add(act, w, ids, out=z(3, 48)),
-                lambda: ops.lowrank_add(z(33, 128), w, z(33, dtype=torch.int32), ws=z(1, dtype=torch.uint8)),
+                lambda: ops.lowrank_add(z(129, 128), w, z(129, dtype=torch.int32), ws=z(1, dtype=torch.uint8)),
                 lambda: ops.pack_lowrank(z(2, 129, 128), z(2, 40, 129), None, 16),
                 lambda: ops.lowrank_add(x, ops.LowRank(z(2, 16, 128), z(2, 40, 16), z(3, dtype=torch.float32)), ids)):
         with pytest.raises(ValueError):

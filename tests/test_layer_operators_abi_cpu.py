@@ -89,10 +89,11 @@ def test_lowrank_add(lib, p):
             (ESHAPE, [dict(m=-1), dict(m=2**31 - 16), dict(n=0), dict(n=(1 << 20) + 1), dict(k=0), dict(k=64), dict(r=0),
                       dict(r=8), dict(r=24), dict(r=144), dict(l=0), dict(l=16385)]),
             (EINVAL, [dict(act=False), dict(codes=None), dict(scale=None), dict(a=None), dict(b=None), dict(ids=None),
-                      dict(y=None), dict(m=33, ws=None), dict(epi=2), dict(epi=3), dict(epi=-1), dict(base=p, bf=p)]),
+                      dict(y=None), dict(m=129, ws=None), dict(epi=2), dict(epi=3), dict(epi=-1), dict(base=p, bf=p)]),
             (EALIGN, [dict(codes=p + 8), dict(scale=p + 2), dict(x=p + 8), dict(a=p + 8), dict(b=p + 4), dict(al=p + 2),
                       dict(ids=p + 2), dict(base=p + 1), dict(bf=p + 2), dict(epi=2, res=p + 1), dict(y=p + 1),
                       dict(yf=p + 2), dict(ws=p + 8)]),
             (0, [dict(m=0, act=False, a=None, b=None, ids=None, y=None, ws=None)]))
-    for m in (0, 1, 32, 33, 1001):  # what the binding allocates
-        assert lib.sixbit_lowrank_workspace_bytes(m, 64) == (0 if m <= 32 else m * 64 * 6 + 2 * ((4 * m + 15) // 16 * 16))
+    for r, few in ((32, 128), (48, 64)):  # what the binding allocates
+        for m in (0, 1, few, few + 1, 1001):
+            assert lib.sixbit_lowrank_workspace_bytes(m, r) == (0 if m <= few else m * r * 6 + 2 * ((4 * m + 15) // 16 * 16))

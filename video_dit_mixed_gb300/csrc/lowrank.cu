@@ -14,9 +14,9 @@
 // rounding.
 //
 // Rows are taken in the order of their adapters, 32 positions a tile, so that an
-// MMA's rows share one however requests are mixed.  Up to 32 rows every warp sorts
-// them by itself, and one launch does both products; above, a counting sort goes
-// first.  The order of rows of one adapter is not fixed (atomics), and does not
+// MMA's rows share one however requests are mixed.  Of few rows (up to 64 or 128)
+// every warp sorts 32 by itself, and one launch does both products; of more a
+// counting sort goes first.  The order of rows of one adapter is not fixed (atomics), and does not
 // matter: a row's sums do not depend on its place.
 //
 // The floor is bytes, of which base and result are nearly all for many rows.
@@ -40,7 +40,9 @@ namespace lowrank {
 constexpr int kTile = 32;        // positions of a tile
 constexpr int kWarps = 8;
 constexpr int kUnit = 64;        // k of a warp's turn
-constexpr int kFew = kTile;      // rows that need no sorting kernel
+// Rows that need no sorting kernel.  (7680 x 1920, rank 16: 33 mixed rows 11 us against
+// 35, 128 21 against 24; rank 64: 64 rows 28 against 39, 128 51 against 31.)
+constexpr int few_rows(int R) { return R > 32 ? 64 : 128; }
 constexpr int kChunk = 256;      // positions of a CTA that applies B, at most
 constexpr int kManyBytes = 113 * 1024;  // its shared memory: two on an SM
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -186,9 +188,10 @@ __device__ __forceinline__ Tile tile_at(const LowRankParams& p, int64_t pos0) {
   mark_heads(t);
   return t;
 }
-// All rows, up to 32, sorted by the warp; scratch: 32 words of its own.
-__device__ __forceinline__ Tile tile_of_few(const LowRankParams& p, int* scratch, bool report) {
-  const int lane = threadIdx.x & 31, id = lane < p.M ? adapter_of(p, lane, report) : INT_MAX;
+// 32 rows from row0 on, sorted by the warp; scratch: 32 words of its own, which then
+// hold the rows.
+__device__ __forceinline__ Tile tile_of_few(const LowRankParams& p, int row0, int* scratch, bool report) {
+  const int lane = threadIdx.x & 31, id = row0 + lane < p.M ? adapter_of(p, row0 + lane, report) : INT_MAX;
   int rank = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
@@ -198,9 +201,11 @@ __device__ __forceinline__ Tile tile_of_few(const LowRankParams& p, int* scratch
   scratch[rank] = lane;
   __syncwarp();
   Tile t;
-  t.row = scratch[lane];
-  t.id = __shfl_sync(kAll, id, t.row);
-  if (t.id == INT_MAX) t.row = 0;
+  const int from = scratch[lane];
+  t.id = __shfl_sync(kAll, id, from);
+  t.row = t.id == INT_MAX ? 0 : row0 + from;
+  scratch[lane] = t.row;
+  __syncwarp();
   mark_heads(t);
   return t;
 }
@@ -626,17 +631,14 @@ __device__ __forceinline__ void finish_rows(const LowRankParams& p, const float 
     if (live[h] && n < p.N) store8(p, row[h] * p.N + n, y + 4 * h);
 }
 // The same for rows that are not 16-byte aligned: through the warp's `turn` [16][33],
-// so that a lane has one column of all 16 rows.  What is added to them, the base and
-// the residual, is loaded in front of the products.
-__device__ __forceinline__ void turn_load(const LowRankParams& p, const size_t (&row)[2], const bool (&live)[2], int n,
-                                          float (&add)[16]) {
+// so that a lane has one column of all 16 rows, rows[0 .. count) of them.  What is
+// added to them, the base and the residual, is loaded in front of the products.
+__device__ __forceinline__ void turn_load(const LowRankParams& p, const int* rows, int count, int n, float (&add)[16]) {
   // (dead rows read the first one's place: loads under a condition would wait for each other)
   size_t at[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4) != 0 && n < p.N;
-    const size_t from = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4) * p.N + n;
-    at[i] = in ? from : 0;
+    at[i] = i < count && n < p.N ? static_cast<size_t>(rows[i]) * p.N + n : 0;
     add[i] = 0.f;
   }
   if (p.base_f32 != nullptr) {
@@ -657,8 +659,8 @@ __device__ __forceinline__ void turn_load(const LowRankParams& p, const size_t (
     for (int i = 0; i < 16; ++i) add[i] += __uint_as_float(static_cast<uint32_t>(w[i]) << 16);
   }
 }
-__device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&acc)[4][4], const size_t (&row)[2],
-                                          const bool (&live)[2], int n0, const float (&add)[16], float* turn) {
+__device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&acc)[4][4], const int* rows, int count,
+                                          int n0, const float (&add)[16], float* turn) {
   const int lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3, n = n0 + lane;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -671,18 +673,20 @@ __device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&
   uint64_t y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    y[i] = f2_pack(turn[2 * i * 33 + lane] + add[2 * i], turn[(2 * i + 1) * 33 + lane] + add[2 * i + 1]);
+    y[i] = f2_add(f2_pack(turn[2 * i * 33 + lane], turn[(2 * i + 1) * 33 + lane]), f2_pack(add[2 * i], add[2 * i + 1]));
   if (p.epilogue == SIXBIT_EPI_GELU) gelu_pairs(y);
+  if (n < p.N) {
+    if (p.Yf != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const size_t at = __shfl_sync(kAll, row[i >> 3], (i & 7) * 4) * p.N + n;
-    const bool in = __shfl_sync(kAll, static_cast<int>(live[i >> 3]), (i & 7) * 4) != 0 && n < p.N;
-    if (!in) continue;
-    const float o = (i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2]);
-    if (p.Yf != nullptr)
-      p.Yf[at] = o;
-    else
-      p.Y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+      for (int i = 0; i < 16; ++i)
+        if (i < count) p.Yf[static_cast<size_t>(rows[i]) * p.N + n] = (i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < count)
+          p.Y[static_cast<size_t>(rows[i]) * p.N + n] =
+              __bfloat16_as_ushort(__float2bfloat16_rn((i & 1) ? f2_hi(y[i / 2]) : f2_lo(y[i / 2])));
+    }
   }
   __syncwarp();
 }
@@ -692,11 +696,11 @@ __host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 m
   const int bytes = R * 2 * PARTS;
   return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
 }
-// Up to 32 rows: everything in one launch.  A cluster of eight CTAs takes one of the
-// batch's runs and a share of the columns: its 64 warps split K, their sums meet in
+// Few rows: everything in one launch.  A cluster of eight CTAs takes one of a
+// tile's runs and a share of the columns: its 64 warps split K, their sums meet in
 // shared memory (the warps' of a CTA, then the CTAs' through the cluster), every CTA
 // keeps v in parts, and its warps go through their strips.  Grid: 8 shares of the
-// columns x runs (a cluster without one ends).
+// columns x slots (of a tile's runs; a cluster without one ends) x tiles.
 constexpr int kCluster = 8;
 template <int PARTS, int RT>
 constexpr int few_bytes(int R) {
@@ -714,103 +718,104 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
   const auto cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
   const int rank = blockIdx.x % kCluster, stride = v_stride<PARTS>(p.R);
-  const Tile t = tile_of_few(p, scratch[warp], blockIdx.x == 0 && blockIdx.y == 0 && warp == 0);
+  const Tile t = tile_of_few(p, blockIdx.z * kTile, scratch[warp], blockIdx.x == 0 && blockIdx.y == 0 && warp == 0);
   uint32_t left = t.heads;
-  for (unsigned turn = 0; turn < blockIdx.y; ++turn) left &= left - 1;
-  if (left == 0) return;  // (the same in the whole cluster)
-  const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
-  if (id >= 0) {
-    size_t at[4];
-    bool live[4];
+  for (int turn = 0; left != 0; ++turn, left &= left - 1) {  // (the same in the whole cluster)
+    if (turn % gridDim.y != blockIdx.y) continue;
+    const int first = __ffs(left) - 1, id = __shfl_sync(kAll, t.id, first), count = run_length(t, first);
+    if (id >= 0) {
+      size_t at[4];
+      bool live[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      live[i] = g8 + 8 * i < count;
-      at[i] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + g8 + 8 * i) & 31)) * p.K;
+      for (int i = 0; i < 4; ++i) {
+        live[i] = g8 + 8 * i < count;
+        at[i] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + g8 + 8 * i) & 31)) * p.K;
+      }
+      const float alpha = p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f;
+      for (int r0 = 0; r0 < p.R; r0 += 8 * RT) {
+        const int tiles = min(RT, (p.R - r0) / 8), quads = 2 * tiles;
+        sums_of<INT8, RT>(p, p.a + (static_cast<size_t>(id) * p.R + r0 + g8) * p.K, tiles, at, live, count,
+                          rank * kWarps + warp, kCluster * kWarps, part + warp * kTile * kP);
+        __syncthreads();
+        for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
+          float4* mine = reinterpret_cast<float4*>(&part[(i / quads) * kP + i % quads * 4]);
+          float4 v = *mine;
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) {
+            const float4 f = mine[w * kTile * kP / 4];
+            v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+          }
+          *mine = v;
+        }
+        cluster.sync();
+        for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
+          const int n = i / quads, r = i % quads * 4, row = scratch[0][first + n];
+          float v[4] = {};
+#pragma unroll
+          for (int z = 0; z < kCluster; ++z) {
+            const float4 f = *reinterpret_cast<const float4*>(&cluster.map_shared_rank(part, z)[n * kP + r]);
+            v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+          }
+          const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * alpha;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] *= f;
+          store_parts<PARTS>(vs + n * stride + (r0 + r) * (2 * PARTS), v);
+        }
+        cluster.sync();  // (no CTA writes its sums again, or leaves, while another reads them)
+      }
     }
-    const float alpha = p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f;
-    for (int r0 = 0; r0 < p.R; r0 += 8 * RT) {
-      const int tiles = min(RT, (p.R - r0) / 8), quads = 2 * tiles;
-      sums_of<INT8, RT>(p, p.a + (static_cast<size_t>(id) * p.R + r0 + g8) * p.K, tiles, at, live, count,
-                        rank * kWarps + warp, kCluster * kWarps, part + warp * kTile * kP);
-      __syncthreads();
-      for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
-        float4* mine = reinterpret_cast<float4*>(&part[(i / quads) * kP + i % quads * 4]);
-        float4 v = *mine;
+    for (int n0 = (blockIdx.x * kWarps + warp) * 32; n0 < p.N; n0 += gridDim.x * kWarps * 32) {
+      const int n = n0 + 8 * q;
+      for (int m = 0; m < count; m += 16) {
+        size_t row[2];
+        bool live[2];
+        Eight<true> wide[2] = {};
+        Eight<false> base[2] = {};
+        uint4 res[2] = {};
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float4 f = mine[w * kTile * kP / 4];
-          v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
-        }
-        *mine = v;
-      }
-      cluster.sync();
-      for (int i = threadIdx.x; i < count * quads; i += kWarps * 32) {
-        const int n = i / quads, r = i % quads * 4, row = scratch[0][first + n];
-        float v[4] = {};
-#pragma unroll
-        for (int z = 0; z < kCluster; ++z) {
-          const float4 f = *reinterpret_cast<const float4*>(&cluster.map_shared_rank(part, z)[n * kP + r]);
-          v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-        }
-        const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * alpha;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] *= f;
-        store_parts<PARTS>(vs + n * stride + (r0 + r) * (2 * PARTS), v);
-      }
-      cluster.sync();  // (no CTA writes its sums again, or leaves, while another reads them)
-    }
-  }
-  for (int n0 = (blockIdx.x * kWarps + warp) * 32; n0 < p.N; n0 += gridDim.x * kWarps * 32) {
-    const int n = n0 + 8 * q;
-    for (int m = 0; m < count; m += 16) {
-      size_t row[2];
-      bool live[2];
-      Eight<true> wide[2] = {};
-      Eight<false> base[2] = {};
-      uint4 res[2] = {};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        live[h] = g8 + 8 * h < count - m;
-        row[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31));
-        if (VEC && live[h] && n < p.N) {
-          if (p.base_f32 != nullptr)
-            wide[h].load(p, row[h] * p.N + n);
-          else
-            base[h].load(p, row[h] * p.N + n);
-          if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n);
-        }
-      }
-      float add[16];
-      if constexpr (!VEC) turn_load(p, row, live, n0 + lane, add);
-      float acc[4][4] = {};
-      if (id >= 0) {
-        const unsigned char* from = vs + (m + g8) * stride + q * 8 * PARTS;
-        for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
-          Strip<KS> strip;
-          strip.load(p, id, n0, s0);
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            if (BIG && s0 + s >= p.R / 16) break;
-            uint2 lo[PARTS], hi[PARTS];
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
-            step_mma<PARTS>(acc, lo, hi, strip.b[s]);
+        for (int h = 0; h < 2; ++h) {
+          live[h] = g8 + 8 * h < count - m;
+          row[h] = static_cast<size_t>(__shfl_sync(kAll, t.row, (first + m + g8 + 8 * h) & 31));
+          if (VEC && live[h] && n < p.N) {
+            if (p.base_f32 != nullptr)
+              wide[h].load(p, row[h] * p.N + n);
+            else
+              base[h].load(p, row[h] * p.N + n);
+            if (p.epilogue == SIXBIT_EPI_RESIDUAL) res[h] = *reinterpret_cast<const uint4*>(p.residual + row[h] * p.N + n);
           }
         }
-      }
-      if constexpr (VEC) {
-        if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
-          if (p.base_f32 != nullptr)
-            finish_rows<true, true>(p, acc, row, live, n, wide, res);
-          else
-            finish_rows<false, true>(p, acc, row, live, n, base, res);
-        } else if (p.base_f32 != nullptr) {
-          finish_rows<true, false>(p, acc, row, live, n, wide, res);
-        } else {
-          finish_rows<false, false>(p, acc, row, live, n, base, res);
+        float add[16];
+        if constexpr (!VEC) turn_load(p, scratch[warp] + first + m, count - m, n0 + lane, add);
+        float acc[4][4] = {};
+        if (id >= 0) {
+          const unsigned char* from = vs + (m + g8) * stride + q * 8 * PARTS;
+          for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
+            Strip<KS> strip;
+            strip.load(p, id, n0, s0);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              if (BIG && s0 + s >= p.R / 16) break;
+              uint2 lo[PARTS], hi[PARTS];
+              load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
+              load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
+              step_mma<PARTS>(acc, lo, hi, strip.b[s]);
+            }
+          }
         }
-      } else {
-        turn_rows(p, acc, row, live, n0, add, turns[warp]);
+        if constexpr (VEC) {
+          if (p.epilogue == SIXBIT_EPI_RESIDUAL) {
+            if (p.base_f32 != nullptr)
+              finish_rows<true, true>(p, acc, row, live, n, wide, res);
+            else
+              finish_rows<false, true>(p, acc, row, live, n, base, res);
+          } else if (p.base_f32 != nullptr) {
+            finish_rows<true, false>(p, acc, row, live, n, wide, res);
+          } else {
+            finish_rows<false, false>(p, acc, row, live, n, base, res);
+          }
+        } else {
+          turn_rows(p, acc, scratch[warp] + first + m, count - m, n0, add, turns[warp]);
+        }
       }
     }
   }
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
       const bool live[2] = {g8 < count, g8 + 8 < count};
       const size_t row[2] = {static_cast<size_t>(rows[at + g8]), static_cast<size_t>(rows[at + g8 + 8])};
       float add[16];
-      if constexpr (!VEC) turn_load(p, row, live, n0 + lane, add);
+      if constexpr (!VEC) turn_load(p, rows + at, count, n0 + lane, add);
       float acc[4][4] = {};
       if (id >= 0) {
         // (rows of the MMA that are not live hold anything: they stay apart)
@@ -956,7 +961,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
         ask(t + kAhead);
         finish_rows<F32, RES>(p, acc, row, live, n, base, res);
       } else {
-        turn_rows(p, acc, row, live, n0, add, turns[warp]);
+        turn_rows(p, acc, rows + at, count, n0, add, turns[warp]);
       }
     }
     copies_wait<0>();
@@ -993,10 +998,11 @@ cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
   const cudaError_t e =
       set_smem_once<few_kernel<VEC, INT8, PARTS, KS, BIG>>(few_bytes<PARTS, 2 * KS>(BIG ? SIXBIT_MAX_RANK : 16 * KS));
   if (e != cudaSuccess) return e;
-  // a strip a warp, as far as all runs' clusters together come to about two CTAs an SM
-  const int strips = (p.N + 31) / 32, most = 304 / kCluster / p.M > 0 ? 304 / kCluster / p.M : 1;
-  const int shares = (strips + kCluster * kWarps - 1) / (kCluster * kWarps);
-  Launch l(dim3(kCluster * (shares < most ? shares : most), p.M), kWarps * 32, smem, st, false, dim3(kCluster));
+  // a cluster for each run there may be and a strip a warp, as far as all clusters come to about two CTAs an SM
+  const int strips = (p.N + 31) / 32, shares = (strips + kCluster * kWarps - 1) / (kCluster * kWarps);
+  const int tiles = (p.M + kTile - 1) / kTile, all = 304 / kCluster / tiles, rows = p.M < kTile ? p.M : kTile;
+  const int slots = rows < all || tiles == 1 ? rows : all, most = all / slots > 0 ? all / slots : 1;
+  Launch l(dim3(kCluster * (shares < most ? shares : most), slots, tiles), kWarps * 32, smem, st, false, dim3(kCluster));
   note_launch();
   return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, INT8, PARTS, KS, BIG>, p);
 }
@@ -1082,7 +1088,7 @@ cudaError_t launch(const LowRankParams& p, cudaStream_t st) {
   const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
   const bool vec = p.N % 8 == 0 && a16(p.base) && a16(p.base_f32) && a16(p.residual) && a16(p.Y) && a16(p.Yf);
   const bool int8 = p.codes != nullptr, f32 = p.base_f32 != nullptr;
-  if (p.M <= kFew) {
+  if (p.M <= few_rows(p.R)) {
     if (vec) return int8 ? launch_few<true, true, PARTS>(p, st) : launch_few<true, false, PARTS>(p, st);
     return int8 ? launch_few<false, true, PARTS>(p, st) : launch_few<false, false, PARTS>(p, st);
   }
@@ -1099,11 +1105,11 @@ cudaError_t launch(const LowRankParams& p, cudaStream_t st) {
 size_t lowrank_workspace(int M, int R) {
   // v in up to three parts, the rows' order and their adapters
   const size_t rows = static_cast<size_t>(M), order = (rows * 4 + 15) / 16 * 16;
-  return M > lowrank::kFew ? rows * R * 6 + 2 * order : 0;
+  return M > lowrank::few_rows(R) ? rows * R * 6 + 2 * order : 0;
 }
 
 cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
-  if (p.M > lowrank::kFew) {
+  if (p.M > lowrank::few_rows(p.R)) {
     const size_t order = (static_cast<size_t>(p.M) * 4 + 15) / 16 * 16;
     p.perm = static_cast<int32_t*>(workspace);
     p.sid = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + order);

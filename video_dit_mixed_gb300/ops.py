@@ -718,7 +718,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    need = 0 if m <= 32 else m * r * 6 + 2 * ((4 * m + 15) // 16 * 16)  # sixbit_lowrank_workspace_bytes
+    need = 0 if m <= (64 if r > 32 else 128) else m * r * 6 + 2 * ((4 * m + 15) // 16 * 16)  # sixbit_lowrank_workspace_bytes
     if ws is None:
         if need:
             ws = _empty((need,), _U8, device, stream)
