@@ -156,6 +156,32 @@ def test_infinite_logits(ops):
     assert r.experts[3, 0] == 4 and r.weights[3, 0] == 1
 
 
+@pytest.mark.parametrize("e,k,groups", [(12, 2, 1), (12, 6, 3), (64, 8, 1), (64, 5, 8), (300, 10, 1), (300, 12, 4)])
+def test_infinite_and_nan_biases(ops, e, k, groups):
+    """Biases that put experts in front of or behind all others."""
+    z, bias = _logits(37, e, e + k)
+    for n, value in ((1, np.inf), (k - 1, np.inf), (k + 3, np.inf), (1, -np.inf), (e // 2, -np.inf), (e - 1, -np.inf), (2, 3e38)):
+        b = bias.clone()
+        b[torch.randperm(e, generator=torch.Generator().manual_seed(n))[:n]] = value
+        for score in (0, 1):
+            kw = dict(groups=groups, top_groups=(groups + 1) // 2)
+            if groups > 1 and value < 0:
+                continue  # (whole groups of the same score: any of them)
+            r = ops.moe_route(z.cuda(), k, score, bias=b.cuda(), **kw)
+            ex, w = _ref(z, k, bool(score), b, **kw)
+            assert np.array_equal(r.experts.cpu().numpy(), ex)
+            assert np.allclose(r.weights.cpu().numpy(), w, rtol=1e-5, atol=1e-30)
+            _check_places(r, e)
+    bias[[3, 5]] = np.nan  # first, by their numbers
+    r = ops.moe_route(z.cuda(), k, 1, bias=bias.cuda())
+    assert bool((r.experts[:, :2].cpu() == torch.tensor([3, 5])).all())
+    _check_places(r, e)
+    for value in (np.nan, np.inf, -np.inf):
+        r = ops.moe_route(z.cuda(), k, 1, bias=torch.full((e,), float(value)).cuda(), groups=groups, top_groups=groups)
+        assert bool((r.experts.cpu() == torch.arange(k)).all())  # all alike
+        _check_places(r, e)
+
+
 @pytest.mark.parametrize("groups", [1, 3])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_nan_logits_stay_in_their_row(ops, with_bias, groups):

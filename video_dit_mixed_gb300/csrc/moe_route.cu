@@ -23,8 +23,8 @@
 //
 // Bytes are next to nothing (4 an expert and token): it is bound by the chain of a
 // token's steps, a warp's maximum and the lowest lane that has it for each choice.
-// One token 3.3 us; 226 over 256 experts, 4 of 8 groups, top 8: 13; 17,776 over 64,
-// top 2: 17; 4,444 over 256 in groups 37.
+// One token 3.2 us; 226 over 256 experts, 4 of 8 groups, top 8: 10.6; 17,776 over 64,
+// top 2: 16; 4,444 over 256 in groups 29, 17,776 66.
 #include <cstdint>
 
 #include "common.cuh"
@@ -171,8 +171,8 @@ __device__ __forceinline__ bool top_k(const uint32_t (&key)[N], int k, float tol
     for (int i = 0; i < N; ++i) best = max(best, key[i]);
     uint32_t from = __shfl_sync(kAll, sorted(best), k - 1);
     if (CHECK && from != 0) {
-      const float v = value_of(from);
-      from = ordered(v - (tol + rel * fabsf(v)));
+      const float v = value_of(from), below = v - (tol + rel * fabsf(v));
+      from = below == below ? ordered(below) : 0;  // (an infinity or a NaN: all)
     }
     if (from == 0) from = 1;
     int total = 0;
@@ -202,7 +202,8 @@ __device__ __forceinline__ bool top_k(const uint32_t (&key)[N], int k, float tol
   const float v = value_of(o);
   *least = __shfl_sync(kAll, v, k - 1);
   // (what is not on the list is further away; lane 31 has no next)
-  return __all_sync(kAll, lane >= k || lane == 31 || next == 0 || v - value_of(next) > tol + rel * fabsf(v));
+  const bool apart = lane == 31 || next == 0 || v - value_of(next) > tol + rel * fabsf(v);
+  return __all_sync(kAll, lane >= k || (o != 0 && apart));
 }
 
 // Bits of the groups that are kept.  keys: the warp's E keys in shared memory.
@@ -528,6 +529,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant_
       if (!choose<N, true, float>(p, l, bias, lmax, reinterpret_cast<uint32_t*>(keys), lists[warp], &mine, &open))
         mine = choose64<N>(p, t, lmax, keys, lists[warp], open.all, open.listed);
       const bool live = lane < p.k;
+      mine = static_cast<int>(min(static_cast<unsigned>(mine), static_cast<unsigned>(p.E - 1)));  // (lanes beyond k hold anything)
       const float w = weight_of<N>(p, l, lmax, live ? logit_at(p, t, mine) : -INFINITY, live);
       if (live) {
         const size_t at = static_cast<size_t>(t) * p.k + lane;
