@@ -693,7 +693,8 @@ sixbit_status sixbit_graph_switch_end(sixbit_switch* sw);
 
 /*
  * Test setting for the GEMMs' failure path (every GEMM launched after the
- * call, process-wide).  Every wait in the GEMM kernels is bounded; this
+ * call, process-wide; and every sixbit_gated_rmsnorm_quant, whose copies of many
+ * rows are waited for in the same way).  Every wait in the GEMM kernels is bounded; this
  * lets a test make those waits run out on purpose, without faulting anything:
  * wait_limit_ns replaces the 2 s limit (0 restores it), and with
  * withhold_first_stage = 1 the producer of every CTA skips the copies of its

@@ -721,6 +721,10 @@ sixbit_status sixbit_gated_rmsnorm_quant(const uint16_t* X, const uint16_t* resi
     g.row_scale = out->row_scale;
   }
   g.err = err_dev;
+  GemmParams dbg;
+  gemm_debug_params(dbg);
+  g.wait_ns = dbg.wait_ns;
+  g.withhold_first = dbg.withhold_first;
   return cuda_status(launch_gated_norm(g, had_block, static_cast<cudaStream_t>(stream)));
 }
 

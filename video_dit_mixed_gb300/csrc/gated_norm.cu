@@ -193,11 +193,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
     if (lane == 0) {
       mbar_init(&arrived[warp], 1);
       fence_barrier_init();
-      if (copies && row0 + team < row1) fetch(row0 + team);
+      if (copies && row0 + team < row1 && !g.withhold_first) fetch(row0 + team);
     }
     __syncwarp();
   }
-  uint32_t buf = 0;
+  uint32_t buf = 0, lost = 0;
   bool dead = false;  // a copy did not arrive in time: reported, and waited for no more
 
   // One row; HELD: its factors are in shared memory from `mine` on.
@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
     const size_t base = static_cast<size_t>(row) * g.K;
     uint32_t xr[V][8], rr[V][8];
     if (STAGE) {
-      if (copies && !dead && !mbar_wait(&arrived[warp], buf, nullptr)) {
+      if (copies && !dead && !mbar_wait(&arrived[warp], buf, nullptr, g.wait_ns)) {
         dead = true;
+        lost = buf;
         set_error(g.err, SIXBIT_ETIMEOUT);
       }
     }
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
     }
     from = to;
   }
-  if (STAGE && dead) mbar_wait(&arrived[warp], buf, nullptr);  // (the copy in flight, once more with a limit)
+  if (STAGE && dead) mbar_wait(&arrived[warp], lost, nullptr, g.wait_ns);  // (the copy in flight, once more with a limit)
 }
 
 template <int V, int W, bool STAGE>

@@ -181,6 +181,8 @@ struct GatedNormParams {
   int8_t* codes;
   float* row_scale;
   int32_t* err;
+  uint64_t wait_ns;      // as in GemmParams
+  int withhold_first;
 };
 cudaError_t launch_gated_norm(const GatedNormParams& g, int b, cudaStream_t st);
 
