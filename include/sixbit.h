@@ -642,9 +642,10 @@ enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 16384 };
  * summed in FP32; A_l x enters the second product to 2^-16 of itself (2^-24 with Y_f32).
  * Epilogues as for sixbit_qgemm: NONE, GELU, RESIDUAL (+ residual [M, N] bf16).
  * Y [M, N] bf16, or Y_f32 when it is non-NULL; Y may be base or residual, Y_f32
- * base_f32 (in place).  M >= 0 (0: nothing is enqueued), 1 <= N <= 2^20,
- * K % 128 == 0, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, 1 <= L <= SIXBIT_MAX_ADAPTERS.  Codes, x_bf16,
- * lr_a, lr_b and the workspace 16-byte aligned, the others to their type.
+ * base_f32 (in place).  0 <= M <= 2^31 - 513 (0: nothing is enqueued), 1 <= N <=
+ * 2^20, K % 128 == 0, K <= 2^20, R % 16 == 0, 16 <= R <= SIXBIT_MAX_RANK, 1 <= L <=
+ * SIXBIT_MAX_ADAPTERS.  Codes, x_bf16, lr_a, lr_b and the workspace 16-byte aligned,
+ * the others to their type.
  * workspace: device memory of sixbit_lowrank_workspace_bytes(M, R) bytes (NULL
  * where that is 0), scratch.  With mode_dev, runs only when the mode word is INT8.
  */

@@ -86,7 +86,7 @@ def test_lowrank_add(lib, p):
                                       res, y, yf, ws, None, None)
 
     _expect(lib, call,
-            (ESHAPE, [dict(m=-1), dict(m=2**31 - 16), dict(n=0), dict(n=(1 << 20) + 1), dict(k=0), dict(k=64), dict(r=0),
+            (ESHAPE, [dict(m=-1), dict(m=2**31 - 16), dict(n=0), dict(n=(1 << 20) + 1), dict(k=0), dict(k=64), dict(k=(1 << 20) + 128), dict(r=0),
                       dict(r=8), dict(r=24), dict(r=144), dict(l=0), dict(l=16385)]),
             (EINVAL, [dict(act=False), dict(codes=None), dict(scale=None), dict(a=None), dict(b=None), dict(ids=None),
                       dict(y=None), dict(m=129, ws=None), dict(epi=2), dict(epi=3), dict(epi=-1), dict(base=p, bf=p)]),

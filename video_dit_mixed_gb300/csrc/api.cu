@@ -816,7 +816,7 @@ sixbit_status sixbit_lowrank_add(const sixbit_qact* A, const uint16_t* x_bf16, c
                                  int32_t* err_dev, void* stream) {
   if (epilogue != SIXBIT_EPI_NONE && epilogue != SIXBIT_EPI_GELU && epilogue != SIXBIT_EPI_RESIDUAL)
     return SIXBIT_EINVAL;
-  if (M < 0 || M > INT32_MAX - 32 || N < 1 || N > 1 << 20 || K <= 0 || K % 128 != 0 || R < 16 ||
+  if (M < 0 || M > INT32_MAX - 512 || N < 1 || N > 1 << 20 || K <= 0 || K > 1 << 20 || K % 128 != 0 || R < 16 ||
       R > SIXBIT_MAX_RANK || R % 16 != 0 || L < 1 || L > SIXBIT_MAX_ADAPTERS)
     return SIXBIT_ESHAPE;
   if (base != nullptr && base_f32 != nullptr) return SIXBIT_EINVAL;

@@ -16,15 +16,15 @@
 // Rows are taken in the order of their adapters, 32 positions a tile, so that an
 // MMA's rows share one however requests are mixed.  Of few rows (up to 64 or 128)
 // every warp sorts 32 by itself, and one launch does both products; of more a
-// counting sort goes first.  The order of rows of one adapter is not fixed (atomics), and does not
-// matter: a row's sums do not depend on its place.
+// counting sort goes first.  The order of rows of one adapter is not fixed (atomics),
+// and does not matter: a row's sums do not depend on its place.
 //
 // The floor is bytes, of which base and result are nearly all for many rows.
 // 17,776 x 7680 outputs, bf16 base and result: rank 16 118 us (floor 84), rank 64
 // with GELU 222 (GELU is 337 of a tile's some 530 instructions' worth of the FP32
 // pipe, 80 us by itself); 1920 outputs of K 7680, rank 64, residual: 120 (A's product
-// 70 of it).  One row beside 7680 x 1920 5.3 us, 32 rows of 32 requests beside 1920 x
-// 7680 8.9, 226 rows 19, 2000 mixed rows of 32 adapters 46.
+// 70 of it).  One row beside 7680 x 1920 4.9 us, 32 rows of 32 requests beside 1920 x
+// 7680 9.4, 226 rows 19, 2000 mixed rows of 32 adapters 46.
 #include <climits>
 #include <cooperative_groups.h>
 #include <cstdint>
