@@ -274,6 +274,8 @@ def test_refusals(ffn, ops):
     with pytest.raises(ValueError):
         ffn.FFN(up, down, down_adapters=lora)
     x = torch.zeros((3, hid), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        ffn.FFN(up, down, had_block=b)(x, adapters=torch.zeros(3, dtype=torch.int32, device="cuda"))
     layer = ffn.FFN(up, down, had_block=b, up_adapters=lora)
     with pytest.raises(ValueError):
         layer(x, adapters=torch.zeros(2, dtype=torch.int32, device="cuda"))

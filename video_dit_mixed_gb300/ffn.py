@@ -11,9 +11,9 @@ modulate the norm behind it:
 
     h = residual_scale residual + gate [post norm](x),  y = down(GELU(up(norm(h) (1 + scale) + shift)))
 
-and ``FFN`` may have low-rank adapters of many requests beside its projections.  Neither synchronises with the host.  Both run on the current stream and
-take their buffers from torch's allocator for the call, so that calls on different streams, from different threads or
-captured into CUDA graphs do not share any.
+and ``FFN`` may have low-rank adapters of many requests beside its projections.  Neither synchronises with the host.
+Both run on the current stream and take their buffers from torch's allocator for the call, so that calls on different
+streams, from different threads or captured into CUDA graphs do not share any.
 
 The products' waits are bounded.  One that runs out leaves its output unfinished and records that in the layer's
 ``err`` word; ``layer.check()`` waits for the stream and raises ``SixbitError`` then.
@@ -66,6 +66,8 @@ class FFN(_Layer):
                  segment=None, adapters: torch.Tensor | None = None):
         """gate, scale, shift, segment: as ops.gated_rmsnorm_quant takes them.  adapters: int32 [T] on the GPU, each
         token's adapter or -1 (None: no token has one)."""
+        if adapters is not None and self.up_adapters is None and self.down_adapters is None:
+            raise ValueError("adapters named of a layer that has none")
         a, h = self._norm(x, residual, gate, scale, shift, segment)
         if a.m == 0:
             return torch.empty_like(h), h
