@@ -639,7 +639,7 @@ enum { SIXBIT_MAX_RANK = 128, SIXBIT_MAX_ADAPTERS = 16384 };
  * [M, K] (A is ignored).  Codes are those of rotated rows, so the adapters' A has
  * to be rotated by the same blocks.  lr_a [L][R][K], lr_b [L][N][R] bf16, alpha [L]
  * float or NULL (1).  base [M, N] bf16, or base_f32, or neither (0).  Products are
- * summed in FP32; A_l x enters the second product to 2^-16 of itself (2^-24 with Y_f32).
+ * summed in FP32; A_l x enters the second product to 2^-24 of itself.
  * Epilogues as for sixbit_qgemm: NONE, GELU, RESIDUAL (+ residual [M, N] bf16).
  * Y [M, N] bf16, or Y_f32 when it is non-NULL; Y may be base or residual, Y_f32
  * base_f32 (in place).  0 <= M <= 2^31 - 513 (0: nothing is enqueued), 1 <= N <=

@@ -240,7 +240,8 @@ struct LowRankParams {
   float* Yf;
   const int32_t* mode_dev;
   int32_t* err;
-  void* v;                       // in the workspace, as are the rows' order and their adapters
+  void* v;                       // in the workspace: its first two parts,
+  void* v_last;                  // its third, the rows' order and their adapters
   int32_t* perm;
   int32_t* sid;
   int chunk, chunks_per_cta;     // set by the launch

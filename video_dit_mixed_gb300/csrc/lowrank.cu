@@ -9,9 +9,10 @@
 // product with B_l to the base and applies the epilogue.  Both run on
 // mma.m16n8k16 with bf16 operands and FP32 sums, rows as the 16-row operand.
 // Codes are exact in bf16.  v, with the row's scale and alpha on it, enters the
-// second product as two bf16 parts (v to 2^-16; three and 2^-24 where the result
-// is FP32): one part alone would add an error as large as the output's own
-// rounding.
+// second product as three bf16 parts, v to 2^-24 whatever the result's type.  (Of two,
+// 2^-16, the error passed a bf16 output's rounding where the base cancels the product,
+// and one output in 1,400 of 17,776 x 7680 was rounded to its other neighbour, where
+// now one in 5,600 is; GELU over them took 222 us.)
 //
 // Rows are taken in the order of their adapters, 32 positions a tile, so that an
 // MMA's rows share one however requests are mixed.  Of few rows (up to 64 or 128)
@@ -20,11 +21,11 @@
 // and does not matter: a row's sums do not depend on its place.
 //
 // The floor is bytes, of which base and result are nearly all for many rows.
-// 17,776 x 7680 outputs, bf16 base and result: rank 16 118 us (floor 84), rank 64
-// with GELU 222 (GELU is 337 of a tile's some 530 instructions' worth of the FP32
-// pipe, 80 us by itself); 1920 outputs of K 7680, rank 64, residual: 120 (A's product
-// 70 of it).  One row beside 7680 x 1920 4.9 us, 32 rows of 32 requests beside 1920 x
-// 7680 9.4, 226 rows 19, 2000 mixed rows of 32 adapters 46.
+// 17,776 x 7680 outputs, bf16 base and result: rank 16 119 us (floor 84), rank 64
+// with GELU 248 (GELU takes 80 us of the FP32 pipe by itself, the 48 MMAs of a tile of
+// 16 x 32 some 88 of theirs); 1920 outputs of K 7680, rank 64, residual: 126 (A's
+// product 70 of it).  One row beside 7680 x 1920 5.1 us, 32 rows of 32 requests beside
+// 1920 x 7680 9.5, 226 rows 20, 2000 mixed rows of 32 adapters 47.
 #include <climits>
 #include <cooperative_groups.h>
 #include <cstdint>
@@ -216,23 +217,30 @@ __device__ __forceinline__ int run_length(const Tile& t, int first) {
   return (later != 0 ? __ffs(later) - 1 : __popc(live)) - first;
 }
 
-// v as the second product takes it: for each position and four ranks PARTS times
-// four bf16.
-template <int PARTS>
-__device__ __forceinline__ void store_parts(unsigned char* to, float (&v)[4]) {
-  uint2* o = reinterpret_cast<uint2*>(to);
+// v as the second product takes it, three bf16 parts of four ranks at a time: for
+// each position and four ranks 16 bytes of the first two parts, and in an array
+// behind them 8 of the third.
+constexpr int kParts = 3;
+struct Parts {
+  uint4 first;  // [2][4]
+  uint2 last;   // [4]
+};
+__device__ __forceinline__ Parts parts_of(float (&v)[4]) {
+  uint2 w[kParts];
 #pragma unroll
-  for (int s = 0; s < PARTS; ++s) {
-    const uint2 w = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-    o[s] = w;
-    v[0] = rest(v[0], w.x << 16), v[1] = rest(v[1], w.x & 0xFFFF0000u);
-    v[2] = rest(v[2], w.y << 16), v[3] = rest(v[3], w.y & 0xFFFF0000u);
+  for (int s = 0; s < kParts; ++s) {
+    w[s] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    v[0] = rest(v[0], w[s].x << 16), v[1] = rest(v[1], w[s].x & 0xFFFF0000u);
+    v[2] = rest(v[2], w[s].y << 16), v[3] = rest(v[3], w[s].y & 0xFFFF0000u);
   }
+  return {make_uint4(w[0].x, w[0].y, w[1].x, w[1].y), w[2]};
 }
-
-template <int PARTS>
-__device__ __forceinline__ unsigned char* v_at(const LowRankParams& p, int64_t pos, int r) {
-  return static_cast<unsigned char*>(p.v) + (pos * (p.R / 4) + r / 4) * (8 * PARTS);
+// v of ranks r .. r + 3 of a position, to the workspace.
+__device__ __forceinline__ void store_v(const LowRankParams& p, int64_t pos, int r, float (&v)[4]) {
+  const Parts w = parts_of(v);
+  const int64_t at = pos * (p.R / 4) + r / 4;
+  static_cast<uint4*>(p.v)[at] = w.first;
+  static_cast<uint2*>(p.v_last)[at] = w.last;
 }
 
 // One warp's share of A_l x for up to 32 rows: k units first, first + step, ..., 8 RT
@@ -294,7 +302,7 @@ __device__ __forceinline__ void sums_of(const LowRankParams& p, const uint16_t* 
 // v of one tile.  Grid: tiles x slots x splits; slot s takes the tile's runs s,
 // s + slots, ...; a cluster of `splits` CTAs and their warps share K, and their
 // sums meet in shared memory in a fixed order.  RT: tiles of eight ranks at a time.
-template <bool INT8, int RT, int PARTS>
+template <bool INT8, int RT>
 __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankParams p) {
   namespace cg = cooperative_groups;
   next_may_start();
@@ -342,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) shrink_kernel(const LowRankPar
         const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * (p.alpha != nullptr ? __ldg(p.alpha + id) : 1.f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] *= f;
-        store_parts<PARTS>(v_at<PARTS>(p, pos0 + first + n, r0 + r), v);
+        store_v(p, pos0 + first + n, r0 + r, v);
       }
       if (gridDim.z > 1)
         cluster.sync();
@@ -384,7 +392,7 @@ struct Staged {
 // four neighbouring chunks of two rows, a half warp's 8-byte ones two of four.
 __device__ __forceinline__ int chunk256(int row, int ch) { return row * 256 + ((ch ^ ((row & 1) << 2)) << 4); }
 __device__ __forceinline__ int chunk128(int row, int ch) { return row * 128 + ((ch ^ ((row & 3) << 1)) << 4); }
-template <bool INT8, int RT, int PARTS>
+template <bool INT8, int RT>
 __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRankParams p) {
   using S = Staged<INT8, RT>;
   constexpr int kStages = S::kStages;
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(kStagedThreads, 2) staged_kernel(const LowRank
       const float4 f = *reinterpret_cast<const float4*>(&sums[n * S::kP + r]);
       const float by = (INT8 ? __ldg(p.row_scale + rows[n]) : 1.f) * alpha;
       float v[4] = {f.x * by, f.y * by, f.z * by, f.w * by};
-      store_parts<PARTS>(v_at<PARTS>(p, pos0 + n, r0 + r), v);
+      store_v(p, pos0 + n, r0 + r, v);
     }
     __syncthreads();
     first = end;
@@ -581,31 +589,16 @@ struct Strip {
       }
   }
 };
-// acc += the strip times a step of v: lo, hi: this lane's parts of rows g8 and g8 + 8.
-template <int PARTS>
-__device__ __forceinline__ void step_mma(float (&acc)[4][4], const uint2 (&lo)[PARTS], const uint2 (&hi)[PARTS],
-                                         const uint2 (&b)[4]) {
+// acc += the strip times a step of v, the smallest part first: lo, hi: this lane's
+// parts of rows g8 and g8 + 8.
+__device__ __forceinline__ void step_mma(float (&acc)[4][4], const Parts& lo, const Parts& hi, const uint2 (&b)[4]) {
+  const uint32_t a[kParts][4] = {{lo.last.x, hi.last.x, lo.last.y, hi.last.y},
+                                 {lo.first.z, hi.first.z, lo.first.w, hi.first.w},
+                                 {lo.first.x, hi.first.x, lo.first.y, hi.first.y}};
 #pragma unroll
-  for (int w = PARTS - 1; w >= 0; --w) {
-    const uint32_t a[4] = {lo[w].x, hi[w].x, lo[w].y, hi[w].y};
+  for (int w = 0; w < kParts; ++w)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) mma(acc[j], a, b[j].x, b[j].y);
-  }
-}
-template <int PARTS>
-__device__ __forceinline__ void load_v(const unsigned char* from, bool live, uint2 (&v)[PARTS]) {
-  const uint2* u = reinterpret_cast<const uint2*>(from);
-#pragma unroll
-  for (int w = 0; w < PARTS; ++w) v[w] = make_uint2(0, 0);
-  if (!live) return;
-  if constexpr (PARTS == 2) {
-    const uint4 f = *reinterpret_cast<const uint4*>(u);
-    v[0] = make_uint2(f.x, f.y);
-    v[1] = make_uint2(f.z, f.w);
-  } else {
-#pragma unroll
-    for (int w = 0; w < PARTS; ++w) v[w] = u[w];
-  }
+    for (int j = 0; j < 4; ++j) mma(acc[j], a[w], b[j].x, b[j].y);
 }
 // The outputs of a tile of 16 rows, columns n .. n + 7 of this lane's two.
 template <bool F32, bool RES>
@@ -691,22 +684,42 @@ __device__ __forceinline__ void turn_rows(const LowRankParams& p, const float (&
   __syncwarp();
 }
 
-template <int PARTS>
-__host__ __device__ constexpr int v_stride(int R) {  // bytes of a row's v; 64 more than a multiple of 128 spares conflicts
-  const int bytes = R * 2 * PARTS;
-  return PARTS == 2 ? (bytes % 128 == 0 ? bytes + 64 : bytes) : bytes + 16;
-}
+// Rows of v in shared memory, the first two parts and the third apart: a quarter warp
+// reads 64 bytes of each of two rows, then a half warp 32 of each of four, and with
+// these strides no two lie in the same banks (but for rank 128, whose rows have to
+// leave room for the base's and the residual's pieces).
+__host__ __device__ constexpr int first_stride(int R) { return R * 4 % 128 == 64 ? R * 4 : R * 4 + 64; }
+__host__ __device__ constexpr int last_stride(int R) { return R * 2 % 64 == 32 ? R * 2 : R * 2 + (R < 128 ? 32 : 16); }
+struct Held {  // v of some rows in shared memory
+  unsigned char *first, *last;
+  int first_row, last_row;
+  __device__ __forceinline__ Held(unsigned char* at, int rows, int R)
+      : first(at), last(at + rows * first_stride(R)), first_row(first_stride(R)), last_row(last_stride(R)) {}
+  // four ranks, quad q of step s
+  __device__ __forceinline__ uint4* first_of(int row, int s, int q) const {
+    return reinterpret_cast<uint4*>(first + row * first_row + s * 64 + q * 16);
+  }
+  __device__ __forceinline__ uint2* last_of(int row, int s, int q) const {
+    return reinterpret_cast<uint2*>(last + row * last_row + s * 32 + q * 8);
+  }
+  __device__ __forceinline__ Parts get(int row, int s, int q, bool live) const {
+    Parts w = {make_uint4(0, 0, 0, 0), make_uint2(0, 0)};
+    if (live) w = {*first_of(row, s, q), *last_of(row, s, q)};
+    return w;
+  }
+};
+__host__ __device__ constexpr int held_bytes(int rows, int R) { return rows * (first_stride(R) + last_stride(R)); }
 // Few rows: everything in one launch.  A cluster of eight CTAs takes one of a
 // tile's runs and a share of the columns: its 64 warps split K, their sums meet in
 // shared memory (the warps' of a CTA, then the CTAs' through the cluster), every CTA
 // keeps v in parts, and its warps go through their strips.  Grid: 8 shares of the
 // columns x slots (of a tile's runs; a cluster without one ends) x tiles.
 constexpr int kCluster = 8;
-template <int PARTS, int RT>
+template <int RT>
 constexpr int few_bytes(int R) {
-  return kWarps * kTile * (8 * RT + 4) * 4 + kTile * v_stride<PARTS>(R);
+  return kWarps * kTile * (8 * RT + 4) * 4 + held_bytes(kTile, R);
 }
-template <bool VEC, bool INT8, int PARTS, int KS, bool BIG>
+template <bool VEC, bool INT8, int KS, bool BIG>
 __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p) {
   namespace cg = cooperative_groups;
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
@@ -714,10 +727,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
   __shared__ int scratch[kWarps][32];
   __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
   constexpr int RT = 2 * KS, kP = 8 * RT + 4;
-  unsigned char* vs = reinterpret_cast<unsigned char*>(part + kWarps * kTile * kP);
+  const Held vs(reinterpret_cast<unsigned char*>(part + kWarps * kTile * kP), kTile, p.R);
   const auto cluster = cg::this_cluster();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
-  const int rank = blockIdx.x % kCluster, stride = v_stride<PARTS>(p.R);
+  const int rank = blockIdx.x % kCluster;
   const Tile t = tile_of_few(p, blockIdx.z * kTile, scratch[warp], blockIdx.x == 0 && blockIdx.y == 0 && warp == 0);
   uint32_t left = t.heads;
   for (int turn = 0; left != 0; ++turn, left &= left - 1) {  // (the same in the whole cluster)
@@ -759,7 +772,9 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
           const float f = (INT8 ? __ldg(p.row_scale + row) : 1.f) * alpha;
 #pragma unroll
           for (int c = 0; c < 4; ++c) v[c] *= f;
-          store_parts<PARTS>(vs + n * stride + (r0 + r) * (2 * PARTS), v);
+          const Parts w = parts_of(v);
+          *vs.first_of(n, 0, (r0 + r) / 4) = w.first;
+          *vs.last_of(n, 0, (r0 + r) / 4) = w.last;
         }
         cluster.sync();  // (no CTA writes its sums again, or leaves, while another reads them)
       }
@@ -788,17 +803,13 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
         if constexpr (!VEC) turn_load(p, scratch[warp] + first + m, count - m, n0 + lane, add);
         float acc[4][4] = {};
         if (id >= 0) {
-          const unsigned char* from = vs + (m + g8) * stride + q * 8 * PARTS;
           for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
             Strip<KS> strip;
             strip.load(p, id, n0, s0);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               if (BIG && s0 + s >= p.R / 16) break;
-              uint2 lo[PARTS], hi[PARTS];
-              load_v<PARTS>(from + (s0 + s) * 32 * PARTS, live[0], lo);
-              load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, live[1], hi);
-              step_mma<PARTS>(acc, lo, hi, strip.b[s]);
+              step_mma(acc, vs.get(m + g8, s0 + s, q, live[0]), vs.get(m + g8 + 8, s0 + s, q, live[1]), strip.b[s]);
             }
           }
         }
@@ -823,33 +834,36 @@ __global__ void __launch_bounds__(kWarps * 32) few_kernel(const LowRankParams p)
 
 // More rows.  Grid: groups of eight strips x chunks of positions, whose v, rows and
 // tiles (up to 16 positions of one adapter) the CTA keeps in shared memory.  Each
-// lane copies the base, and the residual, of its outputs kAhead tiles ahead into
+// lane copies the base, and the residual, of its outputs some tiles ahead into
 // pieces of its own: with one tile ahead, in registers, 16 KB an SM were on their
-// way, a quarter of what it takes.
-constexpr int kAhead = 3;
+// way, a quarter of what it takes.  Four tiles for rank 16, whose v is small, and two
+// above it, which leaves room for longer chunks (17,776 x 7680: rank 16 119 us and 124
+// with three; rank 32 to GELU 215, and 225 with three).
+__host__ __device__ constexpr int ahead_of(int KS) { return KS == 1 ? 4 : 2; }
 // Pieces of 16 bytes a lane has of each row: base, residual.
 template <bool VEC, bool F32>
 __host__ __device__ constexpr int pieces_of(bool residual) {
   return !VEC ? 0 : (F32 ? 2 : 1) + (residual ? 1 : 0);
 }
-template <bool VEC, bool F32, int PARTS>
-int many_bytes(int chunk, int R, bool residual) {
-  return (3 * chunk + 48) * 4 + (chunk + 16) * v_stride<PARTS>(R) + kWarps * kAhead * 1024 * pieces_of<VEC, F32>(residual);
+template <bool VEC, bool F32, int KS>
+constexpr int many_bytes(int chunk, int R, bool residual) {
+  return (3 * chunk + 48) * 4 + held_bytes(chunk + 16, R) + kWarps * ahead_of(KS) * 1024 * pieces_of<VEC, F32>(residual);
 }
-template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
+static_assert(many_bytes<true, true, 4>(kTile, SIXBIT_MAX_RANK, true) <= kManyBytes, "the smallest chunk fits");
+template <bool VEC, bool F32, bool RES, int KS, bool BIG>
 __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParams p) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float turns[VEC ? 1 : kWarps][16 * 33];
   __shared__ int counts[kWarps];
-  constexpr int kPieces = pieces_of<VEC, F32>(RES);
-  const int padded = p.chunk + 16, stride = v_stride<PARTS>(p.R);
+  constexpr int kPieces = pieces_of<VEC, F32>(RES), kAhead = ahead_of(KS);
+  const int padded = p.chunk + 16;
   int* rows = reinterpret_cast<int*>(smem);
   int* ids = rows + padded;
   int* tiles = ids + padded;  // where each begins, and the last ends
-  unsigned char* vs = smem + (3 * p.chunk + 48) * 4;
+  const Held vs(smem + (3 * p.chunk + 48) * 4, padded, p.R);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, q = lane & 3;
   const int n0 = (blockIdx.x * kWarps + warp) * 32, n = n0 + 8 * q;
-  unsigned char* ring = vs + padded * stride + warp * kAhead * 1024 * kPieces + lane * 16;
+  unsigned char* ring = vs.last + padded * vs.last_row + warp * kAhead * 1024 * kPieces + lane * 16;
   before_done();
   if (p.mode_dev != nullptr && SIXBIT_MODE_OF(*p.mode_dev) != SIXBIT_MODE_INT8) return;
   for (int chunk = 0; chunk < p.chunks_per_cta; ++chunk) {
@@ -857,10 +871,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
     if (pos0 >= p.M) break;
     const int live_rows = static_cast<int>(min(static_cast<int64_t>(p.chunk), p.M - pos0));
     if (chunk > 0) __syncthreads();
-    const int pieces = p.R * PARTS / 8;  // 16 bytes each, of a row's v
-    const unsigned char* v = static_cast<const unsigned char*>(p.v) + pos0 * (static_cast<size_t>(p.R) * 2 * PARTS);
-    for (int i = threadIdx.x; i < live_rows * pieces; i += kWarps * 32)
-      copy16(vs + (i / pieces) * stride + (i % pieces) * 16, v + static_cast<size_t>(i) * 16, true);
+    const int quads = p.R / 4;  // (a piece of 16 bytes each of the first parts, half of one of the last)
+    const uint4* first = static_cast<const uint4*>(p.v) + pos0 * quads;
+    const uint4* last = static_cast<const uint4*>(p.v_last) + pos0 * (quads / 2);
+    for (int i = threadIdx.x; i < live_rows * quads; i += kWarps * 32) copy16(vs.first_of(i / quads, 0, i % quads), first + i, true);
+    for (int i = threadIdx.x; i < live_rows * (quads / 2); i += kWarps * 32)
+      copy16(vs.last_of(i / (quads / 2), 0, i % (quads / 2) * 2), last + i, true);
     copies_commit();
     for (int i = threadIdx.x; i < padded; i += kWarps * 32) {
       rows[i] = i < live_rows ? p.perm[pos0 + i] : 0;
@@ -930,17 +946,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) many_kernel(const LowRankParam
       float acc[4][4] = {};
       if (id >= 0) {
         // (rows of the MMA that are not live hold anything: they stay apart)
-        const unsigned char* from = vs + (at + g8) * stride + q * 8 * PARTS;
         for (int s0 = 0; s0 < (BIG ? p.R / 16 : KS); s0 += KS) {
           if (BIG || held != id) strip.load(p, id, n0, s0);
           held = id;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             if (BIG && s0 + s >= p.R / 16) break;
-            uint2 lo[PARTS], hi[PARTS];
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS, true, lo);
-            load_v<PARTS>(from + (s0 + s) * 32 * PARTS + 8 * stride, true, hi);
-            step_mma<PARTS>(acc, lo, hi, strip.b[s]);
+            step_mma(acc, vs.get(at + g8, s0 + s, q, true), vs.get(at + g8 + 8, s0 + s, q, true), strip.b[s]);
           }
         }
       }
@@ -992,11 +1004,11 @@ struct Launch {
   }
 };
 
-template <bool VEC, bool INT8, int PARTS, int KS, bool BIG>
+template <bool VEC, bool INT8, int KS, bool BIG>
 cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
-  const int smem = few_bytes<PARTS, 2 * KS>(p.R);
+  const int smem = few_bytes<2 * KS>(p.R);
   const cudaError_t e =
-      set_smem_once<few_kernel<VEC, INT8, PARTS, KS, BIG>>(few_bytes<PARTS, 2 * KS>(BIG ? SIXBIT_MAX_RANK : 16 * KS));
+      set_smem_once<few_kernel<VEC, INT8, KS, BIG>>(few_bytes<2 * KS>(BIG ? SIXBIT_MAX_RANK : 16 * KS));
   if (e != cudaSuccess) return e;
   // a cluster for each run there may be and a strip a warp, as far as all clusters come to about two CTAs an SM
   const int strips = (p.N + 31) / 32, shares = (strips + kCluster * kWarps - 1) / (kCluster * kWarps);
@@ -1004,36 +1016,36 @@ cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
   const int slots = rows < all || tiles == 1 ? rows : all, most = all / slots > 0 ? all / slots : 1;
   Launch l(dim3(kCluster * (shares < most ? shares : most), slots, tiles), kWarps * 32, smem, st, false, dim3(kCluster));
   note_launch();
-  return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, INT8, PARTS, KS, BIG>, p);
+  return cudaLaunchKernelEx(&l.cfg, few_kernel<VEC, INT8, KS, BIG>, p);
 }
 
-template <bool VEC, bool INT8, int PARTS>
+template <bool VEC, bool INT8>
 cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
   switch (p.R) {
-    case 16: return launch_few<VEC, INT8, PARTS, 1, false>(p, st);
-    case 32: return launch_few<VEC, INT8, PARTS, 2, false>(p, st);
-    case 48: return launch_few<VEC, INT8, PARTS, 3, false>(p, st);
-    case 64: return launch_few<VEC, INT8, PARTS, 4, false>(p, st);
-    default: return launch_few<VEC, INT8, PARTS, 4, true>(p, st);
+    case 16: return launch_few<VEC, INT8, 1, false>(p, st);
+    case 32: return launch_few<VEC, INT8, 2, false>(p, st);
+    case 48: return launch_few<VEC, INT8, 3, false>(p, st);
+    case 64: return launch_few<VEC, INT8, 4, false>(p, st);
+    default: return launch_few<VEC, INT8, 4, true>(p, st);
   }
 }
 
-template <bool INT8, int RT, int PARTS>
+template <bool INT8, int RT>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   // For many rows x and A pass through shared memory: K 1920, rank 64, 2047 rows 44 us
   // against 56, but 1024 mixed ones 50 against 42; rank 16, 2047 rows 30.6 against 30.2,
   // 4096 44.1 against 44.0, 8192 69 against 70.
   if (p.M >= (p.R > 32 ? 1536 : 4096)) {
     constexpr int smem = Staged<INT8, RT>::kBytes;
-    const cudaError_t e = set_smem_once<staged_kernel<INT8, RT, PARTS>>(smem);
+    const cudaError_t e = set_smem_once<staged_kernel<INT8, RT>>(smem);
     if (e != cudaSuccess) return e;
     Launch l(dim3((p.M + kBlock - 1) / kBlock, (p.R + 8 * RT - 1) / (8 * RT), 2), kStagedThreads, smem, st, true);
     note_launch();
-    return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT, PARTS>, p);
+    return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT>, p);
   }
   constexpr int smem = kWarps * kTile * (8 * RT + 4) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT, PARTS>>(smem);
+    const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT>>(smem);
     if (e != cudaSuccess) return e;
   }
   // about two CTAs an SM: first up to four for a tile's runs, then K over clusters
@@ -1043,67 +1055,66 @@ cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   if (splits > kCluster) splits = kCluster;
   Launch l(dim3(tiles, slots, splits), kWarps * 32, smem, st, true, dim3(1, 1, splits));
   note_launch();
-  return cudaLaunchKernelEx(&l.cfg, shrink_kernel<INT8, RT, PARTS>, p);
+  return cudaLaunchKernelEx(&l.cfg, shrink_kernel<INT8, RT>, p);
 }
 
-template <bool INT8, int PARTS>
+template <bool INT8>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
-  if (p.R <= 16) return launch_shrink<INT8, 2, PARTS>(p, st);
-  if (p.R <= 32) return launch_shrink<INT8, 4, PARTS>(p, st);
-  if (p.R == 48 || p.R == 96) return launch_shrink<INT8, 6, PARTS>(p, st);
-  return launch_shrink<INT8, 8, PARTS>(p, st);
+  if (p.R <= 16) return launch_shrink<INT8, 2>(p, st);
+  if (p.R <= 32) return launch_shrink<INT8, 4>(p, st);
+  if (p.R == 48 || p.R == 96) return launch_shrink<INT8, 6>(p, st);
+  return launch_shrink<INT8, 8>(p, st);
 }
 
-template <bool VEC, bool F32, bool RES, int PARTS, int KS, bool BIG>
+template <bool VEC, bool F32, bool RES, int KS, bool BIG>
 cudaError_t launch_many(LowRankParams p, cudaStream_t st) {
-  // the largest chunks that let two CTAs share an SM, smaller ones where they would leave SMs idle
+  // the largest chunks that let two CTAs share an SM (rank 64, residual: 160 positions), smaller ones where they would leave SMs idle
   const int groups = ((p.N + 31) / 32 + kWarps - 1) / kWarps;
   p.chunk = kChunk;
-  while (p.chunk > kTile && (many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES) > kManyBytes ||
-                             static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304))
-    p.chunk /= 2;
+  while (many_bytes<VEC, F32, KS>(p.chunk, p.R, RES) > kManyBytes) p.chunk -= kTile;
+  while (p.chunk > kTile && static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304)
+    p.chunk = p.chunk / 2 > kTile ? (p.chunk / 2 + 15) / 16 * 16 : kTile;
   const int chunks = (p.M + p.chunk - 1) / p.chunk;
   p.chunks_per_cta = (chunks + 65534) / 65535;
-  const cudaError_t e = set_smem_once<many_kernel<VEC, F32, RES, PARTS, KS, BIG>>(kManyBytes);
+  const cudaError_t e = set_smem_once<many_kernel<VEC, F32, RES, KS, BIG>>(kManyBytes);
   if (e != cudaSuccess) return e;
   Launch l(dim3(groups, (chunks + p.chunks_per_cta - 1) / p.chunks_per_cta), kWarps * 32,
-           many_bytes<VEC, F32, PARTS>(p.chunk, p.R, RES), st, true);
+           many_bytes<VEC, F32, KS>(p.chunk, p.R, RES), st, true);
   note_launch();
-  return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, RES, PARTS, KS, BIG>, p);
+  return cudaLaunchKernelEx(&l.cfg, many_kernel<VEC, F32, RES, KS, BIG>, p);
 }
 
-template <bool VEC, bool F32, bool RES, int PARTS>
+template <bool VEC, bool F32, bool RES>
 cudaError_t launch_many(const LowRankParams& p, cudaStream_t st) {
   switch (p.R) {
-    case 16: return launch_many<VEC, F32, RES, PARTS, 1, false>(p, st);
-    case 32: return launch_many<VEC, F32, RES, PARTS, 2, false>(p, st);
-    case 48: return launch_many<VEC, F32, RES, PARTS, 3, false>(p, st);
-    case 64: return launch_many<VEC, F32, RES, PARTS, 4, false>(p, st);
-    default: return launch_many<VEC, F32, RES, PARTS, 4, true>(p, st);
+    case 16: return launch_many<VEC, F32, RES, 1, false>(p, st);
+    case 32: return launch_many<VEC, F32, RES, 2, false>(p, st);
+    case 48: return launch_many<VEC, F32, RES, 3, false>(p, st);
+    case 64: return launch_many<VEC, F32, RES, 4, false>(p, st);
+    default: return launch_many<VEC, F32, RES, 4, true>(p, st);
   }
 }
 
-template <int PARTS>
 cudaError_t launch(const LowRankParams& p, cudaStream_t st) {
   const auto a16 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
   const bool vec = p.N % 8 == 0 && a16(p.base) && a16(p.base_f32) && a16(p.residual) && a16(p.Y) && a16(p.Yf);
   const bool int8 = p.codes != nullptr, f32 = p.base_f32 != nullptr;
   if (p.M <= few_rows(p.R)) {
-    if (vec) return int8 ? launch_few<true, true, PARTS>(p, st) : launch_few<true, false, PARTS>(p, st);
-    return int8 ? launch_few<false, true, PARTS>(p, st) : launch_few<false, false, PARTS>(p, st);
+    if (vec) return int8 ? launch_few<true, true>(p, st) : launch_few<true, false>(p, st);
+    return int8 ? launch_few<false, true>(p, st) : launch_few<false, false>(p, st);
   }
-  const cudaError_t e = int8 ? launch_shrink<true, PARTS>(p, st) : launch_shrink<false, PARTS>(p, st);
+  const cudaError_t e = int8 ? launch_shrink<true>(p, st) : launch_shrink<false>(p, st);
   if (e != cudaSuccess) return e;
-  if (!vec) return launch_many<false, false, false, PARTS>(p, st);
+  if (!vec) return launch_many<false, false, false>(p, st);
   if (p.epilogue == SIXBIT_EPI_RESIDUAL)
-    return f32 ? launch_many<true, true, true, PARTS>(p, st) : launch_many<true, false, true, PARTS>(p, st);
-  return f32 ? launch_many<true, true, false, PARTS>(p, st) : launch_many<true, false, false, PARTS>(p, st);
+    return f32 ? launch_many<true, true, true>(p, st) : launch_many<true, false, true>(p, st);
+  return f32 ? launch_many<true, true, false>(p, st) : launch_many<true, false, false>(p, st);
 }
 
 }  // namespace lowrank
 
 size_t lowrank_workspace(int M, int R) {
-  // v in up to three parts, the rows' order and their adapters
+  // v in three parts, the rows' order and their adapters
   const size_t rows = static_cast<size_t>(M), order = (rows * 4 + 15) / 16 * 16;
   return M > lowrank::few_rows(R) ? rows * R * 6 + 2 * order : 0;
 }
@@ -1114,6 +1125,7 @@ cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
     p.perm = static_cast<int32_t*>(workspace);
     p.sid = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + order);
     p.v = static_cast<uint8_t*>(workspace) + 2 * order;
+    p.v_last = static_cast<uint8_t*>(p.v) + static_cast<size_t>(p.M) * p.R * 4;
     const int smem = 2 * (p.L + 1) * 4;
     if (smem > 48 * 1024) {
       const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
@@ -1126,7 +1138,7 @@ cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
     if (e != cudaSuccess) return e;
   }
-  return p.Yf != nullptr ? lowrank::launch<3>(p, st) : lowrank::launch<2>(p, st);
+  return lowrank::launch(p, st);
 }
 
 }  // namespace sixbit
