@@ -208,7 +208,7 @@ __device__ __forceinline__ bool top_k(const uint32_t (&key)[N], int k, float tol
 
 // Bits of the groups that are kept.  keys: the warp's E keys in shared memory.
 template <bool CHECK, typename O>
-__device__ __forceinline__ bool keep_groups(const RouteParams& p, const O* keys, float tol, float rel, uint32_t* kept) {
+__device__ __forceinline__ bool keep_groups(const RouteParams& p, const O* keys, float tol, uint32_t* kept) {
   const int lane = threadIdx.x & 31, size = p.E / p.groups;
   __syncwarp();
   // 1 << p.team lanes a group, each every so many keys of it; their two largest are joined in a tree
@@ -230,19 +230,29 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const O* keys,
   // lane g: group g's
   const int from = (lane << p.team) & 31;
   a = __shfl_sync(kAll, a, from), b = __shfl_sync(kAll, b, from);
-  O score = lane < p.groups ? (p.best > 1 && size > 1 ? ordered(value_of(a) + value_of(b)) : a) : O(0);
+  const bool two = p.best > 1 && size > 1;
+  O score = lane < p.groups ? (two ? ordered(value_of(a) + value_of(b)) : a) : O(0);
+  const O sum = score;
   uint32_t bits = 0;
-  O top = 0;
   for (int j = 0; j < p.top_groups; ++j) {
-    top = warp_max(score);
+    const O top = warp_max(score);
     const int g = __ffs(__ballot_sync(kAll, score == top)) - 1;
     bits |= 1u << g;
     if (lane == g) score = 0;
   }
   bool clear = true;
-  if (CHECK && p.top_groups < p.groups) {  // (which of the kept comes first does not matter)
-    const float v = static_cast<float>(value_of(top)), next = static_cast<float>(value_of(warp_max(score)));
-    clear = v - next > 2.f * tol + rel * fabsf(v);
+  if constexpr (CHECK) {
+    if (p.top_groups < p.groups) {  // (which of the kept comes first does not matter)
+      // A key is off by its score's error and 2^-24 of its own size, however small the sum that it cancels in, and the sum
+      // by that of both keys and 2^-24 of its own; a quarter more, and the sum's once more, for the arithmetic here.
+      // An infinite bias is exact.  (What overflows leaves a NaN, which is not clear.)
+      const float fa = value_of(a), fb = two ? value_of(b) : 0.f, s = value_of(sum);
+      const float off = fa == -INFINITY || fb == -INFINITY ? 0.f : 0x1.4p-24f * (fabsf(fa) + fabsf(fb) + 2.f * fabsf(s));
+      const bool in = (bits >> lane) & 1;
+      const float least = value_of(__reduce_min_sync(kAll, in ? ordered(s - off) : kAll));
+      const float next = value_of(__reduce_max_sync(kAll, in || lane >= p.groups ? 0u : ordered(s + off)));
+      clear = least - next > 2.f * tol;
+    }
   }
   __syncwarp();
   *kept = bits;
@@ -328,7 +338,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[N]
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
-    clear = keep_groups<CHECK>(p, keys, tol, rel, &kept);
+    clear = keep_groups<CHECK>(p, keys, tol, &kept);
   }
   float least = 0.f;
   if (by_logit) {
