@@ -1044,10 +1044,8 @@ cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
     return cudaLaunchKernelEx(&l.cfg, staged_kernel<INT8, RT>, p);
   }
   constexpr int smem = kWarps * kTile * (8 * RT + 4) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT>>(smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT>>(smem);
+  if (e != cudaSuccess) return e;
   // about two CTAs an SM: first up to four for a tile's runs, then K over clusters
   const int tiles = (p.M + kTile - 1) / kTile, most = 304 / tiles > 0 ? 304 / tiles : 1, slots = most < 4 ? most : 4;
   const int turns = (p.K / kUnit + kWarps - 1) / kWarps, left = most / slots > 0 ? most / slots : 1;
@@ -1127,15 +1125,13 @@ cudaError_t launch_lowrank(LowRankParams p, void* workspace, cudaStream_t st) {
     p.v = static_cast<uint8_t*>(workspace) + 2 * order;
     p.v_last = static_cast<uint8_t*>(p.v) + static_cast<size_t>(p.M) * p.R * 4;
     const int smem = 2 * (p.L + 1) * 4;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
-      if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = set_smem_once<lowrank::plan_kernel>(2 * (SIXBIT_MAX_ADAPTERS + 1) * 4);
+    if (e != cudaSuccess) return e;
     // (a cluster where one CTA would go around more than once)
     const int ctas = p.M > lowrank::kPlanAtOnce * lowrank::kPlanThreads ? lowrank::kPlanCluster : 1;
     lowrank::Launch l(dim3(ctas), lowrank::kPlanThreads, smem, st, false, dim3(ctas));
     note_launch();
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
+    e = cudaLaunchKernelEx(&l.cfg, lowrank::plan_kernel, p);
     if (e != cudaSuccess) return e;
   }
   return lowrank::launch(p, st);

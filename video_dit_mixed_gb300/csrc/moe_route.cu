@@ -505,6 +505,10 @@ __host__ __device__ constexpr size_t keys_at(int E, int k) {
   return ((static_cast<size_t>(E) * 2 + 1 + kBlock * k) * 4 + 7) / 8 * 8;
 }
 
+// (with the kernel's static shared memory, 4 KB, below what a CTA can have)
+constexpr int kSmemBytes = 200 * 1024;
+static_assert(keys_at(SIXBIT_MAX_EXPERTS, SIXBIT_MAX_TOP_K) + kWarps * SIXBIT_MAX_EXPERTS * 8 <= kSmemBytes, "the largest launch");
+
 template <int N>
 __global__ void __launch_bounds__(kThreads) choose_kernel(const __grid_constant__ RouteParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -628,14 +632,12 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const RouteParams p) {
 
 template <int N>
 cudaError_t launch(const RouteParams& p, int ctas, cudaStream_t st) {
-  size_t smem = keys_at(p.E, p.k) + (p.groups > 1 ? static_cast<size_t>(kWarps) * p.E * 8 : 0);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = set_smem_once<choose_kernel<N>>(200 * 1024);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = keys_at(p.E, p.k) + (p.groups > 1 ? static_cast<size_t>(kWarps) * p.E * 8 : 0);
+  cudaError_t e = set_smem_once<choose_kernel<N>>(kSmemBytes);
+  if (e != cudaSuccess) return e;
   note_launch();
   choose_kernel<N><<<ctas, kThreads, smem, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
