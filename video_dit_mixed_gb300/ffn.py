@@ -99,7 +99,8 @@ class MoEFFN(_Layer):
 
     Each token goes to the top_k experts of softmax(router h), or with normed_router of softmax(router norm(h)), as
     a pre-norm block trains it (norm_weight included); their outputs are summed with the probabilities renormalised
-    over those experts.  The router reads the new stream h in bf16, in FP32.  score, bias (float32 [E]), groups,
+    over those experts.  The router reads the new stream h in bf16, in FP32; where it requires a gradient, y and route()'s
+    weights carry one to it (y to nothing else: the quantized products have none).  score, bias (float32 [E]), groups,
     top_groups, group_best, renormalize and route_scale are ops.moe_route's; post_weight and residual_scale are
     FFN's."""
 
@@ -134,10 +135,10 @@ class MoEFFN(_Layer):
         """(row of each token's choices [T, k], weights [T, k], token of each row [T k], offsets int32 [E + 1]): the
         T k rows are sorted by expert, rows of one expert by token.  On the host the default rule alone."""
         logits = self.logits(h)
-        k = min(self.top_k, ops.MAX_TOP_K)
-        if k == self.top_k and logits.is_cuda:
-            r = ops.moe_route(logits, k, **self.rule)
-            return r.rows.long(), r.weights, r.token.long(), r.offsets
+        if self.top_k <= ops.MAX_TOP_K and logits.is_cuda:
+            r = ops.moe_route(logits, self.top_k, **self.rule)
+            weights = self._weights(logits, r.experts.long()) if logits.requires_grad else r.weights
+            return r.rows.long(), weights, r.token.long(), r.offsets
         if not self.plain_rule:
             raise ValueError(f"this rule routes on the GPU, to {ops.MAX_TOP_K} experts at most")
         top = logits.topk(self.top_k, dim=1)
@@ -148,6 +149,16 @@ class MoEFFN(_Layer):
         rows[order] = torch.arange(order.numel(), device=order.device)
         return rows.view_as(weights), weights, order // self.top_k, offsets
 
+    def _weights(self, logits: torch.Tensor, experts: torch.Tensor) -> torch.Tensor:
+        """The chosen experts' weights by torch operations, which carry a gradient to the router."""
+        chosen = logits.gather(1, experts)
+        sigmoid = self.rule["score"] == ops.SCORE_SIGMOID
+        if self.rule["renormalize"]:  # (the logarithms of sigmoid scores: their softmax is the scores over their sum)
+            w = torch.softmax(torch.nn.functional.logsigmoid(chosen) if sigmoid else chosen, dim=1)
+        else:
+            w = torch.sigmoid(chosen) if sigmoid else torch.softmax(logits, dim=1).gather(1, experts)
+        return w if self.rule["scale"] == 1.0 else w * self.rule["scale"]
+
     def __call__(self, x: torch.Tensor, residual: torch.Tensor | None = None, gate=None, scale=None, shift=None,
                  segment=None):
         """gate, scale, shift, segment: as ops.gated_rmsnorm_quant takes them (no scale or shift with normed_router)."""
@@ -156,14 +167,16 @@ class MoEFFN(_Layer):
         a, h = self._norm(x, residual, gate, scale, shift, segment)
         if a.m == 0:
             return torch.empty_like(h), h
-        if self.top_k <= ops.MAX_TOP_K:
-            _, weights, rows, token, offsets = ops.moe_route(self.logits(h), self.top_k, **self.rule)
+        logits = self.logits(h)
+        fused = self.top_k <= ops.MAX_TOP_K and not logits.requires_grad
+        if fused:
+            _, weights, rows, token, offsets = ops.moe_route(logits, self.top_k, **self.rule)
         else:
             rows, weights, token, offsets = self.route(h)
         a = ops.int8_act(a.i8_codes[token], a.row_scale[token])
         u = ops.qgemm_grouped(a, self.up, offsets, ops.EPI_GELU, err=self.err)
         q = ops.hadamard_quant(u, self.had_block, ops.MODE_INT8, out=ops.QActTensors(*u.shape, u.device, nvfp4=False))
         d = ops.qgemm_grouped(q, self.down, offsets, out_f32=True, err=self.err)
-        if self.top_k <= ops.MAX_TOP_K:
+        if fused:
             return ops.moe_combine(d, rows, weights, err=self.err), h
         return (d[rows] * weights.unsqueeze(-1)).sum(1).to(torch.bfloat16), h
