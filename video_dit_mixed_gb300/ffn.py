@@ -20,9 +20,11 @@ The products' waits are bounded.  One that runs out leaves its output unfinished
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
-from . import ops
+from . import abi, ops
 
 
 class _Layer:
@@ -120,8 +122,24 @@ class MoEFFN(_Layer):
         self.rule = dict(score=score, bias=bias, groups=groups, top_groups=top_groups, group_best=group_best,
                          renormalize=renormalize, scale=route_scale)
         self.plain_rule = score == ops.SCORE_SOFTMAX and bias is None and groups == 1 and renormalize and route_scale == 1.0
+        self._check_rule(up.experts)
         self.ids = torch.arange(up.experts + 1, device=router.device)
         self.err = torch.zeros(1, dtype=torch.int32, device=up.i4_codes.device)
+
+    def _check_rule(self, e: int) -> None:
+        """Refuses a rule that no call could follow: as ops.moe_route would, but when the layer is built."""
+        r = self.rule
+        bias, groups, top_groups = r["bias"], r["groups"], r["top_groups"]
+        if bias is not None and (tuple(bias.shape) != (e,) or bias.dtype != torch.float32 or not bias.is_contiguous() or
+                                 bias.device != self.router.device):
+            raise ValueError(f"bias: dense float32 [{e}] on {self.router.device} expected")
+        if self.top_k > ops.MAX_TOP_K and not self.plain_rule:
+            raise ValueError(f"this rule routes to {ops.MAX_TOP_K} experts at most, not to {self.top_k}")
+        if (r["score"] not in (ops.SCORE_SOFTMAX, ops.SCORE_SIGMOID) or r["group_best"] not in (1, 2) or
+                not math.isfinite(r["scale"]) or not 1 <= groups <= ops.MAX_GROUPS or e % groups or
+                not 1 <= top_groups <= groups or self.top_k > top_groups * (e // groups)):
+            raise abi.SixbitError(f"MoEFFN: no rule of routing {self.top_k} of {e} experts: "
+                                  + ", ".join(f"{k} {v}" for k, v in r.items() if k != "bias"))
 
     def logits(self, h: torch.Tensor) -> torch.Tensor:
         """The router's logits [T, E] of the stream h."""
