@@ -561,7 +561,8 @@ size_t sixbit_qgemm_grouped_workspace_bytes(int M, int K);
  * segment[m], a DEVICE array of int32 in [0, S), or with segment NULL the run of
  * M / S consecutive rows that m lies in (S must divide M).  A segment outside
  * [0, S) is reported as SIXBIT_EDEVICE in err_dev and gives that row's outputs NaN
- * (scale NaN, codes 0).
+ * (scale NaN, codes 0).  So does a copy within the kernel that has not arrived after
+ * 2 s, reported as SIXBIT_ETIMEOUT, to its row and the rows that were to follow it.
  * X, residual, sum_out, Y [M, K] bf16; sum_out may be NULL, X or residual (in
  * place).  Zero rows and rows that hold infinities or NaN, or whose squares'
  * sums overflow FP32, as for sixbit_add_rmsnorm_quant.  M >= 0 (0: nothing is

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
     __syncwarp();
   }
   uint32_t buf = 0, lost = 0;
-  bool dead = false;  // a copy did not arrive in time: reported, and waited for no more
+  bool dead = false;  // a copy did not arrive in time: reported, waited for no more, and this and later rows NaN
 
   // One row; HELD: its factors are in shared memory from `mine` on.
   auto process = [&](auto held, int64_t row, int seg, const float4* mine) {
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
         lost = buf;
         set_error(g.err, SIXBIT_ETIMEOUT);
       }
+      if (dead) seg = -1;  // (what shared memory holds is another row's, or nothing)
     }
     auto part_of = [&](const unsigned char* from, int v, uint32_t (&r)[8]) {
       const uint4* q = reinterpret_cast<const uint4*>(from + (v * 32 + lane) * 32);
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const Params p) {
     }
     if (seg < 0 || seg >= g.S) {
       seg = 0;
-      if (lane == 0) set_error(g.err, SIXBIT_EDEVICE);
+      if (lane == 0 && !dead) set_error(g.err, SIXBIT_EDEVICE);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
