@@ -450,6 +450,9 @@ def qgemm_grouped(a: QActTensors, w: Int4Weights, offsets: torch.Tensor, epilogu
 
 # ---- what stands around those products --------------------------------------
 
+_route_workspace_bytes, _lowrank_workspace_bytes = _lib.sixbit_moe_route_workspace_bytes, _lib.sixbit_lowrank_workspace_bytes
+
+
 def _gpu(t, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -574,7 +577,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
         pe, pw, pr = (_ptr(out.experts, "experts", _I32, tk, dev), _ptr(out.weights, "weights", _F32, tk, dev),
                       _ptr(out.rows, "rows", _I32, tk, dev))
         pt, po = _ptr(out.token, "token", _I32, (t * top_k,), dev), _ptr(out.offsets, "offsets", _I32, (e + 1,), dev)
-    need = 0 if t <= 32 else 304 * ((e + 3) // 4 * 4) * 4  # sixbit_moe_route_workspace_bytes
+    need = _route_workspace_bytes(t, e)
     if ws is None:
         if need:
             ws = _empty((need,), _U8, logits.device, stream)
@@ -588,7 +591,7 @@ def moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias
 
 
 def moe_route_workspace_bytes(t: int, e: int) -> int:
-    return int(_lib.sixbit_moe_route_workspace_bytes(t, e))
+    return int(_route_workspace_bytes(t, e))
 
 
 def moe_combine(d: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor, out=None, out_f32: bool = False, err=None,
@@ -718,7 +721,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
         if epilogue != EPI_RESIDUAL:
             raise ValueError("a residual without the residual epilogue")
         pr = _ptr(residual, "residual", _BF16, (m, n), dev)
-    need = 0 if m <= (64 if r > 32 else 128) else m * r * 6 + 2 * ((4 * m + 15) // 16 * 16)  # sixbit_lowrank_workspace_bytes
+    need = _lowrank_workspace_bytes(m, r)
     if ws is None:
         if need:
             ws = _empty((need,), _U8, device, stream)
@@ -733,7 +736,7 @@ def lowrank_add(x, w: LowRank, ids: torch.Tensor, base: torch.Tensor | None = No
 
 
 def lowrank_workspace_bytes(m: int, r: int) -> int:
-    return int(_lib.sixbit_lowrank_workspace_bytes(m, r))
+    return int(_lowrank_workspace_bytes(m, r))
 
 
 def check_err(err: torch.Tensor, what: str, stream=None) -> None:
