@@ -24,6 +24,17 @@ def test_a_base_that_cancels(ops, m, n, r, int8):  # noqa: F811
     assert torch.equal(got, f32.to(torch.bfloat16))  # the same sums, rounded once
 
 
+@pytest.mark.parametrize("r", [16, 32, 48, 64, 96, 128])
+@pytest.mark.parametrize("base,epilogue", [("bf16", "none"), ("f32", "residual")])
+def test_long_chunks(ops, r, base, epilogue):  # noqa: F811
+    """Rows and columns enough for a CTA to keep as many positions as shared memory holds."""
+    m, n = 2700, 7680
+    c = Case(m, n, 128, r, 4, _mixed(m, 4, r).sort().values, base=base, epilogue=epilogue)
+    want, err = c.ref(3)
+    got = c.call(ops).double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= err + _half_ulp(np.abs(want) + err))
+
+
 @pytest.mark.parametrize("m", [3, 300, 4200])
 @pytest.mark.parametrize("out_f32", [False, True])
 def test_an_infinity_keeps_its_sign(ops, m, out_f32):  # noqa: F811

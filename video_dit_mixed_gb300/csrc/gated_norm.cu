@@ -25,7 +25,8 @@
 // x 7680 67, 2,777 x 12288 79; 1,003 x 7680 gated, to bf16, 23 (floor 9); one row
 // 3.5, 226 rows 4.8.  It is bound by issue and dependence: some 385 instructions a
 // warp for 512 elements, which issue in half of the cycles.  (A CTA a row, one chunk
-// a lane: 66 us, 730 instructions; two rows a CTA at once spilled and took 74.)
+// a lane: 66 us, 730 instructions; two rows a CTA at once spilled and took 74.  Four
+// chunks a lane spill too, 60 to 200 bytes a thread, read again in L1.)
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

@@ -188,7 +188,7 @@ cudaError_t launch_gated_norm(const GatedNormParams& g, int b, cudaStream_t st);
 
 // Routing (sixbit_moe_route).  counts: workspace, [kRouteRuns][pitch].
 constexpr int kRouteTurn = 32;   // tokens of a turn; up to these one CTA does all and needs no workspace
-constexpr int kRouteRuns = 304;  // runs of tokens, a CTA each: two an SM
+constexpr int kRouteRuns = 304;  // runs of tokens, a CTA each: two for each SM (above 64 experts their registers leave room for one at a time)
 struct RouteParams {
   const float* logits;           // [T][E], or
   const uint16_t* logits_bf16;

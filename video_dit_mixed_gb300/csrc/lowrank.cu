@@ -1010,9 +1010,10 @@ cudaError_t launch_few(const LowRankParams& p, cudaStream_t st) {
   const cudaError_t e =
       set_smem_once<few_kernel<VEC, INT8, KS, BIG>>(few_bytes<2 * KS>(BIG ? SIXBIT_MAX_RANK : 16 * KS));
   if (e != cudaSuccess) return e;
-  // a cluster for each run there may be and a strip a warp, as far as all clusters come to about two CTAs an SM
+  // a cluster for each run there may be and a strip a warp, as far as all clusters come to about two CTAs an SM (above
+  // rank 32 a CTA's 162 to 240 registers a thread leave room for one at a time, and the second follows it)
   const int strips = (p.N + 31) / 32, shares = (strips + kCluster * kWarps - 1) / (kCluster * kWarps);
-  const int tiles = (p.M + kTile - 1) / kTile, all = 304 / kCluster / tiles, rows = p.M < kTile ? p.M : kTile;
+  const int tiles = (p.M + kTile - 1) / kTile, all = 2 * sm_count() / kCluster / tiles, rows = p.M < kTile ? p.M : kTile;
   const int slots = rows < all || tiles == 1 ? rows : all, most = all / slots > 0 ? all / slots : 1;
   Launch l(dim3(kCluster * (shares < most ? shares : most), slots, tiles), kWarps * 32, smem, st, false, dim3(kCluster));
   note_launch();
@@ -1034,7 +1035,9 @@ template <bool INT8, int RT>
 cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   // For many rows x and A pass through shared memory: K 1920, rank 64, 2047 rows 44 us
   // against 56, but 1024 mixed ones 50 against 42; rank 16, 2047 rows 30.6 against 30.2,
-  // 4096 44.1 against 44.0, 8192 69 against 70.
+  // 4096 44.1 against 44.0, 8192 69 against 70.  (The border lies where mixed rows need
+  // it: rows in runs would gain from 1024 on at K 7680, 56 against 60, mixed ones lose,
+  // 96 against 64.)
   if (p.M >= (p.R > 32 ? 1536 : 4096)) {
     constexpr int smem = Staged<INT8, RT>::kBytes;
     const cudaError_t e = set_smem_once<staged_kernel<INT8, RT>>(smem);
@@ -1047,7 +1050,8 @@ cudaError_t launch_shrink(const LowRankParams& p, cudaStream_t st) {
   const cudaError_t e = set_smem_once<shrink_kernel<INT8, RT>>(smem);
   if (e != cudaSuccess) return e;
   // about two CTAs an SM: first up to four for a tile's runs, then K over clusters
-  const int tiles = (p.M + kTile - 1) / kTile, most = 304 / tiles > 0 ? 304 / tiles : 1, slots = most < 4 ? most : 4;
+  const int tiles = (p.M + kTile - 1) / kTile, ctas = 2 * sm_count();
+  const int most = ctas / tiles > 0 ? ctas / tiles : 1, slots = most < 4 ? most : 4;
   const int turns = (p.K / kUnit + kWarps - 1) / kWarps, left = most / slots > 0 ? most / slots : 1;
   int splits = turns < left ? turns : left;
   if (splits > kCluster) splits = kCluster;
@@ -1070,7 +1074,7 @@ cudaError_t launch_many(LowRankParams p, cudaStream_t st) {
   const int groups = ((p.N + 31) / 32 + kWarps - 1) / kWarps;
   p.chunk = kChunk;
   while (many_bytes<VEC, F32, KS>(p.chunk, p.R, RES) > kManyBytes) p.chunk -= kTile;
-  while (p.chunk > kTile && static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 304)
+  while (p.chunk > kTile && static_cast<int64_t>(groups) * ((p.M + p.chunk - 1) / p.chunk) < 2 * sm_count())
     p.chunk = p.chunk / 2 > kTile ? (p.chunk / 2 + 15) / 16 * 16 : kTile;
   const int chunks = (p.M + p.chunk - 1) / p.chunk;
   p.chunks_per_cta = (chunks + 65534) / 65535;

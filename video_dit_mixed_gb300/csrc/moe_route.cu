@@ -19,7 +19,9 @@
 // at a time: the choices set one bit for each token in a word for each expert, so
 // that a choice's rank among the run's is a count of bits below its own, whatever
 // order the warps came in.  The runs' counts go to the workspace, and a second
-// kernel adds what lies before each run (a single run needs none).
+// kernel adds what lies before each run (a single run needs none).  Up to 64 experts
+// two CTAs share an SM; above, their 101 to 128 registers a thread leave room for one,
+// and above 256 a token's keys spill.
 //
 // Bytes are next to nothing (4 an expert and token): it is bound by the chain of a
 // token's steps, a warp's maximum and the lowest lane that has it for each choice.
